@@ -102,6 +102,7 @@ enum {
 #define PA_FLAG_SLOT_OOB        0x4u  /* slot_mapping[t] >= num_blocks * block_size */
 #define PA_FLAG_POSITION_OOB    0x8u  /* positions[t] outside [0, max_pos) */
 #define PA_FLAG_TIMEOUT         0x10u /* a copy into shared memory did not land in time */
+#define PA_FLAG_POOL_EXHAUSTED  0x20u /* pa_plan_step: the free list did not reach for a sequence */
 
 /*
  * pa_rope_kv_store -- fused RoPE + KV-cache store for `num_tokens` new tokens
@@ -342,6 +343,217 @@ int pa_decode_step_fp8(const pa_dims* dims, int num_seqs, const void* q, const v
                        const int32_t* block_tables, int max_blocks, const int32_t* context_lens,
                        int max_context_len, float scale, int partition_tokens, void* workspace,
                        size_t workspace_bytes, void* out, unsigned flags, void* stream);
+
+/*
+ * RoPE tables and forms -- [PV] §1 computes RoPE with rotate_half over the whole head from a
+ * table the caller brings; models in use also pair adjacent dims, rotate part of the head, and
+ * stretch the angles for contexts longer than they were trained on.
+ *
+ *  - Rotary dims R: the first R of the head's 128 dims rotate, the others pass through
+ *    unchanged (q and k alike).  R is a multiple of 16 in [16, 128].
+ *  - Layout: PA_ROPE_HALF pairs dims (i, i + R/2), PA_ROPE_INTERLEAVED dims (2i, 2i + 1), for
+ *    i < R/2; pair (x, y) with angle a becomes (x cos a - y sin a, y cos a + x sin a), in fp32
+ *    within about two ulps (even where the products nearly cancel), rounded once to bf16 RNE.
+ *  - Table: cos_sin [max_pos][R] fp32, row p = cos(p w_0 .. p w_{R/2-1}) | sin(...).
+ */
+enum { PA_ROPE_HALF = 0, PA_ROPE_INTERLEAVED = 1 };
+
+typedef struct pa_rope {
+  int32_t rotary_dim; /* R */
+  int32_t layout;     /* PA_ROPE_HALF or PA_ROPE_INTERLEAVED */
+} pa_rope;
+
+/*
+ * How the angles per position w_i = theta^(-2i/R) are stretched; t_i = original_max_pos w_i /
+ * (2 pi) is the number of turns of pair i over the original context:
+ *   PA_ROPE_SCALE_NONE    w_i
+ *   PA_ROPE_SCALE_LINEAR  w_i / factor
+ *   PA_ROPE_SCALE_NTK     the base grows: theta' = theta factor^(R/(R-2))
+ *   PA_ROPE_SCALE_YARN    pairs of many turns keep w_i, pairs of few take w_i / factor, between
+ *                         them a ramp r_i = clamp((i - a)/(b - a), 0, 1) mixes w_i (1 - r_i) +
+ *                         w_i/factor r_i, where d(t) = R ln(original_max_pos / (2 pi t)) / (2 ln
+ *                         theta), a = floor d(high) and b = ceil d(low), both clamped to [0, R - 1] (b - a
+ *                         taken as 0.001 where they are equal); cos and sin are multiplied by
+ *                         `magnitude`, or by 0.1 ln(factor) + 1 where that is 0
+ *   PA_ROPE_SCALE_BANDED  m_i = clamp((t_i - low)/(high - low), 0, 1); w_i m_i + w_i/factor (1 - m_i)
+ */
+enum {
+  PA_ROPE_SCALE_NONE = 0,
+  PA_ROPE_SCALE_LINEAR = 1,
+  PA_ROPE_SCALE_NTK = 2,
+  PA_ROPE_SCALE_YARN = 3,
+  PA_ROPE_SCALE_BANDED = 4
+};
+
+typedef struct pa_rope_scaling {
+  double theta;             /* base, finite and > 1 */
+  double factor;            /* finite and >= 1 (read by every kind but NONE) */
+  double original_max_pos;  /* YARN, BANDED: finite and > 0 */
+  double low, high;         /* YARN, BANDED: turns, 0 < low < high, finite */
+  double magnitude;         /* YARN: factor on cos and sin, finite and >= 0 (0: 0.1 ln(factor) + 1) */
+  int32_t kind;             /* PA_ROPE_SCALE_* */
+} pa_rope_scaling;
+
+/*
+ * pa_rope_table -- build cos_sin [max_pos][rotary_dim] on the GPU.  The angles per position are
+ * computed on the host in 64 bits; the kernel forms p w_i modulo a whole turn in 64-bit fixed
+ * point, so a far position loses nothing, and rounds cos and sin to fp32.
+ *   max_pos     rows, >= 1
+ *   cos_sin     [max_pos][rotary_dim] fp32, written
+ * Returns PA_OK, PA_ERR_NULL, PA_ERR_SHAPE (rotary_dim), PA_ERR_RANGE, PA_ERR_ALIGN or
+ * PA_ERR_CUDA (nothing launched on error).  Launches one kernel.
+ */
+int pa_rope_table(const pa_rope_scaling* scaling, int rotary_dim, int max_pos, float* cos_sin,
+                  void* stream);
+
+/*
+ * pa_rope_kv_store_form -- pa_rope_kv_store with a RoPE form, the rotated q written to q_out
+ * (which may be q itself; otherwise the two must not overlap).
+ *   rope     form; NULL means {128, PA_ROPE_HALF}.  PA_ERR_SHAPE for a bad rotary_dim or layout
+ *   cos_sin  [max_pos][rotary_dim] fp32
+ * Everything else as pa_rope_kv_store; a token whose position is out of range has its q copied
+ * to q_out unrotated.  The slots of one call must be distinct (which token's K and V a slot
+ * named twice holds is unspecified).
+ */
+int pa_rope_kv_store_form(const pa_dims* dims, const pa_rope* rope, int num_tokens, const void* q,
+                          void* q_out, const void* k, const void* v, const int32_t* positions,
+                          const float* cos_sin, int max_pos, const int64_t* slot_mapping,
+                          void* k_cache, void* v_cache, int num_blocks, void* stream);
+
+/*
+ * Block-scaled E4M3 cache -- the E4M3 caches above with a scale for each (block, KV head) in
+ * place of one per KV head, so that a token of large magnitude costs precision in its own block
+ * only and no scale has to be known beforehand ([NV] §学习要点, [15x] §未来展望; the pages fix no
+ * format, the reading below is this library's).
+ *
+ *  - kv_scale [num_blocks][Hkv][2] fp32: the K scale, then the V scale.  Element = code * scale.
+ *    The stores write powers of two in [2^-40, 2^40] only, and read what they find; the
+ *    attention calls take any scale in that range (not checked).
+ *  - The scale a set of values wants: the smallest power of two s with amax <= 448 s, clamped to
+ *    that range, amax their largest finite magnitude.  A power of two costs nothing: E4M3 is a
+ *    floating-point format.
+ *  - Storing into a block, per KV head, for K and for V: the call's tokens that go to the block
+ *    want a scale s.  When one of them goes to slot 0 the block begins anew: its scale becomes s
+ *    and slots the call does not write hold nothing.  Otherwise, with `old` the block's scale,
+ *    the scale becomes max(old, s); where that is more than old, the codes of the slots the call
+ *    does not write are coded anew, E4M3(fp32(value of the code) * fp32(old / s)) -- exact for a
+ *    power of two except for codes that become subnormal -- and where it is not, they are left.
+ *    The tokens' codes are E4M3(fp32(x) * fp32(1 / scale)), coded as above (saturating, NaN kept).
+ *  - A block is written by one sequence only (a shared block is copied before it is written, its
+ *    scales with it).
+ */
+
+/*
+ * pa_rope_kv_store_fp8_block -- pa_rope_kv_store_form into block-scaled E4M3 caches.  The rows
+ * of a call that go to one block follow one another, with at most 15 padding (or skipped) rows
+ * between two of them, as the rows of a sequence do; rows of one block in two places of the call
+ * give that block unspecified contents.
+ *   kv_scale  [num_blocks][Hkv][2] fp32, read and written at the blocks stored to
+ * Everything else as pa_rope_kv_store_form.  Launches one kernel.
+ */
+int pa_rope_kv_store_fp8_block(const pa_dims* dims, const pa_rope* rope, int num_tokens,
+                               const void* q, void* q_out, const void* k, const void* v,
+                               const int32_t* positions, const float* cos_sin, int max_pos,
+                               const int64_t* slot_mapping, void* k_cache, void* v_cache,
+                               float* kv_scale, int num_blocks, void* stream);
+
+/*
+ * pa_decode_fp8_block -- pa_decode over block-scaled E4M3 caches.  Arguments, workspace (same
+ * size: pa_decode_workspace_size), checks and errors as pa_decode, plus kv_scale ([num_blocks]
+ * [Hkv][2] fp32, read only).  Launches one kernel plus the merge.
+ */
+int pa_decode_fp8_block(const pa_dims* dims, int num_seqs, const void* q, const void* k_cache,
+                        const void* v_cache, const float* kv_scale, int num_blocks,
+                        const int32_t* block_tables, int max_blocks, const int32_t* context_lens,
+                        int max_context_len, float scale, int partition_tokens, void* workspace,
+                        size_t workspace_bytes, void* out, void* stream);
+
+/*
+ * pa_decode_step_fp8_block -- pa_decode_step over block-scaled E4M3 caches with a RoPE form:
+ * equals pa_rope_kv_store_fp8_block (position context_lens[s] - 1, that position's slot; the
+ * codes and scales bit for bit) followed by pa_decode_fp8_block, with q left unchanged.  A
+ * position without a cos/sin row: as pa_decode_step.  Arguments as pa_decode_step plus rope
+ * (as pa_rope_kv_store_form) and kv_scale (read, and written at the new tokens' blocks).
+ */
+int pa_decode_step_fp8_block(const pa_dims* dims, const pa_rope* rope, int num_seqs, const void* q,
+                             const void* k, const void* v, const float* cos_sin, int max_pos,
+                             void* k_cache, void* v_cache, float* kv_scale, int num_blocks,
+                             const int32_t* block_tables, int max_blocks,
+                             const int32_t* context_lens, int max_context_len, float scale,
+                             int partition_tokens, void* workspace, size_t workspace_bytes,
+                             void* out, unsigned flags, void* stream);
+
+/*
+ * pa_prefill_fp8_block -- pa_prefill over block-scaled E4M3 caches (whose new tokens
+ * pa_rope_kv_store_fp8_block has stored): the queries of a chunk see every cached token, the
+ * chunk's own among them, as the cache holds it.  Arguments, checks and errors as pa_prefill,
+ * plus kv_scale (read only).  A query whose every block is out of range gives a zero row.
+ * Launches one kernel.
+ */
+int pa_prefill_fp8_block(const pa_dims* dims, int num_seqs, int num_tokens, const void* q,
+                         const int32_t* q_start, int max_query_len, const void* k_cache,
+                         const void* v_cache, const float* kv_scale, int num_blocks,
+                         const int32_t* block_tables, int max_blocks, const int32_t* context_lens,
+                         int max_context_len, float scale, void* out, void* stream);
+
+/*
+ * pa_plan_step -- the metadata of one serving step built on the GPU from request lengths ([ME]
+ * §3.1: the block table of a sequence, grown by blocks taken from the free list; §3.2
+ * append_slot, for any number of new tokens; §3.3: the rows of a chunk): what pa_rope_kv_store*,
+ * pa_decode* and pa_prefill* read, without a round trip to the host.
+ *
+ * Sequence s holds c = cached_lens[s] tokens and brings n = new_lens[s] (>= 0).  In order of s:
+ *   rows         start_s = sum of n over the sequences before s; q_start[s] = start_s, and
+ *                q_start[num_seqs] = the sum of all
+ *   need_s       ceil((c + n) / 16) - ceil(c / 16) blocks, entries ceil(c / 16) .. of the
+ *                sequence's table row; entry number x of all the sequences' new entries in
+ *                order takes free_blocks[F - 1 - x], where F = num_free[0] (a stack, taken
+ *                from its end)
+ *   granted      s is granted its blocks when need_s == 0 or the new entries up to and including
+ *                its own are at most F; so once one sequence is refused, every later one that
+ *                needs a block is (PA_FLAG_POOL_EXHAUSTED).  granted[s] = 1 or 0
+ *   context      context_lens[s] = c + n, or 0 when refused (its rows stay in q_start, so the
+ *                attention calls give them zeros or skip them; nothing of it is stored)
+ *   token i      row r = start_s + i: positions[r] = c + i, slot_mapping[r] = table entry of
+ *                block (c + i) / 16 * 16 + (c + i) % 16; position 0 and slot -1 (padding, for
+ *                the stores) when refused
+ *   rows q_start[num_seqs] .. num_tokens - 1 get position 0 and slot -1, so that a captured step
+ *                of a fixed number of rows can be replayed with fewer
+ *   free list    num_free_out[0] = F - (new entries granted); free_blocks is not written, the
+ *                ids at or past num_free_out[0] are the ones in use
+ * Nothing else of block_tables is written.  The block a sequence's tokens continue (c % 16 != 0)
+ * must not be shared.
+ * Device-side errors: c < 0, n < 0 or > num_tokens, c + n > max_blocks * 16, or rows past
+ * num_tokens -> the sequence is refused and needs no block (an n out of range counts as 0 rows;
+ * q_start stops at num_tokens), PA_FLAG_CONTEXT_LEN_OOB; num_free[0] outside [0, free_capacity]
+ * -> clamped, PA_FLAG_BLOCK_ID_OOB; a block id outside [0, num_blocks), in free_blocks or in the
+ * entry that tokens continue -> a new entry becomes -1, the tokens' slots -1,
+ * PA_FLAG_BLOCK_ID_OOB.
+ *
+ *   dims           block_size (the head counts are checked and otherwise unused)
+ *   num_seqs       0 <= S <= 8192 (0 still writes q_start[0], the padding rows and num_free_out)
+ *   cached_lens, new_lens  [S] int32, read only
+ *   block_tables   [S][max_blocks] int32, read, and written at the new entries
+ *   max_blocks     >= 1, max_blocks * 16 <= 2^31 - 16
+ *   free_blocks    [free_capacity] int32, read only; free_capacity >= 0
+ *   num_free       [1] int32;  num_free_out [1] int32, may be num_free itself
+ *   num_blocks     >= 1
+ *   num_tokens     rows of positions and slot_mapping, >= 0
+ *   context_lens   [S] int32, written; not cached_lens or new_lens
+ *   q_start        [S + 1] int32, written
+ *   positions      [num_tokens] int32;  slot_mapping [num_tokens] int64, written
+ *   granted        [S] int32, written
+ * No output may overlap an input (num_free_out excepted) or another output.  positions and
+ * slot_mapping are 16-byte aligned, every other pointer 4-byte.  Returns PA_OK or a PA_ERR_* code
+ * (nothing launched on error).  Launches one kernel, or two when num_free_out is num_free and
+ * the call is large.
+ */
+int pa_plan_step(const pa_dims* dims, int num_seqs, const int32_t* cached_lens,
+                 const int32_t* new_lens, int32_t* block_tables, int max_blocks,
+                 const int32_t* free_blocks, int free_capacity, const int32_t* num_free,
+                 int32_t* num_free_out, int num_blocks, int num_tokens, int32_t* context_lens,
+                 int32_t* q_start, int32_t* positions, int64_t* slot_mapping, int32_t* granted,
+                 void* stream);
 
 /* Most caches one pa_copy_blocks call can name (K and V of up to 128 layers). */
 #define PA_MAX_BLOCK_CACHES 256

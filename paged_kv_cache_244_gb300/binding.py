@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 from pathlib import Path
+from typing import NamedTuple
 
 import torch
 
@@ -33,6 +34,7 @@ PA_FLAG_CONTEXT_LEN_OOB = 0x2
 PA_FLAG_SLOT_OOB = 0x4
 PA_FLAG_POSITION_OOB = 0x8
 PA_FLAG_TIMEOUT = 0x10
+PA_FLAG_POOL_EXHAUSTED = 0x20
 
 
 class PaError(RuntimeError):
@@ -96,6 +98,7 @@ def lib():
         L.pa_selftest_wait_timeout.restype = i
         L.pa_status_string.argtypes = [i]
         L.pa_status_string.restype = ctypes.c_char_p
+        _declare_serving(L)
         _lib = L
     return _lib
 
@@ -469,3 +472,291 @@ def get_device_status(stream=None) -> tuple[int, int]:
     flags = ctypes.c_uint32(0)
     rc = lib().pa_get_device_status(_stream(stream), ctypes.byref(flags))
     return rc, int(flags.value)
+
+
+# ---- RoPE tables and forms, block-scaled E4M3 caches, step plans ------------------------
+
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "banded": 4}
+
+
+class pa_rope(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("layout", ctypes.c_int32)]
+
+
+class pa_rope_scaling(ctypes.Structure):
+    _fields_ = [("theta", ctypes.c_double), ("factor", ctypes.c_double),
+                ("original_max_pos", ctypes.c_double), ("low", ctypes.c_double),
+                ("high", ctypes.c_double), ("magnitude", ctypes.c_double),
+                ("kind", ctypes.c_int32)]
+
+
+def _declare_serving(L):
+    p, i, f = ctypes.c_void_p, ctypes.c_int, ctypes.c_float
+    pd, pr, sz = ctypes.POINTER(pa_dims), ctypes.POINTER(pa_rope), ctypes.c_size_t
+    L.pa_rope_table.argtypes = [ctypes.POINTER(pa_rope_scaling), i, i, p, p]
+    L.pa_rope_kv_store_form.argtypes = [pd, pr, i, p, p, p, p, p, p, i, p, p, p, i, p]
+    L.pa_rope_kv_store_fp8_block.argtypes = [pd, pr, i, p, p, p, p, p, p, i, p, p, p, p, i, p]
+    L.pa_decode_fp8_block.argtypes = [pd, i, p, p, p, p, i, p, i, p, i, f, i, p, sz, p, p]
+    L.pa_decode_step_fp8_block.argtypes = [pd, pr, i, p, p, p, p, i, p, p, p, i, p, i, p, i, f, i, p,
+                                           sz, p, ctypes.c_uint, p]
+    L.pa_prefill_fp8_block.argtypes = [pd, i, i, p, p, i, p, p, p, i, p, i, p, i, f, p, p]
+    L.pa_plan_step.argtypes = [pd, i, p, p, p, i, p, i, p, p, i, i, p, p, p, p, p, p]
+    for name in ("pa_rope_table", "pa_rope_kv_store_form", "pa_rope_kv_store_fp8_block",
+                 "pa_decode_fp8_block", "pa_decode_step_fp8_block", "pa_prefill_fp8_block",
+                 "pa_plan_step"):
+        getattr(L, name).restype = i
+
+
+def _ptrs(dtypes, **tensors):
+    """Data pointers of contiguous CUDA tensors, all on the current device; `dtypes` in order."""
+    dev = torch.cuda.current_device()
+    out = []
+    for dtype, (name, t) in zip(dtypes, tensors.items()):
+        if t.dtype is not dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} must be a CUDA tensor on the current device (cuda:{dev})")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        out.append(t.data_ptr())
+    return out
+
+
+def _kept(stream, *tensors):
+    """Tensors allocated by a call that runs on `stream`: their memory is not handed out again
+    before that stream has passed the call."""
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(stream)
+
+
+def _rope_form(cos_sin, layout):
+    if cos_sin.dim() != 2:
+        raise ValueError("cos_sin must be [max_pos, rotary_dim]")
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}, got {layout!r}")
+    return pa_rope(cos_sin.shape[1], ROPE_LAYOUTS[layout])
+
+
+def _block_caches(k_cache, v_cache, kv_scale):
+    nb, Hkv, B, D = k_cache.shape
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache differ in shape")
+    if kv_scale.shape != (nb, Hkv, 2):
+        raise ValueError("kv_scale must be [num_blocks, num_kv_heads, 2] float32")
+    return nb, Hkv, B, D
+
+
+def rope_table(max_pos, rotary_dim=128, theta=1e4, scaling="none", factor=1.0, original_max_pos=0,
+               low=0.0, high=0.0, magnitude=0.0, out=None, stream=None):
+    """RoPE table cos | sin [max_pos, rotary_dim] fp32 (pa_rope_table), angles exact at any
+    position.  scaling: "none", "linear", "ntk", "yarn" (low, high: turns over original_max_pos
+    below / above which a pair is interpolated / kept; magnitude 0 gives 0.1 ln(factor) + 1) or
+    "banded" (low, high: the same, mixed linearly in the turns)."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}, got {scaling!r}")
+    if out is None:
+        out = torch.empty((max_pos, rotary_dim), dtype=torch.float32, device="cuda")
+        _kept(stream, out)
+    elif tuple(out.shape) != (max_pos, rotary_dim):
+        raise ValueError("out must be [max_pos, rotary_dim]")
+    spec = pa_rope_scaling(theta, factor, original_max_pos, low, high, magnitude, ROPE_SCALINGS[scaling])
+    (o,) = _ptrs((torch.float32,), out=out)
+    _check(lib().pa_rope_table(ctypes.byref(spec), rotary_dim, max_pos, o, _stream(stream)), "pa_rope_table")
+    return out
+
+
+_STORE_TYPES = (torch.bfloat16,) * 4 + (torch.int32, torch.float32, torch.int64)
+
+
+def _store_shapes(q, k, v, positions, slot_mapping, q_out, nb_shape):
+    T, Hq, D = q.shape
+    nb, Hkv, B, D2 = nb_shape
+    if D2 != D or k.shape != (T, Hkv, D) or v.shape != (T, Hkv, D) or q_out.shape != q.shape:
+        raise ValueError("shape mismatch between q, q_out, k, v and the caches")
+    if positions.shape != (T,) or slot_mapping.shape != (T,):
+        raise ValueError("positions / slot_mapping shape mismatch")
+    return T, pa_dims(Hq, Hkv, D, B), nb
+
+
+def rope_kv_store_form(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, layout="half",
+                       q_out=None, stream=None):
+    """Fused RoPE + KV-cache store with a RoPE form (pa_rope_kv_store_form); returns the rotated q
+    (q_out, or q itself when that is None).
+
+    cos_sin [max_pos, rotary_dim] fp32 says how many dims rotate; layout pairs them "half" or
+    "interleaved".  Everything else as rope_kv_store.
+    """
+    q_out = q if q_out is None else q_out
+    rope = _rope_form(cos_sin, layout)
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache differ in shape")
+    T, dims, nb = _store_shapes(q, k, v, positions, slot_mapping, q_out, k_cache.shape)
+    bf = torch.bfloat16
+    qp, qo, kp, vp, pos, cs, slots, kc, vc = _ptrs(
+        _STORE_TYPES + (bf, bf), q=q, q_out=q_out, k=k, v=v, positions=positions, cos_sin=cos_sin,
+        slot_mapping=slot_mapping, k_cache=k_cache, v_cache=v_cache)
+    _check(lib().pa_rope_kv_store_form(ctypes.byref(dims), ctypes.byref(rope), T, qp, qo, kp, vp, pos, cs,
+                                       cos_sin.shape[0], slots, kc, vc, nb, _stream(stream)),
+           "pa_rope_kv_store_form")
+    return q_out
+
+
+def rope_kv_store_fp8_block(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, kv_scale,
+                            layout="half", q_out=None, stream=None):
+    """rope_kv_store_form into block-scaled E4M3 caches (pa_rope_kv_store_fp8_block): k_cache,
+    v_cache uint8 [num_blocks, Hkv, B, D], kv_scale [num_blocks, Hkv, 2] fp32, all updated."""
+    q_out = q if q_out is None else q_out
+    rope = _rope_form(cos_sin, layout)
+    T, dims, nb = _store_shapes(q, k, v, positions, slot_mapping, q_out,
+                                _block_caches(k_cache, v_cache, kv_scale))
+    qp, qo, kp, vp, pos, cs, slots, kc, vc, sc = _ptrs(
+        _STORE_TYPES + (torch.uint8, torch.uint8, torch.float32), q=q, q_out=q_out, k=k, v=v,
+        positions=positions, cos_sin=cos_sin, slot_mapping=slot_mapping, k_cache=k_cache,
+        v_cache=v_cache, kv_scale=kv_scale)
+    _check(lib().pa_rope_kv_store_fp8_block(ctypes.byref(dims), ctypes.byref(rope), T, qp, qo, kp, vp, pos,
+                                            cs, cos_sin.shape[0], slots, kc, vc, sc, nb, _stream(stream)),
+           "pa_rope_kv_store_fp8_block")
+    return q_out
+
+
+def _decode_shapes(q, k_cache, v_cache, kv_scale, block_tables, context_lens, out):
+    S, Hq, D = q.shape
+    nb, Hkv, B, D2 = _block_caches(k_cache, v_cache, kv_scale)
+    if D2 != D or out.shape != q.shape:
+        raise ValueError("shape mismatch between q, out and the caches")
+    if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.shape != (S,):
+        raise ValueError("block_tables / context_lens shape mismatch")
+    return S, nb, pa_dims(Hq, Hkv, D, B)
+
+
+_DECODE_TYPES = (torch.bfloat16, torch.bfloat16, torch.uint8, torch.uint8, torch.float32, torch.int32,
+                 torch.int32, torch.float32)
+
+
+def decode_fp8_block(q, k_cache, v_cache, kv_scale, block_tables, context_lens, max_context_len,
+                     scale, partition_tokens=0, workspace=None, out=None, stream=None):
+    """Decode attention over block-scaled E4M3 caches (pa_decode_fp8_block).  Returns out
+    [S, Hq, D] bf16; workspace as for decode()."""
+    if out is None:
+        out = torch.empty_like(q)
+        _kept(stream, out)
+    S, nb, dims = _decode_shapes(q, k_cache, v_cache, kv_scale, block_tables, context_lens, out)
+    if workspace is None:
+        workspace = decode_workspace(q, k_cache, max_context_len, partition_tokens)
+        _kept(stream, workspace)
+    qp, op, kc, vc, sc, bt, ctx, ws = _ptrs(
+        _DECODE_TYPES, q=q, out=out, k_cache=k_cache, v_cache=v_cache, kv_scale=kv_scale,
+        block_tables=block_tables, context_lens=context_lens, workspace=workspace)
+    _check(lib().pa_decode_fp8_block(ctypes.byref(dims), S, qp, kc, vc, sc, nb, bt, block_tables.shape[1], ctx,
+                                     max_context_len, scale, partition_tokens, ws, workspace.numel() * 4, op,
+                                     _stream(stream)),
+           "pa_decode_fp8_block")
+    return out
+
+
+def decode_step_fp8_block(q, k, v, cos_sin, k_cache, v_cache, kv_scale, block_tables, context_lens,
+                          max_context_len, scale, layout="half", partition_tokens=0, workspace=None,
+                          out=None, stream=None, early_metadata=False):
+    """The fused decode step over block-scaled E4M3 caches with a RoPE form
+    (pa_decode_step_fp8_block; q left unchanged); early_metadata as for decode_step."""
+    if out is None:
+        out = torch.empty_like(q)
+        _kept(stream, out)
+    rope = _rope_form(cos_sin, layout)
+    S, nb, dims = _decode_shapes(q, k_cache, v_cache, kv_scale, block_tables, context_lens, out)
+    new = (S, k_cache.shape[1], q.shape[2])
+    if k.shape != new or v.shape != new:
+        raise ValueError("k / v shape mismatch")
+    if workspace is None:
+        workspace = decode_workspace(q, k_cache, max_context_len, partition_tokens)
+        _kept(stream, workspace)
+    qp, op, kc, vc, sc, bt, ctx, ws, kp, vp, cs = _ptrs(
+        _DECODE_TYPES + (torch.bfloat16, torch.bfloat16, torch.float32), q=q, out=out, k_cache=k_cache,
+        v_cache=v_cache, kv_scale=kv_scale, block_tables=block_tables, context_lens=context_lens,
+        workspace=workspace, k=k, v=v, cos_sin=cos_sin)
+    _check(lib().pa_decode_step_fp8_block(
+        ctypes.byref(dims), ctypes.byref(rope), S, qp, kp, vp, cs, cos_sin.shape[0], kc, vc, sc, nb, bt,
+        block_tables.shape[1], ctx, max_context_len, scale, partition_tokens, ws, workspace.numel() * 4, op,
+        PA_STEP_EARLY_METADATA if early_metadata else 0, _stream(stream)), "pa_decode_step_fp8_block")
+    return out
+
+
+def prefill_fp8_block(q, q_start, k_cache, v_cache, kv_scale, block_tables, context_lens, max_query_len,
+                      max_context_len, scale, out=None, stream=None):
+    """Paged (chunked) prefill attention over block-scaled E4M3 caches (pa_prefill_fp8_block).
+    Returns out [T, Hq, D] bf16; arguments as for prefill()."""
+    if out is None:
+        out = torch.empty_like(q)
+        _kept(stream, out)
+    T, Hq, D = q.shape
+    nb, Hkv, B, D2 = _block_caches(k_cache, v_cache, kv_scale)
+    S = context_lens.shape[0]
+    if D2 != D or out.shape != q.shape:
+        raise ValueError("shape mismatch between q, out and the caches")
+    if q_start.shape != (S + 1,) or block_tables.dim() != 2 or block_tables.shape[0] != S:
+        raise ValueError("q_start / block_tables shape mismatch")
+    dims = pa_dims(Hq, Hkv, D, B)
+    qp, op, kc, vc, sc, bt, ctx, qs = _ptrs(
+        _DECODE_TYPES[:7] + (torch.int32,), q=q, out=out, k_cache=k_cache, v_cache=v_cache,
+        kv_scale=kv_scale, block_tables=block_tables, context_lens=context_lens, q_start=q_start)
+    _check(lib().pa_prefill_fp8_block(ctypes.byref(dims), S, T, qp, qs, max_query_len, kc, vc, sc, nb, bt,
+                                      block_tables.shape[1], ctx, max_context_len, scale, op, _stream(stream)),
+           "pa_prefill_fp8_block")
+    return out
+
+
+class StepPlan(NamedTuple):
+    """What plan_step writes: the arguments of the store, decode and prefill calls of one step."""
+    context_lens: torch.Tensor   # [S] int32
+    q_start: torch.Tensor        # [S + 1] int32
+    positions: torch.Tensor      # [T] int32
+    slot_mapping: torch.Tensor   # [T] int64
+    granted: torch.Tensor        # [S] int32
+
+
+def step_plan(num_seqs, num_tokens, device="cuda") -> StepPlan:
+    """Allocate the tensors of a StepPlan (no initialisation needed)."""
+    i32 = dict(dtype=torch.int32, device=device)
+    return StepPlan(torch.empty(num_seqs, **i32), torch.empty(num_seqs + 1, **i32),
+                    torch.empty(num_tokens, **i32), torch.empty(num_tokens, dtype=torch.int64, device=device),
+                    torch.empty(num_seqs, **i32))
+
+
+_PLAN_TYPES = (torch.int32,) * 9 + (torch.int64, torch.int32)
+
+
+def plan_step(cached_lens, new_lens, block_tables, free_blocks, num_free, num_blocks, num_tokens,
+              num_free_out=None, plan=None, stream=None) -> StepPlan:
+    """The metadata of one serving step, built on the GPU (pa_plan_step).
+
+    cached_lens, new_lens [S] int32; block_tables [S, max_blocks] int32, given the new blocks;
+    free_blocks [capacity] int32, a stack of num_free[0] ids ([1] int32) of a pool of num_blocks;
+    num_tokens rows.  num_free_out ([1] int32) receives what is left; None means num_free itself.
+    """
+    S = cached_lens.shape[0]
+    if plan is None:
+        plan = step_plan(S, num_tokens, cached_lens.device)
+        _kept(stream, *plan)
+    if num_free_out is None:
+        num_free_out = num_free
+    ctx, qs, pos, slots, granted = plan
+    if new_lens.shape != (S,) or block_tables.dim() != 2 or block_tables.shape[0] != S:
+        raise ValueError("cached_lens / new_lens / block_tables shape mismatch")
+    if free_blocks.dim() != 1 or num_free.numel() != 1 or num_free_out.numel() != 1:
+        raise ValueError("free_blocks must be [capacity], num_free and num_free_out [1]")
+    if (ctx.shape != (S,) or qs.shape != (S + 1,) or granted.shape != (S,) or pos.shape != (num_tokens,)
+            or slots.shape != (num_tokens,)):
+        raise ValueError("plan does not fit these sequences and rows")
+    c, n, bt, fb, nf, nfo, cx, q0, ps, sl, gr = _ptrs(
+        _PLAN_TYPES, cached_lens=cached_lens, new_lens=new_lens, block_tables=block_tables,
+        free_blocks=free_blocks, num_free=num_free, num_free_out=num_free_out, context_lens=ctx, q_start=qs,
+        positions=pos, slot_mapping=slots, granted=granted)
+    _check(lib().pa_plan_step(ctypes.byref(_PLAN_DIMS), S, c, n, bt, block_tables.shape[1], fb,
+                              free_blocks.shape[0], nf, nfo, num_blocks, num_tokens, cx, q0, ps, sl, gr,
+                              _stream(stream)), "pa_plan_step")
+    return plan
+
+
+_PLAN_DIMS = pa_dims(1, 1, 128, 16)   # the plan depends on the block size alone

@@ -137,6 +137,10 @@ int decode_args(const pa_dims* dims, int num_seqs, const void* q, const void* k_
   a->v_store = nullptr;
   a->k_scale = nullptr;
   a->v_scale = nullptr;
+  a->kv_scale = nullptr;
+  a->kv_scale_store = nullptr;
+  a->rotary_dim = 128;
+  a->interleaved = 0;
   return PA_OK;
 }
 
@@ -202,13 +206,89 @@ int rope_store(const pa_dims* dims, int num_tokens, void* q, const void* k, cons
              : PA_ERR_CUDA;
 }
 
+// A RoPE form (null: the whole head, halves paired).
+int check_rope(const pa_rope* rope, int* rotary_dim, int* interleaved) {
+  *rotary_dim = rope ? rope->rotary_dim : 128;
+  const int layout = rope ? rope->layout : PA_ROPE_HALF;
+  *interleaved = layout == PA_ROPE_INTERLEAVED;
+  if (*rotary_dim < 16 || *rotary_dim > 128 || *rotary_dim % 16 != 0) return PA_ERR_SHAPE;
+  if (layout != PA_ROPE_HALF && layout != PA_ROPE_INTERLEAVED) return PA_ERR_SHAPE;
+  return PA_OK;
+}
+
+// pa_rope_kv_store_form, and with kv_scale its block-scaled E4M3 form.
+int rope_store_form(const pa_dims* dims, const pa_rope* rope, int num_tokens, const void* q, void* q_out,
+                    const void* k, const void* v, const int32_t* positions, const float* cos_sin,
+                    int max_pos, const int64_t* slot_mapping, void* k_cache, void* v_cache,
+                    float* kv_scale, bool block_scaled, int num_blocks, void* stream) {
+  if (const int rc = check_dims(dims)) return rc;
+  pa::RopeFormArgs a{};
+  if (const int rc = check_rope(rope, &a.rotary_dim, &a.interleaved)) return rc;
+  if (num_tokens < 0) return PA_ERR_RANGE;
+  if (num_tokens == 0) return PA_OK;
+  if (!q || !q_out || !k || !v || !positions || !cos_sin || !slot_mapping || !k_cache || !v_cache)
+    return PA_ERR_NULL;
+  if (block_scaled && !kv_scale) return PA_ERR_NULL;
+  if (max_pos < 1 || num_blocks < 1) return PA_ERR_RANGE;
+  const void* ptrs[] = {q, q_out, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, kv_scale};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return PA_ERR_ALIGN;
+  if (const int rc = status_word(&a.status)) return rc;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.q_out = static_cast<__nv_bfloat16*>(q_out);
+  a.k = static_cast<const __nv_bfloat16*>(k);
+  a.v = static_cast<const __nv_bfloat16*>(v);
+  a.positions = positions;
+  a.cos_sin = cos_sin;
+  a.slot_mapping = slot_mapping;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.kv_scale = reinterpret_cast<float2*>(kv_scale);
+  a.num_tokens = num_tokens;
+  a.num_q_heads = dims->num_q_heads;
+  a.num_kv_heads = dims->num_kv_heads;
+  a.max_pos = max_pos;
+  a.num_blocks = num_blocks;
+  return pa::launch_rope_form_store(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK
+                                                                                         : PA_ERR_CUDA;
+}
+
+// The angles per position of pair i of R/2 (see PA_ROPE_SCALE_*), in 64 bits.
+double rope_frequency(const pa_rope_scaling* s, int R, int i) {
+  constexpr double kTwoPi = 6.283185307179586476925;
+  const double w = std::pow(s->theta, -2.0 * i / R);
+  switch (s->kind) {
+    case PA_ROPE_SCALE_LINEAR:
+      return w / s->factor;
+    case PA_ROPE_SCALE_NTK:
+      return std::pow(s->theta * std::pow(s->factor, static_cast<double>(R) / (R - 2)), -2.0 * i / R);
+    case PA_ROPE_SCALE_YARN: {
+      auto pair_of = [&](double turns) {
+        return R * std::log(s->original_max_pos / (turns * kTwoPi)) / (2.0 * std::log(s->theta));
+      };
+      auto clamped = [&](double x) { return std::fmin(std::fmax(x, 0.0), R - 1.0); };
+      const double a = clamped(std::floor(pair_of(s->high))), b = clamped(std::ceil(pair_of(s->low)));
+      const double r = std::fmin(std::fmax((i - a) / (a == b ? 0.001 : b - a), 0.0), 1.0);
+      return w / s->factor * r + w * (1.0 - r);
+    }
+    case PA_ROPE_SCALE_BANDED: {
+      const double turns = s->original_max_pos * w / kTwoPi;
+      const double m = std::fmin(std::fmax((turns - s->low) / (s->high - s->low), 0.0), 1.0);
+      return w / s->factor * (1.0 - m) + w * m;
+    }
+    default:
+      return w;
+  }
+}
+
 // pa_decode_step and its E4M3 form (scales non-null).
 int decode_step(const pa_dims* dims, int num_seqs, const void* q, const void* k, const void* v,
                 const float* cos_sin, int max_pos, void* k_cache, void* v_cache,
                 const float* k_scale, const float* v_scale, int num_blocks,
                 const int32_t* block_tables, int max_blocks, const int32_t* context_lens,
                 int max_context_len, float scale, int partition_tokens, void* workspace,
-                size_t workspace_bytes, void* out, unsigned flags, void* stream) {
+                size_t workspace_bytes, void* out, unsigned flags, void* stream,
+                float* kv_scale = nullptr, int rotary_dim = 128, int interleaved = 0) {
   // The new token's arguments first (host checks only), then everything pa_decode checks.
   if (const int rc = check_dims(dims)) return rc;
   if (flags & ~PA_STEP_EARLY_METADATA) return PA_ERR_RANGE;
@@ -230,12 +310,24 @@ int decode_step(const pa_dims* dims, int num_seqs, const void* q, const void* k,
   a.v_store = static_cast<__nv_bfloat16*>(v_cache);
   a.k_scale = k_scale;
   a.v_scale = v_scale;
+  a.kv_scale = reinterpret_cast<const float2*>(kv_scale);
+  a.kv_scale_store = reinterpret_cast<float2*>(kv_scale);
+  a.rotary_dim = rotary_dim;
+  a.interleaved = interleaved;
   a.early_metadata = (flags & PA_STEP_EARLY_METADATA) ? 1 : 0;
   return pa::launch_decode(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK
                                                                                  : PA_ERR_CUDA;
 }
 
 // Host checks of the E4M3 scale arrays (after the shape and count checks their callers share).
+int block_scale_ok(const pa_dims* dims, int num_seqs, const float* kv_scale) {
+  if (const int rc = check_dims(dims)) return rc;
+  if (num_seqs < 0) return PA_ERR_RANGE;
+  if (num_seqs == 0) return PA_OK;
+  if (!kv_scale) return PA_ERR_NULL;
+  return aligned16(kv_scale) ? PA_OK : PA_ERR_ALIGN;
+}
+
 int scales_ok(const pa_dims* dims, int num_seqs, const float* k_scale, const float* v_scale) {
   if (const int rc = check_dims(dims)) return rc;
   if (num_seqs < 0 || num_seqs > pa::kMaxDecodeSeqs) return PA_ERR_RANGE;
@@ -395,11 +487,13 @@ int pa_decode_fp8(const pa_dims* dims, int num_seqs, const void* q, const void* 
                                                                                  : PA_ERR_CUDA;
 }
 
-int pa_prefill(const pa_dims* dims, int num_seqs, int num_tokens, const void* q,
-               const int32_t* q_start, int max_query_len, const void* k_cache,
-               const void* v_cache, int num_blocks, const int32_t* block_tables, int max_blocks,
-               const int32_t* context_lens, int max_context_len, float scale, void* out,
-               void* stream) {
+namespace {
+
+// pa_prefill, and with kv_scale its block-scaled E4M3 form.
+int prefill(const pa_dims* dims, int num_seqs, int num_tokens, const void* q, const int32_t* q_start,
+            int max_query_len, const void* k_cache, const void* v_cache, const float* kv_scale,
+            int num_blocks, const int32_t* block_tables, int max_blocks, const int32_t* context_lens,
+            int max_context_len, float scale, void* out, void* stream) {
   if (const int rc = check_dims(dims)) return rc;
   if (num_seqs < 0 || num_tokens < 0) return PA_ERR_RANGE;
   if (num_seqs == 0 || num_tokens == 0) return PA_OK;
@@ -436,8 +530,154 @@ int pa_prefill(const pa_dims* dims, int num_seqs, int num_tokens, const void* q,
   a.max_context_len = max_context_len;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.status = status;
-  return pa::launch_prefill(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK
-                                                                                   : PA_ERR_CUDA;
+  a.kv_scale = reinterpret_cast<const float2*>(kv_scale);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return (kv_scale ? pa::launch_prefill_block(a, st) : pa::launch_prefill(a, st)) == cudaSuccess ? PA_OK
+                                                                                               : PA_ERR_CUDA;
+}
+
+}  // namespace
+
+int pa_prefill(const pa_dims* dims, int num_seqs, int num_tokens, const void* q,
+               const int32_t* q_start, int max_query_len, const void* k_cache,
+               const void* v_cache, int num_blocks, const int32_t* block_tables, int max_blocks,
+               const int32_t* context_lens, int max_context_len, float scale, void* out,
+               void* stream) {
+  return prefill(dims, num_seqs, num_tokens, q, q_start, max_query_len, k_cache, v_cache, nullptr,
+                 num_blocks, block_tables, max_blocks, context_lens, max_context_len, scale, out, stream);
+}
+
+int pa_prefill_fp8_block(const pa_dims* dims, int num_seqs, int num_tokens, const void* q,
+                         const int32_t* q_start, int max_query_len, const void* k_cache,
+                         const void* v_cache, const float* kv_scale, int num_blocks,
+                         const int32_t* block_tables, int max_blocks, const int32_t* context_lens,
+                         int max_context_len, float scale, void* out, void* stream) {
+  if (num_seqs > 0 && num_tokens > 0) {
+    if (const int rc = block_scale_ok(dims, num_seqs, kv_scale)) return rc;
+  }
+  return prefill(dims, num_seqs, num_tokens, q, q_start, max_query_len, k_cache, v_cache, kv_scale,
+                 num_blocks, block_tables, max_blocks, context_lens, max_context_len, scale, out, stream);
+}
+
+int pa_decode_fp8_block(const pa_dims* dims, int num_seqs, const void* q, const void* k_cache,
+                        const void* v_cache, const float* kv_scale, int num_blocks,
+                        const int32_t* block_tables, int max_blocks, const int32_t* context_lens,
+                        int max_context_len, float scale, int partition_tokens, void* workspace,
+                        size_t workspace_bytes, void* out, void* stream) {
+  if (const int rc = block_scale_ok(dims, num_seqs, kv_scale)) return rc;
+  pa::DecodeArgs a{};
+  const int rc = decode_args(dims, num_seqs, q, k_cache, v_cache, num_blocks, block_tables, max_blocks,
+                             context_lens, max_context_len, scale, partition_tokens, workspace,
+                             workspace_bytes, out, &a);
+  if (rc != PA_OK || num_seqs == 0) return rc;
+  a.kv_scale = reinterpret_cast<const float2*>(kv_scale);
+  return pa::launch_decode(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK
+                                                                                 : PA_ERR_CUDA;
+}
+
+int pa_decode_step_fp8_block(const pa_dims* dims, const pa_rope* rope, int num_seqs, const void* q,
+                             const void* k, const void* v, const float* cos_sin, int max_pos,
+                             void* k_cache, void* v_cache, float* kv_scale, int num_blocks,
+                             const int32_t* block_tables, int max_blocks,
+                             const int32_t* context_lens, int max_context_len, float scale,
+                             int partition_tokens, void* workspace, size_t workspace_bytes,
+                             void* out, unsigned flags, void* stream) {
+  int rotary_dim = 0, interleaved = 0;
+  if (const int rc = block_scale_ok(dims, num_seqs, kv_scale)) return rc;
+  if (const int rc = check_rope(rope, &rotary_dim, &interleaved)) return rc;
+  return decode_step(dims, num_seqs, q, k, v, cos_sin, max_pos, k_cache, v_cache, nullptr, nullptr,
+                     num_blocks, block_tables, max_blocks, context_lens, max_context_len, scale,
+                     partition_tokens, workspace, workspace_bytes, out, flags, stream, kv_scale,
+                     rotary_dim, interleaved);
+}
+
+int pa_rope_kv_store_form(const pa_dims* dims, const pa_rope* rope, int num_tokens, const void* q,
+                          void* q_out, const void* k, const void* v, const int32_t* positions,
+                          const float* cos_sin, int max_pos, const int64_t* slot_mapping,
+                          void* k_cache, void* v_cache, int num_blocks, void* stream) {
+  return rope_store_form(dims, rope, num_tokens, q, q_out, k, v, positions, cos_sin, max_pos, slot_mapping,
+                         k_cache, v_cache, nullptr, false, num_blocks, stream);
+}
+
+int pa_rope_kv_store_fp8_block(const pa_dims* dims, const pa_rope* rope, int num_tokens,
+                               const void* q, void* q_out, const void* k, const void* v,
+                               const int32_t* positions, const float* cos_sin, int max_pos,
+                               const int64_t* slot_mapping, void* k_cache, void* v_cache,
+                               float* kv_scale, int num_blocks, void* stream) {
+  return rope_store_form(dims, rope, num_tokens, q, q_out, k, v, positions, cos_sin, max_pos, slot_mapping,
+                         k_cache, v_cache, kv_scale, true, num_blocks, stream);
+}
+
+int pa_rope_table(const pa_rope_scaling* scaling, int rotary_dim, int max_pos, float* cos_sin,
+                  void* stream) {
+  if (!scaling || !cos_sin) return PA_ERR_NULL;
+  if (rotary_dim < 16 || rotary_dim > 128 || rotary_dim % 16 != 0) return PA_ERR_SHAPE;
+  const pa_rope_scaling& s = *scaling;
+  if (max_pos < 1 || s.kind < PA_ROPE_SCALE_NONE || s.kind > PA_ROPE_SCALE_BANDED) return PA_ERR_RANGE;
+  if (!(s.theta > 1.0) || !std::isfinite(s.theta)) return PA_ERR_RANGE;
+  if (s.kind != PA_ROPE_SCALE_NONE && (!(s.factor >= 1.0) || !std::isfinite(s.factor))) return PA_ERR_RANGE;
+  pa::RopeTableArgs a{};
+  a.magnitude = 1.f;
+  if (s.kind == PA_ROPE_SCALE_YARN || s.kind == PA_ROPE_SCALE_BANDED) {
+    if (!(s.original_max_pos > 0.0) || !std::isfinite(s.original_max_pos)) return PA_ERR_RANGE;
+    if (!(s.low > 0.0) || !(s.high > s.low) || !std::isfinite(s.high)) return PA_ERR_RANGE;
+  }
+  if (s.kind == PA_ROPE_SCALE_YARN) {
+    if (!(s.magnitude >= 0.0) || !std::isfinite(s.magnitude)) return PA_ERR_RANGE;
+    a.magnitude = static_cast<float>(s.magnitude > 0.0 ? s.magnitude : 0.1 * std::log(s.factor) + 1.0);
+  }
+  if (!aligned16(cos_sin)) return PA_ERR_ALIGN;
+  for (int i = 0; i < rotary_dim / 2; ++i) {
+    const double turns = rope_frequency(&s, rotary_dim, i) / 6.283185307179586476925;  // in [0, 0.16)
+    a.turns[i] = static_cast<unsigned long long>(std::ldexp(turns, 64) + 0.5);
+  }
+  a.cos_sin = cos_sin;
+  a.max_pos = max_pos;
+  a.rotary_dim = rotary_dim;
+  return pa::launch_rope_table(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+int pa_plan_step(const pa_dims* dims, int num_seqs, const int32_t* cached_lens,
+                 const int32_t* new_lens, int32_t* block_tables, int max_blocks,
+                 const int32_t* free_blocks, int free_capacity, const int32_t* num_free,
+                 int32_t* num_free_out, int num_blocks, int num_tokens, int32_t* context_lens,
+                 int32_t* q_start, int32_t* positions, int64_t* slot_mapping, int32_t* granted,
+                 void* stream) {
+  if (const int rc = check_dims(dims)) return rc;
+  if (num_seqs < 0 || num_seqs > pa::kMaxDecodeSeqs || num_tokens < 0) return PA_ERR_RANGE;
+  if (free_capacity < 0 || num_blocks < 1 || max_blocks < 1 || max_blocks > (0x7fffffff - 15) / 16)
+    return PA_ERR_RANGE;
+  if (!num_free || !num_free_out || !q_start) return PA_ERR_NULL;
+  if (num_seqs > 0 && (!cached_lens || !new_lens || !block_tables || !context_lens || !granted))
+    return PA_ERR_NULL;
+  if (num_tokens > 0 && (!positions || !slot_mapping)) return PA_ERR_NULL;
+  if (free_capacity > 0 && !free_blocks) return PA_ERR_NULL;
+  if (!aligned16(positions) || !aligned16(slot_mapping)) return PA_ERR_ALIGN;
+  const void* words[] = {cached_lens, new_lens, block_tables, free_blocks, num_free,
+                         num_free_out, context_lens, q_start, granted};
+  for (const void* p : words)
+    if (reinterpret_cast<uintptr_t>(p) % 4 != 0) return PA_ERR_ALIGN;
+  // lengths must outlive their reading: every thread block reads them while others write
+  if (num_seqs > 0 && (context_lens == cached_lens || context_lens == new_lens)) return PA_ERR_RANGE;
+  pa::PlanArgs a{};
+  if (const int rc = status_word(&a.status)) return rc;
+  a.cached_lens = cached_lens;
+  a.new_lens = new_lens;
+  a.block_tables = block_tables;
+  a.free_blocks = free_blocks;
+  a.num_free = num_free;
+  a.num_free_out = num_free_out;
+  a.context_lens = context_lens;
+  a.q_start = q_start;
+  a.positions = positions;
+  a.slot_mapping = slot_mapping;
+  a.granted = granted;
+  a.num_seqs = num_seqs;
+  a.max_blocks = max_blocks;
+  a.free_capacity = free_capacity;
+  a.num_blocks = num_blocks;
+  a.num_tokens = num_tokens;
+  return pa::launch_plan_step(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 int pa_copy_blocks(const pa_dims* dims, int num_caches, const void* const* src_caches,

@@ -405,4 +405,71 @@ __device__ __forceinline__ void rope_rotate_pairs(uint32_t& lo, uint32_t& hi, fl
   hi = pack_bf16x2(r2, r3);
 }
 
+// rope_rotate_pairs on two adjacent pairs held interleaved, w0 = (x0, y0), w1 = (x1, y1).
+__device__ __forceinline__ void rope_rotate_interleaved(uint32_t& w0, uint32_t& w1, float2 c, float2 s) {
+  uint32_t lo = __byte_perm(w0, w1, 0x5410), hi = __byte_perm(w0, w1, 0x7632);
+  rope_rotate_pairs(lo, hi, c, s);
+  w0 = __byte_perm(lo, hi, 0x5410);
+  w1 = __byte_perm(lo, hi, 0x7632);
+}
+
+// ---- block-scaled E4M3 caches ------------------------------------------------------------
+// The magnitudes of finite bf16 values order as 16-bit integers; infinities and NaN count as 0.
+__device__ __forceinline__ uint32_t finite_magnitudes(uint32_t bf16_pair) {
+  const uint32_t m = bf16_pair & 0x7fff7fffu;
+  return m & __vcmpltu2(m, 0x7f807f80u);
+}
+// Smallest power of two s with amax <= 448 s in [2^-40, 2^40], amax as a finite bf16 magnitude.
+__device__ __forceinline__ float e4m3_scale_for(uint32_t amax_bf16) {
+  // 448 = 1.75 * 2^8: amax = m 2^e wants 2^(e-8), or twice that when m > 1.75
+  int e = static_cast<int>(amax_bf16 >> 7) - 127 - 8 + ((amax_bf16 & 0x7fu) > 0x60u ? 1 : 0);
+  e = e < -40 ? -40 : (e > 40 ? 40 : e);
+  return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+// A block's scale after a store of values that want `want`; fresh: the store begins the block.
+__device__ __forceinline__ float e4m3_grow_scale(float old, float want, bool fresh) {
+  return !fresh && old > want ? old : want;
+}
+// Four E4M3 codes coded anew: code(value * f), round to nearest even, saturating.
+__device__ __forceinline__ uint32_t e4m3x4_rescale(uint32_t w, float f) {
+  uint32_t a, b;
+  e4m3x4_to_f16x2x2(w, a, b);
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(__fmul_rn(f16hi(a), f)), "f"(__fmul_rn(f16lo(a), f)));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(__fmul_rn(f16hi(b), f)), "f"(__fmul_rn(f16lo(b), f)));
+  return lo | (static_cast<uint32_t>(hi) << 16);
+}
+__device__ __forceinline__ uint4 e4m3x16_rescale(uint4 w, float f) {
+  return make_uint4(e4m3x4_rescale(w.x, f), e4m3x4_rescale(w.y, f), e4m3x4_rescale(w.z, f), e4m3x4_rescale(w.w, f));
+}
+
+// Warpgroup-collective: this thread's registers from here on (a multiple of 8).  `inc` waits until
+// the block's own registers, as launched, have that many free.
+template <int kRegs>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+// log2 of a positive normal value: its exponent, exact, plus the log2 of its mantissa in [1, 2)
+// (0 for a power of two).
+__device__ __forceinline__ float log2_of(float x) {
+  const uint32_t b = __float_as_uint(x);
+  return static_cast<float>(static_cast<int>(b >> 23) - 127) +
+         __log2f(__uint_as_float((b & 0x007fffffu) | 0x3f800000u));
+}
+
+// ---- 8-byte asynchronous copy global -> shared, tracked by an mbarrier ---------------------
+__device__ __forceinline__ void cp_async8(uint32_t dst_smem, const void* src_gmem) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst_smem), "l"(src_gmem) : "memory");
+}
+// Arrive once on the mbarrier when this thread's cp.async copies so far have landed (the
+// arrival is one of those the barrier was initialised to expect).
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
 }  // namespace pa

@@ -46,6 +46,49 @@ struct RopeArgs {
   const float* v_scale;             // [Hkv]
 };
 
+// The store with a RoPE form: q_out apart from q, the first rotary_dim dims rotated, halves or
+// adjacent dims paired; bf16 caches, or block-scaled E4M3 caches (kv_scale not null).
+struct RopeFormArgs {
+  const __nv_bfloat16* q;           // [T][Hq][128]
+  __nv_bfloat16* q_out;             // [T][Hq][128], may be q
+  const __nv_bfloat16* k;           // [T][Hkv][128]
+  const __nv_bfloat16* v;           // [T][Hkv][128]
+  const int32_t* positions;         // [T]
+  const float* cos_sin;             // [max_pos][rotary_dim]
+  const int64_t* slot_mapping;      // [T]
+  void* k_cache;                    // [num_blocks][Hkv][16][128] bf16 or codes
+  void* v_cache;
+  float2* kv_scale;                 // [num_blocks][Hkv] (K, V)
+  int num_tokens, num_q_heads, num_kv_heads, max_pos, num_blocks;
+  int rotary_dim;                   // multiple of 16 in [16, 128]
+  int interleaved;
+  unsigned* status;
+};
+
+// RoPE table: pair i of position p turns by frac(p * turns[i] / 2^64) of a whole turn.
+struct RopeTableArgs {
+  unsigned long long turns[64];     // turns per position in 2^-64 (the fraction: w_i / 2 pi mod 1)
+  float* cos_sin;                   // [max_pos][rotary_dim]
+  int max_pos, rotary_dim;
+  float magnitude;                  // factor on cos and sin
+};
+
+struct PlanArgs {
+  const int32_t* cached_lens;       // [S]
+  const int32_t* new_lens;          // [S]
+  int32_t* block_tables;            // [S][max_blocks]
+  const int32_t* free_blocks;       // [free_capacity]
+  const int32_t* num_free;          // [1]
+  int32_t* num_free_out;            // [1]
+  int32_t* context_lens;            // [S]
+  int32_t* q_start;                 // [S + 1]
+  int32_t* positions;               // [T]
+  int64_t* slot_mapping;            // [T]
+  int32_t* granted;                 // [S]
+  int num_seqs, max_blocks, free_capacity, num_blocks, num_tokens;
+  unsigned* status;
+};
+
 struct DecodeArgs {
   const __nv_bfloat16* q;           // [S][Hq][128]
   const __nv_bfloat16* k_cache;     // [num_blocks][Hkv][16][128]
@@ -77,6 +120,12 @@ struct DecodeArgs {
   // Lengths and block table are read before the preceding kernel on the stream has finished
   // (the caller's promise that it writes neither).
   int early_metadata;
+  // Block-scaled E4M3 caches (kv_scale == nullptr otherwise): element = code * scale of its
+  // (block, KV head); the fused step's RoPE form.
+  const float2* kv_scale;           // [num_blocks][Hkv] (K, V)
+  float2* kv_scale_store;           // the same, writable (fused step)
+  int rotary_dim;
+  int interleaved;
   // Gather checksum only: [S][Hkv] words that each (sequence, KV head)'s tile words are XORed
   // into.
   uint32_t* gather_xor;
@@ -108,6 +157,7 @@ struct PrefillArgs {
   int max_query_len, max_context_len;
   float scale_log2;
   unsigned* status;
+  const float2* kv_scale;           // [num_blocks][Hkv] (K, V): block-scaled E4M3 caches; else null
 };
 
 // TMA tensor map of a paged cache viewed as [num_blocks * Hkv * 16][128], 128-byte swizzle;
@@ -118,6 +168,10 @@ bool cache_tensor_map(const void* cache, long long rows, bool fp8, CUtensorMap* 
 
 cudaError_t launch_rope_kv_store(const RopeArgs& a, cudaStream_t stream);
 cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream);
+cudaError_t launch_prefill_block(const PrefillArgs& a, cudaStream_t stream);
+cudaError_t launch_rope_table(const RopeTableArgs& a, cudaStream_t stream);
+cudaError_t launch_rope_form_store(const RopeFormArgs& a, cudaStream_t stream);
+cudaError_t launch_plan_step(const PlanArgs& a, cudaStream_t stream);
 cudaError_t launch_copy_blocks(const BlockCopyArgs& a, cudaStream_t stream);
 // n16 16-byte words from src to dst (device or page-locked host addresses the GPU can access)
 cudaError_t launch_stage_copy(void* dst, const void* src, long long n16, cudaStream_t stream);

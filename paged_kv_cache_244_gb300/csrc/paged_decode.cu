@@ -44,7 +44,7 @@
 // chunk c ^ (r % 8); the ldmatrix row addresses apply the same XOR, so all eight rows of a
 // matrix hit distinct banks.
 //
-// Variants (template <kStep, kFp8, kGather, kOnce>):
+// Variants (template <kStep, kFp8, kGather, kOnce, kBlock>):
 //   kStep  the fused decode step ("Pico-vLLM" §2: RoPE fused with the KV cache store): the warp
 //          whose job holds a sequence's new token (position len - 1) stages the token's k, v and
 //          cos/sin row with the tiles, rotates k, writes both rows into the staged tiles before
@@ -53,6 +53,14 @@
 //          12 warps with 2 stages; the byte tiles are read by ldmatrix as 16-bit pairs and widened exactly to
 //          f16 with cvt.f16x2.e4m3x2, the q.K k index permuted alike in both operands; f16 MMAs,
 //          the K scale folded into the softmax scale, the V scale into the output.
+//   kBlock (with kFp8) a scale for each (block, KV head), K and V, brought with the job's tiles
+//          by an 8-byte cp.async on the same mbarrier.  With k_b, v_b the scales of token t's
+//          block the kernel keeps x_t = scale_log2 k_b (q . Kcode_t) + log2 v_b, p_t = 2^(x_t - m),
+//          O = sum p_t Vcode_t and L = sum p_t / v_b: out = O / L, since both sums carry 2^m and
+//          v_b cancels in the second.  The shift m follows the largest contribution p_t, so P
+//          stays within f16 (2^7 to 2^15 at its largest) whatever the scales, a V tile needs no multiply, and the pieces
+//          merge as any others do.  L adds the unrounded fp32 p_t: a block of tiny V scale (an
+//          attention sink) may carry most of the softmax's weight with a p_t below f16.
 //   kGather the tile gather alone (pa_gather_checksum): an XOR of the tile words instead of the
 //          attention, no merge -- the floor of this kernel's access pattern.
 //   kOnce  launched for calls with early metadata (a layer of a chain): the K/V tiles load with
@@ -88,7 +96,7 @@ __host__ __device__ inline int prefix_bytes(int num_seqs) {
 // the prefix of block counts.  Stage: [K tile | V tile | q rows | (kStep) the new token's
 // cos/sin row (fp32), k row and v row (bf16)], a multiple of 1024 bytes so that every tile
 // stays on the 1024-byte boundary its 128-byte swizzle needs.
-template <bool kStep, bool kFp8>
+template <bool kStep, bool kFp8, bool kBlock = false>
 struct Layout {
   static constexpr int kTile = kFp8 ? kTileBytes / 2 : kTileBytes;
   static constexpr int kWarpsN = kFp8 ? 12 : kWarps;
@@ -99,7 +107,8 @@ struct Layout {
   static constexpr int kNewVOff = kNewKOff + kHeadDim * 2;
   static constexpr int kStage = kStep ? kNewVOff + kHeadDim * 2 : kQOff + kQBytes;
   static constexpr int kDescOff = (kWarpsN * kStagesN * 8 + 15) & ~15;
-  static constexpr int kPrefixOff = kDescOff + kWarpsN * kStagesN * 16;
+  static constexpr int kScaleOff = kDescOff + kWarpsN * kStagesN * 16;  // kBlock: a float2 per stage
+  static constexpr int kPrefixOff = (kScaleOff + (kBlock ? kWarpsN * kStagesN * 8 : 0) + 15) & ~15;
   static_assert(kStage % 1024 == 0 && kTile % 1024 == 0, "tiles on 1024-byte boundaries");
   static_assert(kDescOff % 16 == 0 && kPrefixOff % 16 == 0, "descriptor alignment");
   __host__ __device__ static int smem(int num_seqs) {
@@ -153,11 +162,12 @@ __device__ __forceinline__ int clamp_len(int len, int max_len) {
   return len < 0 ? 0 : (len > max_len ? max_len : len);
 }
 
-template <bool kStep, bool kFp8, bool kGather = false, bool kOnce = false>
-__global__ void __launch_bounds__(Layout<kStep, kFp8>::kWarpsN * 32, 1)
+template <bool kStep, bool kFp8, bool kGather = false, bool kOnce = false, bool kBlock = false>
+__global__ void __launch_bounds__(Layout<kStep, kFp8, kBlock>::kWarpsN * 32, 1)
 decode_partition_kernel(const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const DecodeArgs a) {
-  using L = Layout<kStep, kFp8>;
+  using L = Layout<kStep, kFp8, kBlock>;
+  static_assert(!kBlock || (kFp8 && !kGather), "block scales belong to E4M3 attention");
   constexpr int kWarps = L::kWarpsN;           // warps of this variant's CTA
   constexpr int kPool = kWarps * L::kStagesN;  // stages of the CTA
   constexpr int kStageB = L::kStage;
@@ -172,7 +182,7 @@ decode_partition_kernel(const __grid_constant__ CUtensorMap tm_k,
   // 128-byte swizzled TMA destinations must sit on 1024-byte boundaries.
   const uint32_t tile_base = (raw + L::kPrefixOff + prefix_bytes(a.num_seqs) + 1023u) & ~1023u;
   if (tid < kPool) {
-    mbar_init(raw + 8 * tid, 1);
+    mbar_init(raw + 8 * tid, kBlock ? 2 : 1);  // kBlock: and the scales' copy
     fence_mbar_init();
   }
   if (tid == 0) {
@@ -240,6 +250,7 @@ decode_partition_kernel(const __grid_constant__ CUtensorMap tm_k,
   const uint32_t bars = raw + warp * n_st * 8;
   int4* descs = reinterpret_cast<int4*>(smem_raw + L::kDescOff) + warp * n_st;
   const uint32_t tiles = tile_base + warp * n_st * kStageB;
+  float2* scales = reinterpret_cast<float2*>(smem_raw + L::kScaleOff) + warp * n_st;  // kBlock
   const int gq = lane >> 2;  // fragment row group
   const int cq = lane & 3;   // fragment column pair
   const int mi = lane >> 3;  // ldmatrix: matrix this lane addresses
@@ -355,14 +366,25 @@ decode_partition_kernel(const __grid_constant__ CUtensorMap tm_k,
     const int y = ok ? (blk * Hkv + (fl >> 16)) * kBlockSize : 0;
     const uint32_t bar = bars + 8 * st;
     const uint32_t dst = tiles + st * kStageB;
+    const uint32_t cos_sin_bytes = kBlock ? static_cast<uint32_t>(a.rotary_dim) * 4u : kHeadDim * 4u;
     const uint32_t bytes = (ok ? 2u * L::kTile : 0u) + (q_rows ? static_cast<uint32_t>(G) * 256u : 0u) +
-                           (trig ? kHeadDim * 4u : 0u) + (fresh ? kHeadDim * 4u : 0u);
+                           (trig ? cos_sin_bytes : 0u) + (fresh ? kHeadDim * 4u : 0u);
     if (lane == 0) {
       if (!ok) raise_flag(a.status, PA_FLAG_BLOCK_ID_OOB);
       if (kStep && (fl & kNew) && !rope) raise_flag(a.status, PA_FLAG_POSITION_OOB);
       descs[st] = make_int4(seg, fl | (ok ? static_cast<int>(kHasData) : 0), slot, y);
       if (bytes) mbar_arrive_expect_tx(bar, bytes);
       else mbar_arrive(bar);
+    }
+    if constexpr (kBlock) {
+      if (lane == 6) {  // the barrier's second arrival: when the tile's scales have landed
+        if (ok) {
+          cp_async8(smem_addr(scales + st), a.kv_scale + (static_cast<size_t>(blk) * Hkv + (fl >> 16)));
+          cp_async_arrive(bar);
+        } else {
+          mbar_arrive(bar);
+        }
+      }
     }
     // The copies of one job leave from different lanes at once (one thread issues its copies
     // one after another), once lane 0 has armed the stage's barrier.
@@ -383,7 +405,8 @@ decode_partition_kernel(const __grid_constant__ CUtensorMap tm_k,
         bulk_copy_g2s(dst + L::kQOff, a.q + static_cast<size_t>(seg) * G * kHeadDim,
                       static_cast<uint32_t>(G) * 256u, bar);
       } else if (lane == 3 && trig) {
-        bulk_copy_g2s(dst + L::kCosSinOff, a.cos_sin + static_cast<size_t>(pos) * kHeadDim, kHeadDim * 4u, bar);
+        bulk_copy_g2s(dst + L::kCosSinOff, a.cos_sin + static_cast<size_t>(pos) * (kBlock ? a.rotary_dim : kHeadDim), cos_sin_bytes,
+                      bar);
       } else if (lane == 4 && fresh) {  // row seg of the [S, Hkv] new-token rows
         bulk_copy_g2s(dst + L::kNewKOff, a.k_new + static_cast<size_t>(seg) * kHeadDim, kHeadDim * 2u, bar);
       } else if (lane == 5 && fresh) {
@@ -406,6 +429,77 @@ decode_partition_kernel(const __grid_constant__ CUtensorMap tm_k,
   float o[8][4];                         // O^T: dims 16mt + gq (+8), heads 2cq, 2cq+1
 #pragma unroll
   for (int mt = 0; mt < 8; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
+
+  // Fused step, block-scaled caches: the new token (row `row` of the staged tile, whose first cache
+  // row is `y`) is rotated and coded into the staged tile and the cache.  Row 0 begins the block;
+  // otherwise a scale that has to grow codes the whole tile anew, and the tile is written back.
+  // Returns the block's scales after the store.
+  auto store_new_block = [&](unsigned char* stage, float2 held, int row, int y) -> float2 {
+    const uint32_t* kn = reinterpret_cast<const uint32_t*>(stage + L::kNewKOff);
+    const uint32_t* vn = reinterpret_cast<const uint32_t*>(stage + L::kNewVOff);
+    const float* cs = reinterpret_cast<const float*>(stage + L::kCosSinOff);
+    const int R = a.rotary_dim;
+    // Lane l holds two words (dim pairs) of the row: of the half layout words l and l + R/4 for
+    // l < R/4, otherwise words 2l and 2l + 1; the first R/4 lanes rotate theirs.
+    const bool turns = lane < R / 4;
+    const int wa = turns && !a.interleaved ? lane : 2 * lane;
+    const int wb = turns && !a.interleaved ? lane + R / 4 : 2 * lane + 1;
+    uint32_t kx = kn[wa], ky = kn[wb];
+    if (turns) {
+      const float2 co = reinterpret_cast<const float2*>(cs)[lane];
+      const float2 si = reinterpret_cast<const float2*>(cs + R / 2)[lane];
+      if (a.interleaved) rope_rotate_interleaved(kx, ky, co, si);
+      else rope_rotate_pairs(kx, ky, co, si);
+    }
+    const uint32_t vx = vn[wa], vy = vn[wb];
+    const uint32_t km = __vmaxu2(finite_magnitudes(kx), finite_magnitudes(ky));
+    const uint32_t vm = __vmaxu2(finite_magnitudes(vx), finite_magnitudes(vy));
+    const uint32_t ktop = __reduce_max_sync(kFullMask, max(km & 0xffffu, km >> 16));
+    const uint32_t vtop = __reduce_max_sync(kFullMask, max(vm & 0xffffu, vm >> 16));
+    const bool fresh = row == 0;
+    const float2 now = make_float2(e4m3_grow_scale(held.x, e4m3_scale_for(ktop), fresh),
+                                   e4m3_grow_scale(held.y, e4m3_scale_for(vtop), fresh));
+    uint8_t* const caches[2] = {reinterpret_cast<uint8_t*>(a.k_store) + static_cast<size_t>(y) * kHeadDim,
+                                reinterpret_cast<uint8_t*>(a.v_store) + static_cast<size_t>(y) * kHeadDim};
+    // byte 2w of a row, through the 128-byte swizzle
+    auto at = [&](int w) { return row * 128 + (((w >> 3) ^ (row & 7)) << 4) + 2 * (w & 7); };
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      const float old = kv ? held.y : held.x, s = kv ? now.y : now.x;
+      const float inv = __frcp_rn(s);
+      const uint16_t cx = e4m3x2_of(kv ? vx : kx, inv), cy = e4m3x2_of(kv ? vy : ky, inv);
+      unsigned char* tile = stage + kv * L::kTile;
+      const bool grown = !fresh && s != old;
+      if (grown) {
+        const float f = __fdiv_rn(old, s);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint4* w = reinterpret_cast<uint4*>(tile) + lane + 32 * i;
+          *w = e4m3x16_rescale(*w, f);
+        }
+        __syncwarp();
+      }
+      *reinterpret_cast<uint16_t*>(tile + at(wa)) = cx;
+      *reinterpret_cast<uint16_t*>(tile + at(wb)) = cy;
+      if (grown) {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int c = lane + 32 * i, rr = c >> 3;   // 16-byte chunk c of the tile
+          reinterpret_cast<uint4*>(caches[kv])[rr * 8 + ((c & 7) ^ (rr & 7))] = reinterpret_cast<const uint4*>(tile)[c];
+        }
+      } else {
+        uint16_t* dst = reinterpret_cast<uint16_t*>(caches[kv] + row * kHeadDim);
+        dst[wa] = cx;
+        dst[wb] = cy;
+      }
+    }
+    if (lane == 0) a.kv_scale_store[y / kBlockSize] = now;
+    // These generic writes precede a later TMA write into the same stage.
+    fence_proxy_async_smem();
+    __syncwarp();
+    return now;
+  };
 
   uint32_t gx = 0;  // gather: this lane's XOR of the piece's tile words
   auto consume = [&](int st) {
@@ -449,7 +543,34 @@ decode_partition_kernel(const __grid_constant__ CUtensorMap tm_k,
         uint2 w[8];
 #pragma unroll
         for (int c = 0; c < 8; ++c) w[c] = qrow[4 * c + cq];
-        if (kStep && (fl & kRope)) {
+        if (kBlock && kStep && (fl & kRope) && (a.interleaved || a.rotary_dim != kHeadDim)) {
+          // Another form: dims d .. d+3 (d = 16c + 4cq) rotate if d < R, within the word pair when
+          // interleaved, else with the dims R/2 away, read from the staged row.
+          const float* cs = reinterpret_cast<const float*>(stage + L::kCosSinOff);
+          const uint32_t* row = reinterpret_cast<const uint32_t*>(stage + L::kQOff + gq * 256);
+          const int R = a.rotary_dim, half = R / 2;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const int d = 16 * c + 4 * cq;
+            if (d >= R) continue;
+            if (a.interleaved) {
+              rope_rotate_interleaved(w[c].x, w[c].y, *reinterpret_cast<const float2*>(cs + d / 2),
+                                      *reinterpret_cast<const float2*>(cs + half + d / 2));
+            } else {
+              const int i = d < half ? d : d - half;  // angle of the first dim
+              const int o = d < half ? d + half : i;  // its partner
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                uint32_t own = e ? w[c].y : w[c].x, other = row[o / 2 + e];
+                const float2 co = *reinterpret_cast<const float2*>(cs + i + 2 * e);
+                const float2 si = *reinterpret_cast<const float2*>(cs + half + i + 2 * e);
+                if (d < half) rope_rotate_pairs(own, other, co, si);
+                else rope_rotate_pairs(other, own, co, si);
+                (e ? w[c].y : w[c].x) = own;
+              }
+            }
+          }
+        } else if (kStep && (fl & kRope)) {
           const float* cs = reinterpret_cast<const float*>(stage + L::kCosSinOff);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -465,9 +586,13 @@ decode_partition_kernel(const __grid_constant__ CUtensorMap tm_k,
           qb[c][0] = gq < G ? bf16x2_to_f16x2(w[c].x) : 0u;
           qb[c][1] = gq < G ? bf16x2_to_f16x2(w[c].y) : 0u;
         }
-        const int g = d.x % Hkv;
-        k_fold = a.scale_log2 * a.k_scale[g];
-        v_fold = a.v_scale[g];
+        if constexpr (kBlock) {
+          v_fold = 1.f;
+        } else {
+          const int g = d.x % Hkv;
+          k_fold = a.scale_log2 * a.k_scale[g];
+          v_fold = a.v_scale[g];
+        }
       } else {
         // q rows sit unswizzled at 256-byte stride; rows >= G are not real heads.
         const uint32_t qt = kt + L::kQOff + static_cast<uint32_t>(r * 256);
@@ -502,7 +627,11 @@ decode_partition_kernel(const __grid_constant__ CUtensorMap tm_k,
     }
     if (fl & kHasData) {
       const int valid = static_cast<int>((fl >> 8) & 0xffu);
-      if (kStep && (fl & kNew) && (fl & kRope)) {
+      float2 bs = make_float2(1.f, 1.f);  // kBlock: the tile's K and V scales
+      if constexpr (kBlock) bs = scales[st];
+      if (kBlock && kStep && (fl & kNew) && (fl & kRope)) {
+        bs = store_new_block(stage, bs, valid - 1, d.w);
+      } else if (kStep && (fl & kNew) && (fl & kRope)) {
         // The new token (row valid - 1 of this tile): rotate its k, write k and v into the
         // staged tiles before they are read, and store both into the cache slot.
         const int row = valid - 1;
@@ -573,8 +702,14 @@ decode_partition_kernel(const __grid_constant__ CUtensorMap tm_k,
           // two accumulator chains, as for bf16: the MMAs issue in program order
           mma_f16_16816(sc2, lo0, lo1, hi0, hi1, qb[2 * c2 + 1][0], qb[2 * c2 + 1][1]);
         }
+        if constexpr (kBlock) {
+          const float fold_b = a.scale_log2 * bs.x, lift = log2_of(bs.y);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sc[i] = (sc[i] + sc2[i]) * k_fold;
+          for (int i = 0; i < 4; ++i) sc[i] = fmaf(sc[i] + sc2[i], fold_b, lift);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sc[i] = (sc[i] + sc2[i]) * k_fold;
+        }
       } else {
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) {
@@ -605,9 +740,12 @@ decode_partition_kernel(const __grid_constant__ CUtensorMap tm_k,
       }
       // Shifts m0, m1 in the log2 domain: a head's shift moves to its maximum only when that
       // passes it by more than 8, so P stays at most 2^8 and O is rescaled far less often.
-      const float bs0 = bm0 * fold, bs1 = bm1 * fold;
-      const float mn0 = bs0 > m0 + 8.f ? bs0 : m0;
-      const float mn1 = bs1 > m1 + 8.f ? bs1 : m1;
+      const float top0 = bm0 * fold, top1 = bm1 * fold;
+      // Block scales: P is held 2^7 higher (at most 2^15 in f16), so that tokens far below the
+      // largest contribution stay normal f16 values.
+      constexpr float kLag = kBlock ? 15.f : 8.f, kRaise = kBlock ? 7.f : 0.f;
+      const float mn0 = top0 > m0 + kLag ? top0 - kRaise : m0;
+      const float mn1 = top1 > m1 + kLag ? top1 - kRaise : m1;
       const float al0 = ex2_ftz(m0 - mn0);
       const float al1 = ex2_ftz(m1 - mn1);
       m0 = mn0;
@@ -620,8 +758,14 @@ decode_partition_kernel(const __grid_constant__ CUtensorMap tm_k,
       if constexpr (kFp8) {
         p_lo = pack_f16x2(e0, e1);
         p_hi = pack_f16x2(e2, e3);
-        l0 = fmaf(l0, al0, f16lo(p_lo) + f16lo(p_hi));
-        l1 = fmaf(l1, al1, f16hi(p_lo) + f16hi(p_hi));
+        if constexpr (kBlock) {
+          const float iv = __frcp_rn(bs.y);
+          l0 = fmaf(l0, al0, (e0 + e2) * iv);
+          l1 = fmaf(l1, al1, (e1 + e3) * iv);
+        } else {
+          l0 = fmaf(l0, al0, f16lo(p_lo) + f16lo(p_hi));
+          l1 = fmaf(l1, al1, f16hi(p_lo) + f16hi(p_hi));
+        }
       } else {
         p_lo = pack_bf16x2(e0, e1);
         p_hi = pack_bf16x2(e2, e3);
@@ -694,8 +838,9 @@ decode_partition_kernel(const __grid_constant__ CUtensorMap tm_k,
         const bool h0 = 2 * cq < G;
         const bool h1 = 2 * cq + 1 < G;
         if (fl & kWhole) {
-          const float i0 = v_fold / L0;
-          const float i1 = v_fold / L1;
+          // kBlock: a sequence whose every block is out of range has L = 0 and gives zeros
+          const float i0 = kBlock && L0 == 0.f ? 0.f : v_fold / L0;
+          const float i1 = kBlock && L1 == 0.f ? 0.f : v_fold / L1;
           uint32_t* orow0 = reinterpret_cast<uint32_t*>(a.out + (head0 + 2 * cq) * kHeadDim);
           uint32_t* orow1 = orow0 + kHeadDim / 2;
 #pragma unroll
@@ -952,9 +1097,9 @@ decode_merge_kernel(const DecodeArgs a) {
       Lt = fmaf(Lt, al, ml.y * be);
       At = fmaf(At, al, s_acc[q][quarter][lane] * be);
     }
-    *orow = __float2bfloat16_rn(At / Lt);
+    *orow = __float2bfloat16_rn(a.kv_scale && Lt == 0.f ? 0.f : At / Lt);
   } else {
-    *orow = __float2bfloat16_rn(acc / L);
+    *orow = __float2bfloat16_rn(a.kv_scale && L == 0.f ? 0.f : acc / L);
   }
 }
 
@@ -977,7 +1122,7 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 // Persistent grid size for this device: SMs x resident CTAs per SM, capped so that the grid
 // has at most kMaxDecodeWarps warps (looked up once per device and kernel variant, at the
 // largest shared-memory footprint the kernel can ask for).
-template <bool kStep, bool kFp8>
+template <bool kStep, bool kFp8, bool kBlock = false>
 cudaError_t persistent_ctas(int* ctas) {
   static std::mutex mu;
   static int cached[64] = {};
@@ -987,15 +1132,16 @@ cudaError_t persistent_ctas(int* ctas) {
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   std::lock_guard<std::mutex> lock(mu);
   if (!cached[dev]) {
-    const int smem = Layout<kStep, kFp8>::smem(kMaxDecodeSeqs);
-    auto kernel = decode_partition_kernel<kStep, kFp8>;
+    using L = Layout<kStep, kFp8, kBlock>;
+    const int smem = L::smem(kMaxDecodeSeqs);
+    auto kernel = decode_partition_kernel<kStep, kFp8, false, false, kBlock>;
     err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess) return err;
     // the early-metadata variant and (unfused) the gather run the same kernel shape
-    err = cudaFuncSetAttribute(decode_partition_kernel<kStep, kFp8, false, true>,
+    err = cudaFuncSetAttribute(decode_partition_kernel<kStep, kFp8, false, true, kBlock>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess) return err;
-    if (!kStep) {
+    if constexpr (!kStep && !kBlock) {
       err = cudaFuncSetAttribute(decode_partition_kernel<false, kFp8, true>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
       if (err != cudaSuccess) return err;
@@ -1003,38 +1149,39 @@ cudaError_t persistent_ctas(int* ctas) {
     int sms = 0, per_sm = 0;
     err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (err != cudaSuccess) return err;
-    err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, Layout<kStep, kFp8>::kWarpsN * 32, smem);
+    err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, L::kWarpsN * 32, smem);
     if (err != cudaSuccess) return err;
     if (per_sm < 1) return cudaErrorInvalidConfiguration;
-    cached[dev] = min(sms * per_sm, kMaxDecodeWarps / Layout<kStep, kFp8>::kWarpsN);
+    cached[dev] = min(sms * per_sm, kMaxDecodeWarps / L::kWarpsN);
   }
   *ctas = cached[dev];
   return cudaSuccess;
 }
 
-template <bool kStep, bool kFp8, bool kGather = false>
+template <bool kStep, bool kFp8, bool kGather = false, bool kBlock = false>
 cudaError_t launch_partition(DecodeArgs& a, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                              const cudaLaunchAttribute* attr, cudaStream_t stream) {
   int max_ctas = 0;
-  cudaError_t err = persistent_ctas<kStep, kFp8>(&max_ctas);
+  cudaError_t err = persistent_ctas<kStep, kFp8, kBlock>(&max_ctas);
   if (err != cudaSuccess) return err;
   // No more CTAs than there can be ranges (ranges are dealt to the CTAs one at a time).
   const long long jobs_bound = static_cast<long long>(a.num_seqs) * a.num_kv_heads *
                                ((a.max_context_len + kBlockSize - 1) / kBlockSize);
   const long long want = (jobs_bound + kMinRangeBlocks - 1) / kMinRangeBlocks;
   const long long ctas = min(static_cast<long long>(max_ctas), want);
-  constexpr int kWarpsN = Layout<kStep, kFp8>::kWarpsN;
+  using L = Layout<kStep, kFp8, kBlock>;
+  constexpr int kWarpsN = L::kWarpsN;
   a.num_warps = static_cast<int>(ctas) * kWarpsN;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(kWarpsN * 32);
-  cfg.dynamicSmemBytes = Layout<kStep, kFp8>::smem(a.num_seqs);
+  cfg.dynamicSmemBytes = L::smem(a.num_seqs);
   cfg.stream = stream;
   cfg.attrs = const_cast<cudaLaunchAttribute*>(attr);
   cfg.numAttrs = 1;
-  auto kernel = decode_partition_kernel<kStep, kFp8, kGather>;
+  auto kernel = decode_partition_kernel<kStep, kFp8, kGather, false, kBlock>;
   if constexpr (!kGather)
-    if (a.early_metadata) kernel = decode_partition_kernel<kStep, kFp8, false, true>;
+    if (a.early_metadata) kernel = decode_partition_kernel<kStep, kFp8, false, true, kBlock>;
   return cudaLaunchKernelEx(&cfg, kernel, tm_k, tm_v, a);
 }
 
@@ -1118,7 +1265,8 @@ cudaError_t launch_decode(const DecodeArgs& args, cudaStream_t stream) {
   const int G = a.num_q_heads / a.num_kv_heads;
   if (G < 1 || G > 8 || a.num_seqs > kMaxDecodeSeqs) return cudaErrorInvalidValue;
   const bool step = a.k_new != nullptr;
-  const bool fp8 = a.k_scale != nullptr;
+  const bool block = a.kv_scale != nullptr;
+  const bool fp8 = a.k_scale != nullptr || block;
   const long long rows = static_cast<long long>(a.num_blocks) * a.num_kv_heads * kBlockSize;
   CUtensorMap tm_k, tm_v;
   if (!cache_tensor_map(a.k_cache, rows, fp8, &tm_k) || !cache_tensor_map(a.v_cache, rows, fp8, &tm_v))
@@ -1127,7 +1275,9 @@ cudaError_t launch_decode(const DecodeArgs& args, cudaStream_t stream) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaError_t err;
-  if (fp8) err = step ? launch_partition<true, true>(a, tm_k, tm_v, attr, stream)
+  if (block) err = step ? launch_partition<true, true, false, true>(a, tm_k, tm_v, attr, stream)
+                        : launch_partition<false, true, false, true>(a, tm_k, tm_v, attr, stream);
+  else if (fp8) err = step ? launch_partition<true, true>(a, tm_k, tm_v, attr, stream)
                       : launch_partition<false, true>(a, tm_k, tm_v, attr, stream);
   else err = step ? launch_partition<true, false>(a, tm_k, tm_v, attr, stream)
                   : launch_partition<false, false>(a, tm_k, tm_v, attr, stream);

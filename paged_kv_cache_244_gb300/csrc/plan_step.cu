@@ -1,0 +1,257 @@
+// The metadata of one serving step, built on the GPU from request lengths (pa_plan_step).
+//
+// "从零实现 LLM 推理引擎：深挖 vLLM 的六大核心优化", §3.1 (block tables grown from a free list),
+// §3.2 (append_slot) and §3.3 (the rows of a chunk).
+//
+// Two exclusive sums over the sequences say everything: start_s of their new rows and x_s of
+// their new table entries (a sequence that is in error brings neither).  Entry x takes
+// free_blocks[F - 1 - x]; s is granted when it needs no block or x_{s+1} <= F, so the granted
+// entries are exactly x < `taken`.  Rows and entries are then written independently: a thread
+// finds the sequence of its row (or entry) by binary search in the sums.
+//
+// Every CTA forms both sums for itself in shared memory (S <= 8192: at most 64 KiB read from
+// L2) and writes its own slice of the sequences, entries and rows, so there is one launch and
+// nothing to wait for between CTAs.  num_free is read by every CTA: where num_free_out is the
+// same word, a grid of several CTAs leaves it to a second launch of one CTA.
+
+#include <mutex>
+
+#include "pa_device.cuh"
+#include "pa_launch.h"
+
+namespace pa {
+namespace {
+
+constexpr int kPlanThreads = 512;
+constexpr int kPlanRowsPerThread = 4;
+// Rows that one CTA takes before another is launched.
+constexpr int kPlanRowsPerCta = kPlanThreads * kPlanRowsPerThread;
+constexpr int kPlanMaxCtas = 608;   // 4 CTAs of 512 threads on each of 152 SMs
+
+// start [S + 1], x [S + 1] (int32), good [S] (bytes)
+__host__ __device__ inline int plan_smem(int S) { return 2 * 4 * (S + 1) + S + 16; }
+
+// Largest s with sums[s] <= v, for 0 <= v < sums[n].
+__device__ __forceinline__ int plan_find(const int* sums, int n, int v) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (sums[mid] <= v) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// Exclusive sum over the CTA's threads (v may be long long); *total receives the whole sum.
+template <typename T>
+__device__ __forceinline__ T block_exclusive(T v, T* total) {
+  __shared__ T sums[kPlanThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  T incl = v;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const T y = __shfl_up_sync(kFullMask, incl, d);
+    if (lane >= d) incl += y;
+  }
+  __syncthreads();  // the array is free of an earlier call's readers
+  if (lane == 31) sums[warp] = incl;
+  __syncthreads();
+  T before = 0, all = 0;
+  for (int w = 0; w < kPlanThreads / 32; ++w) {
+    if (w < warp) before += sums[w];
+    all += sums[w];
+  }
+  *total = all;
+  return before + incl - v;
+}
+
+__device__ __forceinline__ int blocks_of(int tokens) { return (tokens + kBlockSize - 1) / kBlockSize; }
+
+// count_only: only num_free_out is written (the second launch of an in-place count).
+template <bool kCountOnly>
+__global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanArgs a, const int write_count) {
+  extern __shared__ int smem[];
+  pdl_wait_prior_grid();
+  pdl_allow_next_grid();
+  const int S = a.num_seqs, T = a.num_tokens, tid = threadIdx.x;
+  int* start = smem;             // [S + 1]
+  int* x = smem + S + 1;         // [S + 1]
+  unsigned char* good = reinterpret_cast<unsigned char*>(smem + 2 * (S + 1));
+  const bool first_cta = blockIdx.x == 0;
+
+  // ---- the two sums: each thread takes a contiguous share of the sequences ----------------
+  const int per = (S + kPlanThreads - 1) / kPlanThreads;
+  const int s0 = min(S, tid * per), s1 = min(S, s0 + per);
+  const long long table_tokens = static_cast<long long>(a.max_blocks) * kBlockSize;
+  long long rows = 0;
+  for (int s = s0; s < s1; ++s) {
+    const int n = a.new_lens[s];
+    if (n > 0 && n <= T) rows += n;
+  }
+  long long all_rows;
+  long long r = block_exclusive<long long>(rows, &all_rows);
+  // Needs: of the sequences whose lengths and rows are in order.  Each is at most max_blocks
+  // < 2^27 blocks and there are at most 8192, so their sum is kept in 64 bits, and clamped
+  // to 2^31 - 1 where it is stored (a free list is shorter, so the order is unchanged).
+  long long need_sum = 0;
+  for (int s = s0; s < s1; ++s) {
+    const int n = a.new_lens[s], c = a.cached_lens[s];
+    const bool in_rows = n >= 0 && n <= T;
+    start[s] = static_cast<int>(min(r, static_cast<long long>(T)));
+    if (in_rows) r += n;
+    const bool ok = in_rows && c >= 0 && static_cast<long long>(c) + n <= table_tokens && r <= T;
+    good[s] = ok ? 1 : 0;
+    if (!ok && first_cta && !kCountOnly) raise_flag(a.status, PA_FLAG_CONTEXT_LEN_OOB);
+    if (ok) need_sum += blocks_of(c + n) - blocks_of(c);
+  }
+  long long all_need;
+  long long e = block_exclusive<long long>(need_sum, &all_need);
+  constexpr long long kTop = 0x7fffffffll;
+  for (int s = s0; s < s1; ++s) {
+    x[s] = static_cast<int>(min(e, kTop));
+    if (good[s]) {
+      const int c = a.cached_lens[s];
+      e += blocks_of(c + a.new_lens[s]) - blocks_of(c);
+    }
+  }
+  const int total_rows = static_cast<int>(min(all_rows, static_cast<long long>(T)));
+  if (tid == 0) {
+    start[S] = total_rows;
+    x[S] = static_cast<int>(min(all_need, kTop));
+  }
+  int F = a.num_free[0];
+  if (F < 0 || F > a.free_capacity) {
+    if (first_cta && tid == 0 && !kCountOnly) raise_flag(a.status, PA_FLAG_BLOCK_ID_OOB);
+    F = F < 0 ? 0 : a.free_capacity;
+  }
+  __syncthreads();
+  // taken = the largest x_{s} <= F: the sums do not fall, so it is found by binary search
+  int taken;
+  if (x[S] <= F) {
+    taken = x[S];
+  } else {
+    taken = x[plan_find(x, S, F)];   // x[S] > F: largest s with x[s] <= F
+  }
+  if (write_count && first_cta && tid == 0) a.num_free_out[0] = F - taken;
+  if (kCountOnly) return;
+
+  // granted: x[s + 1] <= F, or nothing needed
+  auto is_granted = [&](int s) { return good[s] && (x[s + 1] == x[s] || x[s + 1] <= F); };
+  const int nb = static_cast<int>(gridDim.x), b = static_cast<int>(blockIdx.x);
+  const int gtid = b * kPlanThreads + tid, gthreads = nb * kPlanThreads;
+
+  for (int s = gtid; s <= S; s += gthreads) {
+    a.q_start[s] = start[s];
+    if (s == S) break;
+    const bool g = is_granted(s);
+    a.context_lens[s] = g ? a.cached_lens[s] + a.new_lens[s] : 0;
+    a.granted[s] = g ? 1 : 0;
+    if (!g && good[s]) raise_flag(a.status, PA_FLAG_POOL_EXHAUSTED);
+  }
+  // new table entries
+  for (int k = gtid; k < taken; k += gthreads) {
+    const int s = plan_find(x, S, k);
+    int id = a.free_blocks[F - 1 - k];
+    if (id < 0 || id >= a.num_blocks) {
+      raise_flag(a.status, PA_FLAG_BLOCK_ID_OOB);
+      id = -1;
+    }
+    a.block_tables[static_cast<size_t>(s) * a.max_blocks + blocks_of(a.cached_lens[s]) + (k - x[s])] = id;
+  }
+  // rows: each thread takes groups of kPlanRowsPerThread neighbours
+  const int groups = (T + kPlanRowsPerThread - 1) / kPlanRowsPerThread;
+  for (int gidx = gtid; gidx < groups; gidx += gthreads) {
+    const int t0 = gidx * kPlanRowsPerThread;
+    int s = t0 < total_rows ? plan_find(start, S, t0) : S;
+    int pos[kPlanRowsPerThread];
+    long long slot[kPlanRowsPerThread];
+    int cur = -1, c = 0, old = 0, id = -1, id_block = -1;
+    bool live = false;
+#pragma unroll
+    for (int i = 0; i < kPlanRowsPerThread; ++i) {
+      const int t = t0 + i;
+      pos[i] = 0;
+      slot[i] = -1;
+      if (t >= total_rows) continue;
+      while (start[s + 1] <= t) ++s;   // sequences without rows are passed over
+      if (s != cur) {
+        cur = s;
+        live = is_granted(s);
+        c = a.cached_lens[s];
+        old = blocks_of(c);
+        id_block = -1;
+      }
+      if (!live) continue;
+      const int p = c + (t - start[s]);
+      const int j = p / kBlockSize;
+      if (j != id_block) {
+        id_block = j;
+        id = j < old ? a.block_tables[static_cast<size_t>(s) * a.max_blocks + j]
+                     : a.free_blocks[F - 1 - (x[s] + (j - old))];
+        if (id < 0 || id >= a.num_blocks) {
+          raise_flag(a.status, PA_FLAG_BLOCK_ID_OOB);
+          id = -1;
+        }
+      }
+      pos[i] = p;
+      slot[i] = id < 0 ? -1 : static_cast<long long>(id) * kBlockSize + (p % kBlockSize);
+    }
+    if (t0 + kPlanRowsPerThread <= T) {
+      *reinterpret_cast<int4*>(a.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+      longlong2* dst = reinterpret_cast<longlong2*>(a.slot_mapping + t0);
+      dst[0] = make_longlong2(slot[0], slot[1]);
+      dst[1] = make_longlong2(slot[2], slot[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPlanRowsPerThread; ++i) {
+        if (t0 + i >= T) break;
+        a.positions[t0 + i] = pos[i];
+        a.slot_mapping[t0 + i] = slot[i];
+      }
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_plan_step(const PlanArgs& a, cudaStream_t stream) {
+  const int smem = plan_smem(a.num_seqs);
+  if (smem > 48 * 1024) {  // opt in to the largest size once per device
+    static std::mutex mu;
+    static bool done[64] = {};
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(mu);
+    if (!done[dev]) {
+      err = cudaFuncSetAttribute(plan_step_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 plan_smem(kMaxDecodeSeqs));
+      if (err == cudaSuccess)
+        err = cudaFuncSetAttribute(plan_step_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   plan_smem(kMaxDecodeSeqs));
+      if (err != cudaSuccess) return err;
+      done[dev] = true;
+    }
+  }
+  long long ctas = (static_cast<long long>(a.num_tokens) + kPlanRowsPerCta - 1) / kPlanRowsPerCta;
+  if (ctas < 1) ctas = 1;
+  if (ctas > kPlanMaxCtas) ctas = kPlanMaxCtas;
+  const bool later = a.num_free == a.num_free_out && ctas > 1;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t err = cudaLaunchKernelEx(&cfg, plan_step_kernel<false>, a, later ? 0 : 1);
+  if (err != cudaSuccess || !later) return err;
+  cfg.gridDim = dim3(1);
+  return cudaLaunchKernelEx(&cfg, plan_step_kernel<true>, a, 1);
+}
+
+}  // namespace pa

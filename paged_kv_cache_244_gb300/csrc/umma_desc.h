@@ -56,6 +56,12 @@ PA_HOST_DEVICE inline uint64_t umma_smem_desc(uint32_t smem_addr, uint32_t leadi
   return d;
 }
 
+// f16 x f16 -> f32 (otherwise as umma_idesc_bf16).
+PA_HOST_DEVICE inline uint32_t umma_idesc_f16(int M, int N, bool a_mn_major, bool b_mn_major) {
+  return (1u << 4) | ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) |
+         ((static_cast<uint32_t>(N) >> 3) << 17) | ((static_cast<uint32_t>(M) >> 4) << 24);
+}
+
 // bf16 x bf16 -> f32, M x N tile; *_mn_major: the operand is stored with M (or N) contiguous.
 PA_HOST_DEVICE inline uint32_t umma_idesc_bf16(int M, int N, bool a_mn_major, bool b_mn_major) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn_major ? 1u : 0u) << 15) |
