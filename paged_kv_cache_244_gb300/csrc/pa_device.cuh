@@ -245,6 +245,16 @@ __device__ __forceinline__ void umma_bf16_tmem_a(uint32_t d_tmem, uint32_t a_tme
       ::"r"(d_tmem), "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
       : "memory");
 }
+// kind::f8f6f4 (8-bit operands): A read from tensor memory (row r of A in lane r, four codes a
+// column, K = 32 elements in 8 columns starting at a_tmem).
+__device__ __forceinline__ void umma_e4m3_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
+                                                 bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
 // True in exactly one lane of the (converged) warp.  Work issued under it keeps the warp's
 // values uniform, so descriptors stay in uniform registers.
 __device__ __forceinline__ bool elect_one() {
@@ -379,6 +389,13 @@ __device__ __forceinline__ uint16_t e4m3x2_of(uint32_t bf16_pair, float inv) {
   return r;
 }
 
+// E4M3 codes of two floats, round to nearest even, saturating; low byte = lo.
+__device__ __forceinline__ uint16_t e4m3x2_of_floats(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 // a b - c d in fp32 with the rounding error of c d recovered by an FMA (the compensated
 // difference of products: w = c d rounded, e = w - c d exactly, result (a b - w) + e).  Within
 // about two fp32 ulps of the exact value even when a b and c d nearly cancel, where the plain
@@ -441,6 +458,11 @@ __device__ __forceinline__ uint32_t e4m3x4_rescale(uint32_t w, float f) {
 }
 __device__ __forceinline__ uint4 e4m3x16_rescale(uint4 w, float f) {
   return make_uint4(e4m3x4_rescale(w.x, f), e4m3x4_rescale(w.y, f), e4m3x4_rescale(w.z, f), e4m3x4_rescale(w.w, f));
+}
+
+// Barrier of `threads` threads of the block (named barrier `id`, 1..15).
+__device__ __forceinline__ void named_barrier(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
 // Warpgroup-collective: this thread's registers from here on (a multiple of 8).  `inc` waits until

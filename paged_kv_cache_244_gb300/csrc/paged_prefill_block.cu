@@ -6,28 +6,38 @@
 //
 // The work is cut as in the bf16 prefill: CTA = (sequence, KV head, tile of floor(128 / G)
 // queries), 128 matrix rows = (query, head) pairs, keys 64 at a time (four blocks), two CTAs per
-// SM.  E4M3 codes widen exactly to f16, so they enter the matrix products unscaled and the
-// scales k_b, v_b of key t's block act on the scores:
+// SM.  The codes enter the matrix products unscaled, and the scales k_b, v_b of key t's block act
+// on the scores:
 //   x_t = scale_log2 k_b (q . Kcode_t) + log2 v_b,   p_t = 2^(x_t - m),
 //   O = sum p_t Vcode_t,   L = sum p_t / v_b,   out = O / L.
 // Both sums carry 2^m, and v_b cancels in the second.  The shift m follows the largest
 // contribution p_t lazily, from 7 below it (the largest p_t is 2^7 when the shift is set and at
 // most 2^15 before it moves), so P fits f16 whatever the scales and tokens far below the largest
-// are still normal f16 values.
-// Inside a block k_b and v_b are constants: the row maximum is taken per block on the raw
-// products (k_b > 0) and then scaled, each exponent's argument stays one FMA, and L costs one FMA
-// a block.
+// are still normal f16 values.  Inside a block k_b and v_b are constants: the row maximum is taken
+// per block on the raw products (k_b > 0) and then scaled, each exponent's argument stays one FMA,
+// and L costs one FMA a block.
+//
+// K codes are the B operand as they lie in the cache (kind::f8f6f4).  A bf16 q has 8 significant
+// bits and E4M3 four, so a row of q, scaled by a power of two to put its largest magnitude in
+// [128, 256), is the sum of two E4M3 rows, q = hi + lo, exact down to 2^-10 against that
+// largest (values below 2^-18 of it are lost): S = hi K + lo K, two products of twice the f16
+// rate, with no K tile to widen.  V codes widen exactly to f16 (P V in f16 keeps P's 11 bits).
 //
 // Warpgroups of a CTA (registers split with setmaxnreg):
 //   0   softmax, one thread per row
 //   1   warp 4 K tiles and warp 6 V tiles by TMA (one 2 KiB box a block), warp 5 the MMAs
-//   2   converters: 128 threads widen a stage's K codes, then its V codes, from the TMA's ring
-//       into the f16 operand ring, 16 codes a load, in the layouts that the MMAs read (K-major
-//       K as two 64-dim halves, MN-major V as two halves a block, 128-byte swizzle).  V rows past
-//       the context, and V of absent blocks, are written as zeros.
-// Tensor memory per CTA (256 columns): Q as f16 pairs 0-63, S 64-127, O 128-255.
-// Shared memory per CTA (113 KB): two 32 KiB f16 stages, two 16 KiB code stages, the 16 KiB P
-// buffer, barriers.  Every wait is bounded.
+//   2   converters: 128 threads widen a stage's V codes from the TMA's ring into the f16 operand
+//       ring, 16 codes a load, in the MN-major layout that the MMA reads (two 64-dim halves a
+//       block, 128-byte swizzle).  V rows past the context, and V of absent blocks, are written
+//       as zeros.
+// Tensor memory per CTA (256 columns): q hi 0-31, q lo 32-63 (four codes a column), S 64-127, O
+// 128-255.  Shared memory per CTA: three 8 KiB K stages, two 8 KiB stages of V codes, three 16 KiB
+// stages of f16 V, the 16 KiB P buffer (which also carries Q in and O out, so that both move in
+// whole lines), barriers: 105 KiB.  Every wait is bounded.
+//
+// What bounds it: the shared-memory data path.  A first form that widened K too and gave each
+// thread its own row of q and out to load and store kept that path 88% busy (ncu, 4 x 2048
+// tokens: LSU 68.6% of its wavefronts, tensor core 19.6%) with the tensor pipe 26% active, 87 us.
 
 #include <mutex>
 
@@ -43,38 +53,32 @@ namespace {
 constexpr int kBpRows = 128;
 constexpr int kBpKB = 4;                             // key blocks per stage
 constexpr int kBpKeys = kBpKB * kBlockSize;          // 64
-constexpr int kBpRing = 2;                           // stages of codes, and of f16 operands
-constexpr int kBpHalf = kBlockSize * 128;            // 16 rows x 64 f16, and a block's codes: 2 KiB
-constexpr int kBpCodes = kBpKB * kBpHalf;            // codes of K (or V) of a stage: 8 KiB
-constexpr int kBpKHalf = kBpKB * kBpHalf;            // one f16 K half of a stage: 8 KiB
-constexpr int kBpVOff = 2 * kBpKHalf;                // f16 V after the K halves
-constexpr int kBpStage = 2 * kBpVOff;                // 32 KiB
-constexpr int kBpCodeOff = kBpRing * kBpStage;       // code stages: [K | V]
-constexpr int kBpCodeStage = 2 * kBpCodes;           // 16 KiB
-constexpr int kBpPOff = kBpCodeOff + kBpRing * kBpCodeStage;
+constexpr int kBpKRing = 3, kBpCRing = 2, kBpVRing = 3;   // stages of K codes, V codes, f16 V
+constexpr int kBpTile = kBlockSize * 128;            // a block's codes, or 16 rows x 64 f16: 2 KiB
+constexpr int kBpCodes = kBpKB * kBpTile;            // codes of K (or V) of a stage: 8 KiB
+constexpr int kBpVStage = 2 * kBpCodes;              // f16 V of a stage: 16 KiB
+constexpr int kBpCOff = kBpKRing * kBpCodes;
+constexpr int kBpVOff = kBpCOff + kBpCRing * kBpCodes;
+constexpr int kBpPOff = kBpVOff + kBpVRing * kBpVStage;
 constexpr int kBpPBytes = kBpRows * kBpKeys * 2;     // 16 KiB
 constexpr int kBpHdrOff = kBpPOff + kBpPBytes;
 constexpr int kBpHeader = 256;
-// As in the bf16 kernel: the header sits in the padding before the first 1024-byte boundary when
-// it fits there, else after the P buffer; either way the layout ends within kBpSmem.
-constexpr int kBpSmem = kBpHdrOff + kBpHeader + 768;
+constexpr int kBpFoldOff = kBpHdrOff + kBpHeader;    // a float per row
+constexpr int kBpSmem = kBpFoldOff + kBpRows * 4 + 1024;  // + alignment of the first stage
 static_assert(2 * (kBpSmem + 1024) <= 228 * 1024, "two CTAs per SM");
-static_assert(1008 + kBpHdrOff <= kBpSmem && kBpHeader - 1 + kBpHdrOff + kBpHeader <= kBpSmem, "layout");
 constexpr int kBpThreads = 384;
 // registers per thread at launch, and the split (their sums per warpgroup are equal)
-constexpr int kBpRegsSoftmax = 120, kBpRegsIssue = 56, kBpRegsConvert = 64;
+constexpr int kBpRegsSoftmax = 136, kBpRegsIssue = 48, kBpRegsConvert = 56;
 static_assert(kBpRegsSoftmax + kBpRegsIssue + kBpRegsConvert <= 3 * 80, "of the 80 a thread launched with");
 constexpr uint32_t kBpTmemCols = 256, kBpQCol = 0, kBpSCol = 64, kBpOCol = 128;
 
 // header (byte offsets)
-constexpr int kCodesKFull = 0;     // [2] K TMA -> converters
-constexpr int kCodesVFull = 16;    // [2] V TMA -> converters
-constexpr int kCodesKFree = 32;    // [2] converters (128) -> K TMA
-constexpr int kCodesVFree = 48;    // [2] converters (128) -> V TMA
-constexpr int kKFull = 64;         // [2] converters (128) -> MMA (S)
-constexpr int kVFull = 80;         // [2] converters (128) -> MMA (P V)
-constexpr int kKFree = 96;         // [2] MMA (S done) -> converters
-constexpr int kVFree = 112;        // [2] MMA (P V done) -> converters, softmax (P buffer, O)
+constexpr int kKFull = 0;          // [3] K TMA -> MMA (S)
+constexpr int kKFree = 24;         // [3] MMA (S done) -> K TMA
+constexpr int kCFull = 48;         // [2] V TMA -> converters
+constexpr int kCFree = 64;         // [2] converters (a warp each: 4) -> V TMA
+constexpr int kVFull = 80;         // [3] converters (4) -> MMA (P V)
+constexpr int kVFree = 104;        // [3] MMA (P V done) -> converters, softmax (P buffer, O)
 constexpr int kSFull = 128;        // MMA (S done) -> softmax
 constexpr int kSFree = 136;        // softmax (128) -> MMA
 constexpr int kPFull = 144;        // [2] softmax (128) -> MMA
@@ -82,6 +86,17 @@ constexpr int kDone = 160;         // MMA: its last MMAs finished
 constexpr int kQReady = 168;       // softmax (128) -> MMA
 constexpr int kTmemAt = 176;
 static_assert(kTmemAt + 4 <= kBpHeader, "header");
+
+// Four bf16 values times `raise` (a power of two) as the sum of two E4M3 values each: the codes of
+// the nearest, and of what it leaves.
+__device__ __forceinline__ void split_e4m3(uint32_t w0, uint32_t w1, float raise, uint32_t& hi, uint32_t& lo) {
+  const float x0 = bf16lo(w0) * raise, x1 = bf16hi(w0) * raise, x2 = bf16lo(w1) * raise, x3 = bf16hi(w1) * raise;
+  const uint16_t h0 = e4m3x2_of_floats(x0, x1), h1 = e4m3x2_of_floats(x2, x3);
+  const uint32_t b0 = e4m3x2_to_f16x2(h0), b1 = e4m3x2_to_f16x2(h1);
+  hi = h0 | (static_cast<uint32_t>(h1) << 16);
+  lo = e4m3x2_of_floats(x0 - f16lo(b0), x1 - f16hi(b0)) |
+       (static_cast<uint32_t>(e4m3x2_of_floats(x2 - f16lo(b1), x3 - f16hi(b1))) << 16);
+}
 
 __global__ void __launch_bounds__(kBpThreads, 2)
 prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -118,9 +133,8 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
 
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t stages = (raw + 1023u) & ~1023u;
-  const uint32_t pad = stages - raw;
-  const uint32_t hdr = pad >= static_cast<uint32_t>(kBpHeader) ? stages - kBpHeader : stages + kBpHdrOff;
-  unsigned char* const base = smem_raw + pad;
+  const uint32_t hdr = stages + kBpHdrOff;
+  unsigned char* const base = smem_raw + (stages - raw);
   unsigned char* const hdr_gen = smem_raw + (hdr - raw);
 
   // Lane k holds the id of block 32 w + k of the current window w, and the next window's.
@@ -142,15 +156,15 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     return static_cast<int>(__ballot_sync(kFullMask, in_pool(id)) & ((1u << kBpKB) - 1));
   };
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kBpRing; ++i) {
-      mbar_init(hdr + kCodesKFull + 8 * i, 1);
-      mbar_init(hdr + kCodesVFull + 8 * i, 1);
-      mbar_init(hdr + kCodesKFree + 8 * i, 128);
-      mbar_init(hdr + kCodesVFree + 8 * i, 128);
-      mbar_init(hdr + kKFull + 8 * i, 128);
-      mbar_init(hdr + kVFull + 8 * i, 128);
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(hdr + kKFull + 8 * i, 1);
       mbar_init(hdr + kKFree + 8 * i, 1);
+      mbar_init(hdr + kVFull + 8 * i, 4);
       mbar_init(hdr + kVFree + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(hdr + kCFull + 8 * i, 1);
+      mbar_init(hdr + kCFree + 8 * i, 4);
       mbar_init(hdr + kPFull + 8 * i, 128);
     }
     mbar_init(hdr + kSFull, 1);
@@ -169,7 +183,7 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(hdr_gen + kTmemAt);
 
   if (warp >= 8) {
-    // ---- converters ------------------------------------------------------------------------
+    // ---- converters of V -------------------------------------------------------------------
     regs_dec<kBpRegsConvert>();
     const int t = threadIdx.x - 256;                // 0..127
     const int c = t & 7;                            // 16-code chunk of a row: dims 16c .. 16c + 15
@@ -188,48 +202,25 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       e4m3x4_to_f16x2x2(w.z, hi.x, hi.y);
       e4m3x4_to_f16x2x2(w.w, hi.z, hi.w);
     };
-    // the codes have landed and (after the ring's first round) their operand slot is free: the
-    // whole warp goes on or gives up
-    auto wait_both = [&](uint32_t full, uint32_t slot_free, uint32_t ph, bool used) {
-      bool ok = mbar_wait_bounded(full, ph);
-      if (ok && used) ok = mbar_wait_bounded(slot_free, ph ^ 1u);
-      return __all_sync(kFullMask, ok) != 0;
-    };
     bool failed = false;
     for (int j = 0; j < nst; ++j) {
-      const int st = j % kBpRing;
-      const uint32_t ph = (j / kBpRing) & 1;
+      const int cst = j % kBpCRing, vst = j % kBpVRing;
       next_window(j);
       const int mask = stage_mask(j);
-      // K: rows of absent blocks keep what the slot held (their scores are masked)
-      if (!wait_both(hdr + kCodesKFull + 8 * st, hdr + kKFree + 8 * st, ph, j >= kBpRing)) {
+      // the codes have landed and (after the ring's first round) the f16 slot is free: the whole
+      // warp goes on or gives up
+      bool ok = mbar_wait_bounded(hdr + kCFull + 8 * cst, (j / kBpCRing) & 1);
+      if (ok && j >= kBpVRing) ok = mbar_wait_bounded(hdr + kVFree + 8 * vst, ((j / kBpVRing) - 1) & 1);
+      if (!__all_sync(kFullMask, ok)) {
         failed = true;
         break;
       }
-      unsigned char* const codes = base + kBpCodeOff + st * kBpCodeStage;
-      unsigned char* const ops = base + st * kBpStage;
+      const unsigned char* codes = base + kBpCOff + cst * kBpCodes;
+      unsigned char* const ops = base + kBpVOff + vst * kBpVStage;
       uint4 w[kBpKB];
 #pragma unroll
-      for (int b = 0; b < kBpKB; ++b) w[b] = *reinterpret_cast<const uint4*>(codes + b * kBpHalf + in_off);
-#pragma unroll
       for (int b = 0; b < kBpKB; ++b) {
-        uint4 lo, hi;
-        widen(w[b], lo, hi);
-        unsigned char* dst = ops + half * kBpKHalf + b * kBpHalf;
-        *reinterpret_cast<uint4*>(dst + out0) = half ? hi : lo;
-        *reinterpret_cast<uint4*>(dst + out1) = half ? lo : hi;
-      }
-      mbar_arrive(hdr + kCodesKFree + 8 * st);
-      fence_proxy_async_smem();                     // before the tensor core reads them
-      mbar_arrive(hdr + kKFull + 8 * st);
-      // V: zeros for absent blocks and rows past the context
-      if (!wait_both(hdr + kCodesVFull + 8 * st, hdr + kVFree + 8 * st, ph, j >= kBpRing)) {
-        failed = true;
-        break;
-      }
-#pragma unroll
-      for (int b = 0; b < kBpKB; ++b) {
-        w[b] = *reinterpret_cast<const uint4*>(codes + kBpCodes + b * kBpHalf + in_off);
+        w[b] = *reinterpret_cast<const uint4*>(codes + b * kBpTile + in_off);
         const bool live = ((mask >> b) & 1) && (kBpKB * j + b != last_blk || r8 < valid_last);
         if (!live) w[b] = make_uint4(0u, 0u, 0u, 0u);
       }
@@ -237,13 +228,16 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       for (int b = 0; b < kBpKB; ++b) {
         uint4 lo, hi;
         widen(w[b], lo, hi);
-        unsigned char* dst = ops + kBpVOff + b * 2 * kBpHalf + half * kBpHalf;
+        unsigned char* dst = ops + (2 * b + half) * kBpTile;
         *reinterpret_cast<uint4*>(dst + out0) = half ? hi : lo;
         *reinterpret_cast<uint4*>(dst + out1) = half ? lo : hi;
       }
-      mbar_arrive(hdr + kCodesVFree + 8 * st);
-      fence_proxy_async_smem();
-      mbar_arrive(hdr + kVFull + 8 * st);
+      fence_proxy_async_smem();                     // before the tensor core reads them
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(hdr + kCFree + 8 * cst);
+        mbar_arrive(hdr + kVFull + 8 * vst);
+      }
     }
     if (failed) raise_flag(a.status, PA_FLAG_TIMEOUT);
   } else if (warp >= 4) {
@@ -253,63 +247,69 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       const bool is_k = warp == 4;
       const CUtensorMap* tm = is_k ? &tm_k : &tm_v;
       if (lane == 0) prefetch_tensor_map(tm);
-      const uint32_t full = hdr + (is_k ? kCodesKFull : kCodesVFull);
-      const uint32_t free_ = hdr + (is_k ? kCodesKFree : kCodesVFree);
+      const int ring = is_k ? kBpKRing : kBpCRing;
+      const uint32_t full = hdr + (is_k ? kKFull : kCFull);
+      const uint32_t free_ = hdr + (is_k ? kKFree : kCFree);
+      const uint32_t slots = stages + (is_k ? 0 : kBpCOff);
+      int st = 0;
+      uint32_t ph = 1;                              // parity of the slot's previous release
       int issued = 0;
       bool failed = false;
       for (int j = 0; j < nst; ++j) {
-        const int st = j % kBpRing;
         next_window(j);
         const int mask = stage_mask(j);
         const int blk = __shfl_sync(kFullMask, ids, ((kBpKB * j) & 31) + (lane & (kBpKB - 1)));
         bool ok = true;
-        if (lane == 0 && j >= kBpRing) ok = mbar_wait_bounded(free_ + 8 * st, ((j / kBpRing) - 1) & 1);
+        if (lane == 0 && j >= ring) ok = mbar_wait_bounded(free_ + 8 * st, ph);
         if (!__shfl_sync(kFullMask, ok, 0)) {
           failed = true;
           break;
         }
         const uint32_t bar = full + 8 * st;
         if (lane == 0) {
-          if (mask) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(__popc(mask)) * kBpHalf);
+          if (mask) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(__popc(mask)) * kBpTile);
           else mbar_arrive(bar);
         }
         __syncwarp();
         if (is_k && lane < kBpKB && kBpKB * j + lane < nblocks && !((mask >> lane) & 1))
           raise_flag(a.status, PA_FLAG_BLOCK_ID_OOB);
         if (lane < kBpKB && ((mask >> lane) & 1)) {
-          const uint32_t dst = stages + kBpCodeOff + st * kBpCodeStage + (is_k ? 0 : kBpCodes) + lane * kBpHalf;
-          tma_load_2d(dst, tm, 0, (blk * Hkv + g) * kBlockSize, bar);
+          tma_load_2d(slots + st * kBpCodes + lane * kBpTile, tm, 0, (blk * Hkv + g) * kBlockSize, bar);
         }
         issued = j + 1;
+        if (++st == ring) {
+          st = 0;
+          ph ^= 1u;
+        }
       }
       if (lane == 0) {
         if (failed) raise_flag(a.status, PA_FLAG_TIMEOUT);
         // let the copies still in flight land before the CTA exits
-        for (int j = max(0, issued - kBpRing); j < issued; ++j)
-          mbar_wait_bounded(full + 8 * (j % kBpRing), (j / kBpRing) & 1, 10000000ull);
+        for (int j = max(0, issued - ring); j < issued; ++j)
+          mbar_wait_bounded(full + 8 * (j % ring), (j / ring) & 1, 10000000ull);
       }
     } else if (warp == 5) {
       // ---- MMA issuer --------------------------------------------------------------------------
-      const uint32_t id_s = umma_idesc_f16(kBpRows, kBpKeys, false, false);
+      const uint32_t id_s = umma_idesc_e4m3(kBpRows, kBpKeys);
       const uint32_t id_pv = umma_idesc_f16(kBpRows, kHeadDim, false, true);
       const uint64_t k_desc0 = umma_smem_desc(stages, 16, 1024);
       const uint64_t p_desc = umma_smem_desc(stages + kBpPOff, 16, 1024);
-      const uint64_t v_desc0 = umma_smem_desc(stages + kBpVOff, kBpHalf, 1024);
+      const uint64_t v_desc0 = umma_smem_desc(stages + kBpVOff, kBpTile, 1024);
       auto wait_all = [&](uint32_t bar, uint32_t parity) {
         return __all_sync(kFullMask, mbar_wait_bounded(bar, parity));
       };
-      // S_j = Q K_j^T once K_j is widened and the softmax has loaded S_{j-1}
+      // S_j = Q K_j^T once K_j has landed and the softmax has loaded S_{j-1}
       auto issue_s = [&](int j) {
-        const int st = j % kBpRing;
-        if (!wait_all(hdr + kKFull + 8 * st, (j / kBpRing) & 1)) return false;
+        const int st = j % kBpKRing;
+        if (!wait_all(hdr + kKFull + 8 * st, (j / kBpKRing) & 1)) return false;
         if (j > 0 && !wait_all(hdr + kSFree, (j - 1) & 1)) return false;
         tc_fence_after();
-        const uint64_t kd = k_desc0 + static_cast<uint64_t>((st * kBpStage) >> 4);
+        const uint64_t kd = k_desc0 + static_cast<uint64_t>((st * kBpCodes) >> 4);
         if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            umma_bf16_tmem_a(tmem + kBpSCol, tmem + kBpQCol + 8 * kk,
-                             kd + static_cast<uint64_t>(((kk >> 2) * kBpKHalf + (kk & 3) * 32) >> 4), id_s, kk > 0);
+          for (int kk = 0; kk < 8; ++kk)            // q hi, then q lo, over the four 32-dim steps of K
+            umma_e4m3_tmem_a(tmem + kBpSCol, tmem + kBpQCol + 8 * kk, kd + static_cast<uint64_t>(((kk & 3) * 32) >> 4),
+                             id_s, kk > 0);
           umma_commit(hdr + kSFull);
           umma_commit(hdr + kKFree + 8 * st);
         }
@@ -326,18 +326,18 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
           failed = true;
           break;
         }
-        const int st = j % kBpRing;
-        if (!wait_all(hdr + kPFull + 8 * (j & 1), (j >> 1) & 1) || !wait_all(hdr + kVFull + 8 * st, (j / kBpRing) & 1)) {
+        const int st = j % kBpVRing;
+        if (!wait_all(hdr + kPFull + 8 * (j & 1), (j >> 1) & 1) || !wait_all(hdr + kVFull + 8 * st, (j / kBpVRing) & 1)) {
           failed = true;
           break;
         }
         tc_fence_after();
-        const uint64_t vd = v_desc0 + static_cast<uint64_t>((st * kBpStage) >> 4);
+        const uint64_t vd = v_desc0 + static_cast<uint64_t>((st * kBpVStage) >> 4);
         if (elect_one()) {
 #pragma unroll
           for (int i = 0; i < kBpKB; ++i)
             umma_bf16(tmem + kBpOCol, p_desc + static_cast<uint64_t>((32 * i) >> 4),
-                      vd + static_cast<uint64_t>((i * 2 * kBpHalf) >> 4), id_pv, j > 0 || i > 0);
+                      vd + static_cast<uint64_t>((i * 2 * kBpTile) >> 4), id_pv, j > 0 || i > 0);
           umma_commit(hdr + kVFree + 8 * st);
         }
         __syncwarp();
@@ -353,29 +353,92 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     // ---- Q into TMEM, then the softmax: thread = row r of the tile ------------------------------
     regs_inc<kBpRegsSoftmax>();
     const int r = threadIdx.x;
-    const int i = r / G, h = r - (r / G) * G;
-    const int p_r = pos0 + i;
+    const int p_r = pos0 + r / G;
     const uint32_t trow = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    unsigned char* const pbuf = base + kBpPOff;
+    // Q (and later out) passes through the P buffer a 64-dim half at a time, 8 lanes a row, so that
+    // global memory sees whole 128-byte lines; 16-byte chunk c of row x sits at c ^ (x % 8).
+    const int hr = r >> 3, hc = r & 7;              // rows hr + 16 k, chunk hc of the half
+    auto global_row = [&](int x) {                  // matrix row x of q and out, -1 past the queries
+      const int xi = x / G;
+      return xi < rows_q ? (static_cast<long long>(q0 + i0 + xi) * a.num_q_heads + g * G + (x - xi * G)) * kHeadDim
+                         : -1ll;
+    };
+    float* const folds = reinterpret_cast<float*>(base + kBpFoldOff);
     {
-      const uint4* src = reinterpret_cast<const uint4*>(
-          a.q + (static_cast<size_t>(q0 + i0 + (i < rows_q ? i : 0)) * a.num_q_heads + g * G + h) * kHeadDim);
+      // Rows hr + 16 k, their dims 8 hc .. + 7 and 64 + 8 hc .. + 7 in this thread.  The row's
+      // largest magnitude (over its 8 lanes) gives the power of two that brings it to [128, 256);
+      // an infinity or a NaN makes the row's scores NaN.  hi codes go through the P buffer now, lo
+      // codes after them.
+      uint2 lo[8][2];
 #pragma unroll
-      for (int part = 0; part < 2; ++part) {
-        uint32_t qv[32];
+      for (int k4 = 0; k4 < 8; k4 += 4) {
+        uint4 v[4][2];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const long long at = global_row(hr + 16 * (k4 + k));
+          v[k][0] = v[k][1] = make_uint4(0u, 0u, 0u, 0u);
+          if (at >= 0) {
+            v[k][0] = reinterpret_cast<const uint4*>(a.q + at)[hc];
+            v[k][1] = reinterpret_cast<const uint4*>(a.q + at)[8 + hc];
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int x = hr + 16 * (k4 + k);
+          uint32_t top = 0;
+#pragma unroll
+          for (int p = 0; p < 2; ++p)
+            top = __vmaxu2(top, __vmaxu2(__vmaxu2(v[k][p].x & 0x7fff7fffu, v[k][p].y & 0x7fff7fffu),
+                                         __vmaxu2(v[k][p].z & 0x7fff7fffu, v[k][p].w & 0x7fff7fffu)));
+#pragma unroll
+          for (int o = 1; o < 8; o <<= 1) top = __vmaxu2(top, __shfl_xor_sync(kFullMask, top, o));
+          top = max(top & 0xffffu, top >> 16);
+          int e = 7 + 127 - static_cast<int>(top >> 7);
+          e = (top >> 7) == 0 ? 0 : min(max(e, -126), 126);
+          const float raise = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+          if (hc == 0)
+            folds[x] = top >= 0x7f80u ? __uint_as_float(0x7fc00000u)
+                                      : __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            uint2 hi;
+            split_e4m3(v[k][p].x, v[k][p].y, raise, hi.x, lo[k4 + k][p].x);
+            split_e4m3(v[k][p].z, v[k][p].w, raise, hi.y, lo[k4 + k][p].y);
+            *reinterpret_cast<uint2*>(pbuf + x * 128 + (((4 * p + (hc >> 1)) ^ (x & 7)) << 4) + 8 * (hc & 1)) = hi;
+          }
+        }
+      }
+#pragma unroll
+      for (int part = 0; part < 2; ++part) {        // hi, then lo
+        if (part) {
+          named_barrier(1, 128);                    // hi has been read
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int x = hr + 16 * k;
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+              *reinterpret_cast<uint2*>(pbuf + x * 128 + (((4 * p + (hc >> 1)) ^ (x & 7)) << 4) + 8 * (hc & 1)) = lo[k][p];
+          }
+        }
+        named_barrier(1, 128);
+        uint32_t codes[32];
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-          const uint4 v = i < rows_q ? src[8 * part + c] : make_uint4(0u, 0u, 0u, 0u);
-          qv[4 * c] = bf16x2_to_f16x2(v.x);
-          qv[4 * c + 1] = bf16x2_to_f16x2(v.y);
-          qv[4 * c + 2] = bf16x2_to_f16x2(v.z);
-          qv[4 * c + 3] = bf16x2_to_f16x2(v.w);
+          const uint4 w = *reinterpret_cast<const uint4*>(pbuf + r * 128 + ((c ^ (r & 7)) << 4));
+          codes[4 * c] = w.x;
+          codes[4 * c + 1] = w.y;
+          codes[4 * c + 2] = w.z;
+          codes[4 * c + 3] = w.w;
         }
-        tmem_st32(trow + kBpQCol + 32 * part, qv);
+        tmem_st32(trow + kBpQCol + 32 * part, codes);
       }
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(hdr + kQReady);
     }
+    const float row_fold = folds[r];                // q = row_fold (hi + lo)
+    named_barrier(1, 128);                          // the P buffer is free for P
     // Scales of the lane's block of the window: factor on q . Kcode, lift of the exponent, weight in L
     float fold = 0.f, lift = 0.f, weigh = 0.f, fold_next = 0.f, lift_next = 0.f, weigh_next = 0.f;
     auto load_scales = [&](int id, float& f, float& e, float& w) {
@@ -401,7 +464,7 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
 #pragma unroll
       for (int b = 0; b < kBpKB; ++b) {
         const int src = ((kBpKB * j) & 31) + b;
-        f[b] = __shfl_sync(kFullMask, fold, src);
+        f[b] = __shfl_sync(kFullMask, fold, src) * row_fold;
         e[b] = __shfl_sync(kFullMask, lift, src);
         w[b] = __shfl_sync(kFullMask, weigh, src);
       }
@@ -466,7 +529,7 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       // P V of stage j - 1 must be done before P_j overwrites its buffer and before O is rescaled
       if (j > 0) {
         const int pj = j - 1;
-        if (!__all_sync(kFullMask, mbar_wait_bounded(hdr + kVFree + 8 * (pj % kBpRing), (pj / kBpRing) & 1))) {
+        if (!__all_sync(kFullMask, mbar_wait_bounded(hdr + kVFree + 8 * (pj % kBpVRing), (pj / kBpVRing) & 1))) {
           failed = true;
           break;
         }
@@ -485,7 +548,7 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         tmem_wait_st();
       }
       {
-        unsigned char* prow = base + kBpPOff + r * 128;
+        unsigned char* prow = pbuf + r * 128;
 #pragma unroll
         for (int c = 0; c < 8; ++c)
           *reinterpret_cast<uint4*>(prow + ((c ^ (r & 7)) << 4)) =
@@ -495,33 +558,42 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       tc_fence_before();
       mbar_arrive(hdr + kPFull + 8 * (j & 1));
     }
-    if (failed) {
-      if (lane == 0) raise_flag(a.status, PA_FLAG_TIMEOUT);
-    } else if (__all_sync(kFullMask, mbar_wait_bounded(hdr + kDone, 0))) {
+    // A warp that gave up still takes part in the barriers below (its rows' values are undefined).
+    const bool ok = !failed && __all_sync(kFullMask, mbar_wait_bounded(hdr + kDone, 0));
+    if (!ok && lane == 0) raise_flag(a.status, PA_FLAG_TIMEOUT);
+    {
       tc_fence_after();
       // a row whose every key was skipped has l = 0: zeros
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      const bool store = i < rows_q;
-      uint4* dst = reinterpret_cast<uint4*>(
-          a.out + (static_cast<size_t>(q0 + i0 + (store ? i : 0)) * a.num_q_heads + g * G + h) * kHeadDim);
 #pragma unroll 1
-      for (int q4 = 0; q4 < 4; ++q4) {
-        uint32_t ov[32];
-        tmem_ld32(trow + kBpOCol + 32 * q4, ov);
-        tmem_wait_ld();
-        if (store) {
+      for (int part = 0; part < 2; ++part) {
+        if (part) named_barrier(1, 128);            // the first half has been stored
+#pragma unroll
+        for (int q2 = 0; q2 < 2; ++q2) {
+          uint32_t ov[32];
+          if (ok) {
+            tmem_ld32(trow + kBpOCol + 64 * part + 32 * q2, ov);
+            tmem_wait_ld();
+          }
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             uint32_t o[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u)
               o[u] = pack_bf16x2(__uint_as_float(ov[8 * k + 2 * u]) * inv, __uint_as_float(ov[8 * k + 2 * u + 1]) * inv);
-            dst[4 * q4 + k] = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(pbuf + r * 128 + (((4 * q2 + k) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
           }
         }
+        named_barrier(1, 128);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int x = hr + 16 * k;
+          const long long at = global_row(x);
+          if (at >= 0)
+            reinterpret_cast<uint4*>(a.out + at)[8 * part + hc] =
+                *reinterpret_cast<const uint4*>(pbuf + x * 128 + ((hc ^ (x & 7)) << 4));
+        }
       }
-    } else if (lane == 0) {
-      raise_flag(a.status, PA_FLAG_TIMEOUT);
     }
   }
   tc_fence_before();

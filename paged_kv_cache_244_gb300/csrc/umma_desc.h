@@ -62,6 +62,12 @@ PA_HOST_DEVICE inline uint32_t umma_idesc_f16(int M, int N, bool a_mn_major, boo
          ((static_cast<uint32_t>(N) >> 3) << 17) | ((static_cast<uint32_t>(M) >> 4) << 24);
 }
 
+// Instruction descriptor of kind::f8f6f4: as kind::f16 with the A and B formats 0 E4M3, 1 E5M2.
+// E4M3 x E4M3 -> f32, both K-major.
+PA_HOST_DEVICE inline uint32_t umma_idesc_e4m3(int M, int N) {
+  return (1u << 4) | ((static_cast<uint32_t>(N) >> 3) << 17) | ((static_cast<uint32_t>(M) >> 4) << 24);
+}
+
 // bf16 x bf16 -> f32, M x N tile; *_mn_major: the operand is stored with M (or N) contiguous.
 PA_HOST_DEVICE inline uint32_t umma_idesc_bf16(int M, int N, bool a_mn_major, bool b_mn_major) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn_major ? 1u : 0u) << 15) |

@@ -71,6 +71,24 @@ def test_a_short_pool_refuses_in_order():
     assert got["q_start"].tolist() == [0, 17, 18, 21] and got["context_lens"].tolist() == [17, 0, 8]
 
 
+def test_instruction_descriptors_of_the_8_bit_and_f16_products(tmp_path):
+    """The PTX ISA's bit positions written out: accumulator f32 at 4, A format at 7, B format at 10,
+    majors at 15 and 16, N / 8 at 17, M / 16 at 24; E4M3 is 0 in kind::f8f6f4, f16 0 in kind::f16."""
+    import shutil
+    import subprocess
+    from pathlib import Path
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        pytest.skip("no host C++ compiler")
+    src, exe = tmp_path / "d.cpp", tmp_path / "d"
+    src.write_text('#include <cstdio>\n#include "umma_desc.h"\nint main() { printf("%u %u %u", pa::umma_idesc_e4m3(128, 64), '
+                   'pa::umma_idesc_f16(128, 128, false, true), pa::umma_idesc_f16(64, 16, true, false)); }\n')
+    inc = Path(__file__).resolve().parents[1] / "paged_kv_cache_244_gb300" / "csrc"
+    subprocess.run([cxx, "-std=c++17", f"-I{inc}", str(src), "-o", str(exe)], check=True)
+    got = [int(x) for x in subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.split()]
+    assert got == [1 << 4 | 8 << 17 | 8 << 24, 1 << 4 | 1 << 16 | 16 << 17 | 8 << 24, 1 << 4 | 1 << 15 | 2 << 17 | 4 << 24]
+
+
 # ---- refusals ---------------------------------------------------------------------------
 
 A = 0x10000          # an aligned address that is never read: every call below is refused first
