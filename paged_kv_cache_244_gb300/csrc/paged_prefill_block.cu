@@ -31,9 +31,9 @@
 //       block, 128-byte swizzle).  V rows past the context, and V of absent blocks, are written
 //       as zeros.
 // Tensor memory per CTA (256 columns): q hi 0-31, q lo 32-63 (four codes a column), S 64-127, O
-// 128-255.  Shared memory per CTA: three 8 KiB K stages, two 8 KiB stages of V codes, three 16 KiB
-// stages of f16 V, the 16 KiB P buffer (which also carries Q in and O out, so that both move in
-// whole lines), barriers: 105 KiB.  Every wait is bounded.
+// 128-255.  Shared memory per CTA: three 8 KiB K stages, two 8 KiB stages of V codes, two 16 KiB
+// stages of f16 V, two 16 KiB P buffers (the first also carries Q in and O out, so that both move
+// in whole lines), barriers, the scales of 8 stages: 106 KiB.  Every wait is bounded.
 //
 // What bounds it: the shared-memory data path.  A first form that widened K too and gave each
 // thread its own row of q and out to load and store kept that path 88% busy (ncu, 4 x 2048
@@ -53,7 +53,7 @@ namespace {
 constexpr int kBpRows = 128;
 constexpr int kBpKB = 4;                             // key blocks per stage
 constexpr int kBpKeys = kBpKB * kBlockSize;          // 64
-constexpr int kBpKRing = 3, kBpCRing = 2, kBpVRing = 3;   // stages of K codes, V codes, f16 V
+constexpr int kBpKRing = 3, kBpCRing = 2, kBpVRing = 2;   // stages of K codes, V codes, f16 V
 constexpr int kBpTile = kBlockSize * 128;            // a block's codes, or 16 rows x 64 f16: 2 KiB
 constexpr int kBpCodes = kBpKB * kBpTile;            // codes of K (or V) of a stage: 8 KiB
 constexpr int kBpVStage = 2 * kBpCodes;              // f16 V of a stage: 16 KiB
@@ -61,10 +61,12 @@ constexpr int kBpCOff = kBpKRing * kBpCodes;
 constexpr int kBpVOff = kBpCOff + kBpCRing * kBpCodes;
 constexpr int kBpPOff = kBpVOff + kBpVRing * kBpVStage;
 constexpr int kBpPBytes = kBpRows * kBpKeys * 2;     // 16 KiB
-constexpr int kBpHdrOff = kBpPOff + kBpPBytes;
+constexpr int kBpHdrOff = kBpPOff + 2 * kBpPBytes;   // P_j in buffer j & 1
 constexpr int kBpHeader = 256;
 constexpr int kBpFoldOff = kBpHdrOff + kBpHeader;    // a float per row
-constexpr int kBpSmem = kBpFoldOff + kBpRows * 4 + 1024;  // + alignment of the first stage
+constexpr int kBpScaleOff = kBpFoldOff + kBpRows * 4;   // a float4 per block of the stage, stage j in slot j % 8
+constexpr int kBpScaleSlots = 8;
+constexpr int kBpSmem = kBpScaleOff + kBpScaleSlots * kBpKB * 16 + 1024;  // + alignment of the first stage
 static_assert(2 * (kBpSmem + 1024) <= 228 * 1024, "two CTAs per SM");
 constexpr int kBpThreads = 384;
 // registers per thread at launch, and the split (their sums per warpgroup are equal)
@@ -77,11 +79,11 @@ constexpr int kKFull = 0;          // [3] K TMA -> MMA (S)
 constexpr int kKFree = 24;         // [3] MMA (S done) -> K TMA
 constexpr int kCFull = 48;         // [2] V TMA -> converters
 constexpr int kCFree = 64;         // [2] converters (a warp each: 4) -> V TMA
-constexpr int kVFull = 80;         // [3] converters (4) -> MMA (P V)
-constexpr int kVFree = 104;        // [3] MMA (P V done) -> converters, softmax (P buffer, O)
-constexpr int kSFull = 128;        // MMA (S done) -> softmax
-constexpr int kSFree = 136;        // softmax (128) -> MMA
-constexpr int kPFull = 144;        // [2] softmax (128) -> MMA
+constexpr int kVFull = 80;         // [2] converters (4) -> MMA (P V)
+constexpr int kVFree = 104;        // [2] MMA (P V done) -> converters, softmax (O, when it rescales)
+constexpr int kSFull = 128;        // MMA (S_j done, and P_{j-2} V_{j-2}) -> softmax
+constexpr int kSFree = 136;        // softmax (a warp each: 4) -> MMA
+constexpr int kPFull = 144;        // [2] softmax (4) -> MMA
 constexpr int kDone = 160;         // MMA: its last MMAs finished
 constexpr int kQReady = 168;       // softmax (128) -> MMA
 constexpr int kTmemAt = 176;
@@ -159,16 +161,16 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     for (int i = 0; i < 3; ++i) {
       mbar_init(hdr + kKFull + 8 * i, 1);
       mbar_init(hdr + kKFree + 8 * i, 1);
-      mbar_init(hdr + kVFull + 8 * i, 4);
-      mbar_init(hdr + kVFree + 8 * i, 1);
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(hdr + kVFull + 8 * i, 4);
+      mbar_init(hdr + kVFree + 8 * i, 1);
       mbar_init(hdr + kCFull + 8 * i, 1);
       mbar_init(hdr + kCFree + 8 * i, 4);
-      mbar_init(hdr + kPFull + 8 * i, 128);
+      mbar_init(hdr + kPFull + 8 * i, 4);
     }
     mbar_init(hdr + kSFull, 1);
-    mbar_init(hdr + kSFree, 128);
+    mbar_init(hdr + kSFree, 4);
     mbar_init(hdr + kDone, 1);
     mbar_init(hdr + kQReady, 128);
     fence_mbar_init();
@@ -253,10 +255,26 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       const uint32_t slots = stages + (is_k ? 0 : kBpCOff);
       int st = 0;
       uint32_t ph = 1;                              // parity of the slot's previous release
+      // K: the scales of the lane's block of the window and the next, as the softmax wants them --
+      // factor on q . Kcode, lift of the exponent, weight in L, whether the block is there.  Stage
+      // j's lanes write theirs to slot j % 8 before the stage's barrier: the softmax reads them
+      // after S_j, and the slot is written again for stage j + 8, after S_{j+5}, which the softmax
+      // let through when it had done with stage j.
+      auto load_scales = [&](int id) {
+        if (!is_k) return make_float4(0.f, 0.f, 0.f, 0.f);
+        const bool there = in_pool(id);
+        const float2 kv = there ? a.kv_scale[static_cast<size_t>(id) * Hkv + g] : make_float2(1.f, 1.f);
+        return make_float4(a.scale_log2 * kv.x, log2_of(kv.y), __frcp_rn(kv.y), there ? 1.f : 0.f);
+      };
+      float4 scales = load_scales(ids), scales_next = load_scales(ids_next);
+      float4* const scale_slots = reinterpret_cast<float4*>(base + kBpScaleOff);
       int issued = 0;
       bool failed = false;
       for (int j = 0; j < nst; ++j) {
-        next_window(j);
+        if (next_window(j)) {
+          scales = scales_next;
+          scales_next = load_scales(ids_next);
+        }
         const int mask = stage_mask(j);
         const int blk = __shfl_sync(kFullMask, ids, ((kBpKB * j) & 31) + (lane & (kBpKB - 1)));
         bool ok = true;
@@ -266,6 +284,11 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
           break;
         }
         const uint32_t bar = full + 8 * st;
+        if (is_k) {
+          const int b = lane - ((kBpKB * j) & 31);
+          if (b >= 0 && b < kBpKB) scale_slots[(j % kBpScaleSlots) * kBpKB + b] = scales;
+          __syncwarp();
+        }
         if (lane == 0) {
           if (mask) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(__popc(mask)) * kBpTile);
           else mbar_arrive(bar);
@@ -336,7 +359,7 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         if (elect_one()) {
 #pragma unroll
           for (int i = 0; i < kBpKB; ++i)
-            umma_bf16(tmem + kBpOCol, p_desc + static_cast<uint64_t>((32 * i) >> 4),
+            umma_bf16(tmem + kBpOCol, p_desc + static_cast<uint64_t>(((j & 1) * kBpPBytes + 32 * i) >> 4),
                       vd + static_cast<uint64_t>((i * 2 * kBpTile) >> 4), id_pv, j > 0 || i > 0);
           umma_commit(hdr + kVFree + 8 * st);
         }
@@ -439,35 +462,11 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     }
     const float row_fold = folds[r];                // q = row_fold (hi + lo)
     named_barrier(1, 128);                          // the P buffer is free for P
-    // Scales of the lane's block of the window: factor on q . Kcode, lift of the exponent, weight in L
-    float fold = 0.f, lift = 0.f, weigh = 0.f, fold_next = 0.f, lift_next = 0.f, weigh_next = 0.f;
-    auto load_scales = [&](int id, float& f, float& e, float& w) {
-      const float2 kv = in_pool(id) ? a.kv_scale[static_cast<size_t>(id) * Hkv + g] : make_float2(1.f, 1.f);
-      f = a.scale_log2 * kv.x;
-      e = log2_of(kv.y);
-      w = __frcp_rn(kv.y);
-    };
-    load_scales(ids, fold, lift, weigh);
-    load_scales(ids_next, fold_next, lift_next, weigh_next);
     float m = -INFINITY, l = 0.f;
     bool failed = false;
     const uint32_t sbuf = trow + kBpSCol;
+    const float4* const scale_slots = reinterpret_cast<const float4*>(base + kBpScaleOff);
     for (int j = 0; j < nst; ++j) {
-      if (next_window(j)) {
-        fold = fold_next;
-        lift = lift_next;
-        weigh = weigh_next;
-        load_scales(ids_next, fold_next, lift_next, weigh_next);
-      }
-      const int mask = stage_mask(j);
-      float f[kBpKB], e[kBpKB], w[kBpKB];
-#pragma unroll
-      for (int b = 0; b < kBpKB; ++b) {
-        const int src = ((kBpKB * j) & 31) + b;
-        f[b] = __shfl_sync(kFullMask, fold, src) * row_fold;
-        e[b] = __shfl_sync(kFullMask, lift, src);
-        w[b] = __shfl_sync(kFullMask, weigh, src);
-      }
       if (!__all_sync(kFullMask, mbar_wait_bounded(hdr + kSFull, j & 1))) {
         failed = true;
         break;
@@ -475,24 +474,37 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       tc_fence_after();
       float sc[kBpKeys];
       {
-        uint32_t sv[32];
-        tmem_ld32(sbuf, sv);
+        uint32_t s0[32], s1[32];
+        tmem_ld32(sbuf, s0);
+        tmem_ld32(sbuf + 32, s1);
         tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 32; ++c) sc[c] = __uint_as_float(sv[c]);
-        tmem_ld32(sbuf + 32, sv);
-        tmem_wait_ld();
-#pragma unroll
-        for (int c = 0; c < 32; ++c) sc[32 + c] = __uint_as_float(sv[c]);
+        for (int c = 0; c < 32; ++c) {
+          sc[c] = __uint_as_float(s0[c]);
+          sc[32 + c] = __uint_as_float(s1[c]);
+        }
       }
       tc_fence_before();
-      mbar_arrive(hdr + kSFree);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(hdr + kSFree);
+      float f[kBpKB], e[kBpKB], w[kBpKB];
+      bool all_there = true;
+      bool there[kBpKB];
+#pragma unroll
+      for (int b = 0; b < kBpKB; ++b) {
+        const float4 v = scale_slots[(j % kBpScaleSlots) * kBpKB + b];
+        f[b] = v.x * row_fold;
+        e[b] = v.y;
+        w[b] = v.z;
+        there[b] = v.w != 0.f;
+        all_there = all_there && there[b];
+      }
       // causal mask and absent blocks -> -inf, only on a stage that needs it
-      if (mask != (1 << kBpKB) - 1 || kBpKeys * (j + 1) - 1 > pos0) {
+      if (!all_there || kBpKeys * (j + 1) - 1 > pos0) {
         const int lim = p_r - kBpKeys * j;
 #pragma unroll
         for (int c = 0; c < kBpKeys; ++c)
-          if (!((mask >> (c / kBlockSize)) & 1) || c > lim) sc[c] = -INFINITY;
+          if (!there[c / kBlockSize] || c > lim) sc[c] = -INFINITY;
       }
       float mrow = -INFINITY;
 #pragma unroll
@@ -506,36 +518,41 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       const float sh = mn == -INFINITY ? 0.f : mn;
       const float alpha = (mn == m || m == -INFINITY) ? 1.f : ex2_ftz(m - sh);
       m = mn;
-      uint32_t pw[kBpKeys / 2];
+      // P_j goes to buffer j & 1, which P_{j-2} V_{j-2} has left (S_j's completion covers it), block
+      // by block as it is made: 16 keys = chunks 2b and 2b + 1 of the row, chunk c at c ^ (r % 8).
+      unsigned char* const prow = pbuf + (j & 1) * kBpPBytes + r * 128;
       l *= alpha;
 #pragma unroll
       for (int b = 0; b < kBpKB; ++b) {
         const float es = e[b] - sh;
         const uint64_t f2 = pack_f32x2(f[b], f[b]), e2 = pack_f32x2(es, es);
         uint64_t sum[2] = {0ull, 0ull};
+        uint32_t pw[kBlockSize / 2];
 #pragma unroll
         for (int k = 0; k < kBlockSize / 2; ++k) {
           const int c = kBlockSize * b + 2 * k;
           float x0, x1;
           unpack_f32x2(fma_f32x2(pack_f32x2(sc[c], sc[c + 1]), f2, e2), x0, x1);
           const float p0 = ex2_ftz(x0), p1 = ex2_ftz(x1);
-          pw[c / 2] = pack_f16x2(p0, p1);
+          pw[k] = pack_f16x2(p0, p1);
           sum[k & 1] = add_f32x2(sum[k & 1], pack_f32x2(p0, p1));
         }
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          *reinterpret_cast<uint4*>(prow + (((2 * b + c) ^ (r & 7)) << 4)) =
+              make_uint4(pw[4 * c], pw[4 * c + 1], pw[4 * c + 2], pw[4 * c + 3]);
         float s0, s1;
         unpack_f32x2(add_f32x2(sum[0], sum[1]), s0, s1);
         l = fmaf(s0 + s1, w[b], l);
       }
-      // P V of stage j - 1 must be done before P_j overwrites its buffer and before O is rescaled
-      if (j > 0) {
+      // O *= alpha where a row's shift moved (warp-collective), once P V of stage j - 1 is done
+      if (j > 0 && __any_sync(kFullMask, alpha != 1.f)) {
         const int pj = j - 1;
         if (!__all_sync(kFullMask, mbar_wait_bounded(hdr + kVFree + 8 * (pj % kBpVRing), (pj / kBpVRing) & 1))) {
           failed = true;
           break;
         }
         tc_fence_after();
-      }
-      if (j > 0 && __any_sync(kFullMask, alpha != 1.f)) {
 #pragma unroll 1
         for (int q4 = 0; q4 < 4; ++q4) {
           uint32_t ov[32];
@@ -547,16 +564,10 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         }
         tmem_wait_st();
       }
-      {
-        unsigned char* prow = pbuf + r * 128;
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          *reinterpret_cast<uint4*>(prow + ((c ^ (r & 7)) << 4)) =
-              make_uint4(pw[4 * c], pw[4 * c + 1], pw[4 * c + 2], pw[4 * c + 3]);
-      }
       fence_proxy_async_smem();
       tc_fence_before();
-      mbar_arrive(hdr + kPFull + 8 * (j & 1));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(hdr + kPFull + 8 * (j & 1));
     }
     // A warp that gave up still takes part in the barriers below (its rows' values are undefined).
     const bool ok = !failed && __all_sync(kFullMask, mbar_wait_bounded(hdr + kDone, 0));
