@@ -30,10 +30,13 @@
 //       ring, 16 codes a load, in the MN-major layout that the MMA reads (two 64-dim halves a
 //       block, 128-byte swizzle).  V rows past the context, and V of absent blocks, are written
 //       as zeros.
-// Tensor memory per CTA (256 columns): q hi 0-31, q lo 32-63 (four codes a column), S 64-127, O
-// 128-255.  Shared memory per CTA: three 8 KiB K stages, two 8 KiB stages of V codes, two 16 KiB
-// stages of f16 V, two 16 KiB P buffers (the first also carries Q in and O out, so that both move
-// in whole lines), barriers, the scales of 8 stages: 106 KiB.  Every wait is bounded.
+// Tensor memory per CTA (256 columns): S_j in columns 64 (j & 1) .. + 63, O in 128-255; a row's
+// P_j (64 f16, 32 columns) is written by its thread over the S_j it has read, and is the A operand
+// of P V from there.  So S_{j+1} is computed while the softmax works on S_j, and S_{j+2}, which
+// takes the columns of P_j, is issued behind P_j V_j.  Shared memory per CTA: q hi and lo (16 KiB
+// each, the A operand of S; out leaves through the first), three 8 KiB K stages, two 8 KiB stages of
+// V codes, two 16 KiB stages of f16 V, barriers, the scales of 8 stages: 106 KiB.  Every wait is
+// bounded.
 //
 // What bounds it: the shared-memory data path.  A first form that widened K too and gave each
 // thread its own row of q and out to load and store kept that path 88% busy (ncu, 4 x 2048
@@ -59,9 +62,9 @@ constexpr int kBpCodes = kBpKB * kBpTile;            // codes of K (or V) of a s
 constexpr int kBpVStage = 2 * kBpCodes;              // f16 V of a stage: 16 KiB
 constexpr int kBpCOff = kBpKRing * kBpCodes;
 constexpr int kBpVOff = kBpCOff + kBpCRing * kBpCodes;
-constexpr int kBpPOff = kBpVOff + kBpVRing * kBpVStage;
-constexpr int kBpPBytes = kBpRows * kBpKeys * 2;     // 16 KiB
-constexpr int kBpHdrOff = kBpPOff + 2 * kBpPBytes;   // P_j in buffer j & 1
+constexpr int kBpQOff = kBpVOff + kBpVRing * kBpVStage;
+constexpr int kBpQBytes = kBpRows * kHeadDim;        // hi (or lo) codes of the rows: 16 KiB
+constexpr int kBpHdrOff = kBpQOff + 2 * kBpQBytes;
 constexpr int kBpHeader = 256;
 constexpr int kBpFoldOff = kBpHdrOff + kBpHeader;    // a float per row
 constexpr int kBpScaleOff = kBpFoldOff + kBpRows * 4;   // a float4 per block of the stage, stage j in slot j % 8
@@ -72,7 +75,7 @@ constexpr int kBpThreads = 384;
 // registers per thread at launch, and the split (their sums per warpgroup are equal)
 constexpr int kBpRegsSoftmax = 136, kBpRegsIssue = 48, kBpRegsConvert = 56;
 static_assert(kBpRegsSoftmax + kBpRegsIssue + kBpRegsConvert <= 3 * 80, "of the 80 a thread launched with");
-constexpr uint32_t kBpTmemCols = 256, kBpQCol = 0, kBpSCol = 64, kBpOCol = 128;
+constexpr uint32_t kBpTmemCols = 256, kBpSCols = 64, kBpOCol = 128;   // S (and P) at 0 and 64
 
 // header (byte offsets)
 constexpr int kKFull = 0;          // [3] K TMA -> MMA (S)
@@ -81,12 +84,11 @@ constexpr int kCFull = 48;         // [2] V TMA -> converters
 constexpr int kCFree = 64;         // [2] converters (a warp each: 4) -> V TMA
 constexpr int kVFull = 80;         // [2] converters (4) -> MMA (P V)
 constexpr int kVFree = 104;        // [2] MMA (P V done) -> converters, softmax (O, when it rescales)
-constexpr int kSFull = 128;        // MMA (S_j done, and P_{j-2} V_{j-2}) -> softmax
-constexpr int kSFree = 136;        // softmax (a warp each: 4) -> MMA
-constexpr int kPFull = 144;        // [2] softmax (4) -> MMA
-constexpr int kDone = 160;         // MMA: its last MMAs finished
-constexpr int kQReady = 168;       // softmax (128) -> MMA
-constexpr int kTmemAt = 176;
+constexpr int kSFull = 120;        // [2] MMA (S done) -> softmax
+constexpr int kPFull = 136;        // [2] softmax (a warp each: 4) -> MMA
+constexpr int kDone = 152;         // MMA: its last MMAs finished
+constexpr int kQReady = 160;       // softmax (128) -> MMA
+constexpr int kTmemAt = 168;
 static_assert(kTmemAt + 4 <= kBpHeader, "header");
 
 // Four bf16 values times `raise` (a power of two) as the sum of two E4M3 values each: the codes of
@@ -168,9 +170,8 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       mbar_init(hdr + kCFull + 8 * i, 1);
       mbar_init(hdr + kCFree + 8 * i, 4);
       mbar_init(hdr + kPFull + 8 * i, 4);
+      mbar_init(hdr + kSFull + 8 * i, 1);
     }
-    mbar_init(hdr + kSFull, 1);
-    mbar_init(hdr + kSFree, 4);
     mbar_init(hdr + kDone, 1);
     mbar_init(hdr + kQReady, 128);
     fence_mbar_init();
@@ -258,8 +259,8 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       // K: the scales of the lane's block of the window and the next, as the softmax wants them --
       // factor on q . Kcode, lift of the exponent, weight in L, whether the block is there.  Stage
       // j's lanes write theirs to slot j % 8 before the stage's barrier: the softmax reads them
-      // after S_j, and the slot is written again for stage j + 8, after S_{j+5}, which the softmax
-      // let through when it had done with stage j.
+      // after S_j, and the slot is written again for stage j + 8, after S_{j+5}, which was issued
+      // behind P_{j+3} V_{j+3}, so when the softmax had done with stage j.
       auto load_scales = [&](int id) {
         if (!is_k) return make_float4(0.f, 0.f, 0.f, 0.f);
         const bool there = in_pool(id);
@@ -316,24 +317,23 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       const uint32_t id_s = umma_idesc_e4m3(kBpRows, kBpKeys);
       const uint32_t id_pv = umma_idesc_f16(kBpRows, kHeadDim, false, true);
       const uint64_t k_desc0 = umma_smem_desc(stages, 16, 1024);
-      const uint64_t p_desc = umma_smem_desc(stages + kBpPOff, 16, 1024);
+      const uint64_t q_desc = umma_smem_desc(stages + kBpQOff, 16, 1024);
       const uint64_t v_desc0 = umma_smem_desc(stages + kBpVOff, kBpTile, 1024);
       auto wait_all = [&](uint32_t bar, uint32_t parity) {
         return __all_sync(kFullMask, mbar_wait_bounded(bar, parity));
       };
-      // S_j = Q K_j^T once K_j has landed and the softmax has loaded S_{j-1}
+      // S_j = Q K_j^T once K_j has landed (its columns hold P_{j-2}, read by P V issued before)
       auto issue_s = [&](int j) {
         const int st = j % kBpKRing;
         if (!wait_all(hdr + kKFull + 8 * st, (j / kBpKRing) & 1)) return false;
-        if (j > 0 && !wait_all(hdr + kSFree, (j - 1) & 1)) return false;
         tc_fence_after();
         const uint64_t kd = k_desc0 + static_cast<uint64_t>((st * kBpCodes) >> 4);
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)            // q hi, then q lo, over the four 32-dim steps of K
-            umma_e4m3_tmem_a(tmem + kBpSCol, tmem + kBpQCol + 8 * kk, kd + static_cast<uint64_t>(((kk & 3) * 32) >> 4),
-                             id_s, kk > 0);
-          umma_commit(hdr + kSFull);
+            umma_e4m3(tmem + kBpSCols * (j & 1), q_desc + static_cast<uint64_t>(((kk >> 2) * kBpQBytes + (kk & 3) * 32) >> 4),
+                      kd + static_cast<uint64_t>(((kk & 3) * 32) >> 4), id_s, kk > 0);
+          umma_commit(hdr + kSFull + 8 * (j & 1));
           umma_commit(hdr + kKFree + 8 * st);
         }
         __syncwarp();
@@ -342,13 +342,9 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       bool failed = !wait_all(hdr + kQReady, 0);
       if (!failed) {
         tc_fence_after();
-        failed = !issue_s(0);
+        failed = !issue_s(0) || (nst > 1 && !issue_s(1));
       }
       for (int j = 0; j < nst && !failed; ++j) {
-        if (j + 1 < nst && !issue_s(j + 1)) {
-          failed = true;
-          break;
-        }
         const int st = j % kBpVRing;
         if (!wait_all(hdr + kPFull + 8 * (j & 1), (j >> 1) & 1) || !wait_all(hdr + kVFull + 8 * st, (j / kBpVRing) & 1)) {
           failed = true;
@@ -359,11 +355,11 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         if (elect_one()) {
 #pragma unroll
           for (int i = 0; i < kBpKB; ++i)
-            umma_bf16(tmem + kBpOCol, p_desc + static_cast<uint64_t>(((j & 1) * kBpPBytes + 32 * i) >> 4),
-                      vd + static_cast<uint64_t>((i * 2 * kBpTile) >> 4), id_pv, j > 0 || i > 0);
+            umma_bf16_tmem_a(tmem + kBpOCol, tmem + kBpSCols * (j & 1) + 8 * i, vd + static_cast<uint64_t>((i * 2 * kBpTile) >> 4), id_pv, j > 0 || i > 0);
           umma_commit(hdr + kVFree + 8 * st);
         }
         __syncwarp();
+        if (j + 2 < nst && !issue_s(j + 2)) failed = true;
       }
       if (lane == 0) {
         if (failed) raise_flag(a.status, PA_FLAG_TIMEOUT);
@@ -373,14 +369,14 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       __syncwarp();
     }
   } else {
-    // ---- Q into TMEM, then the softmax: thread = row r of the tile ------------------------------
+    // ---- q into shared memory, then the softmax: thread = row r of the tile ---------------------
     regs_inc<kBpRegsSoftmax>();
     const int r = threadIdx.x;
     const int p_r = pos0 + r / G;
     const uint32_t trow = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-    unsigned char* const pbuf = base + kBpPOff;
-    // Q (and later out) passes through the P buffer a 64-dim half at a time, 8 lanes a row, so that
-    // global memory sees whole 128-byte lines; 16-byte chunk c of row x sits at c ^ (x % 8).
+    // q comes in and out leaves 8 lanes a row, so that global memory sees whole 128-byte lines; a
+    // 16-byte chunk c of row x of a 128-byte-wide buffer sits at c ^ (x % 8).
+    unsigned char* const qbuf = base + kBpQOff;
     const int hr = r >> 3, hc = r & 7;              // rows hr + 16 k, chunk hc of the half
     auto global_row = [&](int x) {                  // matrix row x of q and out, -1 past the queries
       const int xi = x / G;
@@ -391,9 +387,7 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     {
       // Rows hr + 16 k, their dims 8 hc .. + 7 and 64 + 8 hc .. + 7 in this thread.  The row's
       // largest magnitude (over its 8 lanes) gives the power of two that brings it to [128, 256);
-      // an infinity or a NaN makes the row's scores NaN.  hi codes go through the P buffer now, lo
-      // codes after them.
-      uint2 lo[8][2];
+      // an infinity or a NaN makes the row's scores NaN.
 #pragma unroll
       for (int k4 = 0; k4 < 8; k4 += 4) {
         uint4 v[4][2];
@@ -425,53 +419,30 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                                       : __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 #pragma unroll
           for (int p = 0; p < 2; ++p) {
-            uint2 hi;
-            split_e4m3(v[k][p].x, v[k][p].y, raise, hi.x, lo[k4 + k][p].x);
-            split_e4m3(v[k][p].z, v[k][p].w, raise, hi.y, lo[k4 + k][p].y);
-            *reinterpret_cast<uint2*>(pbuf + x * 128 + (((4 * p + (hc >> 1)) ^ (x & 7)) << 4) + 8 * (hc & 1)) = hi;
+            uint2 hi, lo;
+            split_e4m3(v[k][p].x, v[k][p].y, raise, hi.x, lo.x);
+            split_e4m3(v[k][p].z, v[k][p].w, raise, hi.y, lo.y);
+            unsigned char* at = qbuf + x * 128 + (((4 * p + (hc >> 1)) ^ (x & 7)) << 4) + 8 * (hc & 1);
+            *reinterpret_cast<uint2*>(at) = hi;
+            *reinterpret_cast<uint2*>(at + kBpQBytes) = lo;
           }
         }
       }
-#pragma unroll
-      for (int part = 0; part < 2; ++part) {        // hi, then lo
-        if (part) {
-          named_barrier(1, 128);                    // hi has been read
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int x = hr + 16 * k;
-#pragma unroll
-            for (int p = 0; p < 2; ++p)
-              *reinterpret_cast<uint2*>(pbuf + x * 128 + (((4 * p + (hc >> 1)) ^ (x & 7)) << 4) + 8 * (hc & 1)) = lo[k][p];
-          }
-        }
-        named_barrier(1, 128);
-        uint32_t codes[32];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const uint4 w = *reinterpret_cast<const uint4*>(pbuf + r * 128 + ((c ^ (r & 7)) << 4));
-          codes[4 * c] = w.x;
-          codes[4 * c + 1] = w.y;
-          codes[4 * c + 2] = w.z;
-          codes[4 * c + 3] = w.w;
-        }
-        tmem_st32(trow + kBpQCol + 32 * part, codes);
-      }
-      tmem_wait_st();
-      tc_fence_before();
+      fence_proxy_async_smem();                     // before the tensor core reads them
       mbar_arrive(hdr + kQReady);
+      named_barrier(1, 128);                        // the rows' factors are in place
     }
     const float row_fold = folds[r];                // q = row_fold (hi + lo)
-    named_barrier(1, 128);                          // the P buffer is free for P
     float m = -INFINITY, l = 0.f;
     bool failed = false;
-    const uint32_t sbuf = trow + kBpSCol;
     const float4* const scale_slots = reinterpret_cast<const float4*>(base + kBpScaleOff);
     for (int j = 0; j < nst; ++j) {
-      if (!__all_sync(kFullMask, mbar_wait_bounded(hdr + kSFull, j & 1))) {
+      if (!__all_sync(kFullMask, mbar_wait_bounded(hdr + kSFull + 8 * (j & 1), (j >> 1) & 1))) {
         failed = true;
         break;
       }
       tc_fence_after();
+      const uint32_t sbuf = trow + kBpSCols * (j & 1);
       float sc[kBpKeys];
       {
         uint32_t s0[32], s1[32];
@@ -484,9 +455,6 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
           sc[32 + c] = __uint_as_float(s1[c]);
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(hdr + kSFree);
       float f[kBpKB], e[kBpKB], w[kBpKB];
       bool all_there = true;
       bool there[kBpKB];
@@ -518,33 +486,27 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       const float sh = mn == -INFINITY ? 0.f : mn;
       const float alpha = (mn == m || m == -INFINITY) ? 1.f : ex2_ftz(m - sh);
       m = mn;
-      // P_j goes to buffer j & 1, which P_{j-2} V_{j-2} has left (S_j's completion covers it), block
-      // by block as it is made: 16 keys = chunks 2b and 2b + 1 of the row, chunk c at c ^ (r % 8).
-      unsigned char* const prow = pbuf + (j & 1) * kBpPBytes + r * 128;
+      uint32_t pw[kBpKeys / 2];
       l *= alpha;
 #pragma unroll
       for (int b = 0; b < kBpKB; ++b) {
         const float es = e[b] - sh;
         const uint64_t f2 = pack_f32x2(f[b], f[b]), e2 = pack_f32x2(es, es);
         uint64_t sum[2] = {0ull, 0ull};
-        uint32_t pw[kBlockSize / 2];
 #pragma unroll
         for (int k = 0; k < kBlockSize / 2; ++k) {
           const int c = kBlockSize * b + 2 * k;
           float x0, x1;
           unpack_f32x2(fma_f32x2(pack_f32x2(sc[c], sc[c + 1]), f2, e2), x0, x1);
           const float p0 = ex2_ftz(x0), p1 = ex2_ftz(x1);
-          pw[k] = pack_f16x2(p0, p1);
+          pw[c / 2] = pack_f16x2(p0, p1);
           sum[k & 1] = add_f32x2(sum[k & 1], pack_f32x2(p0, p1));
         }
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-          *reinterpret_cast<uint4*>(prow + (((2 * b + c) ^ (r & 7)) << 4)) =
-              make_uint4(pw[4 * c], pw[4 * c + 1], pw[4 * c + 2], pw[4 * c + 3]);
         float s0, s1;
         unpack_f32x2(add_f32x2(sum[0], sum[1]), s0, s1);
         l = fmaf(s0 + s1, w[b], l);
       }
+      tmem_st32(sbuf, pw);                          // P_j over S_j
       // O *= alpha where a row's shift moved (warp-collective), once P V of stage j - 1 is done
       if (j > 0 && __any_sync(kFullMask, alpha != 1.f)) {
         const int pj = j - 1;
@@ -562,9 +524,8 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
           for (int c = 0; c < 32; ++c) ov[c] = __float_as_uint(__uint_as_float(ov[c]) * alpha);
           tmem_st32(trow + kBpOCol + 32 * q4, ov);
         }
-        tmem_wait_st();
       }
-      fence_proxy_async_smem();
+      tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(hdr + kPFull + 8 * (j & 1));
@@ -592,7 +553,7 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
 #pragma unroll
             for (int u = 0; u < 4; ++u)
               o[u] = pack_bf16x2(__uint_as_float(ov[8 * k + 2 * u]) * inv, __uint_as_float(ov[8 * k + 2 * u + 1]) * inv);
-            *reinterpret_cast<uint4*>(pbuf + r * 128 + (((4 * q2 + k) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(qbuf + r * 128 + (((4 * q2 + k) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
           }
         }
         named_barrier(1, 128);
@@ -602,7 +563,7 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
           const long long at = global_row(x);
           if (at >= 0)
             reinterpret_cast<uint4*>(a.out + at)[8 * part + hc] =
-                *reinterpret_cast<const uint4*>(pbuf + x * 128 + ((hc ^ (x & 7)) << 4));
+                *reinterpret_cast<const uint4*>(qbuf + x * 128 + ((hc ^ (x & 7)) << 4));
         }
       }
     }
