@@ -88,6 +88,25 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
   }
 }
 
+// The same wait, parked: each try may suspend the thread for up to 10 us (it is woken when the
+// phase completes), so that waiting warps leave the issue slots to the others.
+__device__ __forceinline__ bool mbar_wait_parked(uint32_t bar, uint32_t parity, uint64_t limit_ns = kWaitLimitNs) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+  while (true) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity), "r"(10000u)
+        : "memory");
+    if (done) return true;
+    if (global_ns() - t0 > limit_ns) return false;
+  }
+}
+
 // ---- bulk asynchronous copy global -> shared (no tensor map) -------------------------
 // `bytes` must be a multiple of 16 and both addresses 16-byte aligned.
 __device__ __forceinline__ void bulk_copy_g2s(uint32_t dst_smem, const void* src_gmem,

@@ -212,8 +212,8 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       const int mask = stage_mask(j);
       // the codes have landed and (after the ring's first round) the f16 slot is free: the whole
       // warp goes on or gives up
-      bool ok = mbar_wait_bounded(hdr + kCFull + 8 * cst, (j / kBpCRing) & 1);
-      if (ok && j >= kBpVRing) ok = mbar_wait_bounded(hdr + kVFree + 8 * vst, ((j / kBpVRing) - 1) & 1);
+      bool ok = mbar_wait_parked(hdr + kCFull + 8 * cst, (j / kBpCRing) & 1);
+      if (ok && j >= kBpVRing) ok = mbar_wait_parked(hdr + kVFree + 8 * vst, ((j / kBpVRing) - 1) & 1);
       if (!__all_sync(kFullMask, ok)) {
         failed = true;
         break;
@@ -279,7 +279,7 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         const int mask = stage_mask(j);
         const int blk = __shfl_sync(kFullMask, ids, ((kBpKB * j) & 31) + (lane & (kBpKB - 1)));
         bool ok = true;
-        if (lane == 0 && j >= ring) ok = mbar_wait_bounded(free_ + 8 * st, ph);
+        if (lane == 0 && j >= ring) ok = mbar_wait_parked(free_ + 8 * st, ph);
         if (!__shfl_sync(kFullMask, ok, 0)) {
           failed = true;
           break;
@@ -310,7 +310,7 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         if (failed) raise_flag(a.status, PA_FLAG_TIMEOUT);
         // let the copies still in flight land before the CTA exits
         for (int j = max(0, issued - ring); j < issued; ++j)
-          mbar_wait_bounded(full + 8 * (j % ring), (j / ring) & 1, 10000000ull);
+          mbar_wait_parked(full + 8 * (j % ring), (j / ring) & 1, 10000000ull);
       }
     } else if (warp == 5) {
       // ---- MMA issuer --------------------------------------------------------------------------
@@ -320,7 +320,7 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       const uint64_t q_desc = umma_smem_desc(stages + kBpQOff, 16, 1024);
       const uint64_t v_desc0 = umma_smem_desc(stages + kBpVOff, kBpTile, 1024);
       auto wait_all = [&](uint32_t bar, uint32_t parity) {
-        return __all_sync(kFullMask, mbar_wait_bounded(bar, parity));
+        return __all_sync(kFullMask, mbar_wait_parked(bar, parity));
       };
       // S_j = Q K_j^T once K_j has landed (its columns hold P_{j-2}, read by P V issued before)
       auto issue_s = [&](int j) {
@@ -364,7 +364,7 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       if (lane == 0) {
         if (failed) raise_flag(a.status, PA_FLAG_TIMEOUT);
         umma_commit(hdr + kDone);
-        mbar_wait_bounded(hdr + kDone, 0);
+        mbar_wait_parked(hdr + kDone, 0);
       }
       __syncwarp();
     }
@@ -437,7 +437,7 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     bool failed = false;
     const float4* const scale_slots = reinterpret_cast<const float4*>(base + kBpScaleOff);
     for (int j = 0; j < nst; ++j) {
-      if (!__all_sync(kFullMask, mbar_wait_bounded(hdr + kSFull + 8 * (j & 1), (j >> 1) & 1))) {
+      if (!__all_sync(kFullMask, mbar_wait_parked(hdr + kSFull + 8 * (j & 1), (j >> 1) & 1))) {
         failed = true;
         break;
       }
@@ -510,7 +510,7 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       // O *= alpha where a row's shift moved (warp-collective), once P V of stage j - 1 is done
       if (j > 0 && __any_sync(kFullMask, alpha != 1.f)) {
         const int pj = j - 1;
-        if (!__all_sync(kFullMask, mbar_wait_bounded(hdr + kVFree + 8 * (pj % kBpVRing), (pj / kBpVRing) & 1))) {
+        if (!__all_sync(kFullMask, mbar_wait_parked(hdr + kVFree + 8 * (pj % kBpVRing), (pj / kBpVRing) & 1))) {
           failed = true;
           break;
         }
@@ -531,7 +531,7 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       if (lane == 0) mbar_arrive(hdr + kPFull + 8 * (j & 1));
     }
     // A warp that gave up still takes part in the barriers below (its rows' values are undefined).
-    const bool ok = !failed && __all_sync(kFullMask, mbar_wait_bounded(hdr + kDone, 0));
+    const bool ok = !failed && __all_sync(kFullMask, mbar_wait_parked(hdr + kDone, 0));
     if (!ok && lane == 0) raise_flag(a.status, PA_FLAG_TIMEOUT);
     {
       tc_fence_after();
