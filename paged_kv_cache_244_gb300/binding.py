@@ -508,19 +508,30 @@ def _declare_serving(L):
         getattr(L, name).restype = i
 
 
-def _ptrs(dtypes, **tensors):
-    """Data pointers of contiguous CUDA tensors, all on the current device; `dtypes` in order."""
+def _ptrs(spec, *tensors):
+    """Data pointers of contiguous CUDA tensors on the current device, checked against `spec`, a
+    (name, dtype) for each; and the current device."""
     dev = torch.cuda.current_device()
     out = []
-    for dtype, (name, t) in zip(dtypes, tensors.items()):
-        if t.dtype is not dtype:
-            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.get_device() != dev:
-            raise ValueError(f"{name} must be a CUDA tensor on the current device (cuda:{dev})")
-        if not t.is_contiguous():
+    for (name, dtype), t in zip(spec, tensors):
+        if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+            if t.dtype is not dtype:
+                raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+            if t.get_device() != dev:
+                raise ValueError(f"{name} must be a CUDA tensor on the current device (cuda:{dev})")
             raise ValueError(f"{name} must be contiguous")
         out.append(t.data_ptr())
-    return out
+    return out, dev
+
+
+# The current stream's handle without building a Stream object (3 us a call), where torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(stream, dev):
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
 
 
 def _kept(stream, *tensors):
@@ -562,12 +573,16 @@ def rope_table(max_pos, rotary_dim=128, theta=1e4, scaling="none", factor=1.0, o
     elif tuple(out.shape) != (max_pos, rotary_dim):
         raise ValueError("out must be [max_pos, rotary_dim]")
     spec = pa_rope_scaling(theta, factor, original_max_pos, low, high, magnitude, ROPE_SCALINGS[scaling])
-    (o,) = _ptrs((torch.float32,), out=out)
-    _check(lib().pa_rope_table(ctypes.byref(spec), rotary_dim, max_pos, o, _stream(stream)), "pa_rope_table")
+    (o,), dev = _ptrs((("out", torch.float32),), out)
+    _check(lib().pa_rope_table(ctypes.byref(spec), rotary_dim, max_pos, o, _stream_of(stream, dev)),
+           "pa_rope_table")
     return out
 
 
-_STORE_TYPES = (torch.bfloat16,) * 4 + (torch.int32, torch.float32, torch.int64)
+_STORE = tuple((n, torch.bfloat16) for n in ("q", "q_out", "k", "v")) + (
+    ("positions", torch.int32), ("cos_sin", torch.float32), ("slot_mapping", torch.int64))
+_STORE_BF16 = _STORE + (("k_cache", torch.bfloat16), ("v_cache", torch.bfloat16))
+_STORE_BLOCK = _STORE + (("k_cache", torch.uint8), ("v_cache", torch.uint8), ("kv_scale", torch.float32))
 
 
 def _store_shapes(q, k, v, positions, slot_mapping, q_out, nb_shape):
@@ -593,12 +608,10 @@ def rope_kv_store_form(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cac
     if v_cache.shape != k_cache.shape:
         raise ValueError("k_cache and v_cache differ in shape")
     T, dims, nb = _store_shapes(q, k, v, positions, slot_mapping, q_out, k_cache.shape)
-    bf = torch.bfloat16
-    qp, qo, kp, vp, pos, cs, slots, kc, vc = _ptrs(
-        _STORE_TYPES + (bf, bf), q=q, q_out=q_out, k=k, v=v, positions=positions, cos_sin=cos_sin,
-        slot_mapping=slot_mapping, k_cache=k_cache, v_cache=v_cache)
+    (qp, qo, kp, vp, pos, cs, slots, kc, vc), dev = _ptrs(
+        _STORE_BF16, q, q_out, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache)
     _check(lib().pa_rope_kv_store_form(ctypes.byref(dims), ctypes.byref(rope), T, qp, qo, kp, vp, pos, cs,
-                                       cos_sin.shape[0], slots, kc, vc, nb, _stream(stream)),
+                                       cos_sin.shape[0], slots, kc, vc, nb, _stream_of(stream, dev)),
            "pa_rope_kv_store_form")
     return q_out
 
@@ -611,12 +624,11 @@ def rope_kv_store_fp8_block(q, k, v, positions, cos_sin, slot_mapping, k_cache, 
     rope = _rope_form(cos_sin, layout)
     T, dims, nb = _store_shapes(q, k, v, positions, slot_mapping, q_out,
                                 _block_caches(k_cache, v_cache, kv_scale))
-    qp, qo, kp, vp, pos, cs, slots, kc, vc, sc = _ptrs(
-        _STORE_TYPES + (torch.uint8, torch.uint8, torch.float32), q=q, q_out=q_out, k=k, v=v,
-        positions=positions, cos_sin=cos_sin, slot_mapping=slot_mapping, k_cache=k_cache,
-        v_cache=v_cache, kv_scale=kv_scale)
+    (qp, qo, kp, vp, pos, cs, slots, kc, vc, sc), dev = _ptrs(
+        _STORE_BLOCK, q, q_out, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, kv_scale)
     _check(lib().pa_rope_kv_store_fp8_block(ctypes.byref(dims), ctypes.byref(rope), T, qp, qo, kp, vp, pos,
-                                            cs, cos_sin.shape[0], slots, kc, vc, sc, nb, _stream(stream)),
+                                            cs, cos_sin.shape[0], slots, kc, vc, sc, nb,
+                                            _stream_of(stream, dev)),
            "pa_rope_kv_store_fp8_block")
     return q_out
 
@@ -631,8 +643,11 @@ def _decode_shapes(q, k_cache, v_cache, kv_scale, block_tables, context_lens, ou
     return S, nb, pa_dims(Hq, Hkv, D, B)
 
 
-_DECODE_TYPES = (torch.bfloat16, torch.bfloat16, torch.uint8, torch.uint8, torch.float32, torch.int32,
-                 torch.int32, torch.float32)
+_ATTEND = (("q", torch.bfloat16), ("out", torch.bfloat16), ("k_cache", torch.uint8), ("v_cache", torch.uint8),
+           ("kv_scale", torch.float32), ("block_tables", torch.int32), ("context_lens", torch.int32))
+_DECODE = _ATTEND + (("workspace", torch.float32),)
+_STEP = _DECODE + (("k", torch.bfloat16), ("v", torch.bfloat16), ("cos_sin", torch.float32))
+_PREFILL = _ATTEND + (("q_start", torch.int32),)
 
 
 def decode_fp8_block(q, k_cache, v_cache, kv_scale, block_tables, context_lens, max_context_len,
@@ -646,12 +661,11 @@ def decode_fp8_block(q, k_cache, v_cache, kv_scale, block_tables, context_lens, 
     if workspace is None:
         workspace = decode_workspace(q, k_cache, max_context_len, partition_tokens)
         _kept(stream, workspace)
-    qp, op, kc, vc, sc, bt, ctx, ws = _ptrs(
-        _DECODE_TYPES, q=q, out=out, k_cache=k_cache, v_cache=v_cache, kv_scale=kv_scale,
-        block_tables=block_tables, context_lens=context_lens, workspace=workspace)
+    (qp, op, kc, vc, sc, bt, ctx, ws), dev = _ptrs(
+        _DECODE, q, out, k_cache, v_cache, kv_scale, block_tables, context_lens, workspace)
     _check(lib().pa_decode_fp8_block(ctypes.byref(dims), S, qp, kc, vc, sc, nb, bt, block_tables.shape[1], ctx,
                                      max_context_len, scale, partition_tokens, ws, workspace.numel() * 4, op,
-                                     _stream(stream)),
+                                     _stream_of(stream, dev)),
            "pa_decode_fp8_block")
     return out
 
@@ -672,14 +686,12 @@ def decode_step_fp8_block(q, k, v, cos_sin, k_cache, v_cache, kv_scale, block_ta
     if workspace is None:
         workspace = decode_workspace(q, k_cache, max_context_len, partition_tokens)
         _kept(stream, workspace)
-    qp, op, kc, vc, sc, bt, ctx, ws, kp, vp, cs = _ptrs(
-        _DECODE_TYPES + (torch.bfloat16, torch.bfloat16, torch.float32), q=q, out=out, k_cache=k_cache,
-        v_cache=v_cache, kv_scale=kv_scale, block_tables=block_tables, context_lens=context_lens,
-        workspace=workspace, k=k, v=v, cos_sin=cos_sin)
+    (qp, op, kc, vc, sc, bt, ctx, ws, kp, vp, cs), dev = _ptrs(
+        _STEP, q, out, k_cache, v_cache, kv_scale, block_tables, context_lens, workspace, k, v, cos_sin)
     _check(lib().pa_decode_step_fp8_block(
         ctypes.byref(dims), ctypes.byref(rope), S, qp, kp, vp, cs, cos_sin.shape[0], kc, vc, sc, nb, bt,
         block_tables.shape[1], ctx, max_context_len, scale, partition_tokens, ws, workspace.numel() * 4, op,
-        PA_STEP_EARLY_METADATA if early_metadata else 0, _stream(stream)), "pa_decode_step_fp8_block")
+        PA_STEP_EARLY_METADATA if early_metadata else 0, _stream_of(stream, dev)), "pa_decode_step_fp8_block")
     return out
 
 
@@ -698,12 +710,11 @@ def prefill_fp8_block(q, q_start, k_cache, v_cache, kv_scale, block_tables, cont
     if q_start.shape != (S + 1,) or block_tables.dim() != 2 or block_tables.shape[0] != S:
         raise ValueError("q_start / block_tables shape mismatch")
     dims = pa_dims(Hq, Hkv, D, B)
-    qp, op, kc, vc, sc, bt, ctx, qs = _ptrs(
-        _DECODE_TYPES[:7] + (torch.int32,), q=q, out=out, k_cache=k_cache, v_cache=v_cache,
-        kv_scale=kv_scale, block_tables=block_tables, context_lens=context_lens, q_start=q_start)
+    (qp, op, kc, vc, sc, bt, ctx, qs), dev = _ptrs(
+        _PREFILL, q, out, k_cache, v_cache, kv_scale, block_tables, context_lens, q_start)
     _check(lib().pa_prefill_fp8_block(ctypes.byref(dims), S, T, qp, qs, max_query_len, kc, vc, sc, nb, bt,
-                                      block_tables.shape[1], ctx, max_context_len, scale, op, _stream(stream)),
-           "pa_prefill_fp8_block")
+                                      block_tables.shape[1], ctx, max_context_len, scale, op,
+                                      _stream_of(stream, dev)), "pa_prefill_fp8_block")
     return out
 
 
@@ -724,7 +735,9 @@ def step_plan(num_seqs, num_tokens, device="cuda") -> StepPlan:
                     torch.empty(num_seqs, **i32))
 
 
-_PLAN_TYPES = (torch.int32,) * 9 + (torch.int64, torch.int32)
+_PLAN = tuple((n, torch.int32) for n in ("cached_lens", "new_lens", "block_tables", "free_blocks", "num_free",
+                                         "num_free_out", "context_lens", "q_start", "positions")) + (
+    ("slot_mapping", torch.int64), ("granted", torch.int32))
 
 
 def plan_step(cached_lens, new_lens, block_tables, free_blocks, num_free, num_blocks, num_tokens,
@@ -749,13 +762,12 @@ def plan_step(cached_lens, new_lens, block_tables, free_blocks, num_free, num_bl
     if (ctx.shape != (S,) or qs.shape != (S + 1,) or granted.shape != (S,) or pos.shape != (num_tokens,)
             or slots.shape != (num_tokens,)):
         raise ValueError("plan does not fit these sequences and rows")
-    c, n, bt, fb, nf, nfo, cx, q0, ps, sl, gr = _ptrs(
-        _PLAN_TYPES, cached_lens=cached_lens, new_lens=new_lens, block_tables=block_tables,
-        free_blocks=free_blocks, num_free=num_free, num_free_out=num_free_out, context_lens=ctx, q_start=qs,
-        positions=pos, slot_mapping=slots, granted=granted)
+    (c, n, bt, fb, nf, nfo, cx, q0, ps, sl, gr), dev = _ptrs(
+        _PLAN, cached_lens, new_lens, block_tables, free_blocks, num_free, num_free_out, ctx, qs, pos, slots,
+        granted)
     _check(lib().pa_plan_step(ctypes.byref(_PLAN_DIMS), S, c, n, bt, block_tables.shape[1], fb,
                               free_blocks.shape[0], nf, nfo, num_blocks, num_tokens, cx, q0, ps, sl, gr,
-                              _stream(stream)), "pa_plan_step")
+                              _stream_of(stream, dev)), "pa_plan_step")
     return plan
 
 

@@ -282,45 +282,74 @@ __global__ void __launch_bounds__(kFormWarps * 32) rope_block_store_kernel(const
 // ---- the table -------------------------------------------------------------------------------
 // Pair i at position p turns by p * turns[i] / 2^64 of a whole turn, modulo 1: the low 64 bits of
 // the product are exact but for the 2^-65 to which turns[i] was rounded (2^-34 of a turn at
-// position 2^31).  The nearest quarter turn is taken off in these integers too, so that what is
-// rounded to fp32 is an angle of at most pi/4, relative to its own size, and sin and cos keep
-// their relative accuracy next to their zeros.  On that interval the Taylor sums of sin to x^9
-// and of cos to x^10 are within 2^-29.  A thread makes four pairs of a row: one 16-byte word of
-// cos, one of sin.
+// position 2^31).  The nearest quarter turn is taken off in the product's high word, so that what
+// is rounded to fp32 is an angle of at most pi/4, relative to its own size (the low word joins in
+// one FMA), and sin and cos keep their relative accuracy next to their zeros.  On that interval
+// the Taylor sums of sin to x^9 and of cos to x^10 are within 2^-29; both are formed for two pairs
+// at a time in packed fp32.  A thread keeps four neighbouring pairs and goes down the rows: one
+// 16-byte word of cos, one of sin a row.
+//
+// Bound by the 8 bytes a pair it writes, with about 30 instructions a pair beside them (131,072 x 128:
+// a first form with a 64-bit division per word and sign handling in 64 bits took 17.1 us, 58% of
+// the copy rate).
 constexpr int kTableThreads = 256;
 
 __global__ void __launch_bounds__(kTableThreads) rope_table_kernel(const RopeTableArgs a) {
-  __shared__ unsigned long long turns[64];
+  __shared__ unsigned long long all_turns[64];
   pdl_wait_prior_grid();
   pdl_allow_next_grid();
-  if (threadIdx.x < 64) turns[threadIdx.x] = a.turns[threadIdx.x];
+  if (threadIdx.x < 64) all_turns[threadIdx.x] = a.turns[threadIdx.x];
   __syncthreads();
-  const int R = a.rotary_dim, words = R >> 3;   // 16-byte words of cos in a row
-  const long long total = static_cast<long long>(a.max_pos) * words;
-  const long long step = static_cast<long long>(gridDim.x) * kTableThreads;
-  for (long long idx = static_cast<long long>(blockIdx.x) * kTableThreads + threadIdx.x; idx < total; idx += step) {
-    const long long p = idx / words;
-    const int c = static_cast<int>(idx - p * words);
-    float cs[4], sn[4];
+  const int R = a.rotary_dim, words = R >> 3;       // 16-byte words of cos in a row, 2 .. 16
+  const int rows = kTableThreads / words;           // rows of a pass of the CTA
+  const int r = threadIdx.x / words, c = threadIdx.x - r * words;
+  if (r >= rows) return;
+  unsigned t_lo[4], t_hi[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    t_lo[i] = static_cast<unsigned>(all_turns[4 * c + i]);
+    t_hi[i] = static_cast<unsigned>(all_turns[4 * c + i] >> 32);
+  }
+  auto both = [](float x) { return pack_f32x2(x, x); };
+  const long long step = static_cast<long long>(gridDim.x) * rows;
+  for (long long p = static_cast<long long>(blockIdx.x) * rows + r; p < a.max_pos; p += step) {
+    const unsigned pos = static_cast<unsigned>(p);
+    float x[4];
+    unsigned quarter[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const unsigned long long f = turns[4 * c + i] * static_cast<unsigned long long>(p);
-      const unsigned quarter = static_cast<unsigned>((f + (1ull << 61)) >> 62);        // 0 .. 3
-      const long long rest = static_cast<long long>(f - (static_cast<unsigned long long>(quarter) << 62));
-      const unsigned long long mag = rest < 0 ? 0ull - static_cast<unsigned long long>(rest)
-                                              : static_cast<unsigned long long>(rest);
-      float x = fmaf(static_cast<float>(static_cast<unsigned>(mag >> 32)), 0x1p32f,
-                     static_cast<float>(static_cast<unsigned>(mag))) * (6.28318530717958647692f * 0x1p-64f);
-      if (rest < 0) x = -x;
-      const float y = x * x;
-      const float sn0 = fmaf(x * y, fmaf(y, fmaf(y, fmaf(y, 1.f / 362880.f, -1.f / 5040.f), 1.f / 120.f), -1.f / 6.f), x);
-      const float cs0 = fmaf(y, fmaf(y, fmaf(y, fmaf(y, fmaf(y, -1.f / 3628800.f, 1.f / 40320.f), -1.f / 720.f), 1.f / 24.f),
-                                     -0.5f), 1.f);
-      const float c1 = (quarter & 1) ? sn0 : cs0, s1 = (quarter & 1) ? cs0 : sn0;
-      cs[i] = (quarter == 1 || quarter == 2) ? -c1 : c1;
-      sn[i] = quarter >= 2 ? -s1 : s1;
-      cs[i] *= a.magnitude;
-      sn[i] *= a.magnitude;
+      const unsigned long long f = static_cast<unsigned long long>(t_lo[i]) * pos +
+                                   (static_cast<unsigned long long>(t_hi[i] * pos) << 32);
+      const unsigned hi = static_cast<unsigned>(f >> 32);
+      quarter[i] = (hi + (1u << 29)) >> 30;          // 0 .. 3 (wraps past 7/8)
+      const int rest = static_cast<int>(hi - (quarter[i] << 30));
+      x[i] = fmaf(static_cast<float>(static_cast<unsigned>(f)), 0x1p-32f, static_cast<float>(rest)) *
+             (6.28318530717958647692f * 0x1p-32f);
+    }
+    float cs[4], sn[4];
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      const uint64_t v = pack_f32x2(x[i], x[i + 1]);
+      const uint64_t y = fma_f32x2(v, v, 0ull);
+      uint64_t s = fma_f32x2(y, both(1.f / 362880.f), both(-1.f / 5040.f));
+      s = fma_f32x2(s, y, both(1.f / 120.f));
+      s = fma_f32x2(s, y, both(-1.f / 6.f));
+      s = fma_f32x2(fma_f32x2(v, y, 0ull), s, v);
+      uint64_t q = fma_f32x2(y, both(-1.f / 3628800.f), both(1.f / 40320.f));
+      q = fma_f32x2(q, y, both(-1.f / 720.f));
+      q = fma_f32x2(q, y, both(1.f / 24.f));
+      q = fma_f32x2(q, y, both(-0.5f));
+      q = fma_f32x2(q, y, both(1.f));
+      float s0[2], c0[2];
+      unpack_f32x2(s, s0[0], s0[1]);
+      unpack_f32x2(q, c0[0], c0[1]);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const unsigned k = quarter[i + u];
+        const float c1 = (k & 1) ? s0[u] : c0[u], s1 = (k & 1) ? c0[u] : s0[u];
+        cs[i + u] = __uint_as_float(__float_as_uint(c1 * a.magnitude) ^ (((k + 1) & 2u) << 30));
+        sn[i + u] = __uint_as_float(__float_as_uint(s1 * a.magnitude) ^ ((k & 2u) << 30));
+      }
     }
     float* row = a.cos_sin + p * R;
     *reinterpret_cast<float4*>(row + 4 * c) = make_float4(cs[0], cs[1], cs[2], cs[3]);
@@ -365,9 +394,9 @@ cudaError_t launch_rope_form_store(const RopeFormArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_rope_table(const RopeTableArgs& a, cudaStream_t stream) {
-  const long long items = static_cast<long long>(a.max_pos) * (a.rotary_dim / 8);
-  long long ctas = (items + kTableThreads - 1) / kTableThreads;
-  if (ctas > 152 * 8) ctas = 152 * 8;
+  const int rows = kTableThreads / (a.rotary_dim / 8);
+  long long ctas = (static_cast<long long>(a.max_pos) + rows - 1) / rows;
+  if (ctas > 152 * 8) ctas = 152 * 8;   // 8 CTAs of 256 threads fit an SM
   cudaLaunchAttribute attr;
   cudaLaunchConfig_t cfg = chained(static_cast<unsigned>(ctas), kTableThreads, &attr, stream);
   return cudaLaunchKernelEx(&cfg, rope_table_kernel, a);
