@@ -331,6 +331,13 @@ __device__ __forceinline__ float ex2_ftz(float x) {
   return y;
 }
 
+// 1 / x within an ulp (rcp.approx)
+__device__ __forceinline__ float rcp_ftz(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // max(a, b, c) in one instruction (a NaN operand is ignored, as by fmaxf)
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
   float r;
@@ -406,6 +413,17 @@ __device__ __forceinline__ uint16_t e4m3x2_of(uint32_t bf16_pair, float inv) {
   return r;
 }
 
+// E4M3 codes of an f16 pair, round to nearest even, saturating; low byte = low half.
+__device__ __forceinline__ uint16_t e4m3x2_of_f16x2(uint32_t x) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 // E4M3 codes of two floats, round to nearest even, saturating; low byte = lo.
 __device__ __forceinline__ uint16_t e4m3x2_of_floats(float lo, float hi) {
   uint16_t r;
@@ -501,14 +519,30 @@ __device__ __forceinline__ float log2_of(float x) {
          __log2f(__uint_as_float((b & 0x007fffffu) | 0x3f800000u));
 }
 
-// ---- 8-byte asynchronous copy global -> shared, tracked by an mbarrier ---------------------
+// ---- per-thread asynchronous copies global -> shared, in commit groups -----------------------
 __device__ __forceinline__ void cp_async8(uint32_t dst_smem, const void* src_gmem) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst_smem), "l"(src_gmem) : "memory");
 }
-// Arrive once on the mbarrier when this thread's cp.async copies so far have landed (the
-// arrival is one of those the barrier was initialised to expect).
-__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst_smem, const void* src_gmem) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst_smem), "l"(src_gmem) : "memory");
+}
+__device__ __forceinline__ void cp_async16_hint(uint32_t dst_smem, const void* src_gmem, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst_smem), "l"(src_gmem), "l"(policy)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Wait until at most `later` of this thread's newest groups (0 .. 7) are in flight.
+__device__ __forceinline__ void cp_async_wait_but(int later) {
+  switch (later) {
+    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+    case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+    case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
+    case 6: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 7;" ::: "memory"); break;
+  }
 }
 
 }  // namespace pa

@@ -44,7 +44,7 @@
 // chunk c ^ (r % 8); the ldmatrix row addresses apply the same XOR, so all eight rows of a
 // matrix hit distinct banks.
 //
-// Variants (template <kStep, kFp8, kGather, kOnce, kBlock>):
+// Variants (template <kStep, kFp8, kGather, kOnce>):
 //   kStep  the fused decode step ("Pico-vLLM" §2: RoPE fused with the KV cache store): the warp
 //          whose job holds a sequence's new token (position len - 1) stages the token's k, v and
 //          cos/sin row with the tiles, rotates k, writes both rows into the staged tiles before
@@ -53,14 +53,6 @@
 //          12 warps with 2 stages; the byte tiles are read by ldmatrix as 16-bit pairs and widened exactly to
 //          f16 with cvt.f16x2.e4m3x2, the q.K k index permuted alike in both operands; f16 MMAs,
 //          the K scale folded into the softmax scale, the V scale into the output.
-//   kBlock (with kFp8) a scale for each (block, KV head), K and V, brought with the job's tiles
-//          by an 8-byte cp.async on the same mbarrier.  With k_b, v_b the scales of token t's
-//          block the kernel keeps x_t = scale_log2 k_b (q . Kcode_t) + log2 v_b, p_t = 2^(x_t - m),
-//          O = sum p_t Vcode_t and L = sum p_t / v_b: out = O / L, since both sums carry 2^m and
-//          v_b cancels in the second.  The shift m follows the largest contribution p_t, so P
-//          stays within f16 (2^7 to 2^15 at its largest) whatever the scales, a V tile needs no multiply, and the pieces
-//          merge as any others do.  L adds the unrounded fp32 p_t: a block of tiny V scale (an
-//          attention sink) may carry most of the softmax's weight with a p_t below f16.
 //   kGather the tile gather alone (pa_gather_checksum): an XOR of the tile words instead of the
 //          attention, no merge -- the floor of this kernel's access pattern.
 //   kOnce  launched for calls with early metadata (a layer of a chain): the K/V tiles load with
@@ -72,6 +64,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include "decode_split.cuh"
 #include "pa_device.cuh"
 #include "pa_launch.h"
 
@@ -83,12 +76,6 @@ constexpr int kStages = PA_DECODE_STAGES;
 constexpr int kHalfBytes = kBlockSize * 128;                // 16 rows x 64 bf16
 constexpr int kQBytes = 8 * kHeadDim * 2;                   // q rows of up to 8 heads
 
-// Per CTA in shared memory: the block-count prefix N_s (S + 1 ints), then per sequence the
-// valid rows of its last block (1..16; one byte each).
-__host__ __device__ inline int prefix_bytes(int num_seqs) {
-  return (((num_seqs + 1) * 4 + 15) & ~15) + ((num_seqs + 15) & ~15);
-}
-
 // Shared-memory layout of one kernel variant.  kStep fuses the new token's RoPE + store; kFp8
 // reads E4M3 caches, whose (block, KV head) tiles are 2 KiB instead of 4 KiB: there the CTA
 // runs 12 warps of 2 stages, since its per-job work (widening the codes) is heavier and more
@@ -96,7 +83,7 @@ __host__ __device__ inline int prefix_bytes(int num_seqs) {
 // the prefix of block counts.  Stage: [K tile | V tile | q rows | (kStep) the new token's
 // cos/sin row (fp32), k row and v row (bf16)], a multiple of 1024 bytes so that every tile
 // stays on the 1024-byte boundary its 128-byte swizzle needs.
-template <bool kStep, bool kFp8, bool kBlock = false>
+template <bool kStep, bool kFp8>
 struct Layout {
   static constexpr int kTile = kFp8 ? kTileBytes / 2 : kTileBytes;
   static constexpr int kWarpsN = kFp8 ? 12 : kWarps;
@@ -107,8 +94,7 @@ struct Layout {
   static constexpr int kNewVOff = kNewKOff + kHeadDim * 2;
   static constexpr int kStage = kStep ? kNewVOff + kHeadDim * 2 : kQOff + kQBytes;
   static constexpr int kDescOff = (kWarpsN * kStagesN * 8 + 15) & ~15;
-  static constexpr int kScaleOff = kDescOff + kWarpsN * kStagesN * 16;  // kBlock: a float2 per stage
-  static constexpr int kPrefixOff = (kScaleOff + (kBlock ? kWarpsN * kStagesN * 8 : 0) + 15) & ~15;
+  static constexpr int kPrefixOff = kDescOff + kWarpsN * kStagesN * 16;
   static_assert(kStage % 1024 == 0 && kTile % 1024 == 0, "tiles on 1024-byte boundaries");
   static_assert(kDescOff % 16 == 0 && kPrefixOff % 16 == 0, "descriptor alignment");
   __host__ __device__ static int smem(int num_seqs) {
@@ -116,58 +102,11 @@ struct Layout {
   }
 };
 
-// Job flags (low bits of a descriptor's flag word; valid tokens sit at bits 8-12, the KV head
-// at bits 16-31).
-constexpr uint32_t kFirst = 1u, kLast = 2u, kWhole = 4u, kHasData = 8u;
-constexpr uint32_t kNew = 16u;   // fused step: the block holding the segment's new token
-constexpr uint32_t kRope = 32u;  // fused step: the sequence's position has a cos/sin row
-constexpr uint32_t kGap = 64u;   // the piece starts at a range boundary that is also a partition
-                                 // boundary inside the segment: the slot before it is a gap
-constexpr int kMinRangeBlocks = PA_DECODE_MIN_RANGE;
-
-
-// Flattened-axis ranges: V = min(num_warps, ceil(T / kMinRangeBlocks)) equal ranges, range
-// v = [floor(v T / V), floor((v+1) T / V)), none shorter than kMinRangeBlocks blocks unless T
-// is, so that a small batch is not cut into one-block pieces that the merge must then gather.
-// With V <= #warps of the grid, every warp has at most one range.
-struct Ranges {
-  long long T;
-  int V;
-  __device__ __forceinline__ long long begin(int v) const { return (static_cast<long long>(v) * T) / V; }
-  __device__ __forceinline__ int owner(long long x) const {
-    return static_cast<int>(((x + 1) * V - 1) / T);
-  }
-};
-
-__device__ __forceinline__ Ranges make_ranges(long long T, const DecodeArgs& a) {
-  Ranges r;
-  r.T = T;
-  r.V = static_cast<int>(min(static_cast<long long>(a.num_warps), (T + kMinRangeBlocks - 1) / kMinRangeBlocks));
-  return r;
-}
-
-// Partial slot of the piece of segment `seg` in range v and P-token partition `part` (0
-// without partitions; max_parts = partitions of the longest segment, 1 without).  Along the
-// job axis consecutive pieces differ in range, partition or segment, and each such step
-// raises the slot by at least one, so slots are distinct and below V + (#segments) * max_parts.
-// Within one segment a step raises it by exactly one, except where a range boundary is also a
-// partition boundary: there it skips one slot, which the warp whose range starts there marks
-// empty (shift -inf, sum 0).  So a segment's pieces, with those gaps, fill the slots from
-// v_first + seg * max_parts to v_last + seg * max_parts + (its last partition), in axis order.
-__device__ __forceinline__ long long piece_slot(int v, int seg, int part, int max_parts) {
-  return static_cast<long long>(v) + static_cast<long long>(seg) * max_parts + part;
-}
-
-__device__ __forceinline__ int clamp_len(int len, int max_len) {
-  return len < 0 ? 0 : (len > max_len ? max_len : len);
-}
-
-template <bool kStep, bool kFp8, bool kGather = false, bool kOnce = false, bool kBlock = false>
-__global__ void __launch_bounds__(Layout<kStep, kFp8, kBlock>::kWarpsN * 32, 1)
+template <bool kStep, bool kFp8, bool kGather = false, bool kOnce = false>
+__global__ void __launch_bounds__(Layout<kStep, kFp8>::kWarpsN * 32, 1)
 decode_partition_kernel(const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const DecodeArgs a) {
-  using L = Layout<kStep, kFp8, kBlock>;
-  static_assert(!kBlock || (kFp8 && !kGather), "block scales belong to E4M3 attention");
+  using L = Layout<kStep, kFp8>;
   constexpr int kWarps = L::kWarpsN;           // warps of this variant's CTA
   constexpr int kPool = kWarps * L::kStagesN;  // stages of the CTA
   constexpr int kStageB = L::kStage;
@@ -182,7 +121,7 @@ decode_partition_kernel(const __grid_constant__ CUtensorMap tm_k,
   // 128-byte swizzled TMA destinations must sit on 1024-byte boundaries.
   const uint32_t tile_base = (raw + L::kPrefixOff + prefix_bytes(a.num_seqs) + 1023u) & ~1023u;
   if (tid < kPool) {
-    mbar_init(raw + 8 * tid, kBlock ? 2 : 1);  // kBlock: and the scales' copy
+    mbar_init(raw + 8 * tid, 1);
     fence_mbar_init();
   }
   if (tid == 0) {
@@ -202,40 +141,7 @@ decode_partition_kernel(const __grid_constant__ CUtensorMap tm_k,
   const int G = a.num_q_heads / Hkv;
 
   // ---- CTA prologue: exclusive prefix N_s of per-sequence block counts in shared memory ----
-  {
-    __shared__ int warp_sums[kWarps];
-    const int per = (S + kWarps * 32 - 1) / (kWarps * 32);
-    const int lo = min(S, tid * per), hi = min(S, lo + per);
-    int sum = 0;
-    for (int s = lo; s < hi; ++s) {
-      const int len = a.context_lens[s];
-      if ((len < 0 || len > a.max_context_len) && blockIdx.x == 0)
-        raise_flag(a.status, PA_FLAG_CONTEXT_LEN_OOB);
-      sum += (clamp_len(len, a.max_context_len) + kBlockSize - 1) / kBlockSize;
-    }
-    int incl = sum;
-#pragma unroll
-    for (int x = 1; x < 32; x <<= 1) {
-      const int y = __shfl_up_sync(kFullMask, incl, x);
-      if (lane >= x) incl += y;
-    }
-    if (lane == 31) warp_sums[warp] = incl;
-    __syncthreads();
-    int run = incl - sum;
-    for (int w = 0; w < warp; ++w) run += warp_sums[w];
-    for (int s = lo; s < hi; ++s) {
-      prefix[s] = run;
-      const int len = clamp_len(a.context_lens[s], a.max_context_len);
-      run += (len + kBlockSize - 1) / kBlockSize;
-      last_rows[s] = static_cast<unsigned char>(((len - 1) & (kBlockSize - 1)) + 1);  // unused if len == 0
-    }
-    if (tid == kWarps * 32 - 1) {
-      int total = 0;
-      for (int w = 0; w < kWarps; ++w) total += warp_sums[w];
-      prefix[S] = total;
-    }
-    __syncthreads();
-  }
+  build_prefix<kWarps>(a, prefix, last_rows);
   const long long T = static_cast<long long>(Hkv) * prefix[S];
   const Ranges R = make_ranges(T, a);
   // Stage pool: the CTA's kPool stages are shared out among its warps that have a range.  Range
@@ -250,7 +156,6 @@ decode_partition_kernel(const __grid_constant__ CUtensorMap tm_k,
   const uint32_t bars = raw + warp * n_st * 8;
   int4* descs = reinterpret_cast<int4*>(smem_raw + L::kDescOff) + warp * n_st;
   const uint32_t tiles = tile_base + warp * n_st * kStageB;
-  float2* scales = reinterpret_cast<float2*>(smem_raw + L::kScaleOff) + warp * n_st;  // kBlock
   const int gq = lane >> 2;  // fragment row group
   const int cq = lane & 3;   // fragment column pair
   const int mi = lane >> 3;  // ldmatrix: matrix this lane addresses
@@ -366,25 +271,14 @@ decode_partition_kernel(const __grid_constant__ CUtensorMap tm_k,
     const int y = ok ? (blk * Hkv + (fl >> 16)) * kBlockSize : 0;
     const uint32_t bar = bars + 8 * st;
     const uint32_t dst = tiles + st * kStageB;
-    const uint32_t cos_sin_bytes = kBlock ? static_cast<uint32_t>(a.rotary_dim) * 4u : kHeadDim * 4u;
     const uint32_t bytes = (ok ? 2u * L::kTile : 0u) + (q_rows ? static_cast<uint32_t>(G) * 256u : 0u) +
-                           (trig ? cos_sin_bytes : 0u) + (fresh ? kHeadDim * 4u : 0u);
+                           (trig ? kHeadDim * 4u : 0u) + (fresh ? kHeadDim * 4u : 0u);
     if (lane == 0) {
       if (!ok) raise_flag(a.status, PA_FLAG_BLOCK_ID_OOB);
       if (kStep && (fl & kNew) && !rope) raise_flag(a.status, PA_FLAG_POSITION_OOB);
       descs[st] = make_int4(seg, fl | (ok ? static_cast<int>(kHasData) : 0), slot, y);
       if (bytes) mbar_arrive_expect_tx(bar, bytes);
       else mbar_arrive(bar);
-    }
-    if constexpr (kBlock) {
-      if (lane == 6) {  // the barrier's second arrival: when the tile's scales have landed
-        if (ok) {
-          cp_async8(smem_addr(scales + st), a.kv_scale + (static_cast<size_t>(blk) * Hkv + (fl >> 16)));
-          cp_async_arrive(bar);
-        } else {
-          mbar_arrive(bar);
-        }
-      }
     }
     // The copies of one job leave from different lanes at once (one thread issues its copies
     // one after another), once lane 0 has armed the stage's barrier.
@@ -405,8 +299,7 @@ decode_partition_kernel(const __grid_constant__ CUtensorMap tm_k,
         bulk_copy_g2s(dst + L::kQOff, a.q + static_cast<size_t>(seg) * G * kHeadDim,
                       static_cast<uint32_t>(G) * 256u, bar);
       } else if (lane == 3 && trig) {
-        bulk_copy_g2s(dst + L::kCosSinOff, a.cos_sin + static_cast<size_t>(pos) * (kBlock ? a.rotary_dim : kHeadDim), cos_sin_bytes,
-                      bar);
+        bulk_copy_g2s(dst + L::kCosSinOff, a.cos_sin + static_cast<size_t>(pos) * kHeadDim, kHeadDim * 4u, bar);
       } else if (lane == 4 && fresh) {  // row seg of the [S, Hkv] new-token rows
         bulk_copy_g2s(dst + L::kNewKOff, a.k_new + static_cast<size_t>(seg) * kHeadDim, kHeadDim * 2u, bar);
       } else if (lane == 5 && fresh) {
@@ -429,77 +322,6 @@ decode_partition_kernel(const __grid_constant__ CUtensorMap tm_k,
   float o[8][4];                         // O^T: dims 16mt + gq (+8), heads 2cq, 2cq+1
 #pragma unroll
   for (int mt = 0; mt < 8; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
-
-  // Fused step, block-scaled caches: the new token (row `row` of the staged tile, whose first cache
-  // row is `y`) is rotated and coded into the staged tile and the cache.  Row 0 begins the block;
-  // otherwise a scale that has to grow codes the whole tile anew, and the tile is written back.
-  // Returns the block's scales after the store.
-  auto store_new_block = [&](unsigned char* stage, float2 held, int row, int y) -> float2 {
-    const uint32_t* kn = reinterpret_cast<const uint32_t*>(stage + L::kNewKOff);
-    const uint32_t* vn = reinterpret_cast<const uint32_t*>(stage + L::kNewVOff);
-    const float* cs = reinterpret_cast<const float*>(stage + L::kCosSinOff);
-    const int R = a.rotary_dim;
-    // Lane l holds two words (dim pairs) of the row: of the half layout words l and l + R/4 for
-    // l < R/4, otherwise words 2l and 2l + 1; the first R/4 lanes rotate theirs.
-    const bool turns = lane < R / 4;
-    const int wa = turns && !a.interleaved ? lane : 2 * lane;
-    const int wb = turns && !a.interleaved ? lane + R / 4 : 2 * lane + 1;
-    uint32_t kx = kn[wa], ky = kn[wb];
-    if (turns) {
-      const float2 co = reinterpret_cast<const float2*>(cs)[lane];
-      const float2 si = reinterpret_cast<const float2*>(cs + R / 2)[lane];
-      if (a.interleaved) rope_rotate_interleaved(kx, ky, co, si);
-      else rope_rotate_pairs(kx, ky, co, si);
-    }
-    const uint32_t vx = vn[wa], vy = vn[wb];
-    const uint32_t km = __vmaxu2(finite_magnitudes(kx), finite_magnitudes(ky));
-    const uint32_t vm = __vmaxu2(finite_magnitudes(vx), finite_magnitudes(vy));
-    const uint32_t ktop = __reduce_max_sync(kFullMask, max(km & 0xffffu, km >> 16));
-    const uint32_t vtop = __reduce_max_sync(kFullMask, max(vm & 0xffffu, vm >> 16));
-    const bool fresh = row == 0;
-    const float2 now = make_float2(e4m3_grow_scale(held.x, e4m3_scale_for(ktop), fresh),
-                                   e4m3_grow_scale(held.y, e4m3_scale_for(vtop), fresh));
-    uint8_t* const caches[2] = {reinterpret_cast<uint8_t*>(a.k_store) + static_cast<size_t>(y) * kHeadDim,
-                                reinterpret_cast<uint8_t*>(a.v_store) + static_cast<size_t>(y) * kHeadDim};
-    // byte 2w of a row, through the 128-byte swizzle
-    auto at = [&](int w) { return row * 128 + (((w >> 3) ^ (row & 7)) << 4) + 2 * (w & 7); };
-#pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-      const float old = kv ? held.y : held.x, s = kv ? now.y : now.x;
-      const float inv = __frcp_rn(s);
-      const uint16_t cx = e4m3x2_of(kv ? vx : kx, inv), cy = e4m3x2_of(kv ? vy : ky, inv);
-      unsigned char* tile = stage + kv * L::kTile;
-      const bool grown = !fresh && s != old;
-      if (grown) {
-        const float f = __fdiv_rn(old, s);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint4* w = reinterpret_cast<uint4*>(tile) + lane + 32 * i;
-          *w = e4m3x16_rescale(*w, f);
-        }
-        __syncwarp();
-      }
-      *reinterpret_cast<uint16_t*>(tile + at(wa)) = cx;
-      *reinterpret_cast<uint16_t*>(tile + at(wb)) = cy;
-      if (grown) {
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int c = lane + 32 * i, rr = c >> 3;   // 16-byte chunk c of the tile
-          reinterpret_cast<uint4*>(caches[kv])[rr * 8 + ((c & 7) ^ (rr & 7))] = reinterpret_cast<const uint4*>(tile)[c];
-        }
-      } else {
-        uint16_t* dst = reinterpret_cast<uint16_t*>(caches[kv] + row * kHeadDim);
-        dst[wa] = cx;
-        dst[wb] = cy;
-      }
-    }
-    if (lane == 0) a.kv_scale_store[y / kBlockSize] = now;
-    // These generic writes precede a later TMA write into the same stage.
-    fence_proxy_async_smem();
-    __syncwarp();
-    return now;
-  };
 
   uint32_t gx = 0;  // gather: this lane's XOR of the piece's tile words
   auto consume = [&](int st) {
@@ -543,34 +365,7 @@ decode_partition_kernel(const __grid_constant__ CUtensorMap tm_k,
         uint2 w[8];
 #pragma unroll
         for (int c = 0; c < 8; ++c) w[c] = qrow[4 * c + cq];
-        if (kBlock && kStep && (fl & kRope) && (a.interleaved || a.rotary_dim != kHeadDim)) {
-          // Another form: dims d .. d+3 (d = 16c + 4cq) rotate if d < R, within the word pair when
-          // interleaved, else with the dims R/2 away, read from the staged row.
-          const float* cs = reinterpret_cast<const float*>(stage + L::kCosSinOff);
-          const uint32_t* row = reinterpret_cast<const uint32_t*>(stage + L::kQOff + gq * 256);
-          const int R = a.rotary_dim, half = R / 2;
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const int d = 16 * c + 4 * cq;
-            if (d >= R) continue;
-            if (a.interleaved) {
-              rope_rotate_interleaved(w[c].x, w[c].y, *reinterpret_cast<const float2*>(cs + d / 2),
-                                      *reinterpret_cast<const float2*>(cs + half + d / 2));
-            } else {
-              const int i = d < half ? d : d - half;  // angle of the first dim
-              const int o = d < half ? d + half : i;  // its partner
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                uint32_t own = e ? w[c].y : w[c].x, other = row[o / 2 + e];
-                const float2 co = *reinterpret_cast<const float2*>(cs + i + 2 * e);
-                const float2 si = *reinterpret_cast<const float2*>(cs + half + i + 2 * e);
-                if (d < half) rope_rotate_pairs(own, other, co, si);
-                else rope_rotate_pairs(other, own, co, si);
-                (e ? w[c].y : w[c].x) = own;
-              }
-            }
-          }
-        } else if (kStep && (fl & kRope)) {
+        if (kStep && (fl & kRope)) {
           const float* cs = reinterpret_cast<const float*>(stage + L::kCosSinOff);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -586,13 +381,9 @@ decode_partition_kernel(const __grid_constant__ CUtensorMap tm_k,
           qb[c][0] = gq < G ? bf16x2_to_f16x2(w[c].x) : 0u;
           qb[c][1] = gq < G ? bf16x2_to_f16x2(w[c].y) : 0u;
         }
-        if constexpr (kBlock) {
-          v_fold = 1.f;
-        } else {
-          const int g = d.x % Hkv;
-          k_fold = a.scale_log2 * a.k_scale[g];
-          v_fold = a.v_scale[g];
-        }
+        const int g = d.x % Hkv;
+        k_fold = a.scale_log2 * a.k_scale[g];
+        v_fold = a.v_scale[g];
       } else {
         // q rows sit unswizzled at 256-byte stride; rows >= G are not real heads.
         const uint32_t qt = kt + L::kQOff + static_cast<uint32_t>(r * 256);
@@ -627,11 +418,7 @@ decode_partition_kernel(const __grid_constant__ CUtensorMap tm_k,
     }
     if (fl & kHasData) {
       const int valid = static_cast<int>((fl >> 8) & 0xffu);
-      float2 bs = make_float2(1.f, 1.f);  // kBlock: the tile's K and V scales
-      if constexpr (kBlock) bs = scales[st];
-      if (kBlock && kStep && (fl & kNew) && (fl & kRope)) {
-        bs = store_new_block(stage, bs, valid - 1, d.w);
-      } else if (kStep && (fl & kNew) && (fl & kRope)) {
+      if (kStep && (fl & kNew) && (fl & kRope)) {
         // The new token (row valid - 1 of this tile): rotate its k, write k and v into the
         // staged tiles before they are read, and store both into the cache slot.
         const int row = valid - 1;
@@ -702,14 +489,8 @@ decode_partition_kernel(const __grid_constant__ CUtensorMap tm_k,
           // two accumulator chains, as for bf16: the MMAs issue in program order
           mma_f16_16816(sc2, lo0, lo1, hi0, hi1, qb[2 * c2 + 1][0], qb[2 * c2 + 1][1]);
         }
-        if constexpr (kBlock) {
-          const float fold_b = a.scale_log2 * bs.x, lift = log2_of(bs.y);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sc[i] = fmaf(sc[i] + sc2[i], fold_b, lift);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sc[i] = (sc[i] + sc2[i]) * k_fold;
-        }
+        for (int i = 0; i < 4; ++i) sc[i] = (sc[i] + sc2[i]) * k_fold;
       } else {
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) {
@@ -740,12 +521,9 @@ decode_partition_kernel(const __grid_constant__ CUtensorMap tm_k,
       }
       // Shifts m0, m1 in the log2 domain: a head's shift moves to its maximum only when that
       // passes it by more than 8, so P stays at most 2^8 and O is rescaled far less often.
-      const float top0 = bm0 * fold, top1 = bm1 * fold;
-      // Block scales: P is held 2^7 higher (at most 2^15 in f16), so that tokens far below the
-      // largest contribution stay normal f16 values.
-      constexpr float kLag = kBlock ? 15.f : 8.f, kRaise = kBlock ? 7.f : 0.f;
-      const float mn0 = top0 > m0 + kLag ? top0 - kRaise : m0;
-      const float mn1 = top1 > m1 + kLag ? top1 - kRaise : m1;
+      const float bs0 = bm0 * fold, bs1 = bm1 * fold;
+      const float mn0 = bs0 > m0 + 8.f ? bs0 : m0;
+      const float mn1 = bs1 > m1 + 8.f ? bs1 : m1;
       const float al0 = ex2_ftz(m0 - mn0);
       const float al1 = ex2_ftz(m1 - mn1);
       m0 = mn0;
@@ -758,14 +536,8 @@ decode_partition_kernel(const __grid_constant__ CUtensorMap tm_k,
       if constexpr (kFp8) {
         p_lo = pack_f16x2(e0, e1);
         p_hi = pack_f16x2(e2, e3);
-        if constexpr (kBlock) {
-          const float iv = __frcp_rn(bs.y);
-          l0 = fmaf(l0, al0, (e0 + e2) * iv);
-          l1 = fmaf(l1, al1, (e1 + e3) * iv);
-        } else {
-          l0 = fmaf(l0, al0, f16lo(p_lo) + f16lo(p_hi));
-          l1 = fmaf(l1, al1, f16hi(p_lo) + f16hi(p_hi));
-        }
+        l0 = fmaf(l0, al0, f16lo(p_lo) + f16lo(p_hi));
+        l1 = fmaf(l1, al1, f16hi(p_lo) + f16hi(p_hi));
       } else {
         p_lo = pack_bf16x2(e0, e1);
         p_hi = pack_bf16x2(e2, e3);
@@ -838,9 +610,8 @@ decode_partition_kernel(const __grid_constant__ CUtensorMap tm_k,
         const bool h0 = 2 * cq < G;
         const bool h1 = 2 * cq + 1 < G;
         if (fl & kWhole) {
-          // kBlock: a sequence whose every block is out of range has L = 0 and gives zeros
-          const float i0 = kBlock && L0 == 0.f ? 0.f : v_fold / L0;
-          const float i1 = kBlock && L1 == 0.f ? 0.f : v_fold / L1;
+          const float i0 = v_fold / L0;
+          const float i1 = v_fold / L1;
           uint32_t* orow0 = reinterpret_cast<uint32_t*>(a.out + (head0 + 2 * cq) * kHeadDim);
           uint32_t* orow1 = orow0 + kHeadDim / 2;
 #pragma unroll
@@ -1099,6 +870,7 @@ decode_merge_kernel(const DecodeArgs a) {
     }
     *orow = __float2bfloat16_rn(a.kv_scale && Lt == 0.f ? 0.f : At / Lt);
   } else {
+    // block-scaled caches: a sequence whose every block is out of range gives zeros
     *orow = __float2bfloat16_rn(a.kv_scale && L == 0.f ? 0.f : acc / L);
   }
 }
@@ -1122,7 +894,7 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 // Persistent grid size for this device: SMs x resident CTAs per SM, capped so that the grid
 // has at most kMaxDecodeWarps warps (looked up once per device and kernel variant, at the
 // largest shared-memory footprint the kernel can ask for).
-template <bool kStep, bool kFp8, bool kBlock = false>
+template <bool kStep, bool kFp8>
 cudaError_t persistent_ctas(int* ctas) {
   static std::mutex mu;
   static int cached[64] = {};
@@ -1132,16 +904,15 @@ cudaError_t persistent_ctas(int* ctas) {
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   std::lock_guard<std::mutex> lock(mu);
   if (!cached[dev]) {
-    using L = Layout<kStep, kFp8, kBlock>;
-    const int smem = L::smem(kMaxDecodeSeqs);
-    auto kernel = decode_partition_kernel<kStep, kFp8, false, false, kBlock>;
+    const int smem = Layout<kStep, kFp8>::smem(kMaxDecodeSeqs);
+    auto kernel = decode_partition_kernel<kStep, kFp8>;
     err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess) return err;
     // the early-metadata variant and (unfused) the gather run the same kernel shape
-    err = cudaFuncSetAttribute(decode_partition_kernel<kStep, kFp8, false, true, kBlock>,
+    err = cudaFuncSetAttribute(decode_partition_kernel<kStep, kFp8, false, true>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess) return err;
-    if constexpr (!kStep && !kBlock) {
+    if (!kStep) {
       err = cudaFuncSetAttribute(decode_partition_kernel<false, kFp8, true>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
       if (err != cudaSuccess) return err;
@@ -1149,39 +920,38 @@ cudaError_t persistent_ctas(int* ctas) {
     int sms = 0, per_sm = 0;
     err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (err != cudaSuccess) return err;
-    err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, L::kWarpsN * 32, smem);
+    err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, Layout<kStep, kFp8>::kWarpsN * 32, smem);
     if (err != cudaSuccess) return err;
     if (per_sm < 1) return cudaErrorInvalidConfiguration;
-    cached[dev] = min(sms * per_sm, kMaxDecodeWarps / L::kWarpsN);
+    cached[dev] = min(sms * per_sm, kMaxDecodeWarps / Layout<kStep, kFp8>::kWarpsN);
   }
   *ctas = cached[dev];
   return cudaSuccess;
 }
 
-template <bool kStep, bool kFp8, bool kGather = false, bool kBlock = false>
+template <bool kStep, bool kFp8, bool kGather = false>
 cudaError_t launch_partition(DecodeArgs& a, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                              const cudaLaunchAttribute* attr, cudaStream_t stream) {
   int max_ctas = 0;
-  cudaError_t err = persistent_ctas<kStep, kFp8, kBlock>(&max_ctas);
+  cudaError_t err = persistent_ctas<kStep, kFp8>(&max_ctas);
   if (err != cudaSuccess) return err;
   // No more CTAs than there can be ranges (ranges are dealt to the CTAs one at a time).
   const long long jobs_bound = static_cast<long long>(a.num_seqs) * a.num_kv_heads *
                                ((a.max_context_len + kBlockSize - 1) / kBlockSize);
   const long long want = (jobs_bound + kMinRangeBlocks - 1) / kMinRangeBlocks;
   const long long ctas = min(static_cast<long long>(max_ctas), want);
-  using L = Layout<kStep, kFp8, kBlock>;
-  constexpr int kWarpsN = L::kWarpsN;
+  constexpr int kWarpsN = Layout<kStep, kFp8>::kWarpsN;
   a.num_warps = static_cast<int>(ctas) * kWarpsN;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(kWarpsN * 32);
-  cfg.dynamicSmemBytes = L::smem(a.num_seqs);
+  cfg.dynamicSmemBytes = Layout<kStep, kFp8>::smem(a.num_seqs);
   cfg.stream = stream;
   cfg.attrs = const_cast<cudaLaunchAttribute*>(attr);
   cfg.numAttrs = 1;
-  auto kernel = decode_partition_kernel<kStep, kFp8, kGather, false, kBlock>;
+  auto kernel = decode_partition_kernel<kStep, kFp8, kGather>;
   if constexpr (!kGather)
-    if (a.early_metadata) kernel = decode_partition_kernel<kStep, kFp8, false, true, kBlock>;
+    if (a.early_metadata) kernel = decode_partition_kernel<kStep, kFp8, false, true>;
   return cudaLaunchKernelEx(&cfg, kernel, tm_k, tm_v, a);
 }
 
@@ -1260,36 +1030,14 @@ cudaError_t launch_gather(const DecodeArgs& args, bool fp8, cudaStream_t stream)
              : launch_partition<false, false, true>(a, tm_k, tm_v, attr, stream);
 }
 
-cudaError_t launch_decode(const DecodeArgs& args, cudaStream_t stream) {
-  DecodeArgs a = args;
-  const int G = a.num_q_heads / a.num_kv_heads;
-  if (G < 1 || G > 8 || a.num_seqs > kMaxDecodeSeqs) return cudaErrorInvalidValue;
-  const bool step = a.k_new != nullptr;
-  const bool block = a.kv_scale != nullptr;
-  const bool fp8 = a.k_scale != nullptr || block;
-  const long long rows = static_cast<long long>(a.num_blocks) * a.num_kv_heads * kBlockSize;
-  CUtensorMap tm_k, tm_v;
-  if (!cache_tensor_map(a.k_cache, rows, fp8, &tm_k) || !cache_tensor_map(a.v_cache, rows, fp8, &tm_v))
-    return cudaErrorInvalidValue;
+cudaError_t launch_decode_merge(const DecodeArgs& a, int part_ctas, int per_cta, cudaStream_t stream) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaError_t err;
-  if (block) err = step ? launch_partition<true, true, false, true>(a, tm_k, tm_v, attr, stream)
-                        : launch_partition<false, true, false, true>(a, tm_k, tm_v, attr, stream);
-  else if (fp8) err = step ? launch_partition<true, true>(a, tm_k, tm_v, attr, stream)
-                      : launch_partition<false, true>(a, tm_k, tm_v, attr, stream);
-  else err = step ? launch_partition<true, false>(a, tm_k, tm_v, attr, stream)
-                  : launch_partition<false, false>(a, tm_k, tm_v, attr, stream);
-  if (err != cudaSuccess) return err;
-
   // Narrow merge beside the partition kernel; the wide one when the (sequence, query head)
   // pairs are fewer than the partition kernel's CTAs, so that long segments' many pieces are
   // spread over more warps.
   const long long pairs = static_cast<long long>(a.num_seqs) * a.num_q_heads;
-  int part_ctas = 0;
-  err = fp8 ? persistent_ctas<false, true>(&part_ctas) : persistent_ctas<false, false>(&part_ctas);
-  if (err != cudaSuccess) return err;
   cudaLaunchConfig_t mcfg = {};
   mcfg.stream = stream;
   mcfg.attrs = attr;
@@ -1300,10 +1048,36 @@ cudaError_t launch_decode(const DecodeArgs& args, cudaStream_t stream) {
     return cudaLaunchKernelEx(&mcfg, decode_merge_kernel<kWideGroups>, a);
   }
   const long long merge_warps = pairs * kMergeSplit;
-  const int per_cta = fp8 ? kMergeWarps / 2 : kMergeWarps;
   mcfg.gridDim = dim3(static_cast<unsigned>((merge_warps + per_cta - 1) / per_cta));
   mcfg.blockDim = dim3(per_cta * 32);
   return cudaLaunchKernelEx(&mcfg, decode_merge_kernel<1>, a);
+}
+
+cudaError_t launch_decode(const DecodeArgs& args, cudaStream_t stream) {
+  DecodeArgs a = args;
+  const int G = a.num_q_heads / a.num_kv_heads;
+  if (G < 1 || G > 8 || a.num_seqs > kMaxDecodeSeqs) return cudaErrorInvalidValue;
+  const bool step = a.k_new != nullptr;
+  if (a.kv_scale) return launch_decode_block(a, stream);
+  const bool fp8 = a.k_scale != nullptr;
+  const long long rows = static_cast<long long>(a.num_blocks) * a.num_kv_heads * kBlockSize;
+  CUtensorMap tm_k, tm_v;
+  if (!cache_tensor_map(a.k_cache, rows, fp8, &tm_k) || !cache_tensor_map(a.v_cache, rows, fp8, &tm_v))
+    return cudaErrorInvalidValue;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaError_t err;
+  if (fp8) err = step ? launch_partition<true, true>(a, tm_k, tm_v, attr, stream)
+                      : launch_partition<false, true>(a, tm_k, tm_v, attr, stream);
+  else err = step ? launch_partition<true, false>(a, tm_k, tm_v, attr, stream)
+                  : launch_partition<false, false>(a, tm_k, tm_v, attr, stream);
+  if (err != cudaSuccess) return err;
+
+  int part_ctas = 0;
+  err = fp8 ? persistent_ctas<false, true>(&part_ctas) : persistent_ctas<false, false>(&part_ctas);
+  if (err != cudaSuccess) return err;
+  return launch_decode_merge(a, part_ctas, fp8 ? kMergeWarps / 2 : kMergeWarps, stream);
 }
 
 }  // namespace pa
