@@ -495,6 +495,28 @@ __device__ __forceinline__ uint4 e4m3x16_rescale(uint4 w, float f) {
   return make_uint4(e4m3x4_rescale(w.x, f), e4m3x4_rescale(w.y, f), e4m3x4_rescale(w.z, f), e4m3x4_rescale(w.w, f));
 }
 
+// ---- thread-block clusters -----------------------------------------------------------------
+// Barrier of every thread of the cluster; orders their shared-memory writes.
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();  // the aligned forms want the whole warp at once
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address of CTA `rank`'s copy of a shared-memory location of this CTA.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t smem, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_cluster_f4(uint32_t addr, float4 v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+               : "memory");
+}
+
 // Barrier of `threads` threads of the block (named barrier `id`, 1..15).
 __device__ __forceinline__ void named_barrier(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");

@@ -42,6 +42,13 @@
 // thread its own row of q and out to load and store kept that path 88% busy (ncu, 4 x 2048
 // tokens: LSU 68.6% of its wavefronts, tensor core 19.6%) with the tensor pipe 26% active, 87 us.
 
+// Few tiles over a long context: a tile's stages are split over a cluster of 2, 4 or 8 CTAs
+// (template kSplit; CTA r of C takes stages nst r / C .. nst (r + 1) / C).  The CTAs exchange each
+// row's (m, L) through distributed shared memory, scale their O to the common shift, and CTA r
+// collects dims 128 r / C .. of every row from all of them, in rank order: no workspace, one launch,
+// the same sums whatever the timing.  (11 sequences of one new token after 10,812 cached, 28 / 4 heads:
+// 142.8 us unsplit.)
+
 #include <mutex>
 
 #include <cuda.h>
@@ -69,26 +76,32 @@ constexpr int kBpHeader = 256;
 constexpr int kBpFoldOff = kBpHdrOff + kBpHeader;    // a float per row
 constexpr int kBpScaleOff = kBpFoldOff + kBpRows * 4;   // a float4 per block of the stage, stage j in slot j % 8
 constexpr int kBpScaleSlots = 8;
-constexpr int kBpSmem = kBpScaleOff + kBpScaleSlots * kBpKB * 16 + 1024;  // + alignment of the first stage
+constexpr int kBpMlOff = kBpScaleOff + kBpScaleSlots * kBpKB * 16;   // split: a row's (m, L)
+constexpr int kBpSmem = kBpMlOff + kBpRows * 8 + 1024;
+static_assert(kBpRows * kHeadDim * 4 <= kBpHdrOff, "the partial rows of a split tile fit the stages");  // + alignment of the first stage
 static_assert(2 * (kBpSmem + 1024) <= 228 * 1024, "two CTAs per SM");
 constexpr int kBpThreads = 384;
 // registers per thread at launch, and the split (their sums per warpgroup are equal)
 constexpr int kBpRegsSoftmax = 136, kBpRegsIssue = 48, kBpRegsConvert = 56;
 static_assert(kBpRegsSoftmax + kBpRegsIssue + kBpRegsConvert <= 3 * 80, "of the 80 a thread launched with");
+// A tile's keys are split over 2, 4 or 8 CTAs as long as there are at most kSplitCtas CTAs (two per SM) and
+// at least kMinSplitStages stages for each; not below kSplitFrom stages (the exchange costs what some five
+// stages do).
+constexpr int kSplitCtas = 304, kMinSplitStages = 3, kSplitFrom = 10;
 constexpr uint32_t kBpTmemCols = 256, kBpSCols = 64, kBpOCol = 128;   // S (and P) at 0 and 64
 
-// header (byte offsets)
-constexpr int kKFull = 0;          // [3] K TMA -> MMA (S)
-constexpr int kKFree = 24;         // [3] MMA (S done) -> K TMA
-constexpr int kCFull = 48;         // [2] V TMA -> converters
-constexpr int kCFree = 64;         // [2] converters (a warp each: 4) -> V TMA
-constexpr int kVFull = 80;         // [2] converters (4) -> MMA (P V)
-constexpr int kVFree = 104;        // [2] MMA (P V done) -> converters, softmax (O, when it rescales)
-constexpr int kSFull = 120;        // [2] MMA (S done) -> softmax
-constexpr int kPFull = 136;        // [2] softmax (a warp each: 4) -> MMA
-constexpr int kDone = 152;         // MMA: its last MMAs finished
-constexpr int kQReady = 160;       // softmax (128) -> MMA
-constexpr int kTmemAt = 168;
+// header (byte offsets): mbarriers, one per ring slot, then the TMEM address
+constexpr int kKFull = 0;                            // K TMA -> MMA (S)
+constexpr int kKFree = kKFull + 8 * kBpKRing;        // MMA (S done) -> K TMA
+constexpr int kCFull = kKFree + 8 * kBpKRing;        // V TMA -> converters
+constexpr int kCFree = kCFull + 8 * kBpCRing;        // converters (a warp each: 4) -> V TMA
+constexpr int kVFull = kCFree + 8 * kBpCRing;        // converters (4) -> MMA (P V)
+constexpr int kVFree = kVFull + 8 * kBpVRing;        // MMA (P V done) -> converters, softmax (O, when it rescales)
+constexpr int kSFull = kVFree + 8 * kBpVRing;        // [2] MMA (S done) -> softmax
+constexpr int kPFull = kSFull + 16;                  // [2] softmax (a warp each: 4) -> MMA
+constexpr int kDone = kPFull + 16;                   // MMA: its last MMAs finished
+constexpr int kQReady = kDone + 8;                   // softmax (128) -> MMA
+constexpr int kTmemAt = kQReady + 8;
 static_assert(kTmemAt + 4 <= kBpHeader, "header");
 
 // Four bf16 values times `raise` (a power of two) as the sum of two E4M3 values each: the codes of
@@ -102,6 +115,7 @@ __device__ __forceinline__ void split_e4m3(uint32_t w0, uint32_t w1, float raise
        (static_cast<uint32_t>(e4m3x2_of_floats(x2 - f16lo(b1), x3 - f16hi(b1))) << 16);
 }
 
+template <bool kSplit>
 __global__ void __launch_bounds__(kBpThreads, 2)
 prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const PrefillArgs a) {
@@ -111,11 +125,15 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
   const int Hkv = a.num_kv_heads;
   const int G = a.num_q_heads / Hkv;
   const int Tq = kBpRows / G;
-  // linear order of the CTAs: the same query tile of every (sequence, KV head), latest tile first
-  const unsigned long long pairs = gridDim.y;
-  const unsigned long long lin = static_cast<unsigned long long>(blockIdx.y) * gridDim.x + blockIdx.x;
+  // Linear order of the CTAs (clusters, split): the same query tile of every (sequence, KV head), latest
+  // tile first.
+  const int rank = kSplit ? static_cast<int>(blockIdx.x) : 0;
+  const int ranks = kSplit ? static_cast<int>(gridDim.x) : 1;      // 2, 4 or 8
+  const int log_ranks = 31 - __clz(ranks);
+  const unsigned long long pairs = kSplit ? gridDim.z : gridDim.y, tiles = kSplit ? gridDim.y : gridDim.x;
+  const unsigned long long lin = kSplit ? blockIdx.z * tiles + blockIdx.y : blockIdx.y * tiles + blockIdx.x;
   const int sg = static_cast<int>(lin % pairs);
-  const int tile = static_cast<int>(gridDim.x) - 1 - static_cast<int>(lin / pairs);
+  const int tile = static_cast<int>(tiles) - 1 - static_cast<int>(lin / pairs);
   const int s = sg / Hkv;
   const int g = sg - s * Hkv;
   pdl_wait_prior_grid();
@@ -132,8 +150,14 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
   if (i0 >= n) return;
   const int rows_q = min(Tq, n - i0);
   const int pos0 = ctx - n + i0;
-  const int nblocks = (pos0 + rows_q - 1) / kBlockSize + 1;
-  const int nst = (nblocks + kBpKB - 1) / kBpKB;
+  const int nblocks_all = (pos0 + rows_q - 1) / kBlockSize + 1;
+  const int nst_all = (nblocks_all + kBpKB - 1) / kBpKB;
+  // This CTA's stages j0 .. j0 + nst - 1 and its blocks, numbered from its first.
+  auto first_stage = [&](int k) { return (nst_all * k) >> log_ranks; };   // nst_all < 2^26
+  const int j0 = kSplit ? first_stage(rank) : 0;
+  const int nst = kSplit ? first_stage(rank + 1) - j0 : nst_all;
+  const int block0 = kBpKB * j0;
+  const int nblocks = min(kBpKB * nst, nblocks_all - block0);
 
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t stages = (raw + 1023u) & ~1023u;
@@ -142,7 +166,7 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
   unsigned char* const hdr_gen = smem_raw + (hdr - raw);
 
   // Lane k holds the id of block 32 w + k of the current window w, and the next window's.
-  const int32_t* bt_row = a.block_tables + static_cast<size_t>(s) * a.max_blocks;
+  const int32_t* bt_row = a.block_tables + static_cast<size_t>(s) * a.max_blocks + block0;
   auto load_id = [&](int w) { const int b = 32 * w + lane; return b < nblocks ? bt_row[b] : -1; };
   auto in_pool = [&](int id) { return id >= 0 && id < a.num_blocks; };
   int ids = load_id(0), ids_next = load_id(1);
@@ -160,15 +184,19 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     return static_cast<int>(__ballot_sync(kFullMask, in_pool(id)) & ((1u << kBpKB) - 1));
   };
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 3; ++i) {
+    for (int i = 0; i < kBpKRing; ++i) {
       mbar_init(hdr + kKFull + 8 * i, 1);
       mbar_init(hdr + kKFree + 8 * i, 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(hdr + kVFull + 8 * i, 4);
-      mbar_init(hdr + kVFree + 8 * i, 1);
+    for (int i = 0; i < kBpCRing; ++i) {
       mbar_init(hdr + kCFull + 8 * i, 1);
       mbar_init(hdr + kCFree + 8 * i, 4);
+    }
+    for (int i = 0; i < kBpVRing; ++i) {
+      mbar_init(hdr + kVFull + 8 * i, 4);
+      mbar_init(hdr + kVFree + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(hdr + kPFull + 8 * i, 4);
       mbar_init(hdr + kSFull + 8 * i, 1);
     }
@@ -193,7 +221,7 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     const int r8 = t >> 3;                          // row 0..15 of a block
     const int half = c >> 2;
     const int valid_last = ctx - kBlockSize * ((ctx - 1) / kBlockSize);
-    const int last_blk = (ctx - 1) / kBlockSize;
+    const int last_blk = (ctx - 1) / kBlockSize - block0;
     // the two f16 chunks of the 16 dims, in an order that keeps eight lanes' stores on distinct banks
     const int f0 = 2 * (c & 3) + half, f1 = 2 * (c & 3) + 1 - half;
     const uint32_t in_off = static_cast<uint32_t>(r8 * 128 + ((c ^ (r8 & 7)) << 4));
@@ -243,6 +271,11 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       }
     }
     if (failed) raise_flag(a.status, PA_FLAG_TIMEOUT);
+    if constexpr (kSplit) {
+      __syncwarp();
+      cluster_sync();
+      cluster_sync();
+    }
   } else if (warp >= 4) {
     regs_dec<kBpRegsIssue>();
     if (warp == 4 || warp == 6) {
@@ -342,7 +375,7 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       bool failed = !wait_all(hdr + kQReady, 0);
       if (!failed) {
         tc_fence_after();
-        failed = !issue_s(0) || (nst > 1 && !issue_s(1));
+        failed = (nst > 0 && !issue_s(0)) || (nst > 1 && !issue_s(1));
       }
       for (int j = 0; j < nst && !failed; ++j) {
         const int st = j % kBpVRing;
@@ -366,8 +399,13 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         umma_commit(hdr + kDone);
         mbar_wait_parked(hdr + kDone, 0);
       }
-      __syncwarp();
     }
+    if constexpr (kSplit) {
+      __syncwarp();
+      cluster_sync();
+      cluster_sync();
+    }
+    __syncwarp();
   } else {
     // ---- q into shared memory, then the softmax: thread = row r of the tile ---------------------
     regs_inc<kBpRegsSoftmax>();
@@ -468,8 +506,8 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         all_there = all_there && there[b];
       }
       // causal mask and absent blocks -> -inf, only on a stage that needs it
-      if (!all_there || kBpKeys * (j + 1) - 1 > pos0) {
-        const int lim = p_r - kBpKeys * j;
+      if (!all_there || kBpKeys * (j0 + j + 1) - 1 > pos0) {
+        const int lim = p_r - kBpKeys * (j0 + j);
 #pragma unroll
         for (int c = 0; c < kBpKeys; ++c)
           if (!there[c / kBlockSize] || c > lim) sc[c] = -INFINITY;
@@ -533,7 +571,52 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     // A warp that gave up still takes part in the barriers below (its rows' values are undefined).
     const bool ok = !failed && __all_sync(kFullMask, mbar_wait_parked(hdr + kDone, 0));
     if (!ok && lane == 0) raise_flag(a.status, PA_FLAG_TIMEOUT);
-    {
+    if constexpr (kSplit) {
+      // Every MMA of this CTA is done, so its stages are free; the others' partial rows come there.
+      reinterpret_cast<float2*>(base + kBpMlOff)[r] = make_float2(m, l);
+      tc_fence_before();
+      cluster_sync();
+      tc_fence_after();
+      float top = m, total = 0.f;
+      float2 ml[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        ml[k] = k < ranks ? ld_cluster_f2(cluster_addr(stages + kBpMlOff + 8 * r, k)) : make_float2(-INFINITY, 0.f);
+        top = fmaxf(top, ml[k].x);
+      }
+      const float sh = top == -INFINITY ? 0.f : top;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) total = fmaf(ml[k].y, ml[k].x == -INFINITY ? 0.f : ex2_ftz(ml[k].x - sh), total);
+      const float mine = m == -INFINITY ? 0.f : ex2_ftz(m - sh);
+      const int dims = kHeadDim >> log_ranks;       // of a CTA: 64, 32 or 16
+      // Partial rows: [source CTA][row][dims] floats; 16-byte chunk c of a row at c ^ turn, so that the
+      // eight rows of a store or load instruction's phase lie on distinct banks.
+      const int turn = ranks == 8 ? (r >> 1) & 3 : r & 7;
+      const int xi = r / G;
+      // warps without a query's row, and CTAs without stages, have nothing to send
+#pragma unroll 1
+      for (int q4 = nst > 0 && __any_sync(kFullMask, xi < rows_q) ? 0 : 4; q4 < 4; ++q4) {   // 32 dims of O at a time
+        uint32_t ov[32];
+        if (ok) {
+          tmem_ld32(trow + kBpOCol + 32 * q4, ov);
+          tmem_wait_ld();
+        }
+#pragma unroll
+        for (int c = 0; c < 32; c += 4) {
+          const int dim = 32 * q4 + c, to = dim >> (7 - log_ranks);
+          const bool any = m != -INFINITY;          // a row without keys in this CTA's stages has nothing in O
+          float4 v;
+          v.x = any ? __uint_as_float(ov[c]) * mine : 0.f;
+          v.y = any ? __uint_as_float(ov[c + 1]) * mine : 0.f;
+          v.z = any ? __uint_as_float(ov[c + 2]) * mine : 0.f;
+          v.w = any ? __uint_as_float(ov[c + 3]) * mine : 0.f;
+          const int at = (rank * kBpRows + r) * dims * 4 + ((((dim - to * dims) >> 2) ^ turn) << 4);
+          if (xi < rows_q) st_cluster_f4(cluster_addr(stages + at, to), v);
+        }
+      }
+      folds[r] = total == 0.f ? 0.f : 1.f / total;  // read by the CTA's threads after the barrier
+      cluster_sync();
+    } else {
       tc_fence_after();
       // a row whose every key was skipped has l = 0: zeros
       const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -568,6 +651,27 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       }
     }
   }
+  if constexpr (kSplit) {
+    // This CTA's dims of every row: the sum over the CTAs that had stages, in rank order.
+    const int dims = kHeadDim >> log_ranks, log_chunks = 5 - log_ranks, rows = rows_q * G;
+    for (int u = threadIdx.x; u < rows << log_chunks; u += kBpThreads) {
+      const int x = u >> log_chunks, c = u - (x << log_chunks), xi = x / G;
+      const int turn = ranks == 8 ? (x >> 1) & 3 : x & 7;
+      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k = 0; k < ranks; ++k) {
+        if (first_stage(k + 1) == first_stage(k)) continue;
+        const float4 v = *reinterpret_cast<const float4*>(base + (k * kBpRows + x) * dims * 4 + ((c ^ turn) << 4));
+        sum.x += v.x;
+        sum.y += v.y;
+        sum.z += v.z;
+        sum.w += v.w;
+      }
+      const float inv = reinterpret_cast<const float*>(base + kBpFoldOff)[x];
+      *reinterpret_cast<uint2*>(a.out + (static_cast<size_t>(q0 + i0 + xi) * a.num_q_heads + g * G + (x - xi * G)) * kHeadDim +
+                                rank * dims + 4 * c) =
+          make_uint2(pack_bf16x2(sum.x * inv, sum.y * inv), pack_bf16x2(sum.z * inv, sum.w * inv));
+    }
+  }
   tc_fence_before();
   __syncthreads();
   if (warp == 0) {
@@ -595,26 +699,42 @@ cudaError_t launch_prefill_block(const PrefillArgs& a, cudaStream_t stream) {
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     std::lock_guard<std::mutex> lock(mu);
     if (!done[dev]) {
-      err = cudaFuncSetAttribute(prefill_block_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBpSmem);
-      if (err != cudaSuccess) return err;
-      err = cudaFuncSetAttribute(prefill_block_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                 cudaSharedmemCarveoutMaxShared);
+      auto opt_in = [&](auto kernel) {
+        if (err == cudaSuccess)
+          err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBpSmem);
+        if (err == cudaSuccess)
+          err = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                     cudaSharedmemCarveoutMaxShared);
+      };
+      opt_in(prefill_block_kernel<false>);
+      opt_in(prefill_block_kernel<true>);
       if (err != cudaSuccess) return err;
       done[dev] = true;
     }
   }
-  cudaLaunchAttribute attr[1];
+  // Split the keys while the grid leaves SMs without a CTA and each part keeps kMinSplitStages stages.
+  const long long tiles = (a.max_query_len + Tq - 1) / Tq;
+  const long long pairs = static_cast<long long>(a.num_seqs) * a.num_kv_heads;
+  const int stages = (a.max_context_len + kBpKeys - 1) / kBpKeys;
+  int ranks = 1;
+  while (ranks < 8 && stages >= kSplitFrom && tiles * pairs * ranks * 2 <= kSplitCtas && stages >= 2 * ranks * kMinSplitStages) ranks *= 2;
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(ranks);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((a.max_query_len + Tq - 1) / Tq),
-                     static_cast<unsigned>(a.num_seqs * a.num_kv_heads));
+  cfg.gridDim = ranks > 1 ? dim3(static_cast<unsigned>(ranks), static_cast<unsigned>(tiles), static_cast<unsigned>(pairs))
+                          : dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(pairs));
   cfg.blockDim = dim3(static_cast<unsigned>(kBpThreads));
   cfg.dynamicSmemBytes = kBpSmem;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, prefill_block_kernel, tm_k, tm_v, a);
+  cfg.numAttrs = ranks > 1 ? 2 : 1;
+  return ranks > 1 ? cudaLaunchKernelEx(&cfg, prefill_block_kernel<true>, tm_k, tm_v, a)
+                   : cudaLaunchKernelEx(&cfg, prefill_block_kernel<false>, tm_k, tm_v, a);
 }
 
 }  // namespace pa

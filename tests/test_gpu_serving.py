@@ -485,6 +485,19 @@ def test_prefill_long(pa, lens, new):
     check_prefill(pa, np.random.default_rng(len(lens)), lens, new, 12, 2)
 
 
+@pytest.mark.parametrize("lens,new,hq,kv", [
+    ([10812, 9000, 1, 4097], [1, 1, 1, 1], 28, 4), ([2000], [1], 8, 8), ([700, 130, 64, 900], [20, 130, 3, 40], 5, 1),
+    ([5000], [64], 12, 2), ([1537, 1536, 1535], [16, 17, 15], 64, 8), ([20000, 17], [5, 17], 2, 1)])
+def test_prefill_split_over_the_keys(pa, lens, new, hq, kv):
+    """Few tiles over long contexts: a tile's keys are shared out over a cluster; sequences much
+    shorter than the longest leave most of its CTAs without keys."""
+    pool, out = check_prefill(pa, np.random.default_rng(sum(lens)), lens, new, hq, kv)
+    q = bf16(normal(np.random.default_rng(1), sum(new), hq, D))
+    args = (q, up(np.concatenate([[0], np.cumsum(new)]).astype(np.int32)), *pool.dev(), up(pool.tables), up(pool.lens),
+            max(new), max(lens), D ** -0.5)
+    assert np.array_equal(bits(pa.prefill_fp8_block(*args)), bits(pa.prefill_fp8_block(*args)))
+
+
 def test_prefill_bound_larger_than_needed_and_scales_far_apart(pa):
     rng = np.random.default_rng(30)
     pool = Pool(rng, [200, 350], 2)
