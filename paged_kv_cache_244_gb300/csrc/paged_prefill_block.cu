@@ -104,15 +104,20 @@ constexpr int kQReady = kDone + 8;                   // softmax (128) -> MMA
 constexpr int kTmemAt = kQReady + 8;
 static_assert(kTmemAt + 4 <= kBpHeader, "header");
 
-// Four bf16 values times `raise` (a power of two) as the sum of two E4M3 values each: the codes of
-// the nearest, and of what it leaves.
+// Four bf16 values times `raise` (a power of two that keeps them below 256) as the sum of two E4M3
+// values each: the codes of the nearest, and of what it leaves.  f16 holds the 8 significant bits
+// of a value down to 2^-17, and the difference exactly.
 __device__ __forceinline__ void split_e4m3(uint32_t w0, uint32_t w1, float raise, uint32_t& hi, uint32_t& lo) {
-  const float x0 = bf16lo(w0) * raise, x1 = bf16hi(w0) * raise, x2 = bf16lo(w1) * raise, x3 = bf16hi(w1) * raise;
-  const uint16_t h0 = e4m3x2_of_floats(x0, x1), h1 = e4m3x2_of_floats(x2, x3);
-  const uint32_t b0 = e4m3x2_to_f16x2(h0), b1 = e4m3x2_to_f16x2(h1);
-  hi = h0 | (static_cast<uint32_t>(h1) << 16);
-  lo = e4m3x2_of_floats(x0 - f16lo(b0), x1 - f16hi(b0)) |
-       (static_cast<uint32_t>(e4m3x2_of_floats(x2 - f16lo(b1), x3 - f16hi(b1))) << 16);
+  uint16_t h[2], l[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t w = i ? w1 : w0;
+    const uint32_t x = pack_f16x2(bf16lo(w) * raise, bf16hi(w) * raise);
+    h[i] = e4m3x2_of_f16x2(x);
+    l[i] = e4m3x2_of_f16x2(sub_f16x2(x, e4m3x2_to_f16x2(h[i])));
+  }
+  hi = h[0] | (static_cast<uint32_t>(h[1]) << 16);
+  lo = l[0] | (static_cast<uint32_t>(l[1]) << 16);
 }
 
 template <bool kSplit>
@@ -125,6 +130,8 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
   const int Hkv = a.num_kv_heads;
   const int G = a.num_q_heads / Hkv;
   const int Tq = kBpRows / G;
+  const uint32_t per_g = 65536u / G + 1;              // x / G = x per_g >> 16 for x < 128, G <= 8
+  auto over_g = [&](int x) { return static_cast<int>((static_cast<uint32_t>(x) * per_g) >> 16); };
   // Linear order of the CTAs (clusters, split): the same query tile of every (sequence, KV head), latest
   // tile first.
   const int rank = kSplit ? static_cast<int>(blockIdx.x) : 0;
@@ -317,22 +324,22 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
           failed = true;
           break;
         }
+        // The boxes first: they may land before the arrival that announces them (the phase cannot
+        // complete without it), which for K waits for the blocks' scales.
         const uint32_t bar = full + 8 * st;
+        if (lane < kBpKB && ((mask >> lane) & 1))
+          tma_load_2d(slots + st * kBpCodes + lane * kBpTile, tm, 0, (blk * Hkv + g) * kBlockSize, bar);
         if (is_k) {
           const int b = lane - ((kBpKB * j) & 31);
           if (b >= 0 && b < kBpKB) scale_slots[(j % kBpScaleSlots) * kBpKB + b] = scales;
-          __syncwarp();
         }
+        __syncwarp();
         if (lane == 0) {
           if (mask) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(__popc(mask)) * kBpTile);
           else mbar_arrive(bar);
         }
-        __syncwarp();
         if (is_k && lane < kBpKB && kBpKB * j + lane < nblocks && !((mask >> lane) & 1))
           raise_flag(a.status, PA_FLAG_BLOCK_ID_OOB);
-        if (lane < kBpKB && ((mask >> lane) & 1)) {
-          tma_load_2d(slots + st * kBpCodes + lane * kBpTile, tm, 0, (blk * Hkv + g) * kBlockSize, bar);
-        }
         issued = j + 1;
         if (++st == ring) {
           st = 0;
@@ -410,14 +417,14 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     // ---- q into shared memory, then the softmax: thread = row r of the tile ---------------------
     regs_inc<kBpRegsSoftmax>();
     const int r = threadIdx.x;
-    const int p_r = pos0 + r / G;
+    const int p_r = pos0 + over_g(r);
     const uint32_t trow = tmem + (static_cast<uint32_t>(warp * 32) << 16);
     // q comes in and out leaves 8 lanes a row, so that global memory sees whole 128-byte lines; a
     // 16-byte chunk c of row x of a 128-byte-wide buffer sits at c ^ (x % 8).
     unsigned char* const qbuf = base + kBpQOff;
     const int hr = r >> 3, hc = r & 7;              // rows hr + 16 k, chunk hc of the half
     auto global_row = [&](int x) {                  // matrix row x of q and out, -1 past the queries
-      const int xi = x / G;
+      const int xi = over_g(x);
       return xi < rows_q ? (static_cast<long long>(q0 + i0 + xi) * a.num_q_heads + g * G + (x - xi * G)) * kHeadDim
                          : -1ll;
     };
@@ -592,7 +599,7 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       // Partial rows: [source CTA][row][dims] floats; 16-byte chunk c of a row at c ^ turn, so that the
       // eight rows of a store or load instruction's phase lie on distinct banks.
       const int turn = ranks == 8 ? (r >> 1) & 3 : r & 7;
-      const int xi = r / G;
+      const int xi = over_g(r);
       // warps without a query's row, and CTAs without stages, have nothing to send
 #pragma unroll 1
       for (int q4 = nst > 0 && __any_sync(kFullMask, xi < rows_q) ? 0 : 4; q4 < 4; ++q4) {   // 32 dims of O at a time
@@ -655,7 +662,7 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     // This CTA's dims of every row: the sum over the CTAs that had stages, in rank order.
     const int dims = kHeadDim >> log_ranks, log_chunks = 5 - log_ranks, rows = rows_q * G;
     for (int u = threadIdx.x; u < rows << log_chunks; u += kBpThreads) {
-      const int x = u >> log_chunks, c = u - (x << log_chunks), xi = x / G;
+      const int x = u >> log_chunks, c = u - (x << log_chunks), xi = over_g(x);
       const int turn = ranks == 8 ? (x >> 1) & 3 : x & 7;
       float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int k = 0; k < ranks; ++k) {
