@@ -658,13 +658,15 @@ def decode_fp8_block(q, k_cache, v_cache, kv_scale, block_tables, context_lens, 
         out = torch.empty_like(q)
         _kept(stream, out)
     S, nb, dims = _decode_shapes(q, k_cache, v_cache, kv_scale, block_tables, context_lens, out)
+    if S == 0:
+        return out
     if workspace is None:
         workspace = decode_workspace(q, k_cache, max_context_len, partition_tokens)
         _kept(stream, workspace)
     (qp, op, kc, vc, sc, bt, ctx, ws), dev = _ptrs(
         _DECODE, q, out, k_cache, v_cache, kv_scale, block_tables, context_lens, workspace)
     _check(lib().pa_decode_fp8_block(ctypes.byref(dims), S, qp, kc, vc, sc, nb, bt, block_tables.shape[1], ctx,
-                                     max_context_len, scale, partition_tokens, ws, workspace.numel() * 4, op,
+                                     int(max_context_len), float(scale), int(partition_tokens), ws, workspace.numel() * 4, op,
                                      _stream_of(stream, dev)),
            "pa_decode_fp8_block")
     return out
@@ -683,6 +685,8 @@ def decode_step_fp8_block(q, k, v, cos_sin, k_cache, v_cache, kv_scale, block_ta
     new = (S, k_cache.shape[1], q.shape[2])
     if k.shape != new or v.shape != new:
         raise ValueError("k / v shape mismatch")
+    if S == 0:
+        return out
     if workspace is None:
         workspace = decode_workspace(q, k_cache, max_context_len, partition_tokens)
         _kept(stream, workspace)
@@ -690,7 +694,7 @@ def decode_step_fp8_block(q, k, v, cos_sin, k_cache, v_cache, kv_scale, block_ta
         _STEP, q, out, k_cache, v_cache, kv_scale, block_tables, context_lens, workspace, k, v, cos_sin)
     _check(lib().pa_decode_step_fp8_block(
         ctypes.byref(dims), ctypes.byref(rope), S, qp, kp, vp, cs, cos_sin.shape[0], kc, vc, sc, nb, bt,
-        block_tables.shape[1], ctx, max_context_len, scale, partition_tokens, ws, workspace.numel() * 4, op,
+        block_tables.shape[1], ctx, int(max_context_len), float(scale), int(partition_tokens), ws, workspace.numel() * 4, op,
         PA_STEP_EARLY_METADATA if early_metadata else 0, _stream_of(stream, dev)), "pa_decode_step_fp8_block")
     return out
 
@@ -712,8 +716,8 @@ def prefill_fp8_block(q, q_start, k_cache, v_cache, kv_scale, block_tables, cont
     dims = pa_dims(Hq, Hkv, D, B)
     (qp, op, kc, vc, sc, bt, ctx, qs), dev = _ptrs(
         _PREFILL, q, out, k_cache, v_cache, kv_scale, block_tables, context_lens, q_start)
-    _check(lib().pa_prefill_fp8_block(ctypes.byref(dims), S, T, qp, qs, max_query_len, kc, vc, sc, nb, bt,
-                                      block_tables.shape[1], ctx, max_context_len, scale, op,
+    _check(lib().pa_prefill_fp8_block(ctypes.byref(dims), S, T, qp, qs, int(max_query_len), kc, vc, sc, nb, bt,
+                                      block_tables.shape[1], ctx, int(max_context_len), float(scale), op,
                                       _stream_of(stream, dev)), "pa_prefill_fp8_block")
     return out
 
@@ -766,7 +770,7 @@ def plan_step(cached_lens, new_lens, block_tables, free_blocks, num_free, num_bl
         _PLAN, cached_lens, new_lens, block_tables, free_blocks, num_free, num_free_out, ctx, qs, pos, slots,
         granted)
     _check(lib().pa_plan_step(ctypes.byref(_PLAN_DIMS), S, c, n, bt, block_tables.shape[1], fb,
-                              free_blocks.shape[0], nf, nfo, num_blocks, num_tokens, cx, q0, ps, sl, gr,
+                              free_blocks.shape[0], nf, nfo, int(num_blocks), int(num_tokens), cx, q0, ps, sl, gr,
                               _stream_of(stream, dev)), "pa_plan_step")
     return plan
 

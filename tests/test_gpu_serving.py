@@ -410,6 +410,96 @@ def test_decode_is_reproducible_and_leaves_other_streams_alone(pa):
     assert np.array_equal(bits(first), bits(second))
 
 
+def test_many_sequences(pa):
+    """The most sequences a call takes: their prefix leaves fewer stages, and so fewer warps, to a CTA."""
+    rng = np.random.default_rng(40)
+    S = 8192
+    lens = [int(x) for x in rng.integers(0, 40, S)]
+    pool = Pool(rng, lens, 1)
+    q = normal(rng, S, 8, D)
+    args = (*pool.dev(), up(pool.tables), up(pool.lens), 40, D ** -0.5)
+    out = pa.decode_fp8_block(bf16(q), *args)
+    for s in list(range(0, S, 401)) + [S - 1]:
+        ref, mag = pool.attention(s, q[s:s + 1], D ** -0.5)
+        close(out[s:s + 1], ref, mag, s)
+    assert not f64(out[torch.from_numpy(np.array(lens) == 0).cuda()]).any()
+    clean(pa)
+
+
+def test_a_cache_past_four_gigabytes(pa):
+    """Tiles and scales whose offsets do not fit 32 bits: the store, the decode and the prefill at the far end."""
+    rng = np.random.default_rng(41)
+    kv, nb = 8, 290_000                                   # 4.75 GB of codes each for K and V
+    kc, vc = (torch.empty((nb, kv, B, D), dtype=torch.uint8, device="cuda") for _ in range(2))
+    sc = torch.empty((nb, kv, 2), device="cuda")
+    table = np.array([[nb - 1, 3, nb - 7]], np.int32)
+    T = 40
+    q, k, v = (bf16(normal(rng, T, h, D)) for h in (16, kv, kv))
+    pos = np.arange(T, dtype=np.int32)
+    slots = table[0, pos // B].astype(np.int64) * B + pos % B
+    q2 = pa.rope_kv_store_fp8_block(q, k, v, up(pos), up(table_of(64, 128)), up(slots), kc, vc, sc, q_out=torch.empty_like(q))
+    blocks = torch.from_numpy(table[0].astype(np.int64)).cuda()
+    small = [t[blocks].cpu().numpy() for t in (kc, vc, sc)]
+    args = (kc, vc, sc, up(table), up(np.array([T], np.int32)))
+    out = pa.prefill_fp8_block(q2, up(np.array([0, T], np.int32)), *args, T, T, D ** -0.5)
+    ref, mag = R.attention(f64(q2), *small, np.arange(3), T, D ** -0.5, 0)
+    close(out, ref, mag)
+    one = pa.decode_fp8_block(q2[-1:].contiguous(), *args, T, D ** -0.5)
+    close(one, ref[-1:], mag[-1:])
+    clean(pa)
+
+
+def test_a_query_that_is_not_finite_spoils_its_own_head_only(pa):
+    rng = np.random.default_rng(42)
+    pool = Pool(rng, [300, 40], 2)
+    q = normal(rng, 2, 12, D)
+    q[0, 3, 5], q[1, 7, 9] = np.inf, np.nan
+    out = pa.decode_fp8_block(bf16(q), *pool.dev(), up(pool.tables), up(pool.lens), 300, D ** -0.5)
+    pre = pa.prefill_fp8_block(bf16(q), up(np.array([0, 1, 2], np.int32)), *pool.dev(), up(pool.tables), up(pool.lens), 1, 300,
+                               D ** -0.5)
+    bad = {(0, 3), (1, 7)}
+    for s in range(2):
+        clean_q = np.where(np.isfinite(q[s:s + 1]), q[s:s + 1], 0.0)
+        ref, mag = pool.attention(s, clean_q, D ** -0.5)
+        for h in range(12):
+            for o in (out, pre):
+                if (s, h) in bad:
+                    assert np.isnan(f64(o[s, h])).all()
+                else:
+                    close(f64(o[s, h]), ref[0, h], mag[0, h], (s, h))
+    clean(pa)
+
+
+@pytest.mark.parametrize("size", [2.0 ** -100, 2.0 ** -20, 2.0 ** 15, 2.0 ** 60])
+def test_queries_of_any_magnitude(pa, size):
+    """A power of two on q and its inverse on the softmax scale: the same attention, whatever f16 or
+    E4M3 could hold."""
+    rng = np.random.default_rng(43)
+    pool = Pool(rng, [200], 1)
+    q = normal(rng, 1, 8, D)
+    out = pa.decode_fp8_block(bf16(q * size), *pool.dev(), up(pool.tables), up(pool.lens), 200, D ** -0.5 / size)
+    pre = pa.prefill_fp8_block(bf16(q * size), up(np.array([0, 1], np.int32)), *pool.dev(), up(pool.tables), up(pool.lens), 1,
+                               200, D ** -0.5 / size)
+    ref, mag = pool.attention(0, q, D ** -0.5)
+    close(out, ref, mag)
+    close(pre, ref, mag)
+    clean(pa)
+
+
+def test_nothing_to_do(pa):
+    e = dict(device="cuda")
+    kc, vc = (torch.zeros((2, 1, B, D), dtype=torch.uint8, **e) for _ in range(2))
+    sc, cs = torch.ones((2, 1, 2), **e), torch.zeros((4, 64), **e)
+    q, k = torch.zeros((0, 4, D), dtype=torch.bfloat16, **e), torch.zeros((0, 1, D), dtype=torch.bfloat16, **e)
+    i32, i64 = torch.zeros(0, dtype=torch.int32, **e), torch.zeros(0, dtype=torch.int64, **e)
+    bt = torch.zeros((0, 2), dtype=torch.int32, **e)
+    assert pa.decode_fp8_block(q, kc, vc, sc, bt, i32, 16, 0.1).shape == q.shape
+    assert pa.decode_step_fp8_block(q, k, k, cs, kc, vc, sc, bt, i32, 16, 0.1).shape == q.shape
+    assert pa.rope_kv_store_fp8_block(q, k, k, i32, cs, i64, kc, vc, sc) is q
+    assert pa.prefill_fp8_block(q, torch.zeros(1, dtype=torch.int32, **e), kc, vc, sc, bt, i32, 1, 16, 0.1).shape == q.shape
+    clean(pa)
+
+
 # ---- the fused step -----------------------------------------------------------------------
 
 @pytest.mark.parametrize("early", [False, True])
