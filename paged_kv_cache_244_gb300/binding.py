@@ -9,6 +9,7 @@ fallback, and using any function without the compiled library raises at once.
 from __future__ import annotations
 
 import ctypes
+from functools import lru_cache
 from pathlib import Path
 from typing import NamedTuple
 
@@ -508,6 +509,20 @@ def _declare_serving(L):
         getattr(L, name).restype = i
 
 
+# Small argument structs by their values, as references ready to pass (building one costs half a
+# microsecond of a call).
+@lru_cache(maxsize=256)
+def _dims_ref(num_q_heads, num_kv_heads, head_dim, block_size):
+    return ctypes.byref(pa_dims(num_q_heads, num_kv_heads, head_dim, block_size))
+
+
+@lru_cache(maxsize=64)
+def _rope_ref(rotary_dim, layout):
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}, got {layout!r}")
+    return ctypes.byref(pa_rope(rotary_dim, ROPE_LAYOUTS[layout]))
+
+
 def _ptrs(spec, *tensors):
     """Data pointers of contiguous CUDA tensors on the current device, checked against `spec`, a
     (name, dtype) for each; and the current device."""
@@ -545,9 +560,7 @@ def _kept(stream, *tensors):
 def _rope_form(cos_sin, layout):
     if cos_sin.dim() != 2:
         raise ValueError("cos_sin must be [max_pos, rotary_dim]")
-    if layout not in ROPE_LAYOUTS:
-        raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}, got {layout!r}")
-    return pa_rope(cos_sin.shape[1], ROPE_LAYOUTS[layout])
+    return _rope_ref(cos_sin.shape[1], layout)
 
 
 def _block_caches(k_cache, v_cache, kv_scale):
@@ -592,7 +605,7 @@ def _store_shapes(q, k, v, positions, slot_mapping, q_out, nb_shape):
         raise ValueError("shape mismatch between q, q_out, k, v and the caches")
     if positions.shape != (T,) or slot_mapping.shape != (T,):
         raise ValueError("positions / slot_mapping shape mismatch")
-    return T, pa_dims(Hq, Hkv, D, B), nb
+    return T, _dims_ref(Hq, Hkv, D, B), nb
 
 
 def rope_kv_store_form(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, layout="half",
@@ -610,7 +623,7 @@ def rope_kv_store_form(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cac
     T, dims, nb = _store_shapes(q, k, v, positions, slot_mapping, q_out, k_cache.shape)
     (qp, qo, kp, vp, pos, cs, slots, kc, vc), dev = _ptrs(
         _STORE_BF16, q, q_out, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache)
-    _check(lib().pa_rope_kv_store_form(ctypes.byref(dims), ctypes.byref(rope), T, qp, qo, kp, vp, pos, cs,
+    _check(lib().pa_rope_kv_store_form(dims, rope, T, qp, qo, kp, vp, pos, cs,
                                        cos_sin.shape[0], slots, kc, vc, nb, _stream_of(stream, dev)),
            "pa_rope_kv_store_form")
     return q_out
@@ -626,7 +639,7 @@ def rope_kv_store_fp8_block(q, k, v, positions, cos_sin, slot_mapping, k_cache, 
                                 _block_caches(k_cache, v_cache, kv_scale))
     (qp, qo, kp, vp, pos, cs, slots, kc, vc, sc), dev = _ptrs(
         _STORE_BLOCK, q, q_out, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, kv_scale)
-    _check(lib().pa_rope_kv_store_fp8_block(ctypes.byref(dims), ctypes.byref(rope), T, qp, qo, kp, vp, pos,
+    _check(lib().pa_rope_kv_store_fp8_block(dims, rope, T, qp, qo, kp, vp, pos,
                                             cs, cos_sin.shape[0], slots, kc, vc, sc, nb,
                                             _stream_of(stream, dev)),
            "pa_rope_kv_store_fp8_block")
@@ -640,7 +653,7 @@ def _decode_shapes(q, k_cache, v_cache, kv_scale, block_tables, context_lens, ou
         raise ValueError("shape mismatch between q, out and the caches")
     if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.shape != (S,):
         raise ValueError("block_tables / context_lens shape mismatch")
-    return S, nb, pa_dims(Hq, Hkv, D, B)
+    return S, nb, _dims_ref(Hq, Hkv, D, B)
 
 
 _ATTEND = (("q", torch.bfloat16), ("out", torch.bfloat16), ("k_cache", torch.uint8), ("v_cache", torch.uint8),
@@ -665,7 +678,7 @@ def decode_fp8_block(q, k_cache, v_cache, kv_scale, block_tables, context_lens, 
         _kept(stream, workspace)
     (qp, op, kc, vc, sc, bt, ctx, ws), dev = _ptrs(
         _DECODE, q, out, k_cache, v_cache, kv_scale, block_tables, context_lens, workspace)
-    _check(lib().pa_decode_fp8_block(ctypes.byref(dims), S, qp, kc, vc, sc, nb, bt, block_tables.shape[1], ctx,
+    _check(lib().pa_decode_fp8_block(dims, S, qp, kc, vc, sc, nb, bt, block_tables.shape[1], ctx,
                                      int(max_context_len), float(scale), int(partition_tokens), ws, workspace.numel() * 4, op,
                                      _stream_of(stream, dev)),
            "pa_decode_fp8_block")
@@ -693,7 +706,7 @@ def decode_step_fp8_block(q, k, v, cos_sin, k_cache, v_cache, kv_scale, block_ta
     (qp, op, kc, vc, sc, bt, ctx, ws, kp, vp, cs), dev = _ptrs(
         _STEP, q, out, k_cache, v_cache, kv_scale, block_tables, context_lens, workspace, k, v, cos_sin)
     _check(lib().pa_decode_step_fp8_block(
-        ctypes.byref(dims), ctypes.byref(rope), S, qp, kp, vp, cs, cos_sin.shape[0], kc, vc, sc, nb, bt,
+        dims, rope, S, qp, kp, vp, cs, cos_sin.shape[0], kc, vc, sc, nb, bt,
         block_tables.shape[1], ctx, int(max_context_len), float(scale), int(partition_tokens), ws, workspace.numel() * 4, op,
         PA_STEP_EARLY_METADATA if early_metadata else 0, _stream_of(stream, dev)), "pa_decode_step_fp8_block")
     return out
@@ -713,10 +726,10 @@ def prefill_fp8_block(q, q_start, k_cache, v_cache, kv_scale, block_tables, cont
         raise ValueError("shape mismatch between q, out and the caches")
     if q_start.shape != (S + 1,) or block_tables.dim() != 2 or block_tables.shape[0] != S:
         raise ValueError("q_start / block_tables shape mismatch")
-    dims = pa_dims(Hq, Hkv, D, B)
+    dims = _dims_ref(Hq, Hkv, D, B)
     (qp, op, kc, vc, sc, bt, ctx, qs), dev = _ptrs(
         _PREFILL, q, out, k_cache, v_cache, kv_scale, block_tables, context_lens, q_start)
-    _check(lib().pa_prefill_fp8_block(ctypes.byref(dims), S, T, qp, qs, int(max_query_len), kc, vc, sc, nb, bt,
+    _check(lib().pa_prefill_fp8_block(dims, S, T, qp, qs, int(max_query_len), kc, vc, sc, nb, bt,
                                       block_tables.shape[1], ctx, int(max_context_len), float(scale), op,
                                       _stream_of(stream, dev)), "pa_prefill_fp8_block")
     return out
@@ -769,10 +782,10 @@ def plan_step(cached_lens, new_lens, block_tables, free_blocks, num_free, num_bl
     (c, n, bt, fb, nf, nfo, cx, q0, ps, sl, gr), dev = _ptrs(
         _PLAN, cached_lens, new_lens, block_tables, free_blocks, num_free, num_free_out, ctx, qs, pos, slots,
         granted)
-    _check(lib().pa_plan_step(ctypes.byref(_PLAN_DIMS), S, c, n, bt, block_tables.shape[1], fb,
+    _check(lib().pa_plan_step(_PLAN_DIMS, S, c, n, bt, block_tables.shape[1], fb,
                               free_blocks.shape[0], nf, nfo, int(num_blocks), int(num_tokens), cx, q0, ps, sl, gr,
                               _stream_of(stream, dev)), "pa_plan_step")
     return plan
 
 
-_PLAN_DIMS = pa_dims(1, 1, 128, 16)   # the plan depends on the block size alone
+_PLAN_DIMS = _dims_ref(1, 1, 128, 16)   # the plan depends on the block size alone
