@@ -1,4 +1,6 @@
-"""Compile the CUDA library in-tree: csrc/*.cu -> libpa_gb300.so, for sm_103a only.
+"""Compile the CUDA library in-tree: csrc/*.cu -> libpa_gb300.so, for sm_103a only, and the
+native half of the Python binding, csrc_py/pa_torch.cpp -> _pa_torch.so, with the host compiler
+against this interpreter's PyTorch.
 
 Each translation unit compiles in parallel with nvcc (-gencode arch=compute_103a,
 code=sm_103a, -O3, -lineinfo); the objects link into one shared library with the CUDA
@@ -11,6 +13,7 @@ from __future__ import annotations
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 from pathlib import Path
 
@@ -20,6 +23,8 @@ CSRC = PKG / "csrc"
 INCLUDE = ROOT / "include"
 BUILD_DIR = PKG / "_build"
 LIBRARY = PKG / "libpa_gb300.so"
+NATIVE_SOURCE = PKG / "csrc_py" / "pa_torch.cpp"
+NATIVE = PKG / "_pa_torch.so"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -45,8 +50,46 @@ def up_to_date() -> bool:
     return all(p.stat().st_mtime <= t for p in _deps())
 
 
+def native_up_to_date() -> bool:
+    if not NATIVE.exists():
+        return False
+    t = NATIVE.stat().st_mtime
+    return all(p.stat().st_mtime <= t for p in [NATIVE_SOURCE, *INCLUDE.glob("*.h")])
+
+
+def _compile_native() -> Path:
+    """The binding's object file (its link needs the library)."""
+    import torch
+    inc = Path(torch.__file__).resolve().parent / "include"
+    cuda = Path(nvcc()).resolve().parents[1] / "include"
+    obj = BUILD_DIR / "pa_torch.o"
+    cmd = [os.environ.get("CXX") or "g++", "-c", str(NATIVE_SOURCE), "-o", str(obj), "-O2", "-std=c++17", "-fPIC",
+           f"-I{INCLUDE}", f"-I{inc}", f"-I{inc}/torch/csrc/api/include", f"-I{cuda}",
+           f"-I{sysconfig.get_paths()['include']}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"the compiler failed on {NATIVE_SOURCE.name}:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_native(obj: Path) -> None:
+    import torch
+    libs = Path(torch.__file__).resolve().parent / "lib"
+    tmp = NATIVE.with_name(NATIVE.name + f".tmp{os.getpid()}")
+    cmd = [os.environ.get("CXX") or "g++", "-shared", "-o", str(tmp), str(obj), f"-L{libs}", f"-L{PKG}",
+           "-l:libpa_gb300.so", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+           f"-Wl,-rpath,{libs}", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"linking {NATIVE.name} failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, NATIVE)
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> Path:
     if not force and up_to_date():
+        if not native_up_to_date():
+            BUILD_DIR.mkdir(exist_ok=True)
+            _link_native(_compile_native())
         return LIBRARY
     BUILD_DIR.mkdir(exist_ok=True)
     cc = nvcc()
@@ -63,7 +106,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
             print(r.stdout + r.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
+    with ThreadPoolExecutor(max_workers=max(1, min(12, os.cpu_count() or 1))) as ex:
+        native = ex.submit(_compile_native)
         objs = list(ex.map(compile_one, _sources()))
     tmp = LIBRARY.with_name(LIBRARY.name + f".tmp{os.getpid()}")
     cmd = [cc, "-shared", "-o", str(tmp)] + ARCH + [str(o) for o in objs]
@@ -71,6 +115,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIBRARY)
+    _link_native(native.result())
     return LIBRARY
 
 

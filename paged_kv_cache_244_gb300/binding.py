@@ -2,14 +2,14 @@
 
 Every function here checks tensor devices, dtypes, shapes and contiguity, passes raw
 device pointers and the current CUDA stream to libpa_gb300.so, and turns a negative return
-code into PaError.  All computation happens in the library's CUDA kernels: there is no
+code into PaError.  The serving calls (from rope_table down) make their checks and their call in
+native code, _pa_torch.so.  All computation happens in the library's CUDA kernels: there is no
 fallback, and using any function without the compiled library raises at once.
 """
 
 from __future__ import annotations
 
 import ctypes
-from functools import lru_cache
 from pathlib import Path
 from typing import NamedTuple
 
@@ -509,44 +509,32 @@ def _declare_serving(L):
         getattr(L, name).restype = i
 
 
-# Small argument structs by their values, as references ready to pass (building one costs half a
-# microsecond of a call).
-@lru_cache(maxsize=256)
-def _dims_ref(num_q_heads, num_kv_heads, head_dim, block_size):
-    return ctypes.byref(pa_dims(num_q_heads, num_kv_heads, head_dim, block_size))
+_native_module = None
 
 
-@lru_cache(maxsize=64)
-def _rope_ref(rotary_dim, layout):
-    if layout not in ROPE_LAYOUTS:
-        raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}, got {layout!r}")
-    return ctypes.byref(pa_rope(rotary_dim, ROPE_LAYOUTS[layout]))
+def _native():
+    """The native half of this binding (csrc_py/pa_torch.cpp), which checks the tensors of the serving
+    calls and makes them; raises if it was never built."""
+    global _native_module
+    if _native_module is None:
+        lib()
+        try:
+            from . import _pa_torch
+        except ImportError as e:
+            raise RuntimeError("_pa_torch.so is not built: run __graft_entry__.build()") from e
+        _native_module = _pa_torch
+    return _native_module
 
 
-def _ptrs(spec, *tensors):
-    """Data pointers of contiguous CUDA tensors on the current device, checked against `spec`, a
-    (name, dtype) for each; and the current device."""
-    dev = torch.cuda.current_device()
-    out = []
-    for (name, dtype), t in zip(spec, tensors):
-        if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
-            if t.dtype is not dtype:
-                raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-            if t.get_device() != dev:
-                raise ValueError(f"{name} must be a CUDA tensor on the current device (cuda:{dev})")
-            raise ValueError(f"{name} must be contiguous")
-        out.append(t.data_ptr())
-    return out, dev
+def _handle(stream):
+    return None if stream is None else stream.cuda_stream
 
 
-# The current stream's handle without building a Stream object (3 us a call), where torch has it.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _stream_of(stream, dev):
-    if stream is not None:
-        return stream.cuda_stream
-    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
+def _layout(layout):
+    try:
+        return ROPE_LAYOUTS[layout]
+    except KeyError:
+        raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}, got {layout!r}") from None
 
 
 def _kept(stream, *tensors):
@@ -555,21 +543,6 @@ def _kept(stream, *tensors):
     if stream is not None:
         for t in tensors:
             t.record_stream(stream)
-
-
-def _rope_form(cos_sin, layout):
-    if cos_sin.dim() != 2:
-        raise ValueError("cos_sin must be [max_pos, rotary_dim]")
-    return _rope_ref(cos_sin.shape[1], layout)
-
-
-def _block_caches(k_cache, v_cache, kv_scale):
-    nb, Hkv, B, D = k_cache.shape
-    if v_cache.shape != k_cache.shape:
-        raise ValueError("k_cache and v_cache differ in shape")
-    if kv_scale.shape != (nb, Hkv, 2):
-        raise ValueError("kv_scale must be [num_blocks, num_kv_heads, 2] float32")
-    return nb, Hkv, B, D
 
 
 def rope_table(max_pos, rotary_dim=128, theta=1e4, scaling="none", factor=1.0, original_max_pos=0,
@@ -583,29 +556,9 @@ def rope_table(max_pos, rotary_dim=128, theta=1e4, scaling="none", factor=1.0, o
     if out is None:
         out = torch.empty((max_pos, rotary_dim), dtype=torch.float32, device="cuda")
         _kept(stream, out)
-    elif tuple(out.shape) != (max_pos, rotary_dim):
-        raise ValueError("out must be [max_pos, rotary_dim]")
-    spec = pa_rope_scaling(theta, factor, original_max_pos, low, high, magnitude, ROPE_SCALINGS[scaling])
-    (o,), dev = _ptrs((("out", torch.float32),), out)
-    _check(lib().pa_rope_table(ctypes.byref(spec), rotary_dim, max_pos, o, _stream_of(stream, dev)),
-           "pa_rope_table")
+    _check(_native().rope_table(ROPE_SCALINGS[scaling], theta, factor, original_max_pos, low, high, magnitude,
+                                rotary_dim, max_pos, out, _handle(stream)), "pa_rope_table")
     return out
-
-
-_STORE = tuple((n, torch.bfloat16) for n in ("q", "q_out", "k", "v")) + (
-    ("positions", torch.int32), ("cos_sin", torch.float32), ("slot_mapping", torch.int64))
-_STORE_BF16 = _STORE + (("k_cache", torch.bfloat16), ("v_cache", torch.bfloat16))
-_STORE_BLOCK = _STORE + (("k_cache", torch.uint8), ("v_cache", torch.uint8), ("kv_scale", torch.float32))
-
-
-def _store_shapes(q, k, v, positions, slot_mapping, q_out, nb_shape):
-    T, Hq, D = q.shape
-    nb, Hkv, B, D2 = nb_shape
-    if D2 != D or k.shape != (T, Hkv, D) or v.shape != (T, Hkv, D) or q_out.shape != q.shape:
-        raise ValueError("shape mismatch between q, q_out, k, v and the caches")
-    if positions.shape != (T,) or slot_mapping.shape != (T,):
-        raise ValueError("positions / slot_mapping shape mismatch")
-    return T, _dims_ref(Hq, Hkv, D, B), nb
 
 
 def rope_kv_store_form(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, layout="half",
@@ -617,15 +570,8 @@ def rope_kv_store_form(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cac
     "interleaved".  Everything else as rope_kv_store.
     """
     q_out = q if q_out is None else q_out
-    rope = _rope_form(cos_sin, layout)
-    if v_cache.shape != k_cache.shape:
-        raise ValueError("k_cache and v_cache differ in shape")
-    T, dims, nb = _store_shapes(q, k, v, positions, slot_mapping, q_out, k_cache.shape)
-    (qp, qo, kp, vp, pos, cs, slots, kc, vc), dev = _ptrs(
-        _STORE_BF16, q, q_out, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache)
-    _check(lib().pa_rope_kv_store_form(dims, rope, T, qp, qo, kp, vp, pos, cs,
-                                       cos_sin.shape[0], slots, kc, vc, nb, _stream_of(stream, dev)),
-           "pa_rope_kv_store_form")
+    _check(_native().rope_kv_store_form(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache,
+                                        _layout(layout), q_out, _handle(stream)), "pa_rope_kv_store_form")
     return q_out
 
 
@@ -634,33 +580,10 @@ def rope_kv_store_fp8_block(q, k, v, positions, cos_sin, slot_mapping, k_cache, 
     """rope_kv_store_form into block-scaled E4M3 caches (pa_rope_kv_store_fp8_block): k_cache,
     v_cache uint8 [num_blocks, Hkv, B, D], kv_scale [num_blocks, Hkv, 2] fp32, all updated."""
     q_out = q if q_out is None else q_out
-    rope = _rope_form(cos_sin, layout)
-    T, dims, nb = _store_shapes(q, k, v, positions, slot_mapping, q_out,
-                                _block_caches(k_cache, v_cache, kv_scale))
-    (qp, qo, kp, vp, pos, cs, slots, kc, vc, sc), dev = _ptrs(
-        _STORE_BLOCK, q, q_out, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, kv_scale)
-    _check(lib().pa_rope_kv_store_fp8_block(dims, rope, T, qp, qo, kp, vp, pos,
-                                            cs, cos_sin.shape[0], slots, kc, vc, sc, nb,
-                                            _stream_of(stream, dev)),
+    _check(_native().rope_kv_store_fp8_block(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache,
+                                             kv_scale, _layout(layout), q_out, _handle(stream)),
            "pa_rope_kv_store_fp8_block")
     return q_out
-
-
-def _decode_shapes(q, k_cache, v_cache, kv_scale, block_tables, context_lens, out):
-    S, Hq, D = q.shape
-    nb, Hkv, B, D2 = _block_caches(k_cache, v_cache, kv_scale)
-    if D2 != D or out.shape != q.shape:
-        raise ValueError("shape mismatch between q, out and the caches")
-    if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.shape != (S,):
-        raise ValueError("block_tables / context_lens shape mismatch")
-    return S, nb, _dims_ref(Hq, Hkv, D, B)
-
-
-_ATTEND = (("q", torch.bfloat16), ("out", torch.bfloat16), ("k_cache", torch.uint8), ("v_cache", torch.uint8),
-           ("kv_scale", torch.float32), ("block_tables", torch.int32), ("context_lens", torch.int32))
-_DECODE = _ATTEND + (("workspace", torch.float32),)
-_STEP = _DECODE + (("k", torch.bfloat16), ("v", torch.bfloat16), ("cos_sin", torch.float32))
-_PREFILL = _ATTEND + (("q_start", torch.int32),)
 
 
 def decode_fp8_block(q, k_cache, v_cache, kv_scale, block_tables, context_lens, max_context_len,
@@ -670,18 +593,14 @@ def decode_fp8_block(q, k_cache, v_cache, kv_scale, block_tables, context_lens, 
     if out is None:
         out = torch.empty_like(q)
         _kept(stream, out)
-    S, nb, dims = _decode_shapes(q, k_cache, v_cache, kv_scale, block_tables, context_lens, out)
-    if S == 0:
+    if q.shape[0] == 0:
         return out
     if workspace is None:
         workspace = decode_workspace(q, k_cache, max_context_len, partition_tokens)
         _kept(stream, workspace)
-    (qp, op, kc, vc, sc, bt, ctx, ws), dev = _ptrs(
-        _DECODE, q, out, k_cache, v_cache, kv_scale, block_tables, context_lens, workspace)
-    _check(lib().pa_decode_fp8_block(dims, S, qp, kc, vc, sc, nb, bt, block_tables.shape[1], ctx,
-                                     int(max_context_len), float(scale), int(partition_tokens), ws, workspace.numel() * 4, op,
-                                     _stream_of(stream, dev)),
-           "pa_decode_fp8_block")
+    _check(_native().decode_fp8_block(q, k_cache, v_cache, kv_scale, block_tables, context_lens,
+                                      max_context_len, scale, partition_tokens, workspace, out,
+                                      _handle(stream)), "pa_decode_fp8_block")
     return out
 
 
@@ -693,22 +612,16 @@ def decode_step_fp8_block(q, k, v, cos_sin, k_cache, v_cache, kv_scale, block_ta
     if out is None:
         out = torch.empty_like(q)
         _kept(stream, out)
-    rope = _rope_form(cos_sin, layout)
-    S, nb, dims = _decode_shapes(q, k_cache, v_cache, kv_scale, block_tables, context_lens, out)
-    new = (S, k_cache.shape[1], q.shape[2])
-    if k.shape != new or v.shape != new:
-        raise ValueError("k / v shape mismatch")
-    if S == 0:
+    if q.shape[0] == 0:
         return out
     if workspace is None:
         workspace = decode_workspace(q, k_cache, max_context_len, partition_tokens)
         _kept(stream, workspace)
-    (qp, op, kc, vc, sc, bt, ctx, ws, kp, vp, cs), dev = _ptrs(
-        _STEP, q, out, k_cache, v_cache, kv_scale, block_tables, context_lens, workspace, k, v, cos_sin)
-    _check(lib().pa_decode_step_fp8_block(
-        dims, rope, S, qp, kp, vp, cs, cos_sin.shape[0], kc, vc, sc, nb, bt,
-        block_tables.shape[1], ctx, int(max_context_len), float(scale), int(partition_tokens), ws, workspace.numel() * 4, op,
-        PA_STEP_EARLY_METADATA if early_metadata else 0, _stream_of(stream, dev)), "pa_decode_step_fp8_block")
+    _check(_native().decode_step_fp8_block(q, k, v, cos_sin, k_cache, v_cache, kv_scale, block_tables,
+                                           context_lens, max_context_len, scale, _layout(layout),
+                                           partition_tokens, workspace, out,
+                                           PA_STEP_EARLY_METADATA if early_metadata else 0, _handle(stream)),
+           "pa_decode_step_fp8_block")
     return out
 
 
@@ -719,19 +632,9 @@ def prefill_fp8_block(q, q_start, k_cache, v_cache, kv_scale, block_tables, cont
     if out is None:
         out = torch.empty_like(q)
         _kept(stream, out)
-    T, Hq, D = q.shape
-    nb, Hkv, B, D2 = _block_caches(k_cache, v_cache, kv_scale)
-    S = context_lens.shape[0]
-    if D2 != D or out.shape != q.shape:
-        raise ValueError("shape mismatch between q, out and the caches")
-    if q_start.shape != (S + 1,) or block_tables.dim() != 2 or block_tables.shape[0] != S:
-        raise ValueError("q_start / block_tables shape mismatch")
-    dims = _dims_ref(Hq, Hkv, D, B)
-    (qp, op, kc, vc, sc, bt, ctx, qs), dev = _ptrs(
-        _PREFILL, q, out, k_cache, v_cache, kv_scale, block_tables, context_lens, q_start)
-    _check(lib().pa_prefill_fp8_block(dims, S, T, qp, qs, int(max_query_len), kc, vc, sc, nb, bt,
-                                      block_tables.shape[1], ctx, int(max_context_len), float(scale), op,
-                                      _stream_of(stream, dev)), "pa_prefill_fp8_block")
+    _check(_native().prefill_fp8_block(q, q_start, k_cache, v_cache, kv_scale, block_tables, context_lens,
+                                       max_query_len, max_context_len, scale, out, _handle(stream)),
+           "pa_prefill_fp8_block")
     return out
 
 
@@ -752,11 +655,6 @@ def step_plan(num_seqs, num_tokens, device="cuda") -> StepPlan:
                     torch.empty(num_seqs, **i32))
 
 
-_PLAN = tuple((n, torch.int32) for n in ("cached_lens", "new_lens", "block_tables", "free_blocks", "num_free",
-                                         "num_free_out", "context_lens", "q_start", "positions")) + (
-    ("slot_mapping", torch.int64), ("granted", torch.int32))
-
-
 def plan_step(cached_lens, new_lens, block_tables, free_blocks, num_free, num_blocks, num_tokens,
               num_free_out=None, plan=None, stream=None) -> StepPlan:
     """The metadata of one serving step, built on the GPU (pa_plan_step).
@@ -765,27 +663,11 @@ def plan_step(cached_lens, new_lens, block_tables, free_blocks, num_free, num_bl
     free_blocks [capacity] int32, a stack of num_free[0] ids ([1] int32) of a pool of num_blocks;
     num_tokens rows.  num_free_out ([1] int32) receives what is left; None means num_free itself.
     """
-    S = cached_lens.shape[0]
     if plan is None:
-        plan = step_plan(S, num_tokens, cached_lens.device)
+        plan = step_plan(cached_lens.shape[0], num_tokens, cached_lens.device)
         _kept(stream, *plan)
     if num_free_out is None:
         num_free_out = num_free
-    ctx, qs, pos, slots, granted = plan
-    if new_lens.shape != (S,) or block_tables.dim() != 2 or block_tables.shape[0] != S:
-        raise ValueError("cached_lens / new_lens / block_tables shape mismatch")
-    if free_blocks.dim() != 1 or num_free.numel() != 1 or num_free_out.numel() != 1:
-        raise ValueError("free_blocks must be [capacity], num_free and num_free_out [1]")
-    if (ctx.shape != (S,) or qs.shape != (S + 1,) or granted.shape != (S,) or pos.shape != (num_tokens,)
-            or slots.shape != (num_tokens,)):
-        raise ValueError("plan does not fit these sequences and rows")
-    (c, n, bt, fb, nf, nfo, cx, q0, ps, sl, gr), dev = _ptrs(
-        _PLAN, cached_lens, new_lens, block_tables, free_blocks, num_free, num_free_out, ctx, qs, pos, slots,
-        granted)
-    _check(lib().pa_plan_step(_PLAN_DIMS, S, c, n, bt, block_tables.shape[1], fb,
-                              free_blocks.shape[0], nf, nfo, int(num_blocks), int(num_tokens), cx, q0, ps, sl, gr,
-                              _stream_of(stream, dev)), "pa_plan_step")
+    _check(_native().plan_step(cached_lens, new_lens, block_tables, free_blocks, num_free, num_free_out, num_blocks,
+                               num_tokens, *plan, _handle(stream)), "pa_plan_step")
     return plan
-
-
-_PLAN_DIMS = _dims_ref(1, 1, 128, 16)   # the plan depends on the block size alone

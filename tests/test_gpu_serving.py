@@ -486,6 +486,42 @@ def test_queries_of_any_magnitude(pa, size):
     clean(pa)
 
 
+def test_shapes_that_do_not_fit_are_refused(pa):
+    e = dict(device="cuda")
+    bf = dict(dtype=torch.bfloat16, **e)
+    q, k = torch.zeros((4, 12, D), **bf), torch.zeros((4, 2, D), **bf)
+    kc, vc = (torch.zeros((4, 2, B, D), dtype=torch.uint8, **e) for _ in range(2))
+    sc, cs = torch.ones((4, 2, 2), **e), torch.zeros((8, 64), **e)
+    i32, i64, bt = (torch.zeros(s, dtype=t, **e) for s, t in ((4, torch.int32), (4, torch.int64), ((4, 2), torch.int32)))
+    ws = torch.zeros(1 << 16, **e)
+    qs = torch.zeros(5, dtype=torch.int32, **e)
+    nf, plan = i32[:1].contiguous(), pa.step_plan(4, 5)
+    store = dict(q=q, k=k, v=k, positions=i32, cos_sin=cs, slot_mapping=i64, k_cache=kc, v_cache=vc, kv_scale=sc)
+    dec = dict(q=q, k_cache=kc, v_cache=vc, kv_scale=sc, block_tables=bt, context_lens=i32, max_context_len=16, scale=0.1,
+               workspace=ws)
+    step = dict(dec, k=k, v=k, cos_sin=cs)
+    pre = dict(q=q, q_start=qs, k_cache=kc, v_cache=vc, kv_scale=sc, block_tables=bt, context_lens=i32, max_query_len=4,
+               max_context_len=16, scale=0.1)
+    pl = dict(cached_lens=i32, new_lens=i32, block_tables=bt, free_blocks=i32, num_free=nf, num_blocks=4, num_tokens=5,
+              plan=plan)
+    wide = torch.zeros((4, 2, 2 * D), **bf)[:, :, ::2]
+    for call, good, bad in (
+            (pa.rope_kv_store_fp8_block, store, dict(k=k[:3], v=q, positions=i32[:3], slot_mapping=i64[:3], cos_sin=cs[0],
+                                                     k_cache=kc[:3], kv_scale=sc[:3], q_out=q[:3], q=q[0])),
+            (pa.decode_fp8_block, dec, dict(q=q[:3], block_tables=bt[0], context_lens=i32[:2], out=q[:1], kv_scale=sc[:, :1])),
+            (pa.decode_step_fp8_block, step, dict(k=k[:3], v=q, cos_sin=cs[0], out=q[:3], v_cache=vc[:2])),
+            (pa.prefill_fp8_block, pre, dict(q_start=qs[:4], block_tables=bt[:3], context_lens=i32[:3], out=q[:3])),
+            (pa.plan_step, pl, dict(new_lens=i32[:3], block_tables=bt[:3], num_free=i32[:2], num_tokens=6, free_blocks=bt))):
+        for name, value in bad.items():
+            with pytest.raises(ValueError):
+                call(**dict(good, **{name: value}))
+    with pytest.raises(ValueError, match="contiguous"):
+        pa.rope_kv_store_fp8_block(**dict(store, k=wide))
+    with pytest.raises(pa.PaError):                       # what the library refuses
+        pa.decode_fp8_block(**dict(dec, max_context_len=33))
+    clean(pa)
+
+
 def test_nothing_to_do(pa):
     e = dict(device="cuda")
     kc, vc = (torch.zeros((2, 1, B, D), dtype=torch.uint8, **e) for _ in range(2))

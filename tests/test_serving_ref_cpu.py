@@ -195,23 +195,27 @@ def test_plan_refusals(pa):
 
 
 def test_binding_refuses_wrong_tensors(pa):
-    x = torch.zeros(4, 12, 128)
-    with pytest.raises(ValueError):
+    q, k = torch.zeros(4, 12, 128, dtype=torch.bfloat16), torch.zeros(4, 2, 128, dtype=torch.bfloat16)
+    kc, sc = torch.zeros(4, 2, 16, 128, dtype=torch.uint8), torch.ones(4, 2, 2)
+    i32, i64, cs = torch.zeros(4, dtype=torch.int32), torch.zeros(4, dtype=torch.int64), torch.zeros(8, 64)
+    bt = torch.zeros(4, 2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="scaling"):
         pa.rope_table(16, 64, scaling="cubic")
-    with pytest.raises(ValueError):
-        pa._rope_form(torch.zeros(4), "half")
-    with pytest.raises(ValueError):
-        pa._rope_form(torch.zeros(4, 64), "thirds")
-    kc = torch.zeros(4, 2, 16, 128, dtype=torch.uint8)
-    with pytest.raises(ValueError):
-        pa._block_caches(kc, kc, torch.zeros(4, 2))
-    with pytest.raises(ValueError):
-        pa._block_caches(kc, kc[:2], torch.zeros(4, 2, 2))
-    with pytest.raises(ValueError):
-        pa._store_shapes(x, x, x, torch.zeros(4), torch.zeros(4), x, (4, 2, 16, 128))
-    with pytest.raises(ValueError):
-        pa._decode_shapes(x, kc, kc, torch.zeros(4, 2, 2), torch.zeros(3, 2), torch.zeros(4), x)
+    with pytest.raises(ValueError, match="layout"):
+        pa.rope_kv_store_fp8_block(q, k, k, i32, cs, i64, kc, kc, sc, layout="thirds")
+    # tensors of another type, and tensors that are not on the GPU, are named
+    with pytest.raises(ValueError, match="q must be BFloat16, got Float"):
+        pa.rope_kv_store_fp8_block(q.float(), k, k, i32, cs, i64, kc, kc, sc)
+    for call in (lambda: pa.rope_kv_store_fp8_block(q, k, k, i32, cs, i64, kc, kc, sc),
+                 lambda: pa.rope_kv_store_form(q, k, k, i32, cs, i64, kc, kc),
+                 lambda: pa.decode_fp8_block(q, kc, kc, sc, bt, i32, 16, 0.1, workspace=torch.zeros(8)),
+                 lambda: pa.decode_step_fp8_block(q, k, k, cs, kc, kc, sc, bt, i32, 16, 0.1, workspace=torch.zeros(8)),
+                 lambda: pa.prefill_fp8_block(q, torch.zeros(5, dtype=torch.int32), kc, kc, sc, bt, i32, 4, 16, 0.1),
+                 lambda: pa.plan_step(i32, i32, bt, i32, i32[:1], 4, 5),
+                 lambda: pa.rope_table(4, 64, out=torch.zeros(4, 64))):
+        with pytest.raises(ValueError, match="must be a CUDA tensor on the current device"):
+            call()
     p = pa.step_plan(2, 5, "cpu")
+    with pytest.raises(ValueError, match="cached_lens must be a tensor"):
+        pa.plan_step([0, 1], i32, bt, i32, i32[:1], 4, 5, plan=p)
     assert p.q_start.shape == (3,) and p.slot_mapping.dtype == torch.int64
-    with pytest.raises(ValueError):
-        pa.plan_step(torch.zeros(3), torch.zeros(3), torch.zeros(3, 4), torch.zeros(8), torch.zeros(1), 8, 5, plan=p)
