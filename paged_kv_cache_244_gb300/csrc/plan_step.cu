@@ -13,6 +13,11 @@
 // L2) and writes its own slice of the sequences, entries and rows, so there is one launch and
 // nothing to wait for between CTAs.  num_free is read by every CTA: where num_free_out is the
 // same word, a grid of several CTAs leaves it to a second launch of one CTA.
+//
+// The longest chain of dependent loads and barriers bounds it: lengths, two sums over the CTA, search,
+// free-list entry, store.  256 sequences of one token: 4.6 us replayed from a graph (an empty
+// kernel: 1.9; 5.8 before the loads of a phase were asked for ahead of the sums).  512 prompts of
+// 548,920 rows, where 12 bytes a row are written: 7.0 us, of which the writing takes 1.0 at the copy rate.
 
 #include <mutex>
 
@@ -26,7 +31,9 @@ constexpr int kPlanThreads = 512;
 constexpr int kPlanRowsPerThread = 4;
 // Rows that one CTA takes before another is launched.
 constexpr int kPlanRowsPerCta = kPlanThreads * kPlanRowsPerThread;
-constexpr int kPlanMaxCtas = 608;   // 4 CTAs of 512 threads on each of 152 SMs
+// One CTA an SM: each forms the sums anew, so more of them repeat work and fewer leave the writing
+// thin.  512 prompts, 548,920 rows: 7.0 us with 152 CTAs, 7.6 with 228, 8.5 with 304 and with 608.
+constexpr int kPlanMaxCtas = 152;
 
 // start [S + 1], x [S + 1] (int32), good [S] (bytes)
 __host__ __device__ inline int plan_smem(int S) { return 2 * 4 * (S + 1) + S + 16; }
@@ -42,27 +49,27 @@ __device__ __forceinline__ int plan_find(const int* sums, int n, int v) {
   return lo;
 }
 
-// Exclusive sum over the CTA's threads (v may be long long); *total receives the whole sum.
-template <typename T>
-__device__ __forceinline__ T block_exclusive(T v, T* total) {
-  __shared__ T sums[kPlanThreads / 32];
+// Exclusive sum over the CTA's threads, `sums` a shared word per warp; *total receives the whole sum.
+__device__ __forceinline__ long long block_exclusive(long long v, long long* sums, long long* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  T incl = v;
+  long long incl = v;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const T y = __shfl_up_sync(kFullMask, incl, d);
+    const long long y = __shfl_up_sync(kFullMask, incl, d);
     if (lane >= d) incl += y;
   }
-  __syncthreads();  // the array is free of an earlier call's readers
   if (lane == 31) sums[warp] = incl;
   __syncthreads();
-  T before = 0, all = 0;
-  for (int w = 0; w < kPlanThreads / 32; ++w) {
-    if (w < warp) before += sums[w];
-    all += sums[w];
+  // lane w takes warp w's sum: the warps before this one, and all of them
+  long long upto = lane < kPlanThreads / 32 ? sums[lane] : 0;
+#pragma unroll
+  for (int d = 1; d < kPlanThreads / 32; d <<= 1) {
+    const long long y = __shfl_up_sync(kFullMask, upto, d);
+    if (lane >= d) upto += y;
   }
-  *total = all;
-  return before + incl - v;
+  *total = __shfl_sync(kFullMask, upto, kPlanThreads / 32 - 1);
+  const long long before = __shfl_sync(kFullMask, upto, warp == 0 ? 0 : warp - 1);
+  return (warp == 0 ? 0 : before) + incl - v;
 }
 
 __device__ __forceinline__ int blocks_of(int tokens) { return (tokens + kBlockSize - 1) / kBlockSize; }
@@ -71,6 +78,7 @@ __device__ __forceinline__ int blocks_of(int tokens) { return (tokens + kBlockSi
 template <bool kCountOnly>
 __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanArgs a, const int write_count) {
   extern __shared__ int smem[];
+  __shared__ long long row_sums[kPlanThreads / 32], need_sums[kPlanThreads / 32];
   pdl_wait_prior_grid();
   pdl_allow_next_grid();
   const int S = a.num_seqs, T = a.num_tokens, tid = threadIdx.x;
@@ -83,13 +91,19 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanArgs 
   const int per = (S + kPlanThreads - 1) / kPlanThreads;
   const int s0 = min(S, tid * per), s1 = min(S, s0 + per);
   const long long table_tokens = static_cast<long long>(a.max_blocks) * kBlockSize;
+  // Everything that a later phase waits for is asked for at once: the count, both lengths (the
+  // passes below find them in L1).
+  int F = a.num_free[0];
   long long rows = 0;
+  int touched = 0;
   for (int s = s0; s < s1; ++s) {
     const int n = a.new_lens[s];
+    touched |= a.cached_lens[s];
     if (n > 0 && n <= T) rows += n;
   }
+  asm volatile("" ::"r"(touched));  // the loads of cached_lens stay here
   long long all_rows;
-  long long r = block_exclusive<long long>(rows, &all_rows);
+  long long r = block_exclusive(rows, row_sums, &all_rows);
   // Needs: of the sequences whose lengths and rows are in order.  Each is at most max_blocks
   // < 2^27 blocks and there are at most 8192, so their sum is kept in 64 bits, and clamped
   // to 2^31 - 1 where it is stored (a free list is shorter, so the order is unchanged).
@@ -105,7 +119,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanArgs 
     if (ok) need_sum += blocks_of(c + n) - blocks_of(c);
   }
   long long all_need;
-  long long e = block_exclusive<long long>(need_sum, &all_need);
+  long long e = block_exclusive(need_sum, need_sums, &all_need);
   constexpr long long kTop = 0x7fffffffll;
   for (int s = s0; s < s1; ++s) {
     x[s] = static_cast<int>(min(e, kTop));
@@ -119,7 +133,6 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanArgs 
     start[S] = total_rows;
     x[S] = static_cast<int>(min(all_need, kTop));
   }
-  int F = a.num_free[0];
   if (F < 0 || F > a.free_capacity) {
     if (first_cta && tid == 0 && !kCountOnly) raise_flag(a.status, PA_FLAG_BLOCK_ID_OOB);
     F = F < 0 ? 0 : a.free_capacity;
@@ -140,6 +153,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanArgs 
   const int nb = static_cast<int>(gridDim.x), b = static_cast<int>(blockIdx.x);
   const int gtid = b * kPlanThreads + tid, gthreads = nb * kPlanThreads;
 
+  // In a call of one CTA each kind of output starts with warps of its own, so that their loads overlap.
+  const int entry_tid = nb > 1 ? gtid : (tid + kPlanThreads / 4) % kPlanThreads;
+  const int row_tid = nb > 1 ? gtid : (tid + kPlanThreads / 2) % kPlanThreads;
   for (int s = gtid; s <= S; s += gthreads) {
     a.q_start[s] = start[s];
     if (s == S) break;
@@ -149,7 +165,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanArgs 
     if (!g && good[s]) raise_flag(a.status, PA_FLAG_POOL_EXHAUSTED);
   }
   // new table entries
-  for (int k = gtid; k < taken; k += gthreads) {
+  for (int k = entry_tid; k < taken; k += gthreads) {
     const int s = plan_find(x, S, k);
     int id = a.free_blocks[F - 1 - k];
     if (id < 0 || id >= a.num_blocks) {
@@ -160,7 +176,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanArgs 
   }
   // rows: each thread takes groups of kPlanRowsPerThread neighbours
   const int groups = (T + kPlanRowsPerThread - 1) / kPlanRowsPerThread;
-  for (int gidx = gtid; gidx < groups; gidx += gthreads) {
+  for (int gidx = row_tid; gidx < groups; gidx += gthreads) {
     const int t0 = gidx * kPlanRowsPerThread;
     int s = t0 < total_rows ? plan_find(start, S, t0) : S;
     int pos[kPlanRowsPerThread];

@@ -17,6 +17,8 @@
 namespace pa {
 namespace {
 
+// Bytes bound the large calls: 17,363 rows of 32 + 8 + 8 heads with 96 dims rotated (434 MB) take 65 us,
+// 6.7 TB/s, the copy rate.  The loads' latency bounds the small ones: 64 rows take 2.6 us.
 constexpr int kFormWarps = 8;
 
 struct Angles {
@@ -67,9 +69,11 @@ __device__ __forceinline__ void rotate_chunks(uint4& x, uint4& y, const Angles& 
 
 // One warp, one token: the Hq query heads into q_out (rotated), and unless kQOnly the Hkv keys
 // (rotated) and values into their cache slot, four vectors a pass, kGroup passes loaded before
-// any is stored (the shape of the whole-head half-layout store, and its two group sizes).
+// any is stored (the shape of the whole-head half-layout store, and its two group sizes).  With
+// parts > 1 the warp takes the groups part, part + parts, .. only: where tokens are few, each group
+// of a token has a warp of its own and all loads are in flight at once.
 template <bool kInterleaved, int kGroup, bool kQOnly>
-__device__ __forceinline__ void form_token(const RopeFormArgs& a, int t) {
+__device__ __forceinline__ void form_token(const RopeFormArgs& a, int t, int part = 0, int parts = 1) {
   const int lane = threadIdx.x & 31;
   const int j = lane & 7, sub = lane >> 3;
   const int R = a.rotary_dim;
@@ -94,7 +98,8 @@ __device__ __forceinline__ void form_token(const RopeFormArgs& a, int t) {
   };
   const int pos = a.positions[t];
   const int64_t slot = kQOnly ? -1 : a.slot_mapping[t];
-  load_group(0);
+  const int first = 4 * kGroup * part, step = 4 * kGroup * parts;
+  load_group(first);
   const bool has_pos = pos >= 0 && pos < a.max_pos;
   if (!has_pos && lane == 0) raise_flag(a.status, PA_FLAG_POSITION_OOB);
   bool store = !kQOnly && has_pos && slot >= 0;
@@ -109,8 +114,8 @@ __device__ __forceinline__ void form_token(const RopeFormArgs& a, int t) {
   Angles ang = {};
   if (turns) ang = load_angles(a.cos_sin, pos, R, j);
   const int items = store ? all : Hq;
-  for (int base = 0; base < items; base += 4 * kGroup) {
-    if (base) load_group(base);
+  for (int base = first; base < items; base += step) {
+    if (base != first) load_group(base);
 #pragma unroll
     for (int p = 0; p < kGroup; ++p) {
       const int i = base + 4 * p + sub;
@@ -137,7 +142,7 @@ __global__ void __launch_bounds__(kFormWarps * 32, kGroup == 2 ? 4 : 1) rope_for
   pdl_allow_next_grid();
   const int t = blockIdx.x * kFormWarps + static_cast<int>(threadIdx.x >> 5);
   if (t >= a.num_tokens) return;
-  form_token<kInterleaved, kGroup, false>(a, t);
+  form_token<kInterleaved, kGroup, false>(a, t, blockIdx.y, gridDim.y);
 }
 
 // ---- the store into block-scaled E4M3 caches -----------------------------------------------
@@ -154,13 +159,14 @@ constexpr int kRunTail = kGap * kBlockSize;    // rows past the window that its 
 
 template <bool kInterleaved>
 __global__ void __launch_bounds__(kFormWarps * 32, 4) rope_block_store_kernel(const RopeFormArgs a, const int window,
-                                                                          const int kv_ctas) {
+                                                                             const int kv_ctas, const int q_parts) {
   pdl_wait_prior_grid();
   pdl_allow_next_grid();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (static_cast<int>(blockIdx.x) >= kv_ctas) {
-    const int t = (blockIdx.x - kv_ctas) * kFormWarps + warp;
-    if (t < a.num_tokens) form_token<kInterleaved, 2, true>(a, t);
+    const int unit = static_cast<int>(blockIdx.x) - kv_ctas;
+    const int t = unit / q_parts * kFormWarps + warp;
+    if (t < a.num_tokens) form_token<kInterleaved, 2, true>(a, t, unit % q_parts, q_parts);
     return;
   }
   __shared__ int blocks[kGap + kRunWindow + kRunTail];       // block of a row, -1: not stored
@@ -291,9 +297,9 @@ __global__ void __launch_bounds__(kFormWarps * 32, 4) rope_block_store_kernel(co
 // at a time in packed fp32.  A thread keeps four neighbouring pairs and goes down the rows: one
 // 16-byte word of cos, one of sin a row.
 //
-// Bound by the 8 bytes a pair it writes, with about 30 instructions a pair beside them (131,072 x 128:
-// a first form with a 64-bit division per word and sign handling in 64 bits took 17.1 us, 58% of
-// the copy rate).
+// Bound by the 8 bytes a pair it writes, with about 30 instructions a pair beside them.  131,072 x 128:
+// 10.7 us, 6.3 TB/s (a first form with a 64-bit division per word and sign handling in 64 bits
+// took 17.1 us).
 constexpr int kTableThreads = 256;
 
 __global__ void __launch_bounds__(kTableThreads) rope_table_kernel(const RopeTableArgs a) {
@@ -371,6 +377,14 @@ cudaLaunchConfig_t chained(unsigned ctas, unsigned threads, cudaLaunchAttribute*
   return cfg;
 }
 
+// Warps of a token that has `vectors` head vectors, one for each group of `group`, as long as the grid
+// stays within 304 CTAs (one wave): a lone wave's time is its longest chain of loads.
+int warps_per_token(int vectors, int group, unsigned token_ctas) {
+  const int groups = (vectors + group - 1) / group;
+  const int room = 304 / static_cast<int>(token_ctas > 304 ? 304 : token_ctas);
+  return groups < room ? groups : room;
+}
+
 }  // namespace
 
 cudaError_t launch_rope_form_store(const RopeFormArgs& a, cudaStream_t stream) {
@@ -384,12 +398,14 @@ cudaError_t launch_rope_form_store(const RopeFormArgs& a, cudaStream_t stream) {
     int window = 1;
     while (window < kRunWindow && static_cast<long long>(window) * 2 * 304 <= a.num_tokens) window *= 2;
     const unsigned kv_ctas = static_cast<unsigned>((static_cast<long long>(a.num_tokens) + window - 1) / window);
-    cudaLaunchConfig_t cfg = chained(kv_ctas + token_ctas, kFormWarps * 32, &attr, stream);
-    return a.interleaved ? cudaLaunchKernelEx(&cfg, rope_block_store_kernel<true>, a, window, static_cast<int>(kv_ctas))
-                         : cudaLaunchKernelEx(&cfg, rope_block_store_kernel<false>, a, window, static_cast<int>(kv_ctas));
+    const int q_parts = warps_per_token(a.num_q_heads, 8, token_ctas);
+    cudaLaunchConfig_t cfg = chained(kv_ctas + token_ctas * q_parts, kFormWarps * 32, &attr, stream);
+    auto kernel = a.interleaved ? rope_block_store_kernel<true> : rope_block_store_kernel<false>;
+    return cudaLaunchKernelEx(&cfg, kernel, a, window, static_cast<int>(kv_ctas), q_parts);
   }
   cudaLaunchConfig_t cfg = chained(token_ctas, kFormWarps * 32, &attr, stream);
   const bool many = a.num_tokens > 2048;
+  if (!many) cfg.gridDim.y = warps_per_token(a.num_q_heads + 2 * a.num_kv_heads, 16, token_ctas);
   if (a.interleaved)
     return many ? cudaLaunchKernelEx(&cfg, rope_form_store_kernel<true, 2>, a)
                 : cudaLaunchKernelEx(&cfg, rope_form_store_kernel<true, 4>, a);
