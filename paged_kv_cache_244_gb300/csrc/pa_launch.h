@@ -179,9 +179,6 @@ cudaError_t launch_wait_selftest(unsigned* status, uint64_t limit_ns, cudaStream
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream);
 // Block-scaled E4M3 caches (a.kv_scale set): called by launch_decode.
 cudaError_t launch_decode_block(const DecodeArgs& a, cudaStream_t stream);
-// The merge of split segments after a partition kernel of part_ctas CTAs at most; per_cta warps in
-// a CTA of its narrow form.
-cudaError_t launch_decode_merge(const DecodeArgs& a, int part_ctas, int per_cta, cudaStream_t stream);
 // The decode kernel's gather of K/V tiles alone (no attention, no merge): pa_gather_checksum,
 // over bf16 or E4M3 (fp8) caches.
 cudaError_t launch_gather(const DecodeArgs& a, bool fp8, cudaStream_t stream);

@@ -868,10 +868,9 @@ decode_merge_kernel(const DecodeArgs a) {
       Lt = fmaf(Lt, al, ml.y * be);
       At = fmaf(At, al, s_acc[q][quarter][lane] * be);
     }
-    *orow = __float2bfloat16_rn(a.kv_scale && Lt == 0.f ? 0.f : At / Lt);
+    *orow = __float2bfloat16_rn(At / Lt);
   } else {
-    // block-scaled caches: a sequence whose every block is out of range gives zeros
-    *orow = __float2bfloat16_rn(a.kv_scale && L == 0.f ? 0.f : acc / L);
+    *orow = __float2bfloat16_rn(acc / L);
   }
 }
 
@@ -1030,29 +1029,6 @@ cudaError_t launch_gather(const DecodeArgs& args, bool fp8, cudaStream_t stream)
              : launch_partition<false, false, true>(a, tm_k, tm_v, attr, stream);
 }
 
-cudaError_t launch_decode_merge(const DecodeArgs& a, int part_ctas, int per_cta, cudaStream_t stream) {
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  // Narrow merge beside the partition kernel; the wide one when the (sequence, query head)
-  // pairs are fewer than the partition kernel's CTAs, so that long segments' many pieces are
-  // spread over more warps.
-  const long long pairs = static_cast<long long>(a.num_seqs) * a.num_q_heads;
-  cudaLaunchConfig_t mcfg = {};
-  mcfg.stream = stream;
-  mcfg.attrs = attr;
-  mcfg.numAttrs = 1;
-  if (pairs <= part_ctas) {
-    mcfg.gridDim = dim3(static_cast<unsigned>(pairs));
-    mcfg.blockDim = dim3(kWideGroups * kMergeSplit * 32);
-    return cudaLaunchKernelEx(&mcfg, decode_merge_kernel<kWideGroups>, a);
-  }
-  const long long merge_warps = pairs * kMergeSplit;
-  mcfg.gridDim = dim3(static_cast<unsigned>((merge_warps + per_cta - 1) / per_cta));
-  mcfg.blockDim = dim3(per_cta * 32);
-  return cudaLaunchKernelEx(&mcfg, decode_merge_kernel<1>, a);
-}
-
 cudaError_t launch_decode(const DecodeArgs& args, cudaStream_t stream) {
   DecodeArgs a = args;
   const int G = a.num_q_heads / a.num_kv_heads;
@@ -1074,10 +1050,27 @@ cudaError_t launch_decode(const DecodeArgs& args, cudaStream_t stream) {
                   : launch_partition<false, false>(a, tm_k, tm_v, attr, stream);
   if (err != cudaSuccess) return err;
 
+  // Narrow merge beside the partition kernel; the wide one when the (sequence, query head)
+  // pairs are fewer than the partition kernel's CTAs, so that long segments' many pieces are
+  // spread over more warps.
+  const long long pairs = static_cast<long long>(a.num_seqs) * a.num_q_heads;
   int part_ctas = 0;
   err = fp8 ? persistent_ctas<false, true>(&part_ctas) : persistent_ctas<false, false>(&part_ctas);
   if (err != cudaSuccess) return err;
-  return launch_decode_merge(a, part_ctas, fp8 ? kMergeWarps / 2 : kMergeWarps, stream);
+  cudaLaunchConfig_t mcfg = {};
+  mcfg.stream = stream;
+  mcfg.attrs = attr;
+  mcfg.numAttrs = 1;
+  if (pairs <= part_ctas) {
+    mcfg.gridDim = dim3(static_cast<unsigned>(pairs));
+    mcfg.blockDim = dim3(kWideGroups * kMergeSplit * 32);
+    return cudaLaunchKernelEx(&mcfg, decode_merge_kernel<kWideGroups>, a);
+  }
+  const long long merge_warps = pairs * kMergeSplit;
+  const int per_cta = fp8 ? kMergeWarps / 2 : kMergeWarps;
+  mcfg.gridDim = dim3(static_cast<unsigned>((merge_warps + per_cta - 1) / per_cta));
+  mcfg.blockDim = dim3(per_cta * 32);
+  return cudaLaunchKernelEx(&mcfg, decode_merge_kernel<1>, a);
 }
 
 }  // namespace pa

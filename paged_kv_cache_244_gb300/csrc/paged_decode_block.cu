@@ -7,7 +7,7 @@
 //
 // The work is cut as in the decode over bf16 caches (decode_split.cuh): one axis of (sequence, KV
 // head, block), an equal contiguous range for each warp of a persistent grid, pieces of split
-// segments merged by decode_merge_kernel.  A warp serves the G <= 8 query heads of its KV head
+// segments merged by a kernel after it.  A warp serves the G <= 8 query heads of its KV head
 // and is its own producer and consumer.  What differs:
 //
 //   Jobs of two blocks.  A 2 KiB tile of codes is little work beside what a job costs whatever its
@@ -592,6 +592,143 @@ decode_block_kernel(const DecodeArgs a, const int pool) {
   }
 }
 
+// Merge of the pieces of split segments: kGroups warps take one (sequence, query head), a lane four of its
+// dims, a warp a contiguous share of the pieces with all rows of 8 or 16 pieces asked for at once; the warps'
+// (M, L, acc) are joined in order.  out = sum_p 2^(m_p - M) acc_p / sum_p 2^(m_p - M) L_p; a gap (shift
+// -inf, sum 0) weighs nothing and its row, never written, is not used.  A piece whose shift stayed at -inf
+// over a sum that is not 0 met NaN only, and passes it on.
+//
+// The partition kernel's registers fill an SM, so the merge runs after it and its own length counts: the
+// dependent round trips (lengths, (m, L) and rows) and the instructions of warps with few pieces each.
+constexpr int kMergeCta = 4;        // warps of a CTA at least
+// Warps of a pair, 16, 4 or 1, by the number of pairs: the fewer there are the more pieces each has, and the
+// more warps the GPU has room for.  Contexts of 2000-2900 tokens, us of the whole call with 16 / 4 / 1:
+// 96 pairs 9.3 / 11.7 / 16.3, 192: 11.0 / 12.3 / 16.4, 384: 15.4 / 13.5 / 15.7, 768: 22.8 / 17.0 / 18.3,
+// 1200: 38.3 / 30.3 / 28.6, 2048: 74.2 / 61.2 / 58.3.
+constexpr int kWidePairs = 304, kMidPairs = 1024;
+
+template <int kGroups>
+__global__ void __launch_bounds__((kGroups > kMergeCta ? kGroups : kMergeCta) * 32)
+decode_block_merge_kernel(const DecodeArgs a) {
+  constexpr int kPairs = kGroups > kMergeCta ? 1 : kMergeCta / kGroups;   // of a CTA
+  constexpr int kMergeRows = kGroups > 1 ? 8 : 16;                        // pieces of a round trip
+  __shared__ float4 s_acc[kGroups > 1 ? kPairs * kGroups : 1][32];
+  __shared__ float2 s_ml[kGroups > 1 ? kPairs * kGroups : 1];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int grp = warp % kGroups;
+  const int S = a.num_seqs, Hq = a.num_q_heads, Hkv = a.num_kv_heads;
+  const int w = blockIdx.x * kPairs + warp / kGroups;                     // (sequence, query head)
+  const int G = Hq / Hkv;
+  const int s = w / Hq, h = w - s * Hq, g = h / G;
+  int before = 0, total = 0, ns = 0;
+  if (w < S * Hq) {
+    for (int t = lane; t < S; t += 32) {
+      const int n = (clamp_len(a.context_lens[t], a.max_context_len) + kBlockSize - 1) / kBlockSize;
+      total += n;
+      if (t < s) before += n;
+    }
+    ns = (clamp_len(a.context_lens[s], a.max_context_len) + kBlockSize - 1) / kBlockSize;
+    before = __reduce_add_sync(kFullMask, before);
+    total = __reduce_add_sync(kFullMask, total);
+  }
+  uint2* const orow = reinterpret_cast<uint2*>(a.out + static_cast<size_t>(w) * kHeadDim) + lane;
+  int k0 = 0, k1 = 0, npieces = 0;
+  const float2* ml = nullptr;
+  const float4* rows = nullptr;
+  if (ns > 0) {
+    const Ranges R = make_ranges(static_cast<long long>(Hkv) * total, a);
+    const long long Xi = static_cast<long long>(Hkv) * before + static_cast<long long>(g) * ns;
+    const int v_first = R.owner(Xi), v_last = R.owner(Xi + ns - 1);
+    npieces = v_last - v_first + (a.chunk_blocks ? (ns - 1) / a.chunk_blocks : 0) + 1;
+    const size_t row = static_cast<size_t>(piece_slot(v_first, s * Hkv + g, 0, a.max_parts)) * G + (h - g * G);
+    ml = a.ws_ml + row;
+    rows = reinterpret_cast<const float4*>(a.ws_o + row * kHeadDim) + lane;
+    k0 = static_cast<int>(static_cast<long long>(grp) * npieces / kGroups);
+    k1 = static_cast<int>(static_cast<long long>(grp + 1) * npieces / kGroups);
+  }
+  pdl_wait_prior_grid();
+  pdl_allow_next_grid();
+  // one piece: written directly by the partition kernel
+  const bool merges = npieces > 1;
+  float M = -INFINITY, L = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int base = k0; merges && base < k1; base += kMergeRows) {
+    const int n = min(kMergeRows, k1 - base);
+    const float2 mine = lane < n ? ml[(base + lane) * static_cast<size_t>(G)] : make_float2(-INFINITY, 0.f);
+    float4 r[kMergeRows];
+#pragma unroll
+    for (int c = 0; c < kMergeRows; c += 4) {
+      if (c < n) {
+#pragma unroll
+        for (int u = c; u < c + 4; ++u)
+          if (u < n) r[u] = rows[static_cast<size_t>(base + u) * G * (kHeadDim / 4)];
+      }
+    }
+    float Mb = mine.x;
+#pragma unroll
+    for (int x = kMergeRows / 2; x > 0; x >>= 1) Mb = fmaxf(Mb, __shfl_xor_sync(kFullMask, Mb, x));
+    Mb = __shfl_sync(kFullMask, Mb, 0);
+    const float Mn = fmaxf(M, Mb);
+    const float rescale = M == -INFINITY ? 1.f : exp2f(M - Mn);           // 1: nothing but zeros or NaN so far
+    M = Mn;
+    const float wmine = mine.x == -INFINITY ? (mine.y == 0.f ? 0.f : mine.y) : exp2f(mine.x - M);
+    float lb = wmine * mine.y;
+#pragma unroll
+    for (int x = kMergeRows / 2; x > 0; x >>= 1) lb += __shfl_xor_sync(kFullMask, lb, x);
+    L = fmaf(L, rescale, __shfl_sync(kFullMask, lb, 0));
+    acc.x *= rescale;
+    acc.y *= rescale;
+    acc.z *= rescale;
+    acc.w *= rescale;
+#pragma unroll
+    for (int c = 0; c < kMergeRows; c += 4) {
+      if (c < n) {
+#pragma unroll
+        for (int u = c; u < c + 4; ++u) {
+          const float wu = __shfl_sync(kFullMask, wmine, u);              // 0 past the last piece
+          if (wu != 0.f) {
+            acc.x = fmaf(wu, r[u].x, acc.x);
+            acc.y = fmaf(wu, r[u].y, acc.y);
+            acc.z = fmaf(wu, r[u].z, acc.z);
+            acc.w = fmaf(wu, r[u].w, acc.w);
+          }
+        }
+      }
+    }
+  }
+  if constexpr (kGroups > 1) {
+    s_acc[warp][lane] = acc;
+    if (lane == 0) s_ml[warp] = make_float2(M, L);
+    __syncthreads();
+    if (grp != 0) return;
+    // lane q weighs group q (one without pieces, or with gaps alone, has L = 0); the sum in their order
+    const float2 o = lane < kGroups ? s_ml[warp + lane] : make_float2(-INFINITY, 0.f);
+    M = o.x;
+#pragma unroll
+    for (int x = kGroups / 2; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, x));
+    M = __shfl_sync(kFullMask, M, 0);
+    const float mine = o.x == -INFINITY ? (o.y == 0.f ? 0.f : o.y) : exp2f(o.x - M);
+    L = mine * o.y;
+#pragma unroll
+    for (int x = kGroups / 2; x > 0; x >>= 1) L += __shfl_xor_sync(kFullMask, L, x);
+    L = __shfl_sync(kFullMask, L, 0);
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int q = 0; q < kGroups; ++q) {
+      const float wq = __shfl_sync(kFullMask, mine, q);
+      const float4 v = s_acc[warp + q][lane];
+      acc.x = fmaf(wq, v.x, acc.x);
+      acc.y = fmaf(wq, v.y, acc.y);
+      acc.z = fmaf(wq, v.z, acc.z);
+      acc.w = fmaf(wq, v.w, acc.w);
+    }
+  }
+  if (w >= S * Hq || (ns > 0 && !merges)) return;
+  // no context, or a sequence whose every block is out of range: zeros
+  const float i = L == 0.f ? 0.f : 1.f / L;
+  *orow = make_uint2(pack_bf16x2(acc.x * i, acc.y * i), pack_bf16x2(acc.z * i, acc.w * i));
+}
+
 // CTAs of the persistent grid: one per SM, capped to kMaxDecodeWarps warps (looked up once per
 // device, with the shared-memory opt-in of every variant).
 cudaError_t block_ctas(int* ctas) {
@@ -652,7 +789,15 @@ cudaError_t launch_decode_block(const DecodeArgs& args, cudaStream_t stream) {
                      : decode_block_kernel<false, false>;
   err = cudaLaunchKernelEx(&cfg, kernel, a, pool);
   if (err != cudaSuccess) return err;
-  return launch_decode_merge(a, max_ctas, 4, stream);
+  const long long pairs = static_cast<long long>(a.num_seqs) * a.num_q_heads;
+  const int groups = pairs <= kWidePairs ? 16 : pairs <= kMidPairs ? 4 : 1;
+  const int per_cta = groups > kMergeCta ? groups : kMergeCta;
+  cfg.gridDim = dim3(static_cast<unsigned>((pairs * groups + per_cta - 1) / per_cta));
+  cfg.blockDim = dim3(static_cast<unsigned>(per_cta * 32));
+  cfg.dynamicSmemBytes = 0;
+  auto merge = groups == 16 ? decode_block_merge_kernel<16>
+               : groups == 4 ? decode_block_merge_kernel<4> : decode_block_merge_kernel<1>;
+  return cudaLaunchKernelEx(&cfg, merge, a);
 }
 
 }  // namespace pa

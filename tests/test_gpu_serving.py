@@ -357,6 +357,22 @@ def test_decode_sizes(pa, S, n):
     clean(pa)
 
 
+@pytest.mark.parametrize("P", [0, 64])
+@pytest.mark.parametrize("S,hq,kv", [(3, 12, 2), (40, 12, 2), (64, 10, 2), (700, 8, 1)])
+def test_decode_one_long_sequence_among_short_ones(pa, S, hq, kv, P):
+    """Hundreds of pieces in one sequence and one in the others, in each form of the merge."""
+    rng = np.random.default_rng(S + P)
+    lens = [6000] + [int(x) for x in rng.integers(0, 40, S - 1)]
+    pool = Pool(rng, lens, kv)
+    q = normal(rng, S, hq, D)
+    out = pa.decode_fp8_block(bf16(q), *pool.dev(), up(pool.tables), up(pool.lens), 6000, D ** -0.5, partition_tokens=P)
+    for s in range(0, S, max(1, S // 12)):
+        ref, mag = pool.attention(s, q[s:s + 1], D ** -0.5)
+        close(out[s:s + 1], ref, mag, s)
+    assert not f64(out[torch.from_numpy(np.array(lens) == 0).cuda()]).any()
+    clean(pa)
+
+
 def test_decode_scales_far_apart_and_of_any_value(pa):
     """Blocks whose V scale is 2^-40 (zeros) carry most of the weight; scales that are no powers of
     two; K scales that make scores large."""
