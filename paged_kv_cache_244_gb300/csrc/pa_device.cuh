@@ -424,12 +424,6 @@ __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// E4M3 codes of two floats, round to nearest even, saturating; low byte = lo.
-__device__ __forceinline__ uint16_t e4m3x2_of_floats(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 
 // a b - c d in fp32 with the rounding error of c d recovered by an FMA (the compensated
 // difference of products: w = c d rounded, e = w - c d exactly, result (a b - w) + e).  Within

@@ -38,16 +38,22 @@
 // V codes, two 16 KiB stages of f16 V, barriers, the scales of 8 stages: 106 KiB.  Every wait is
 // bounded.
 //
-// What bounds it: the shared-memory data path.  A first form that widened K too and gave each
-// thread its own row of q and out to load and store kept that path 88% busy (ncu, 4 x 2048
-// tokens: LSU 68.6% of its wavefronts, tensor core 19.6%) with the tensor pipe 26% active, 87 us.
+// What bounds it: the path of shared and tensor memory in an SM, 90% busy (ncu, 4 x 2048 tokens, 12 / 2
+// heads: loads and stores 53.7% of its wavefronts, the tensor core's reads of A and B 18.4% each) with
+// the tensor pipe 37% active.  A tile of 128 rows and 64 keys puts q hi and lo (32 KiB), K twice (16),
+// f16 V (16), S out (32), P in (16), the codes of V in and f16 V out (24) and the TMA's writes (16) on
+// it.  4 x 2048 tokens: 62.8 us, 42% of the measured bf16 peak; 16 chunks of 256
+// over 1792: 61.1 us.  A first form that widened K too and gave each thread its own row of q and out to
+// load and store: 87 us.  Measured and left: S of two stages by one product of 128 keys (a q operand read
+// half as often, but S no longer double: 71 us); two threads a row, 16 softmax warps on an SM (65 us);
+// one lane waiting for its warp at barriers (92 us); eight warps preparing q (65 us).
 
 // Few tiles over a long context: a tile's stages are split over a cluster of 2, 4 or 8 CTAs
 // (template kSplit; CTA r of C takes stages nst r / C .. nst (r + 1) / C).  The CTAs exchange each
 // row's (m, L) through distributed shared memory, scale their O to the common shift, and CTA r
 // collects dims 128 r / C .. of every row from all of them, in rank order: no workspace, one launch,
-// the same sums whatever the timing.  (11 sequences of one new token after 10,812 cached, 28 / 4 heads:
-// 142.8 us unsplit.)
+// the same sums whatever the timing.  11 sequences of one new token after 10,812 cached, 28 / 4 heads:
+// 48.5 us, 142.8 unsplit; 4 of 71 after 2342, 32 / 8 heads: 32.
 
 #include <mutex>
 
@@ -77,8 +83,8 @@ constexpr int kBpFoldOff = kBpHdrOff + kBpHeader;    // a float per row
 constexpr int kBpScaleOff = kBpFoldOff + kBpRows * 4;   // a float4 per block of the stage, stage j in slot j % 8
 constexpr int kBpScaleSlots = 8;
 constexpr int kBpMlOff = kBpScaleOff + kBpScaleSlots * kBpKB * 16;   // split: a row's (m, L)
-constexpr int kBpSmem = kBpMlOff + kBpRows * 8 + 1024;
-static_assert(kBpRows * kHeadDim * 4 <= kBpHdrOff, "the partial rows of a split tile fit the stages");  // + alignment of the first stage
+constexpr int kBpSmem = kBpMlOff + kBpRows * 8 + 1024;   // + alignment of the first stage
+static_assert(kBpRows * kHeadDim * 4 <= kBpHdrOff, "the partial rows of a split tile fit the stages");
 static_assert(2 * (kBpSmem + 1024) <= 228 * 1024, "two CTAs per SM");
 constexpr int kBpThreads = 384;
 // registers per thread at launch, and the split (their sums per warpgroup are equal)
