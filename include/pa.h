@@ -390,7 +390,7 @@ typedef struct pa_rope_scaling {
   double factor;            /* finite and >= 1 (read by every kind but NONE) */
   double original_max_pos;  /* YARN, BANDED: finite and > 0 */
   double low, high;         /* YARN, BANDED: turns, 0 < low < high, finite */
-  double magnitude;         /* YARN: factor on cos and sin, finite and >= 0 (0: 0.1 ln(factor) + 1) */
+  double magnitude;         /* YARN: factor on cos and sin, >= 0 and finite in fp32 (0: 0.1 ln(factor) + 1) */
   int32_t kind;             /* PA_ROPE_SCALE_* */
 } pa_rope_scaling;
 
@@ -460,7 +460,9 @@ int pa_rope_kv_store_fp8_block(const pa_dims* dims, const pa_rope* rope, int num
 /*
  * pa_decode_fp8_block -- pa_decode over block-scaled E4M3 caches.  Arguments, workspace (same
  * size: pa_decode_workspace_size), checks and errors as pa_decode, plus kv_scale ([num_blocks]
- * [Hkv][2] fp32, read only).  Launches one kernel plus the merge.
+ * [Hkv][2] fp32, read only).  q enters the products in f16 after a power of two for each head, so
+ * any finite magnitude does; an infinity or a NaN in it makes its head's row NaN.  A sequence whose
+ * every block is out of range gives zeros.  Launches one kernel plus the merge.
  */
 int pa_decode_fp8_block(const pa_dims* dims, int num_seqs, const void* q, const void* k_cache,
                         const void* v_cache, const float* kv_scale, int num_blocks,
@@ -522,7 +524,9 @@ int pa_prefill_fp8_block(const pa_dims* dims, int num_seqs, int num_tokens, cons
  *   free list    num_free_out[0] = F - (new entries granted); free_blocks is not written, the
  *                ids at or past num_free_out[0] are the ones in use
  * Nothing else of block_tables is written.  The block a sequence's tokens continue (c % 16 != 0)
- * must not be shared.
+ * must not be shared.  A call with PA_STEP_EARLY_METADATA may not be the next on the stream: it
+ * reads the lengths and tables before this kernel has ended (a first layer without the flag, or a
+ * store, between the two is enough).
  * Device-side errors: c < 0, n < 0 or > num_tokens, c + n > max_blocks * 16, or rows past
  * num_tokens -> the sequence is refused and needs no block (an n out of range counts as 0 rows;
  * q_start stops at num_tokens), PA_FLAG_CONTEXT_LEN_OOB; num_free[0] outside [0, free_capacity]

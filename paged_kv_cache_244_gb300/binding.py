@@ -537,12 +537,18 @@ def _layout(layout):
         raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}, got {layout!r}") from None
 
 
-def _kept(stream, *tensors):
-    """Tensors allocated by a call that runs on `stream`: their memory is not handed out again
-    before that stream has passed the call."""
-    if stream is not None:
-        for t in tensors:
-            t.record_stream(stream)
+def _on(stream, allocate):
+    """The tensor (or tuple of them) that a call on `stream` allocates: from that stream's memory, which
+    earlier work of the current stream cannot still be using, and not handed out again before the
+    current stream has passed its release either."""
+    if stream is None:
+        return allocate()
+    current = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        made = allocate()
+    for t in made if isinstance(made, tuple) else (made,):
+        t.record_stream(current)
+    return made
 
 
 def rope_table(max_pos, rotary_dim=128, theta=1e4, scaling="none", factor=1.0, original_max_pos=0,
@@ -554,8 +560,7 @@ def rope_table(max_pos, rotary_dim=128, theta=1e4, scaling="none", factor=1.0, o
     if scaling not in ROPE_SCALINGS:
         raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}, got {scaling!r}")
     if out is None:
-        out = torch.empty((max_pos, rotary_dim), dtype=torch.float32, device="cuda")
-        _kept(stream, out)
+        out = _on(stream, lambda: torch.empty((max_pos, rotary_dim), dtype=torch.float32, device="cuda"))
     _check(_native().rope_table(ROPE_SCALINGS[scaling], theta, factor, original_max_pos, low, high, magnitude,
                                 rotary_dim, max_pos, out, _handle(stream)), "pa_rope_table")
     return out
@@ -591,13 +596,11 @@ def decode_fp8_block(q, k_cache, v_cache, kv_scale, block_tables, context_lens, 
     """Decode attention over block-scaled E4M3 caches (pa_decode_fp8_block).  Returns out
     [S, Hq, D] bf16; workspace as for decode()."""
     if out is None:
-        out = torch.empty_like(q)
-        _kept(stream, out)
+        out = _on(stream, lambda: torch.empty_like(q))
     if q.shape[0] == 0:
         return out
     if workspace is None:
-        workspace = decode_workspace(q, k_cache, max_context_len, partition_tokens)
-        _kept(stream, workspace)
+        workspace = _on(stream, lambda: decode_workspace(q, k_cache, max_context_len, partition_tokens))
     _check(_native().decode_fp8_block(q, k_cache, v_cache, kv_scale, block_tables, context_lens,
                                       max_context_len, scale, partition_tokens, workspace, out,
                                       _handle(stream)), "pa_decode_fp8_block")
@@ -610,13 +613,11 @@ def decode_step_fp8_block(q, k, v, cos_sin, k_cache, v_cache, kv_scale, block_ta
     """The fused decode step over block-scaled E4M3 caches with a RoPE form
     (pa_decode_step_fp8_block; q left unchanged); early_metadata as for decode_step."""
     if out is None:
-        out = torch.empty_like(q)
-        _kept(stream, out)
+        out = _on(stream, lambda: torch.empty_like(q))
     if q.shape[0] == 0:
         return out
     if workspace is None:
-        workspace = decode_workspace(q, k_cache, max_context_len, partition_tokens)
-        _kept(stream, workspace)
+        workspace = _on(stream, lambda: decode_workspace(q, k_cache, max_context_len, partition_tokens))
     _check(_native().decode_step_fp8_block(q, k, v, cos_sin, k_cache, v_cache, kv_scale, block_tables,
                                            context_lens, max_context_len, scale, _layout(layout),
                                            partition_tokens, workspace, out,
@@ -630,8 +631,7 @@ def prefill_fp8_block(q, q_start, k_cache, v_cache, kv_scale, block_tables, cont
     """Paged (chunked) prefill attention over block-scaled E4M3 caches (pa_prefill_fp8_block).
     Returns out [T, Hq, D] bf16; arguments as for prefill()."""
     if out is None:
-        out = torch.empty_like(q)
-        _kept(stream, out)
+        out = _on(stream, lambda: torch.empty_like(q))
     _check(_native().prefill_fp8_block(q, q_start, k_cache, v_cache, kv_scale, block_tables, context_lens,
                                        max_query_len, max_context_len, scale, out, _handle(stream)),
            "pa_prefill_fp8_block")
@@ -664,8 +664,7 @@ def plan_step(cached_lens, new_lens, block_tables, free_blocks, num_free, num_bl
     num_tokens rows.  num_free_out ([1] int32) receives what is left; None means num_free itself.
     """
     if plan is None:
-        plan = step_plan(cached_lens.shape[0], num_tokens, cached_lens.device)
-        _kept(stream, *plan)
+        plan = _on(stream, lambda: step_plan(cached_lens.shape[0], num_tokens, cached_lens.device))
     if num_free_out is None:
         num_free_out = num_free
     _check(_native().plan_step(cached_lens, new_lens, block_tables, free_blocks, num_free, num_free_out, num_blocks,

@@ -625,6 +625,7 @@ int pa_rope_table(const pa_rope_scaling* scaling, int rotary_dim, int max_pos, f
   if (s.kind == PA_ROPE_SCALE_YARN) {
     if (!(s.magnitude >= 0.0) || !std::isfinite(s.magnitude)) return PA_ERR_RANGE;
     a.magnitude = static_cast<float>(s.magnitude > 0.0 ? s.magnitude : 0.1 * std::log(s.factor) + 1.0);
+    if (!std::isfinite(a.magnitude)) return PA_ERR_RANGE;
   }
   if (!aligned16(cos_sin)) return PA_ERR_ALIGN;
   for (int i = 0; i < rotary_dim / 2; ++i) {

@@ -147,7 +147,7 @@ def test_table_refusals(pa):
     nan, inf = float("nan"), float("inf")
     for bad in (dict(theta=1.0), dict(theta=nan), dict(theta=inf), dict(factor=0.5), dict(factor=nan), dict(factor=inf),
                 dict(original_max_pos=0.0), dict(low=0.0), dict(high=1.0), dict(high=inf), dict(low=nan),
-                dict(magnitude=-1.0), dict(magnitude=nan), dict(kind=5), dict(kind=-1), dict(kind=4, original_max_pos=nan)):
+                dict(magnitude=-1.0), dict(magnitude=nan), dict(magnitude=1e300), dict(kind=5), dict(kind=-1), dict(kind=4, original_max_pos=nan)):
         assert call(**bad) == pa.PA_ERR_RANGE, bad
 
 
