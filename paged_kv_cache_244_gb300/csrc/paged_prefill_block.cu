@@ -42,12 +42,14 @@
 // heads: loads and stores 53.7% of its wavefronts, the tensor core's reads of A and B 18.4% each) with
 // the tensor pipe 37% active.  A tile of 128 rows and 64 keys puts q hi and lo (32 KiB), K twice (16),
 // f16 V (16), S out (32), P in (16), the codes of V in and f16 V out (24) and the TMA's writes (16) on
-// it.  4 x 2048 tokens: 62.8 us, 42% of the measured bf16 peak; 16 chunks of 256
-// over 1792: 61.1 us.  A first form that widened K too and gave each thread its own row of q and out to
-// load and store: 87 us.  Measured and left: S of two stages by one product of 128 keys (a q operand read
-// half as often, but S no longer double: 71 us); two threads a row, 16 softmax warps on an SM (65 us);
-// one lane waiting for its warp at barriers (92 us); eight warps preparing q (65 us).
-
+// it.  4 x 2048 tokens: 61.8 us, 0.43 of the measured bf16 peak; 16 chunks of 256 over 1792: 59.6 us.  A
+// first form that widened K too and gave each thread its own row of q and out to load and store: 87 us.
+// Measured and left: S of two stages by one product of 128 keys (a q operand read half as often, but S
+// no longer double: 71 us); two threads a row, 16 softmax warps on an SM (65 us); one lane waiting for its
+// warp at barriers (92 us); eight warps preparing q (65 us); all of q asked for at once, or ahead of the
+// set-up barrier (no change); pairs of CTAs on two SMs sharing B (M = 256: the path is then half idle, but
+// a stage's eight products with N = 64 take as long as before and each hand-over crosses the cluster: 66).
+//
 // Few tiles over a long context: a tile's stages are split over a cluster of 2, 4 or 8 CTAs
 // (template kSplit; CTA r of C takes stages nst r / C .. nst (r + 1) / C).  The CTAs exchange each
 // row's (m, L) through distributed shared memory, scale their O to the common shift, and CTA r
@@ -106,7 +108,7 @@ constexpr int kVFree = kVFull + 8 * kBpVRing;        // MMA (P V done) -> conver
 constexpr int kSFull = kVFree + 8 * kBpVRing;        // [2] MMA (S done) -> softmax
 constexpr int kPFull = kSFull + 16;                  // [2] softmax (a warp each: 4) -> MMA
 constexpr int kDone = kPFull + 16;                   // MMA: its last MMAs finished
-constexpr int kQReady = kDone + 8;                   // softmax (128) -> MMA
+constexpr int kQReady = kDone + 8;                   // softmax (one thread, all rows in place) -> MMA
 constexpr int kTmemAt = kQReady + 8;
 static_assert(kTmemAt + 4 <= kBpHeader, "header");
 
@@ -214,7 +216,7 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       mbar_init(hdr + kSFull + 8 * i, 1);
     }
     mbar_init(hdr + kDone, 1);
-    mbar_init(hdr + kQReady, 128);
+    mbar_init(hdr + kQReady, 1);
     fence_mbar_init();
   }
   if (warp == 0) {
@@ -368,31 +370,31 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       auto wait_all = [&](uint32_t bar, uint32_t parity) {
         return __all_sync(kFullMask, mbar_wait_parked(bar, parity));
       };
-      // S_j = Q K_j^T once K_j has landed (its columns hold P_{j-2}, read by P V issued before)
+      // K_j, V_j are there.  A look at a barrier takes 100 to 150 cycles even when its phase is over, so these
+      // come before the wait for P, off the chain from P_j to S_{j+2} (4 x 2048 tokens: 62.7 -> 61.7 us).
+      auto k_there = [&](int j) { return wait_all(hdr + kKFull + 8 * (j % kBpKRing), (j / kBpKRing) & 1); };
+      auto v_there = [&](int j) { return wait_all(hdr + kVFull + 8 * (j % kBpVRing), (j / kBpVRing) & 1); };
+      // one lane: S_j = Q K_j^T (its columns hold P_{j-2}, read by P V issued before)
       auto issue_s = [&](int j) {
         const int st = j % kBpKRing;
-        if (!wait_all(hdr + kKFull + 8 * st, (j / kBpKRing) & 1)) return false;
-        tc_fence_after();
         const uint64_t kd = k_desc0 + static_cast<uint64_t>((st * kBpCodes) >> 4);
-        if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)            // q hi, then q lo, over the four 32-dim steps of K
-            umma_e4m3(tmem + kBpSCols * (j & 1), q_desc + static_cast<uint64_t>(((kk >> 2) * kBpQBytes + (kk & 3) * 32) >> 4),
-                      kd + static_cast<uint64_t>(((kk & 3) * 32) >> 4), id_s, kk > 0);
-          umma_commit(hdr + kSFull + 8 * (j & 1));
-          umma_commit(hdr + kKFree + 8 * st);
-        }
-        __syncwarp();
-        return true;
+        for (int kk = 0; kk < 8; ++kk)              // q hi, then q lo, over the four 32-dim steps of K
+          umma_e4m3(tmem + kBpSCols * (j & 1), q_desc + static_cast<uint64_t>(((kk >> 2) * kBpQBytes + (kk & 3) * 32) >> 4),
+                    kd + static_cast<uint64_t>(((kk & 3) * 32) >> 4), id_s, kk > 0);
+        umma_commit(hdr + kSFull + 8 * (j & 1));
+        umma_commit(hdr + kKFree + 8 * st);
       };
       bool failed = !wait_all(hdr + kQReady, 0);
-      if (!failed) {
+      for (int j = 0; j < 2 && j < nst && !failed; ++j) {
+        failed = !k_there(j);
         tc_fence_after();
-        failed = (nst > 0 && !issue_s(0)) || (nst > 1 && !issue_s(1));
+        if (!failed && elect_one()) issue_s(j);
+        __syncwarp();
       }
       for (int j = 0; j < nst && !failed; ++j) {
         const int st = j % kBpVRing;
-        if (!wait_all(hdr + kPFull + 8 * (j & 1), (j >> 1) & 1) || !wait_all(hdr + kVFull + 8 * st, (j / kBpVRing) & 1)) {
+        if (!v_there(j) || (j + 2 < nst && !k_there(j + 2)) || !wait_all(hdr + kPFull + 8 * (j & 1), (j >> 1) & 1)) {
           failed = true;
           break;
         }
@@ -403,9 +405,9 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
           for (int i = 0; i < kBpKB; ++i)
             umma_bf16_tmem_a(tmem + kBpOCol, tmem + kBpSCols * (j & 1) + 8 * i, vd + static_cast<uint64_t>((i * 2 * kBpTile) >> 4), id_pv, j > 0 || i > 0);
           umma_commit(hdr + kVFree + 8 * st);
+          if (j + 2 < nst) issue_s(j + 2);
         }
         __syncwarp();
-        if (j + 2 < nst && !issue_s(j + 2)) failed = true;
       }
       if (lane == 0) {
         if (failed) raise_flag(a.status, PA_FLAG_TIMEOUT);
@@ -480,8 +482,8 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         }
       }
       fence_proxy_async_smem();                     // before the tensor core reads them
-      mbar_arrive(hdr + kQReady);
-      named_barrier(1, 128);                        // the rows' factors are in place
+      named_barrier(1, 128);                        // the rows and their factors are in place
+      if (r == 0) mbar_arrive(hdr + kQReady);
     }
     const float row_fold = folds[r];                // q = row_fold (hi + lo)
     float m = -INFINITY, l = 0.f;
