@@ -542,7 +542,7 @@ int pa_prefill_fp8_block(const pa_dims* dims, int num_seqs, int num_tokens, cons
  *   free_blocks    [free_capacity] int32, read only; free_capacity >= 0
  *   num_free       [1] int32;  num_free_out [1] int32, may be num_free itself
  *   num_blocks     >= 1
- *   num_tokens     rows of positions and slot_mapping, >= 0
+ *   num_tokens     rows of positions and slot_mapping, 0 <= T <= 2^31 - 16
  *   context_lens   [S] int32, written; not cached_lens or new_lens
  *   q_start        [S + 1] int32, written
  *   positions      [num_tokens] int32;  slot_mapping [num_tokens] int64, written

@@ -645,7 +645,7 @@ int pa_plan_step(const pa_dims* dims, int num_seqs, const int32_t* cached_lens,
                  int32_t* q_start, int32_t* positions, int64_t* slot_mapping, int32_t* granted,
                  void* stream) {
   if (const int rc = check_dims(dims)) return rc;
-  if (num_seqs < 0 || num_seqs > pa::kMaxDecodeSeqs || num_tokens < 0) return PA_ERR_RANGE;
+  if (num_seqs < 0 || num_seqs > pa::kMaxDecodeSeqs || num_tokens < 0 || num_tokens > 0x7ffffff0) return PA_ERR_RANGE;
   if (free_capacity < 0 || num_blocks < 1 || max_blocks < 1 || max_blocks > (0x7fffffff - 15) / 16)
     return PA_ERR_RANGE;
   if (!num_free || !num_free_out || !q_start) return PA_ERR_NULL;

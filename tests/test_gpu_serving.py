@@ -426,6 +426,51 @@ def test_decode_is_reproducible_and_leaves_other_streams_alone(pa):
     assert np.array_equal(bits(first), bits(second))
 
 
+def test_two_streams_at_once_and_two_graphs_over_one_workspace(pa):
+    """Calls in flight together on streams of their own, and two captured graphs that share a workspace
+    and are replayed in turn: the bits of a lone call."""
+    rng = np.random.default_rng(14)
+    jobs = []
+    for S, hq, kv, n in ((40, 12, 2, 2500), (3, 28, 4, 6000)):
+        lens = [int(x) for x in rng.integers(n // 2, n, S)]
+        pool = Pool(rng, lens, kv)
+        q = bf16(normal(rng, S, hq, D))
+        args = (*pool.dev(), up(pool.tables), up(pool.lens))
+        jobs.append((q, args, max(lens), up(np.arange(S + 1, dtype=np.int32))))
+    ws = max((pa.decode_workspace(q, a[0], n) for q, a, n, _ in jobs), key=lambda t: t.numel())
+
+    def decode(job, out, **kw):
+        q, a, n, _ = job
+        return pa.decode_fp8_block(q, *a, n, D ** -0.5, out=out, **kw)
+
+    def prefill(job, out, **kw):
+        q, a, n, starts = job
+        return pa.prefill_fp8_block(q, starts, *a, 1, n, D ** -0.5, out=out, **kw)
+
+    alone = [[bits(call(job, torch.empty_like(job[0]))) for call in (decode, prefill)] for job in jobs]
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    outs = [torch.empty_like(job[0]) for job in jobs for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for i, st in enumerate(streams):
+            (prefill if i % 2 else decode)(jobs[i // 2], outs[i], stream=st)
+    torch.cuda.synchronize()
+    for i, o in enumerate(outs):
+        assert np.array_equal(bits(o), alone[i // 2][i % 2]), i
+    graphs = []
+    for job, out in zip(jobs, outs[::2]):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            decode(job, out, workspace=ws)
+        graphs.append(g)
+    for _ in range(3):
+        for i, g in enumerate(graphs):
+            outs[2 * i].zero_()
+            g.replay()
+            assert np.array_equal(bits(outs[2 * i]), alone[i][0])
+    clean(pa)
+
+
 def test_many_sequences(pa):
     """The most sequences a call takes: their prefix leaves fewer stages, and so fewer warps, to a CTA."""
     rng = np.random.default_rng(40)

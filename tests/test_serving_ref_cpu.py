@@ -185,7 +185,7 @@ def test_plan_refusals(pa):
         a.update(k)
         return pa.lib().pa_plan_step(a["d"], a["S"], a["c"], a["n"], a["bt"], a["mb"], a["fb"], a["cap"], a["nf"], a["nfo"],
                                      a["nb"], a["T"], a["cx"], a["qs"], a["ps"], a["sl"], a["gr"], None)
-    for bad in (dict(S=-1), dict(S=8193), dict(T=-1), dict(cap=-1), dict(nb=0), dict(mb=0), dict(mb=1 << 27), dict(cx=A)):
+    for bad in (dict(S=-1), dict(S=8193), dict(T=-1), dict(T=2 ** 31 - 1), dict(cap=-1), dict(nb=0), dict(mb=0), dict(mb=1 << 27), dict(cx=A)):
         assert call(**bad) == pa.PA_ERR_RANGE, bad
     for name in ("c", "n", "bt", "fb", "nf", "nfo", "cx", "qs", "ps", "sl", "gr"):
         assert call(**{name: None}) == pa.PA_ERR_NULL, name
