@@ -74,22 +74,22 @@ METRIC = "paged GQA decode: KV-cache HBM GB/s (% of GB300 peak) and attention to
 # the step form and a hash of the CUDA sources it was taken on: once a kernel changes, the
 # hash no longer matches and roofline.traffic is reported as null until it is captured again.
 MEASURED_TRAFFIC = {
-    ("mix64", "fused", "66bc39d37e6f7fac"): 122108928 + 3006464 + 4185600,
-    ("prefix32", "fused", "66bc39d37e6f7fac"): 4348672 + 0 + 3823360,
-    ("long4", "fused", "66bc39d37e6f7fac"): 83981056 + 2105088 + 4823040,
+    ("mix64", "fused", "a57b162c514740ea"): 122119680 + 2944256 + 4185600,
+    ("prefix32", "fused", "a57b162c514740ea"): 4347904 + 0 + 3823616,
+    ("long4", "fused", "a57b162c514740ea"): 83982080 + 2106368 + 4823552,
 }
 FLUSH_BYTES = 512 << 20
 FALLBACK_HBM_GBS = 6800.0
 
 
 def kernel_source_hash() -> str:
-    """Hash of the code the decode kernels compile from (their file, the device helpers, the
-    launch header), with comments and whitespace removed: editing a comment keeps the hash."""
+    """Hash of the code the decode kernels compile from (their file, the split, the device helpers,
+    the launch header), with comments and whitespace removed: editing a comment keeps the hash."""
     import hashlib
     import re
     csrc = ROOT / "paged_kv_cache_244_gb300" / "csrc"
     h = hashlib.sha256()
-    for name in ("paged_decode.cu", "pa_device.cuh", "pa_launch.h"):
+    for name in ("paged_decode.cu", "decode_split.cuh", "pa_device.cuh", "pa_launch.h"):
         text = (csrc / name).read_text()
         text = re.sub(r"/\*.*?\*/", " ", text, flags=re.S)
         text = re.sub(r"//[^\n]*", " ", text)

@@ -35,10 +35,10 @@
 //   p_t: a block of tiny V scale (an attention sink) may carry most of the weight with a p_t below
 //   f16.
 //
-// What bounds it: 64 sequences of 64-4096 tokens, us replayed from a graph.  12 / 2 heads (66 MB): 19.8,
+// What bounds it: 64 sequences of 64-4096 tokens, us replayed from a graph.  12 / 2 heads (66 MB): 19.5,
 // of which 2.9 before the first tile (lengths, table, tile: dependent cold reads), some 10 streaming at the
 // copy rate, 2.4 between the first SM done and the last, the rest launch and merge; a kernel that only
-// gathers the same tiles takes 13.7.  Fused step with 32 / 8 heads (276 MB): 53.1, 5.2 TB/s (gather 43.8).
+// gathers the same tiles takes 13.7.  Fused step with 32 / 8 heads (276 MB): 52.8, 5.2 TB/s (gather 43.8).
 // One sequence of 2048 tokens: 6.4, latency (an empty kernel: 1.9).
 //
 // Per stage: [K tile 0 | K tile 1 | V tile 0 | V tile 1 | q rows | (step) cos/sin row, k row, v row];
@@ -605,7 +605,9 @@ decode_block_kernel(const DecodeArgs a, const int pool) {
 // over a sum that is not 0 met NaN only, and passes it on.
 //
 // The partition kernel's registers fill an SM, so the merge runs after it and its own length counts: the
-// dependent round trips (lengths, (m, L) and rows) and the instructions of warps with few pieces each.
+// dependent round trips (lengths, (m, L) and rows) and the instructions of warps with few pieces each.  Four
+// warps a pair: six CTAs an SM take the 768 pairs of 64 sequences with 12 heads in one wave (call 19.5 us;
+// 19.9 with the 64 registers that eight want, 20.9 where the compiler chooses).
 constexpr int kMergeCta = 4;        // warps of a CTA at least
 // Warps of a pair, 16, 4 or 1, by the number of pairs: the fewer there are the more pieces each has, and the
 // more warps the GPU has room for.  Contexts of 2000-2900 tokens, us of the whole call with 16 / 4 / 1:
@@ -614,7 +616,7 @@ constexpr int kMergeCta = 4;        // warps of a CTA at least
 constexpr int kWidePairs = 304, kMidPairs = 1024;
 
 template <int kGroups>
-__global__ void __launch_bounds__((kGroups > kMergeCta ? kGroups : kMergeCta) * 32)
+__global__ void __launch_bounds__((kGroups > kMergeCta ? kGroups : kMergeCta) * 32, kGroups == kMergeCta ? 6 : 1)
 decode_block_merge_kernel(const DecodeArgs a) {
   constexpr int kPairs = kGroups > kMergeCta ? 1 : kMergeCta / kGroups;   // of a CTA
   constexpr int kMergeRows = kGroups > 1 ? 8 : 16;                        // pieces of a round trip
