@@ -59,13 +59,13 @@ __device__ __forceinline__ int clamp_len(int len, int max_len) {
 }
 
 // Exclusive prefix N_s of per-sequence block counts, and the valid rows of each sequence's last
-// block, by the whole CTA (kWarps warps at most); raises the flag of lengths out of range.
+// block, by the whole CTA (of `threads` threads, kWarps warps at most); raises the flag of lengths out of range.
 template <int kWarps>
-__device__ __forceinline__ void build_prefix(const DecodeArgs& a, int* prefix, unsigned char* last_rows) {
+__device__ __forceinline__ void build_prefix(const DecodeArgs& a, int* prefix, unsigned char* last_rows,
+                                             const int threads = kWarps * 32) {
   const int S = a.num_seqs;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   __shared__ int warp_sums[kWarps];
-  const int threads = blockDim.x;
   const int per = (S + threads - 1) / threads;
   const int lo = min(S, tid * per), hi = min(S, lo + per);
   int sum = 0;

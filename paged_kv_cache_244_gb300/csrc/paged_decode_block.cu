@@ -94,7 +94,7 @@ decode_block_kernel(const DecodeArgs a, const int pool) {
   const int warps = static_cast<int>(blockDim.x >> 5);
   const int stage_bytes = bd_stage(G, kStep);
   const int cos_off = kBdQOff + G * kHeadDim * 2;    // (step)
-  build_prefix<kBdWarps>(a, prefix, last_rows);
+  build_prefix<kBdWarps>(a, prefix, last_rows, blockDim.x);
   const long long T = static_cast<long long>(Hkv) * prefix[S];
   const Ranges R = make_ranges(T, a);
   // Range v goes to warp v / grid of CTA v % grid; the CTA's stages are shared out among its warps
