@@ -29,8 +29,14 @@ constexpr int kMinRangeBlocks = PA_DECODE_MIN_RANGE;
 struct Ranges {
   long long T;
   int V;
-  __device__ __forceinline__ long long begin(int v) const { return (static_cast<long long>(v) * T) / V; }
+  // below 2^20 blocks (V < 2^12) both products fit 32 bits, whose division is several times shorter
+  __device__ __forceinline__ long long begin(int v) const {
+    if (T < (1 << 20)) return static_cast<uint32_t>(v) * static_cast<uint32_t>(T) / static_cast<uint32_t>(V);
+    return (static_cast<long long>(v) * T) / V;
+  }
   __device__ __forceinline__ int owner(long long x) const {
+    if (T < (1 << 20))
+      return static_cast<int>((static_cast<uint32_t>(x + 1) * static_cast<uint32_t>(V) - 1) / static_cast<uint32_t>(T));
     return static_cast<int>(((x + 1) * V - 1) / T);
   }
 };
@@ -66,7 +72,7 @@ __device__ __forceinline__ void build_prefix(const DecodeArgs& a, int* prefix, u
   const int S = a.num_seqs;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   __shared__ int warp_sums[kWarps];
-  const int per = (S + threads - 1) / threads;
+  const int per = S <= threads ? 1 : (S + threads - 1) / threads;
   const int lo = min(S, tid * per), hi = min(S, lo + per);
   int sum = 0;
   for (int s = lo; s < hi; ++s) {
@@ -83,19 +89,16 @@ __device__ __forceinline__ void build_prefix(const DecodeArgs& a, int* prefix, u
   }
   if (lane == 31) warp_sums[warp] = incl;
   __syncthreads();
-  int run = incl - sum;
-  for (int w = 0; w < warp; ++w) run += warp_sums[w];
+  const int of_warp = lane < threads / 32 ? warp_sums[lane] : 0;
+  int run = incl - sum + __reduce_add_sync(kFullMask, lane < warp ? of_warp : 0);
   for (int s = lo; s < hi; ++s) {
     prefix[s] = run;
     const int len = clamp_len(a.context_lens[s], a.max_context_len);
     run += (len + kBlockSize - 1) / kBlockSize;
     last_rows[s] = static_cast<unsigned char>(((len - 1) & (kBlockSize - 1)) + 1);  // unused if len == 0
   }
-  if (tid == threads - 1) {
-    int total = 0;
-    for (int w = 0; w < threads / 32; ++w) total += warp_sums[w];
-    prefix[S] = total;
-  }
+  const int total = __reduce_add_sync(kFullMask, of_warp);
+  if (tid == 0) prefix[S] = total;
   __syncthreads();
 }
 

@@ -169,8 +169,8 @@ decode_block_kernel(const DecodeArgs a, const int pool) {
   cur.x = x0;
   cur.n = static_cast<int>(min(32ll, x1 - x0));
   resolve(cur);
-  next_of(cur, nxt);
-  resolve(nxt);
+  next_of(cur, nxt);   // resolved behind the first jobs: a ring takes at most 16 of a window's 32 blocks
+  static_assert(2 * kBdMaxRing < 32, "the first window outlasts the first jobs");
   int pk = 0;  // next block of `cur`
   uint64_t once = 0;
   if constexpr (kOnce) once = l2_evict_first_policy();
@@ -579,6 +579,7 @@ decode_block_kernel(const DecodeArgs a, const int pool) {
       if (++pst == n_st) pst = 0;
     }
   }
+  resolve(nxt);
   __syncwarp();
   while (ahead > 0) {
     cp_async_wait_but(ahead - 1);      // the oldest job's copies; the warp barrier shows them to every lane
