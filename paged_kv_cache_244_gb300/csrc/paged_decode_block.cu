@@ -35,11 +35,11 @@
 //   p_t: a block of tiny V scale (an attention sink) may carry most of the weight with a p_t below
 //   f16.
 //
-// What bounds it: 64 sequences of 64-4096 tokens, us replayed from a graph.  12 / 2 heads (66 MB): 19.5,
-// of which 2.9 before the first tile (lengths, table, tile: dependent cold reads), some 10 streaming at the
+// What bounds it: 64 sequences of 64-4096 tokens, us replayed from a graph.  12 / 2 heads (66 MB): 18.2,
+// of which some 2.5 before the first tile (lengths, table, tile: dependent cold reads), some 10 streaming at the
 // copy rate, 2.4 between the first SM done and the last, the rest launch and merge; a kernel that only
-// gathers the same tiles takes 13.7.  Fused step with 32 / 8 heads (276 MB): 52.8, 5.2 TB/s (gather 43.8).
-// One sequence of 2048 tokens: 6.4, latency (an empty kernel: 1.9).
+// gathers the same tiles takes 13.7.  Fused step with 32 / 8 heads (276 MB): 50.6, 5.5 TB/s (gather 43.8).
+// One sequence of 2048 tokens: 6.1, latency (an empty kernel: 1.9).
 //
 // Per stage: [K tile 0 | K tile 1 | V tile 0 | V tile 1 | q rows | (step) cos/sin row, k row, v row];
 // 16-byte chunk c of row r of a tile (16 x 128 codes) lies at c ^ (r % 8) of its row.
@@ -68,6 +68,14 @@ constexpr int kBdSmemMax = 226 * 1024;               // beside the static part o
 // Shared memory: int4 descriptors and float2 x 2 scales of every stage, the prefix, the stages.
 constexpr int kBdScaleOff = kBdMaxStages * 16;
 constexpr int kBdPrefixOff = kBdScaleOff + kBdMaxStages * 16;
+
+// Codes are read evict-first (kOnce) from a pool of more than this, and with early metadata: tiles read once a
+// call leave lengths, tables, partial results and the neighbouring kernels' data in L2.  Normal / evict-first,
+// us: 64 sequences of 64-4096 tokens with 12 / 2 heads (66 MB) 19.0 / 18.3, the fused step with 32 / 8 heads
+// (276 MB) 51.8 / 50.7; as one of several layers with a matrix product of 64 MB of weights between (its
+// 12 us included) 31.5 / 30.8 and 65.4 / 63.9.  One sequence of 2048 tokens (1 MB) 6.07 / 6.18.  Against it: 32
+// sequences that share all of a 16,384-token prefix (67 MB) 117.9 / 126.1, a prefix of 2048 tokens 17.6 / 17.6.
+constexpr long long kOncePool = 32ll << 20;
 
 // More job flags: which of the two blocks are there.
 constexpr uint32_t kTwo = 1u << 13, kHas0 = 1u << 14, kHas1 = 1u << 15;
@@ -756,6 +764,7 @@ cudaError_t block_ctas(int* ctas) {
     opt_in(decode_block_kernel<false, false>);
     opt_in(decode_block_kernel<true, false>);
     opt_in(decode_block_kernel<true, true>);
+    opt_in(decode_block_kernel<false, true>);
     int sms = 0;
     if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (err != cudaSuccess) return err;
@@ -794,8 +803,10 @@ cudaError_t launch_decode_block(const DecodeArgs& args, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  auto kernel = step ? (a.early_metadata ? decode_block_kernel<true, true> : decode_block_kernel<true, false>)
-                     : decode_block_kernel<false, false>;
+  const long long pool_bytes = static_cast<long long>(a.num_blocks) * a.num_kv_heads * 2 * kBdTile;
+  const bool once = a.early_metadata || pool_bytes > kOncePool;
+  auto kernel = step ? (once ? decode_block_kernel<true, true> : decode_block_kernel<true, false>)
+                     : (once ? decode_block_kernel<false, true> : decode_block_kernel<false, false>);
   err = cudaLaunchKernelEx(&cfg, kernel, a, pool);
   if (err != cudaSuccess) return err;
   const long long pairs = static_cast<long long>(a.num_seqs) * a.num_q_heads;
