@@ -514,8 +514,9 @@ int pa_prefill_fp8_block(const pa_dims* dims, int num_seqs, int num_tokens, cons
  *   granted      s is granted its blocks when need_s == 0 or the new entries up to and including
  *                its own are at most F; so once one sequence is refused, every later one that
  *                needs a block is (PA_FLAG_POOL_EXHAUSTED).  granted[s] = 1 or 0
- *   context      context_lens[s] = c + n, or 0 when refused (its rows stay in q_start, so the
- *                attention calls give them zeros or skip them; nothing of it is stored)
+ *   context      context_lens[s] = c + n, or 0 when refused (its rows stay in q_start; nothing of it
+ *                is stored; the decode calls give it zeros, the prefill calls skip its rows and
+ *                raise PA_FLAG_CONTEXT_LEN_OOB)
  *   token i      row r = start_s + i: positions[r] = c + i, slot_mapping[r] = table entry of
  *                block (c + i) / 16 * 16 + (c + i) % 16; position 0 and slot -1 (padding, for
  *                the stores) when refused
@@ -617,7 +618,8 @@ int pa_stage_copy(void* dst, const void* src, size_t bytes, void* stream);
 
 /*
  * pa_set_timing_jitter -- test hook for the pipelined kernels' barriers: from the next launch
- * on, every role of the pa_prefill kernel (softmax warps, TMA warps, MMA warp) sleeps a
+ * on, every role of the pa_prefill and pa_prefill_fp8_block kernels (softmax warps, TMA warps, MMA
+ * warp, converters) sleeps a
  * pseudo-random time below max_ns (the same for the whole warp, a function of seed, the CTA,
  * the role and the step) at each step of its pipeline loop, so that tests can drive the
  * barriers through orders of arrival that undisturbed runs rarely take.  Results must not

@@ -29,6 +29,21 @@ __device__ __forceinline__ uint64_t global_ns() {
   return t;
 }
 
+// A pseudo-random sleep below max_ns (0: none), the same for the whole warp: the test hook of the
+// pipelines (pa_set_timing_jitter), {max_ns, seed}.
+__device__ __forceinline__ void jitter_sleep(const uint32_t (&hook)[2], uint32_t role, uint32_t j) {
+  const uint32_t max_ns = hook[0];
+  if (max_ns == 0) return;
+  uint32_t x = hook[1] ^ (blockIdx.x * 0x9E3779B1u) ^ (blockIdx.y * 0x85EBCA77u) ^
+               (role * 0xC2B2AE3Du) ^ (j * 0x27D4EB2Fu);
+  x ^= x >> 16;
+  x *= 0x7FEB352Du;
+  x ^= x >> 15;
+  x *= 0x846CA68Bu;
+  x ^= x >> 16;
+  __nanosleep(x % max_ns);
+}
+
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }

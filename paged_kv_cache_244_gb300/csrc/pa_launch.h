@@ -169,6 +169,8 @@ bool cache_tensor_map(const void* cache, long long rows, bool fp8, CUtensorMap* 
 cudaError_t launch_rope_kv_store(const RopeArgs& a, cudaStream_t stream);
 cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream);
 cudaError_t launch_prefill_block(const PrefillArgs& a, cudaStream_t stream);
+// {max_ns, seed} of its roles' sleeps (pa_set_timing_jitter).
+cudaError_t set_prefill_block_jitter(const uint32_t (&hook)[2]);
 cudaError_t launch_rope_table(const RopeTableArgs& a, cudaStream_t stream);
 cudaError_t launch_rope_form_store(const RopeFormArgs& a, cudaStream_t stream);
 cudaError_t launch_plan_step(const PlanArgs& a, cudaStream_t stream);

@@ -104,18 +104,7 @@ static_assert(kTmemSlot + 4 <= kPfHeader, "header");
 // undisturbed runs rarely take.
 __constant__ uint32_t c_pf_jitter[2];
 
-__device__ __forceinline__ void pf_jitter(uint32_t role, uint32_t j) {
-  const uint32_t max_ns = c_pf_jitter[0];
-  if (max_ns == 0) return;
-  uint32_t x = c_pf_jitter[1] ^ (blockIdx.x * 0x9E3779B1u) ^ (blockIdx.y * 0x85EBCA77u) ^
-               (role * 0xC2B2AE3Du) ^ (j * 0x27D4EB2Fu);
-  x ^= x >> 16;
-  x *= 0x7FEB352Du;
-  x ^= x >> 15;
-  x *= 0x846CA68Bu;
-  x ^= x >> 16;
-  __nanosleep(x % max_ns);
-}
+__device__ __forceinline__ void pf_jitter(uint32_t role, uint32_t j) { jitter_sleep(c_pf_jitter, role, j); }
 
 __global__ void __launch_bounds__(kPfThreads, 2)
 prefill_kernel(const __grid_constant__ CUtensorMap tm_kh, const __grid_constant__ CUtensorMap tm_v,
@@ -611,5 +600,8 @@ cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream) {
 extern "C" int pa_set_timing_jitter(uint32_t max_ns, uint32_t seed) {
   if (max_ns > 1000000u) return PA_ERR_RANGE;
   const uint32_t v[2] = {max_ns, seed};
-  return cudaMemcpyToSymbol(pa::c_pf_jitter, v, sizeof v) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  return cudaMemcpyToSymbol(pa::c_pf_jitter, v, sizeof v) == cudaSuccess &&
+                 pa::set_prefill_block_jitter(v) == cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
 }

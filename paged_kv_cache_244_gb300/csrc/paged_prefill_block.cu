@@ -42,7 +42,8 @@
 // heads: loads and stores 53.7% of its wavefronts, the tensor core's reads of A and B 18.4% each) with
 // the tensor pipe 37% active.  A tile of 128 rows and 64 keys puts q hi and lo (32 KiB), K twice (16),
 // f16 V (16), S out (32), P in (16), the codes of V in and f16 V out (24) and the TMA's writes (16) on
-// it.  4 x 2048 tokens: 61.8 us, 0.43 of the measured bf16 peak; 16 chunks of 256 over 1792: 59.6 us.  A
+// it.  4 x 2048 tokens: 61.8-62.7 us from GPU to GPU, 0.43 of the measured bf16 peak; 16 chunks of 256 over
+// 1792: 59.6-60.7 us.  A
 // first form that widened K too and gave each thread its own row of q and out to load and store: 87 us.
 // Measured and left: S of two stages by one product of 128 keys (a q operand read half as often, but S
 // no longer double: 71 us); two threads a row, 16 softmax warps on an SM (65 us); one lane waiting for its
@@ -57,6 +58,7 @@
 // the same sums whatever the timing.  11 sequences of one new token after 10,812 cached, 28 / 4 heads:
 // 48.5 us, 142.8 unsplit; 4 of 71 after 2342, 32 / 8 heads: 32.
 
+#include <atomic>
 #include <mutex>
 
 #include <cuda.h>
@@ -112,6 +114,11 @@ constexpr int kQReady = kDone + 8;                   // softmax (one thread, all
 constexpr int kTmemAt = kQReady + 8;
 static_assert(kTmemAt + 4 <= kBpHeader, "header");
 
+// Timing jitter, a test hook (pa_set_timing_jitter): a role sleeps below max_ns at each of its stages.  A
+// kernel variant (kJitter), taken while the hook is set, so that the ordinary one has nothing of it in its stages.
+__constant__ uint32_t c_bp_jitter[2];
+std::atomic<bool> jitter_on{false};
+
 // Four bf16 values times `raise` (a power of two that keeps them below 256) as the sum of two E4M3
 // values each: the codes of the nearest, and of what it leaves.  f16 holds the 8 significant bits
 // of a value down to 2^-17, and the difference exactly.
@@ -128,7 +135,7 @@ __device__ __forceinline__ void split_e4m3(uint32_t w0, uint32_t w1, float raise
   lo = l[0] | (static_cast<uint32_t>(l[1]) << 16);
 }
 
-template <bool kSplit>
+template <bool kSplit, bool kJitter>
 __global__ void __launch_bounds__(kBpThreads, 2)
 prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const PrefillArgs a) {
@@ -251,6 +258,7 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     bool failed = false;
     for (int j = 0; j < nst; ++j) {
       const int cst = j % kBpCRing, vst = j % kBpVRing;
+      if constexpr (kJitter) jitter_sleep(c_bp_jitter, warp, j);
       next_window(j);
       const int mask = stage_mask(j);
       // the codes have landed and (after the ring's first round) the f16 slot is free: the whole
@@ -320,6 +328,7 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       int issued = 0;
       bool failed = false;
       for (int j = 0; j < nst; ++j) {
+        if constexpr (kJitter) jitter_sleep(c_bp_jitter, warp, j);
         if (next_window(j)) {
           scales = scales_next;
           scales_next = load_scales(ids_next);
@@ -371,7 +380,7 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         return __all_sync(kFullMask, mbar_wait_parked(bar, parity));
       };
       // K_j, V_j are there.  A look at a barrier takes 100 to 150 cycles even when its phase is over, so these
-      // come before the wait for P, off the chain from P_j to S_{j+2} (4 x 2048 tokens: 62.7 -> 61.7 us).
+      // come before the wait for P, off the chain from P_j to S_{j+2} (4 x 2048 tokens, on one GPU: 63.4 -> 62.7 us).
       auto k_there = [&](int j) { return wait_all(hdr + kKFull + 8 * (j % kBpKRing), (j / kBpKRing) & 1); };
       auto v_there = [&](int j) { return wait_all(hdr + kVFull + 8 * (j % kBpVRing), (j / kBpVRing) & 1); };
       // one lane: S_j = Q K_j^T (its columns hold P_{j-2}, read by P V issued before)
@@ -394,6 +403,7 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       }
       for (int j = 0; j < nst && !failed; ++j) {
         const int st = j % kBpVRing;
+        if constexpr (kJitter) jitter_sleep(c_bp_jitter, warp, j);
         if (!v_there(j) || (j + 2 < nst && !k_there(j + 2)) || !wait_all(hdr + kPFull + 8 * (j & 1), (j >> 1) & 1)) {
           failed = true;
           break;
@@ -490,6 +500,7 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     bool failed = false;
     const float4* const scale_slots = reinterpret_cast<const float4*>(base + kBpScaleOff);
     for (int j = 0; j < nst; ++j) {
+      if constexpr (kJitter) jitter_sleep(c_bp_jitter, warp, j);
       if (!__all_sync(kFullMask, mbar_wait_parked(hdr + kSFull + 8 * (j & 1), (j >> 1) & 1))) {
         failed = true;
         break;
@@ -697,6 +708,11 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
 
 }  // namespace
 
+cudaError_t set_prefill_block_jitter(const uint32_t (&hook)[2]) {
+  jitter_on = hook[0] != 0;
+  return cudaMemcpyToSymbol(c_bp_jitter, hook, sizeof hook);
+}
+
 cudaError_t launch_prefill_block(const PrefillArgs& a, cudaStream_t stream) {
   const int G = a.num_q_heads / a.num_kv_heads;
   if (G < 1 || G > 8) return cudaErrorInvalidValue;
@@ -721,8 +737,10 @@ cudaError_t launch_prefill_block(const PrefillArgs& a, cudaStream_t stream) {
           err = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
                                      cudaSharedmemCarveoutMaxShared);
       };
-      opt_in(prefill_block_kernel<false>);
-      opt_in(prefill_block_kernel<true>);
+      opt_in(prefill_block_kernel<false, false>);
+      opt_in(prefill_block_kernel<true, false>);
+      opt_in(prefill_block_kernel<false, true>);
+      opt_in(prefill_block_kernel<true, true>);
       if (err != cudaSuccess) return err;
       done[dev] = true;
     }
@@ -748,8 +766,10 @@ cudaError_t launch_prefill_block(const PrefillArgs& a, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = ranks > 1 ? 2 : 1;
-  return ranks > 1 ? cudaLaunchKernelEx(&cfg, prefill_block_kernel<true>, tm_k, tm_v, a)
-                   : cudaLaunchKernelEx(&cfg, prefill_block_kernel<false>, tm_k, tm_v, a);
+  const bool jitter = jitter_on;
+  auto kernel = ranks > 1 ? (jitter ? prefill_block_kernel<true, true> : prefill_block_kernel<true, false>)
+                          : (jitter ? prefill_block_kernel<false, true> : prefill_block_kernel<false, false>);
+  return cudaLaunchKernelEx(&cfg, kernel, tm_k, tm_v, a);
 }
 
 }  // namespace pa

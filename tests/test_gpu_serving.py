@@ -685,6 +685,28 @@ def test_prefill_split_over_the_keys(pa, lens, new, hq, kv):
     assert np.array_equal(bits(pa.prefill_fp8_block(*args)), bits(pa.prefill_fp8_block(*args)))
 
 
+@pytest.mark.parametrize("lens,new,hq,kv,seed,max_ns", [
+    ([2048, 700, 1500], [2048, 300, 64], 12, 2, 1, 3000), ([9000, 777, 4100], [150, 40, 300], 12, 2, 2, 8000),
+    ([10812, 9000, 1, 4097], [1, 1, 1, 1], 28, 4, 3, 8000), ([1200] * 9, [100] * 9, 8, 8, 4, 500)])
+def test_prefill_under_timing_jitter_gives_the_same_bits(pa, lens, new, hq, kv, seed, max_ns):
+    """Sleeps at every stage of every role: orders of arrival that undisturbed runs rarely take."""
+    rng = np.random.default_rng(seed)
+    pool = Pool(rng, lens, kv)
+    q = bf16(normal(rng, sum(new), hq, D))
+    args = (q, up(np.concatenate([[0], np.cumsum(new)]).astype(np.int32)), *pool.dev(), up(pool.tables), up(pool.lens),
+            max(new), max(lens), D ** -0.5)
+    want = bits(pa.prefill_fp8_block(*args))
+    torch.cuda.synchronize()
+    pa.set_timing_jitter(max_ns, seed)
+    try:
+        got = bits(pa.prefill_fp8_block(*args))
+        torch.cuda.synchronize()
+    finally:
+        pa.set_timing_jitter(0)
+    clean(pa)
+    assert np.array_equal(got, want)
+
+
 def test_prefill_bound_larger_than_needed_and_scales_far_apart(pa):
     rng = np.random.default_rng(30)
     pool = Pool(rng, [200, 350], 2)
