@@ -74,9 +74,9 @@ METRIC = "paged GQA decode: KV-cache HBM GB/s (% of GB300 peak) and attention to
 # the step form and a hash of the CUDA sources it was taken on: once a kernel changes, the
 # hash no longer matches and roofline.traffic is reported as null until it is captured again.
 MEASURED_TRAFFIC = {
-    ("mix64", "fused", "c162b432e9b6e5bf"): 122102528 + 2996992 + 4185600,
-    ("prefix32", "fused", "c162b432e9b6e5bf"): 4346624 + 0 + 3835904,
-    ("long4", "fused", "c162b432e9b6e5bf"): 83978496 + 1820160 + 4823296,
+    ("mix64", "fused", "f80544bf6cbdeb8d"): 122106368 + 3324160 + 4186624,
+    ("prefix32", "fused", "f80544bf6cbdeb8d"): 4346112 + 0 + 3823616,
+    ("long4", "fused", "f80544bf6cbdeb8d"): 83978496 + 2115840 + 4834304,
 }
 FLUSH_BYTES = 512 << 20
 FALLBACK_HBM_GBS = 6800.0

@@ -16,8 +16,9 @@
 //
 // The longest chain of dependent loads and barriers bounds it: lengths, two sums over the CTA, search,
 // free-list entry, store.  256 sequences of one token: 4.6 us replayed from a graph (an empty
-// kernel: 1.9; 5.8 before the loads of a phase were asked for ahead of the sums).  512 prompts of
-// 548,920 rows, where 12 bytes a row are written: 7.0 us, of which the writing takes 1.0 at the copy rate.
+// kernel: 1.9; 5.8 before the loads of a phase were asked for ahead of the sums).  8192 of one token: 10.0 us
+// (26.3 when each thread read its share of the lengths from memory itself, in one CTA).  512 prompts
+// of 548,920 rows, where 12 bytes a row are written: 6.6 us, of which the writing takes 1.0 at the copy rate.
 
 #include <mutex>
 
@@ -27,13 +28,19 @@
 namespace pa {
 namespace {
 
-constexpr int kPlanThreads = 512;
+constexpr int kPlanThreads = 512;          // of a CTA
 constexpr int kPlanRowsPerThread = 4;
 // Rows that one CTA takes before another is launched.
 constexpr int kPlanRowsPerCta = kPlanThreads * kPlanRowsPerThread;
 // One CTA an SM: each forms the sums anew, so more of them repeat work and fewer leave the writing
-// thin.  512 prompts, 548,920 rows: 7.0 us with 152 CTAs, 7.6 with 228, 8.5 with 304 and with 608.
+// thin.  512 prompts, 548,920 rows, CTAs of 512 threads: 7.0 us with 152, 7.6 with 228, 8.5 with 304 and 608.
 constexpr int kPlanMaxCtas = 152;
+// A call of more rows than those hold takes CTAs of twice the threads; smaller ones stay at 512, whose sums are
+// shorter: 548,864 rows 6.4 us (6.9 with 512), 2 M rows 15.1 (18.2), but 262,144 rows 6.1 (4.7), 256 rows 4.2 (3.9).
+constexpr int kPlanManyThreads = 1024, kPlanManyRows = kPlanMaxCtas * kPlanRowsPerCta;
+// Sequences of a CTA where the count is not in place (an in-place count of several CTAs is a launch more):
+// 2048 sequences of one token 6.9 us (9.0 in one CTA), 8192: 10.0 (13.2).
+constexpr int kPlanSeqsPerCta = 512;
 
 // start [S + 1], x [S + 1] (int32), good [S] (bytes)
 __host__ __device__ inline int plan_smem(int S) { return 2 * 4 * (S + 1) + S + 16; }
@@ -50,6 +57,7 @@ __device__ __forceinline__ int plan_find(const int* sums, int n, int v) {
 }
 
 // Exclusive sum over the CTA's threads, `sums` a shared word per warp; *total receives the whole sum.
+template <int kThreads>
 __device__ __forceinline__ long long block_exclusive(long long v, long long* sums, long long* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   long long incl = v;
@@ -61,13 +69,13 @@ __device__ __forceinline__ long long block_exclusive(long long v, long long* sum
   if (lane == 31) sums[warp] = incl;
   __syncthreads();
   // lane w takes warp w's sum: the warps before this one, and all of them
-  long long upto = lane < kPlanThreads / 32 ? sums[lane] : 0;
+  long long upto = lane < kThreads / 32 ? sums[lane] : 0;
 #pragma unroll
-  for (int d = 1; d < kPlanThreads / 32; d <<= 1) {
+  for (int d = 1; d < kThreads / 32; d <<= 1) {
     const long long y = __shfl_up_sync(kFullMask, upto, d);
     if (lane >= d) upto += y;
   }
-  *total = __shfl_sync(kFullMask, upto, kPlanThreads / 32 - 1);
+  *total = __shfl_sync(kFullMask, upto, kThreads / 32 - 1);
   const long long before = __shfl_sync(kFullMask, upto, warp == 0 ? 0 : warp - 1);
   return (warp == 0 ? 0 : before) + incl - v;
 }
@@ -75,10 +83,10 @@ __device__ __forceinline__ long long block_exclusive(long long v, long long* sum
 __device__ __forceinline__ int blocks_of(int tokens) { return (tokens + kBlockSize - 1) / kBlockSize; }
 
 // count_only: only num_free_out is written (the second launch of an in-place count).
-template <bool kCountOnly>
-__global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanArgs a, const int write_count) {
+template <int kThreads, bool kCountOnly>
+__global__ void __launch_bounds__(kThreads) plan_step_kernel(const PlanArgs a, const int write_count) {
   extern __shared__ int smem[];
-  __shared__ long long row_sums[kPlanThreads / 32], need_sums[kPlanThreads / 32];
+  __shared__ long long row_sums[kThreads / 32], need_sums[kThreads / 32];
   pdl_wait_prior_grid();
   pdl_allow_next_grid();
   const int S = a.num_seqs, T = a.num_tokens, tid = threadIdx.x;
@@ -88,45 +96,48 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanArgs 
   const bool first_cta = blockIdx.x == 0;
 
   // ---- the two sums: each thread takes a contiguous share of the sequences ----------------
-  const int per = (S + kPlanThreads - 1) / kPlanThreads;
+  // The lengths come through the arrays that the sums are formed in, whole lines at a time; shares are of odd
+  // size, so that a warp's lanes meet distinct banks.  Everything that a later phase waits for is asked for
+  // at once: the count, both lengths.
+  int per = (S + kThreads - 1) / kThreads;
+  if (per > 1) per |= 1;
   const int s0 = min(S, tid * per), s1 = min(S, s0 + per);
   const long long table_tokens = static_cast<long long>(a.max_blocks) * kBlockSize;
-  // Everything that a later phase waits for is asked for at once: the count, both lengths (the
-  // passes below find them in L1).
   int F = a.num_free[0];
+  for (int s = tid; s < S; s += kThreads) {
+    start[s] = a.new_lens[s];
+    x[s] = a.cached_lens[s];
+  }
+  if (per > 1) __syncthreads();
   long long rows = 0;
-  int touched = 0;
   for (int s = s0; s < s1; ++s) {
-    const int n = a.new_lens[s];
-    touched |= a.cached_lens[s];
+    const int n = start[s];
     if (n > 0 && n <= T) rows += n;
   }
-  asm volatile("" ::"r"(touched));  // the loads of cached_lens stay here
   long long all_rows;
-  long long r = block_exclusive(rows, row_sums, &all_rows);
+  long long r = block_exclusive<kThreads>(rows, row_sums, &all_rows);
   // Needs: of the sequences whose lengths and rows are in order.  Each is at most max_blocks
   // < 2^27 blocks and there are at most 8192, so their sum is kept in 64 bits, and clamped
   // to 2^31 - 1 where it is stored (a free list is shorter, so the order is unchanged).
   long long need_sum = 0;
   for (int s = s0; s < s1; ++s) {
-    const int n = a.new_lens[s], c = a.cached_lens[s];
+    const int n = start[s], c = x[s];
     const bool in_rows = n >= 0 && n <= T;
     start[s] = static_cast<int>(min(r, static_cast<long long>(T)));
     if (in_rows) r += n;
     const bool ok = in_rows && c >= 0 && static_cast<long long>(c) + n <= table_tokens && r <= T;
     good[s] = ok ? 1 : 0;
     if (!ok && first_cta && !kCountOnly) raise_flag(a.status, PA_FLAG_CONTEXT_LEN_OOB);
-    if (ok) need_sum += blocks_of(c + n) - blocks_of(c);
+    x[s] = ok ? blocks_of(c + n) - blocks_of(c) : 0;
+    need_sum += x[s];
   }
   long long all_need;
-  long long e = block_exclusive(need_sum, need_sums, &all_need);
+  long long e = block_exclusive<kThreads>(need_sum, need_sums, &all_need);
   constexpr long long kTop = 0x7fffffffll;
   for (int s = s0; s < s1; ++s) {
+    const int need = x[s];
     x[s] = static_cast<int>(min(e, kTop));
-    if (good[s]) {
-      const int c = a.cached_lens[s];
-      e += blocks_of(c + a.new_lens[s]) - blocks_of(c);
-    }
+    e += need;
   }
   const int total_rows = static_cast<int>(min(all_rows, static_cast<long long>(T)));
   if (tid == 0) {
@@ -151,11 +162,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanArgs 
   // granted: x[s + 1] <= F, or nothing needed
   auto is_granted = [&](int s) { return good[s] && (x[s + 1] == x[s] || x[s + 1] <= F); };
   const int nb = static_cast<int>(gridDim.x), b = static_cast<int>(blockIdx.x);
-  const int gtid = b * kPlanThreads + tid, gthreads = nb * kPlanThreads;
+  const int gtid = b * kThreads + tid, gthreads = nb * kThreads;
 
   // In a call of one CTA each kind of output starts with warps of its own, so that their loads overlap.
-  const int entry_tid = nb > 1 ? gtid : (tid + kPlanThreads / 4) % kPlanThreads;
-  const int row_tid = nb > 1 ? gtid : (tid + kPlanThreads / 2) % kPlanThreads;
+  const int entry_tid = nb > 1 ? gtid : (tid + kThreads / 4) % kThreads;
+  const int row_tid = nb > 1 ? gtid : (tid + kThreads / 2) % kThreads;
   for (int s = gtid; s <= S; s += gthreads) {
     a.q_start[s] = start[s];
     if (s == S) break;
@@ -241,17 +252,23 @@ cudaError_t launch_plan_step(const PlanArgs& a, cudaStream_t stream) {
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     std::lock_guard<std::mutex> lock(mu);
     if (!done[dev]) {
-      err = cudaFuncSetAttribute(plan_step_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 plan_smem(kMaxDecodeSeqs));
-      if (err == cudaSuccess)
-        err = cudaFuncSetAttribute(plan_step_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   plan_smem(kMaxDecodeSeqs));
+      auto opt_in = [&](auto kernel) {
+        if (err == cudaSuccess)
+          err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, plan_smem(kMaxDecodeSeqs));
+      };
+      opt_in(plan_step_kernel<kPlanThreads, false>);
+      opt_in(plan_step_kernel<kPlanThreads, true>);
+      opt_in(plan_step_kernel<kPlanManyThreads, false>);
       if (err != cudaSuccess) return err;
       done[dev] = true;
     }
   }
   long long ctas = (static_cast<long long>(a.num_tokens) + kPlanRowsPerCta - 1) / kPlanRowsPerCta;
   if (ctas < 1) ctas = 1;
+  if (a.num_free != a.num_free_out) {
+    const long long by_seqs = (a.num_seqs + kPlanSeqsPerCta - 1) / kPlanSeqsPerCta;
+    if (ctas < by_seqs) ctas = by_seqs;
+  }
   if (ctas > kPlanMaxCtas) ctas = kPlanMaxCtas;
   const bool later = a.num_free == a.num_free_out && ctas > 1;
   cudaLaunchAttribute attr[1];
@@ -259,15 +276,18 @@ cudaError_t launch_plan_step(const PlanArgs& a, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-  cfg.blockDim = dim3(kPlanThreads);
+  const bool many = a.num_tokens > kPlanManyRows;
+  cfg.blockDim = dim3(many ? kPlanManyThreads : kPlanThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t err = cudaLaunchKernelEx(&cfg, plan_step_kernel<false>, a, later ? 0 : 1);
+  auto kernel = many ? plan_step_kernel<kPlanManyThreads, false> : plan_step_kernel<kPlanThreads, false>;
+  cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, a, later ? 0 : 1);
   if (err != cudaSuccess || !later) return err;
   cfg.gridDim = dim3(1);
-  return cudaLaunchKernelEx(&cfg, plan_step_kernel<true>, a, 1);
+  cfg.blockDim = dim3(kPlanThreads);
+  return cudaLaunchKernelEx(&cfg, plan_step_kernel<kPlanThreads, true>, a, 1);
 }
 
 }  // namespace pa

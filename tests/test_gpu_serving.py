@@ -810,7 +810,7 @@ def random_plan(rng, S, cached, new, short=False, pad=0):
 @pytest.mark.parametrize("in_place", [False, True])
 @pytest.mark.parametrize("S,cached,new,short,pad", [(1, 0, 1, False, 0), (1, 100, 40, False, 3), (33, 50, 1, False, 7), (256, 4000, 2, True, 1),
                                                     (64, 500, 300, True, 0), (700, 30, 60, False, 5), (1500, 20, 5, True, 2),
-                                                    (8192, 40, 3, False, 9)])
+                                                    (8192, 40, 3, False, 9), (300, 64, 2400, False, 6), (2000, 64, 380, True, 1)])
 def test_plan(pa, S, cached, new, short, pad, in_place):
     check_plan(pa, *random_plan(np.random.default_rng(S + new), S, cached, new, short, pad), in_place=in_place)
 
