@@ -74,22 +74,22 @@ METRIC = "paged GQA decode: KV-cache HBM GB/s (% of GB300 peak) and attention to
 # the step form and a hash of the CUDA sources it was taken on: once a kernel changes, the
 # hash no longer matches and roofline.traffic is reported as null until it is captured again.
 MEASURED_TRAFFIC = {
-    ("mix64", "fused", "f80544bf6cbdeb8d"): 122106368 + 3324160 + 4186624,
-    ("prefix32", "fused", "f80544bf6cbdeb8d"): 4346112 + 0 + 3823616,
-    ("long4", "fused", "f80544bf6cbdeb8d"): 83978496 + 2115840 + 4834304,
+    ("mix64", "fused", "f2331d72aaf0f753"): 122105088 + 2981632 + 4186368,
+    ("prefix32", "fused", "f2331d72aaf0f753"): 4346112 + 0 + 3823616,
+    ("long4", "fused", "f2331d72aaf0f753"): 83979264 + 2099200 + 4824064,
 }
 FLUSH_BYTES = 512 << 20
 FALLBACK_HBM_GBS = 6800.0
 
 
 def kernel_source_hash() -> str:
-    """Hash of the code the decode kernels compile from (their file, the split, the device helpers,
-    the launch header), with comments and whitespace removed: editing a comment keeps the hash."""
+    """Hash of the code the decode kernels compile from (their file, the device helpers, the
+    launch header), with comments and whitespace removed: editing a comment keeps the hash."""
     import hashlib
     import re
     csrc = ROOT / "paged_kv_cache_244_gb300" / "csrc"
     h = hashlib.sha256()
-    for name in ("paged_decode.cu", "decode_split.cuh", "pa_device.cuh", "pa_launch.h"):
+    for name in ("paged_decode.cu", "pa_device.cuh", "pa_launch.h"):
         text = (csrc / name).read_text()
         text = re.sub(r"/\*.*?\*/", " ", text, flags=re.S)
         text = re.sub(r"//[^\n]*", " ", text)

@@ -64,7 +64,6 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
-#include "decode_split.cuh"
 #include "pa_device.cuh"
 #include "pa_launch.h"
 

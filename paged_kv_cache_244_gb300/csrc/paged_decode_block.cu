@@ -5,7 +5,7 @@
 // (Flash Decode); "从零实现 LLM 推理引擎：深挖 vLLM 的六大核心优化", §3.1 Paged KV Cache; "nano-vllm：vLLM
 // 极简实现与大模型推理流程解析", §学习要点 (8-bit quantisation of the cache).
 //
-// The work is cut as in the decode over bf16 caches (decode_split.cuh): one axis of (sequence, KV
+// The work is cut as in the decode over bf16 caches (pa_device.cuh): one axis of (sequence, KV
 // head, block), an equal contiguous range for each warp of a persistent grid, pieces of split
 // segments merged by a kernel after it.  A warp serves the G <= 8 query heads of its KV head
 // and is its own producer and consumer.  What differs:
@@ -46,7 +46,6 @@
 
 #include <mutex>
 
-#include "decode_split.cuh"
 #include "pa_device.cuh"
 #include "pa_launch.h"
 
