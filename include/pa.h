@@ -473,7 +473,7 @@ int pa_decode_fp8_block(const pa_dims* dims, int num_seqs, const void* q, const 
 /*
  * pa_decode_step_fp8_block -- pa_decode_step over block-scaled E4M3 caches with a RoPE form:
  * equals pa_rope_kv_store_fp8_block (position context_lens[s] - 1, that position's slot; the
- * codes and scales bit for bit) followed by pa_decode_fp8_block, with q left unchanged.  A
+ * codes, scales and out bit for bit) followed by pa_decode_fp8_block, with q left unchanged.  A
  * position without a cos/sin row: as pa_decode_step.  Arguments as pa_decode_step plus rope
  * (as pa_rope_kv_store_form) and kv_scale (read, and written at the new tokens' blocks).
  */

@@ -35,10 +35,10 @@
 //   p_t: a block of tiny V scale (an attention sink) may carry most of the weight with a p_t below
 //   f16.
 //
-// What bounds it: 64 sequences of 64-4096 tokens, us replayed from a graph.  12 / 2 heads (66 MB): 18.2,
+// What bounds it: 64 sequences of 64-4096 tokens, us replayed from a graph.  12 / 2 heads (66 MB): 18.5,
 // of which some 2.5 before the first tile (lengths, table, tile: dependent cold reads), some 10 streaming at the
 // copy rate, 2.4 between the first SM done and the last, the rest launch and merge; a kernel that only
-// gathers the same tiles takes 13.7.  Fused step with 32 / 8 heads (276 MB): 50.6, 5.5 TB/s (gather 43.8).
+// gathers the same tiles takes 13.7.  Fused step with 32 / 8 heads (276 MB): 50.8, 5.4 TB/s (gather 43.8).
 // One sequence of 2048 tokens: 6.1, latency (an empty kernel: 1.9).
 //
 // Per stage: [K tile 0 | K tile 1 | V tile 0 | V tile 1 | q rows | (step) cos/sin row, k row, v row];
@@ -782,11 +782,14 @@ cudaError_t launch_decode_block(const DecodeArgs& args, cudaStream_t stream) {
   cudaError_t err = block_ctas(&max_ctas);
   if (err != cudaSuccess) return err;
   // Stages: what fits (24 of 9 KiB without the step and 4 query heads a group, 20 of 10.5 KiB with it and
-  // 6; fewer beside the prefix of thousands of sequences); warps: two stages each, 12 at most.
-  const int stage = bd_stage(a.num_q_heads / a.num_kv_heads, step);
+  // 6; fewer beside the prefix of thousands of sequences).  Warps: two of the step's stages each, 12 at
+  // most, with and without the step, so that both cut sequences alike and give the same bits (64 sequences of
+  // 64-4096 tokens, 6 heads a group: 10 warps and 11 within 1%).
+  const int G = a.num_q_heads / a.num_kv_heads;
   const int fixed = kBdPrefixOff + prefix_bytes(a.num_seqs) + 1024;
+  const int stage = bd_stage(G, step);
   const int pool = min(kBdMaxStages, (kBdSmemMax - fixed) / stage);
-  const int warps = min(kBdWarps, pool / 2);
+  const int warps = min(kBdWarps, (kBdSmemMax - fixed) / bd_stage(G, true) / 2);
   // no more CTAs than there can be ranges (they are dealt to the CTAs one at a time)
   const long long jobs = static_cast<long long>(a.num_seqs) * a.num_kv_heads *
                          ((a.max_context_len + kBlockSize - 1) / kBlockSize);

@@ -627,6 +627,27 @@ def test_step_equals_store_then_decode(pa, layout, Rr, early):
     clean(pa)
 
 
+@pytest.mark.parametrize("S,hq,kv,P", [(200, 8, 1, 0), (200, 16, 4, 0), (40, 21, 3, 32), (1500, 5, 1, 0), (6, 64, 8, 0)])
+def test_step_cuts_sequences_as_the_decode_does(pa, S, hq, kv, P):
+    """Stages of another size, the same pieces: the bits of store and decode for any group and batch."""
+    rng = np.random.default_rng(S + hq)
+    lens = [int(x) for x in rng.integers(0, 60000 // S, S)]
+    pool = Pool(rng, lens, kv)
+    q, k, v = (bf16(normal(rng, S, h, D)) for h in (hq, kv, kv))
+    n = max(lens)
+    cs, bt, ctx = up(table_of(n, 64)), up(pool.tables), up(pool.lens)
+    a, b = pool.dev(), pool.dev()
+    out = pa.decode_step_fp8_block(q, k, v, cs, *a, bt, ctx, n, D ** -0.5, partition_tokens=P)
+    pos = np.maximum(pool.lens - 1, 0)
+    slots = np.where(pool.lens > 0, pool.tables[np.arange(S), pos // B].astype(np.int64) * B + pos % B, -1)
+    q2 = torch.empty_like(q)
+    pa.rope_kv_store_fp8_block(q, k, v, up(pos.astype(np.int32)), cs, up(slots), *b, q_out=q2)
+    for x, y in zip(a, b):
+        assert torch.equal(x, y)
+    assert np.array_equal(bits(out), bits(pa.decode_fp8_block(q2, *b, bt, ctx, n, D ** -0.5, partition_tokens=P)))
+    clean(pa)
+
+
 def test_step_without_a_row_of_the_table_stores_nothing(pa):
     rng = np.random.default_rng(14)
     pool = Pool(rng, [20, 40], 2, canary=False)
