@@ -42,8 +42,8 @@
 // heads: loads and stores 53.7% of its wavefronts, the tensor core's reads of A and B 18.4% each) with
 // the tensor pipe 37% active.  A tile of 128 rows and 64 keys puts q hi and lo (32 KiB), K twice (16),
 // f16 V (16), S out (32), P in (16), the codes of V in and f16 V out (24) and the TMA's writes (16) on
-// it.  4 x 2048 tokens: 61.8-62.7 us from GPU to GPU, 0.43 of the measured bf16 peak; 16 chunks of 256 over
-// 1792: 59.6-60.7 us.  A
+// it.  4 x 2048 tokens: 63.1 us, 0.42 of the measured bf16 peak; 16 chunks of 256 over 1792: 61.7 us (with S_{j+2}
+// issued right behind P_j V_j, an order that nothing guarantees: 61.8-62.7 and 59.6-60.7).  A
 // first form that widened K too and gave each thread its own row of q and out to load and store: 87 us.
 // Measured and left: S of two stages by one product of 128 keys (a q operand read half as often, but S
 // no longer double: 71 us); two threads a row, 16 softmax warps on an SM (65 us); one lane waiting for its
@@ -56,7 +56,7 @@
 // row's (m, L) through distributed shared memory, scale their O to the common shift, and CTA r
 // collects dims 128 r / C .. of every row from all of them, in rank order: no workspace, one launch,
 // the same sums whatever the timing.  11 sequences of one new token after 10,812 cached, 28 / 4 heads:
-// 48.5 us, 142.8 unsplit; 4 of 71 after 2342, 32 / 8 heads: 32.
+// 50.3 us, 142.8 unsplit; 4 of 71 after 2342, 32 / 8 heads: 32.9.
 
 #include <atomic>
 #include <mutex>
@@ -109,7 +109,7 @@ constexpr int kKFree = kKFull + 8 * kBpKRing;        // MMA (S done) -> K TMA
 constexpr int kCFull = kKFree + 8 * kBpKRing;        // V TMA -> converters
 constexpr int kCFree = kCFull + 8 * kBpCRing;        // converters (a warp each: 4) -> V TMA
 constexpr int kVFull = kCFree + 8 * kBpCRing;        // converters (4) -> MMA (P V)
-constexpr int kVFree = kVFull + 8 * kBpVRing;        // MMA (P V done) -> converters, softmax (O, when it rescales)
+constexpr int kVFree = kVFull + 8 * kBpVRing;        // MMA (P V done) -> converters, MMA (S over P), softmax (O, when it rescales)
 constexpr int kSFull = kVFree + 8 * kBpVRing;        // [2] MMA (S done) -> softmax
 constexpr int kPFull = kSFull + 16;                  // [2] softmax (a warp each: 4) -> MMA
 constexpr int kDone = kPFull + 16;                   // MMA: its last MMAs finished
@@ -382,11 +382,12 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       auto wait_all = [&](uint32_t bar, uint32_t parity) {
         return __all_sync(kFullMask, mbar_wait_parked(bar, parity));
       };
-      // K_j, V_j are there.  A look at a barrier takes 100 to 150 cycles even when its phase is over, so these
-      // come before the wait for P, off the chain from P_j to S_{j+2} (4 x 2048 tokens, on one GPU: 63.4 -> 62.7 us).
+      // K_j, V_j are there.  A look at a barrier takes 100 to 150 cycles even when its phase is over, so K_{j+2}'s
+      // comes while P_j V_j runs and V_{j+1}'s behind S_{j+2}, off the chain from P_j to S_{j+2} (4 x 2048 tokens and
+      // 16 chunks of 256, on one GPU: 64.4 and 69.2 us with both before the wait for P_j, 63.5 and 63.9 so).
       auto k_there = [&](int j) { return wait_all(hdr + kKFull + 8 * (j % kBpKRing), (j / kBpKRing) & 1); };
       auto v_there = [&](int j) { return wait_all(hdr + kVFull + 8 * (j % kBpVRing), (j / kBpVRing) & 1); };
-      // one lane: S_j = Q K_j^T (its columns hold P_{j-2}, read by P V issued before)
+      // one lane: S_j = Q K_j^T (its columns hold P_{j-2}, which P V has read)
       auto issue_s = [&](int j) {
         const int st = j % kBpKRing;
         const uint64_t kd = k_desc0 + static_cast<uint64_t>((st * kBpCodes) >> 4);
@@ -404,10 +405,11 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         if (!failed && elect_one()) issue_s(j);
         __syncwarp();
       }
+      if (nst > 0 && !failed) failed = !v_there(0);  // (a split tile may leave a CTA without stages)
       for (int j = 0; j < nst && !failed; ++j) {
         const int st = j % kBpVRing;
         if constexpr (kJitter) jitter_sleep(c_bp_jitter, warp, j);
-        if (!v_there(j) || (j + 2 < nst && !k_there(j + 2)) || !wait_all(hdr + kPFull + 8 * (j & 1), (j >> 1) & 1)) {
+        if (!wait_all(hdr + kPFull + 8 * (j & 1), (j >> 1) & 1)) {
           failed = true;
           break;
         }
@@ -418,9 +420,21 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
           for (int i = 0; i < kBpKB; ++i)
             umma_bf16_tmem_a(tmem + kBpOCol, tmem + kBpSCols * (j & 1) + 8 * i, vd + static_cast<uint64_t>((i * 2 * kBpTile) >> 4), id_pv, j > 0 || i > 0);
           umma_commit(hdr + kVFree + 8 * st);
-          if (j + 2 < nst) issue_s(j + 2);
         }
         __syncwarp();
+        if (j + 1 == nst) break;
+        if (j + 2 < nst) {
+          // S_{j+2} is written over P_j: MMAs keep their order of issue only among those of one accumulator and
+          // shape, so P_j V_j has to be done first (the slot's next phase is this warp's own P_{j+2} V_{j+2}).
+          if (!k_there(j + 2) || !wait_all(hdr + kVFree + 8 * st, (j / kBpVRing) & 1)) {
+            failed = true;
+            break;
+          }
+          tc_fence_after();
+          if (elect_one()) issue_s(j + 2);
+          __syncwarp();
+        }
+        failed = !v_there(j + 1);
       }
       if (lane == 0) {
         if (failed) raise_flag(a.status, PA_FLAG_TIMEOUT);
