@@ -335,10 +335,12 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_kh, const __grid_constant_
       o_started = o_started || mask_cur != 0;
       mask_cur = mask_next;
     }
+    // Every MMA issued has finished before the CTA frees TMEM and exits (a commit follows the MMAs of its
+    // own thread).
+    __syncwarp();
+    if (elect_one()) umma_commit(hdr + kBarDone);
     if (lane == 0) {
       if (failed) raise_flag(a.status, PA_FLAG_TIMEOUT);
-      // Every MMA issued has finished before the CTA frees TMEM and exits.
-      umma_commit(hdr + kBarDone);
       mbar_wait_bounded(hdr + kBarDone, 0);
     }
     __syncwarp();

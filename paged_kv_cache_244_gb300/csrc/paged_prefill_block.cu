@@ -436,9 +436,10 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         }
         failed = !v_there(j + 1);
       }
+      __syncwarp();
+      if (elect_one()) umma_commit(hdr + kDone);    // a commit follows the MMAs of its own thread
       if (lane == 0) {
         if (failed) raise_flag(a.status, PA_FLAG_TIMEOUT);
-        umma_commit(hdr + kDone);
         mbar_wait_parked(hdr + kDone, 0);
       }
     }
