@@ -354,6 +354,14 @@ __device__ __forceinline__ float rcp_ftz(float x) {
   return y;
 }
 
+// A factor on raw scores, held above zero (a NaN stays one): a masked score is -infinity before it is
+// multiplied, and -infinity * 0 is NaN.  Scores that a smaller factor would give are 0 beside the others.
+__device__ __forceinline__ float score_factor(float f) {
+  float r;
+  asm("max.NaN.f32 %0, %1, 0f00800000;" : "=f"(r) : "f"(f));  // 2^-126
+  return r;
+}
+
 // max(a, b, c) in one instruction (a NaN operand is ignored, as by fmaxf)
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
   float r;

@@ -316,7 +316,7 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       int st = 0;
       uint32_t ph = 1;                              // parity of the slot's previous release
       // K: the scales of the lane's block of the window and the next, as the softmax wants them --
-      // factor on q . Kcode, lift of the exponent, weight in L, whether the block is there.  Stage
+      // K scale, lift of the exponent, weight in L, whether the block is there.  Stage
       // j's lanes write theirs to slot j % 8 before the stage's barrier: the softmax reads them
       // after S_j, and the slot is written again for stage j + 8, after S_{j+5}, which was issued
       // behind P_{j+3} V_{j+3}, so when the softmax had done with stage j.
@@ -324,7 +324,7 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         if (!is_k) return make_float4(0.f, 0.f, 0.f, 0.f);
         const bool there = in_pool(id);
         const float2 kv = there ? a.kv_scale[static_cast<size_t>(id) * Hkv + g] : make_float2(1.f, 1.f);
-        return make_float4(a.scale_log2 * kv.x, log2_of(kv.y), __frcp_rn(kv.y), there ? 1.f : 0.f);
+        return make_float4(kv.x, log2_of(kv.y), __frcp_rn(kv.y), there ? 1.f : 0.f);
       };
       float4 scales = load_scales(ids), scales_next = load_scales(ids_next);
       float4* const scale_slots = reinterpret_cast<float4*>(base + kBpScaleOff);
@@ -497,7 +497,7 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
           const float raise = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
           if (hc == 0)
             folds[x] = top >= 0x7f80u ? __uint_as_float(0x7fc00000u)
-                                      : __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                                      : a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 #pragma unroll
           for (int p = 0; p < 2; ++p) {
             uint2 hi, lo;
@@ -513,7 +513,7 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       named_barrier(1, 128);                        // the rows and their factors are in place
       if (r == 0) mbar_arrive(hdr + kQReady);
     }
-    const float row_fold = folds[r];                // q = row_fold (hi + lo)
+    const float row_fold = folds[r];                // scale_log2 q = row_fold (hi + lo)
     float m = -INFINITY, l = 0.f;
     bool failed = false;
     const float4* const scale_slots = reinterpret_cast<const float4*>(base + kBpScaleOff);
@@ -543,7 +543,7 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
 #pragma unroll
       for (int b = 0; b < kBpKB; ++b) {
         const float4 v = scale_slots[(j % kBpScaleSlots) * kBpKB + b];
-        f[b] = v.x * row_fold;
+        f[b] = score_factor(row_fold * v.x);
         e[b] = v.y;
         w[b] = v.z;
         there[b] = v.w != 0.f;

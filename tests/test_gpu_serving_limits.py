@@ -1,0 +1,58 @@
+"""The block-scaled attention where its arithmetic runs out: factors and scores at the ends of fp32, queries below
+its normal range.
+
+Tolerances are those of test_gpu_serving (`close`): half a bf16 step of the result, 2^-8, and 2^-9 of the A that
+the reference gives for weights held in f16.
+"""
+
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+from test_gpu_serving import B, D, Pool, bf16, clean, close, normal, pa, up  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def both(pa, pool, q, lens, new, scale, want=0):
+    """Prefill of the last `new` rows of each sequence and decode of its last row, against the reference."""
+    qs = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    qd = q if hasattr(q, "is_cuda") else bf16(q)
+    q64 = qd.cpu().double().numpy()
+    args = (*pool.dev(), up(pool.tables), up(pool.lens))
+    pre = pa.prefill_fp8_block(qd, up(qs), *args, max(new), max(lens), scale)
+    dec = pa.decode_fp8_block(qd[up(qs[1:].astype(np.int64) - 1)], *args, max(lens), scale)
+    clean(pa, want)
+    for s, (n, m) in enumerate(zip(lens, new)):
+        ref, mag = pool.attention(s, q64[qs[s]:qs[s + 1]], scale, n - m)
+        close(dec[s:s + 1], ref[-1:], mag[-1:], ("decode", s))
+        close(pre[qs[s]:qs[s + 1]], ref, mag, ("prefill", s))
+
+
+CUTS = [([70, 33, 1], [70, 5, 1]), ([2000, 900], [3, 20])]     # whole tiles, and keys split over a cluster
+
+
+@pytest.mark.parametrize("lens,new", CUTS)
+@pytest.mark.parametrize("size", [2.0 ** -95, 2.0 ** -105, 2.0 ** -122])
+def test_small_queries_over_blocks_of_the_least_scale(pa, lens, new, size):
+    """scale * K scale * the power of two of q is below fp32's range, beside masked keys."""
+    rng = np.random.default_rng(1)
+    pool = Pool(rng, lens, 2)
+    for s in range(len(lens)):
+        pool.k[pool.tables[s, : (lens[s] + B - 1) // B : 2]] = 0
+        pool.scale[pool.tables[s, : (lens[s] + B - 1) // B : 2], :, 0] = 2.0 ** -40
+    both(pa, pool, normal(rng, sum(new), 12, D) * size, lens, new, D ** -0.5)
+
+
+@pytest.mark.parametrize("lens,new", CUTS)
+def test_softmax_scale_and_query_far_apart(pa, lens, new):
+    """The power of two of q and the softmax scale cancel; with the K scale alone the latter leaves fp32's range."""
+    rng = np.random.default_rng(2)
+    for k_scale in (2.0 ** -40, 2.0 ** 34):
+        pool = Pool(rng, lens, 2)
+        pool.scale[..., 0] = k_scale
+        size = 2.0 ** 118 if k_scale < 1 else 2.0 ** -110
+        both(pa, pool, normal(rng, sum(new), 12, D) * size, lens, new, D ** -0.5 / size / k_scale * 2.0 ** -7)
+
+
