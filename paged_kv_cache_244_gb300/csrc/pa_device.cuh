@@ -354,11 +354,15 @@ __device__ __forceinline__ float rcp_ftz(float x) {
   return y;
 }
 
-// A factor on raw scores, held above zero (a NaN stays one): a masked score is -infinity before it is
-// multiplied, and -infinity * 0 is NaN.  Scores that a smaller factor would give are 0 beside the others.
-__device__ __forceinline__ float score_factor(float f) {
+// The factor on a query row's raw scores but for the K scale (softmax scale, log2 e, the power of two of q), held
+// to [2^-86, 2^63]; a NaN stays one.  With K scales of 2^-40 to 2^40 and raw scores below 2^24 no product then
+// leaves fp32's range, where -infinity (a masked score) times 0 and 0 times infinity are NaN.  A smaller
+// factor's scores, below 2^-22 as they are, leave the weights as they stand; with a larger one the largest
+// score has all the weight, as it has with this.
+__device__ __forceinline__ float row_factor(float f) {
   float r;
-  asm("max.NaN.f32 %0, %1, 0f00800000;" : "=f"(r) : "f"(f));  // 2^-126
+  asm("max.NaN.f32 %0, %1, 0f14800000;" : "=f"(r) : "f"(f));  // 2^-86
+  asm("min.NaN.f32 %0, %1, 0f5F000000;" : "=f"(r) : "f"(r));  // 2^63
   return r;
 }
 

@@ -389,7 +389,7 @@ decode_block_kernel(const DecodeArgs a, const int pool) {
     }
     // an infinity or a NaN makes the head's scores NaN
     const float fold = top >= 0x7f80u ? __uint_as_float(0x7fc00000u)
-                                      : a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                                      : row_factor(a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23));
     kf0 = __shfl_sync(kFullMask, fold, 8 * cq);
     kf1 = __shfl_sync(kFullMask, fold, 8 * cq + 4);
   };

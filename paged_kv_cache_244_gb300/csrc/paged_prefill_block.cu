@@ -513,7 +513,7 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       named_barrier(1, 128);                        // the rows and their factors are in place
       if (r == 0) mbar_arrive(hdr + kQReady);
     }
-    const float row_fold = folds[r];                // scale_log2 q = row_fold (hi + lo)
+    const float row_fold = row_factor(folds[r]);    // scale_log2 q = row_fold (hi + lo)
     float m = -INFINITY, l = 0.f;
     bool failed = false;
     const float4* const scale_slots = reinterpret_cast<const float4*>(base + kBpScaleOff);
@@ -543,7 +543,7 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
 #pragma unroll
       for (int b = 0; b < kBpKB; ++b) {
         const float4 v = scale_slots[(j % kBpScaleSlots) * kBpKB + b];
-        f[b] = score_factor(row_fold * v.x);
+        f[b] = row_fold * v.x;
         e[b] = v.y;
         w[b] = v.z;
         there[b] = v.w != 0.f;

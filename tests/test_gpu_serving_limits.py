@@ -56,3 +56,16 @@ def test_softmax_scale_and_query_far_apart(pa, lens, new):
         both(pa, pool, normal(rng, sum(new), 12, D) * size, lens, new, D ** -0.5 / size / k_scale * 2.0 ** -7)
 
 
+@pytest.mark.parametrize("lens,new", CUTS)
+def test_large_factors_over_scores_of_zero(pa, lens, new):
+    """scale * K scale * the power of two of q is above fp32's range where q . K is 0."""
+    rng = np.random.default_rng(3)
+    pool = Pool(rng, lens, 2)
+    pool.k[..., :64] = 0
+    pool.scale[..., 0] = 2.0 ** 40
+    q = normal(rng, sum(new), 12, D) * 2.0 ** 120
+    q[..., 64:] = 0
+    for s, n in enumerate(lens):                                # the slots past the context hold NaN still
+        if n % B:
+            pool.k[pool.tables[s, n // B], :, n % B:] = 0x7F
+    both(pa, pool, q, lens, new, D ** -0.5)
