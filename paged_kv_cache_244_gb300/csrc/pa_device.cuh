@@ -366,6 +366,12 @@ __device__ __forceinline__ float row_factor(float f) {
   return r;
 }
 
+// Raw scores are below 2^24, so with a factor up to this the scores are below 2^20 and a weight's exponent is one
+// FMA of raw score, factor and shift.  Past it the exponent takes two steps, the score rounded as the one that
+// set the shift was, then the difference: the FMA would leave the shift's own rounding in it, half a step of
+// the score (64 at 2^30), and weights past f16.
+constexpr float kFarFactor = 0x1p-4f;
+
 // max(a, b, c) in one instruction (a NaN operand is ignored, as by fmaxf)
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
   float r;

@@ -452,9 +452,19 @@ decode_block_kernel(const DecodeArgs a, const int pool) {
     const bool whole_tiles = two && (fl & all) == all && valid == kBlockSize;
     const int n0 = (fl & kHas0) ? (two ? kBlockSize : valid) : 0;   // live tokens of each tile
     const int n1 = (fl & kHas1) ? valid : 0;
-    const float f00 = kf0 * sv.x, f01 = kf1 * sv.x, f10 = kf0 * sv.z, f11 = kf1 * sv.z;
-    const float e0 = log2_of(sv.y), e1 = log2_of(sv.w);
+    float f00 = kf0 * sv.x, f01 = kf1 * sv.x, f10 = kf0 * sv.z, f11 = kf1 * sv.z;
+    float e0 = log2_of(sv.y), e1 = log2_of(sv.w);
     float y[2][4];
+    if (fmaxf(fmax3(f00, f01, f10), f11) > kFarFactor) {   // exponents in two steps
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s[0][i] = fmaf(s[0][i] + t[0][i], (i & 1) ? f01 : f00, e0);
+        s[1][i] = fmaf(s[1][i] + t[1][i], (i & 1) ? f11 : f10, e1);
+        t[0][i] = t[1][i] = 0.f;
+      }
+      f00 = f01 = f10 = f11 = 1.f;
+      e0 = e1 = 0.f;
+    }
     auto exponents = [&](float sh0, float sh1) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -483,7 +493,7 @@ decode_block_kernel(const DecodeArgs a, const int pool) {
         b0 = fmaxf(b0, __shfl_xor_sync(kFullMask, b0, x));
         b1 = fmaxf(b1, __shfl_xor_sync(kFullMask, b1, x));
       }
-      const float mn0 = b0 > m0 + 15.f ? b0 - 7.f : m0, mn1 = b1 > m1 + 15.f ? b1 - 7.f : m1;
+      const float mn0 = b0 - m0 > 15.f ? b0 - 7.f : m0, mn1 = b1 - m1 > 15.f ? b1 - 7.f : m1;
       const float al0 = mn0 == m0 ? 1.f : ex2_ftz(m0 - mn0), al1 = mn1 == m1 ? 1.f : ex2_ftz(m1 - mn1);
       m0 = mn0;
       m1 = mn1;

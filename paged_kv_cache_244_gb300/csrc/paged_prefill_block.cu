@@ -549,8 +549,18 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         there[b] = v.w != 0.f;
         all_there = all_there && there[b];
       }
-      // causal mask and absent blocks -> -inf, only on a stage that needs it
-      if (!all_there || kBpKeys * (j0 + j + 1) - 1 > pos0) {
+      // causal mask and absent blocks -> -inf, exponents in two steps: only on a stage that needs it
+      const bool far = fmaxf(fmax3(f[0], f[1], f[2]), f[3]) > kFarFactor;
+      if (far || !all_there || kBpKeys * (j0 + j + 1) - 1 > pos0) {
+        if (far) {
+#pragma unroll
+          for (int c = 0; c < kBpKeys; ++c) sc[c] = fmaf(sc[c], f[c / kBlockSize], e[c / kBlockSize]);
+#pragma unroll
+          for (int b = 0; b < kBpKB; ++b) {
+            f[b] = 1.f;
+            e[b] = 0.f;
+          }
+        }
         const int lim = p_r - kBpKeys * (j0 + j);
 #pragma unroll
         for (int c = 0; c < kBpKeys; ++c)
@@ -564,7 +574,7 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         const float u3 = fmax3(x[9], x[10], x[11]), u4 = fmax3(x[12], x[13], x[14]);
         mrow = fmaxf(mrow, fmaf(fmax3(fmax3(u0, u1, u2), fmaxf(u3, u4), x[15]), f[b], e[b]));
       }
-      const float mn = mrow > m + 15.f ? mrow - 7.f : m;
+      const float mn = mrow - m > 15.f ? mrow - 7.f : m;
       const float sh = mn == -INFINITY ? 0.f : mn;
       const float alpha = (mn == m || m == -INFINITY) ? 1.f : ex2_ftz(m - sh);
       m = mn;

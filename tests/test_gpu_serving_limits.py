@@ -2,7 +2,9 @@
 its normal range.
 
 Tolerances are those of test_gpu_serving (`close`): half a bf16 step of the result, 2^-8, and 2^-9 of the A that
-the reference gives for weights held in f16.
+the reference gives for weights held in f16.  Scores beyond 2^24 carry an fp32 rounding of their own, up to half
+a step of the score: the tests that use them check on the reference that the largest score leads by more than
+its step times 64, so that the weights are 0 and 1 whatever the rounding.
 """
 
 from __future__ import annotations
@@ -10,6 +12,7 @@ from __future__ import annotations
 import numpy as np
 import pytest
 
+import serving_ref as R
 from test_gpu_serving import B, D, Pool, bf16, clean, close, normal, pa, up  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -68,4 +71,25 @@ def test_large_factors_over_scores_of_zero(pa, lens, new):
     for s, n in enumerate(lens):                                # the slots past the context hold NaN still
         if n % B:
             pool.k[pool.tables[s, n // B], :, n % B:] = 0x7F
+    both(pa, pool, q, lens, new, D ** -0.5)
+
+
+@pytest.mark.parametrize("lens,new", CUTS)
+@pytest.mark.parametrize("k_scale", [2.0 ** 14, 2.0 ** 21, 2.0 ** 40])
+def test_large_scores(pa, lens, new, k_scale):
+    """Scores of 2^24 and more: the step between neighbouring fp32 values passes what a weight can hold."""
+    rng = np.random.default_rng(4)
+    pool = Pool(rng, lens, 2)
+    pool.scale[..., 0] = k_scale
+    q = R.bf16_round(normal(rng, sum(new), 4, D))
+    qs = np.concatenate([[0], np.cumsum(new)])
+    for s, (n, m) in enumerate(zip(lens, new)):                 # the largest score leads clearly, or keys are one
+        ids = pool.tables[s][: (n + B - 1) // B]
+        for g in range(2):
+            K = np.concatenate([R.E4M3[pool.k[b, g]] for b in ids])[:n] * k_scale
+            x = np.einsum("rhd,td->rht", q[qs[s]:qs[s + 1], 2 * g:2 * g + 2], K) * D ** -0.5 * np.log2(np.e)
+            x = np.where(np.arange(n) <= n - m + np.arange(m)[:, None, None], x, -np.inf)
+            top = np.sort(x, axis=-1)
+            if n > 1:
+                assert (np.isinf(top[..., -2]) | (top[..., -1] - top[..., -2] > 64 * 2.0 ** -23 * np.abs(top[..., -1]))).all()
     both(pa, pool, q, lens, new, D ** -0.5)
