@@ -379,8 +379,8 @@ decode_block_kernel(const DecodeArgs a, const int pool) {
     top = __vmaxu2(top, __shfl_xor_sync(kFullMask, top, 1));
     top = __vmaxu2(top, __shfl_xor_sync(kFullMask, top, 2));
     top = max(top & 0xffffu, top >> 16);             // the head's largest magnitude
-    int e = 7 + 127 - static_cast<int>(top >> 7);
-    e = (top >> 7) == 0 ? 0 : min(max(e, -126), 126);
+    // to [128, 256); below 2^-119 not as far: multiples of 2^-133 become multiples of 2^-7, exact all the same
+    const int e = min(7 + 127 - static_cast<int>(top >> 7), 126);
     const float raise = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
 #pragma unroll
     for (int c = 0; c < 8; ++c) {

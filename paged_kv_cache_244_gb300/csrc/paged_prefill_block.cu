@@ -492,8 +492,8 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
 #pragma unroll
           for (int o = 1; o < 8; o <<= 1) top = __vmaxu2(top, __shfl_xor_sync(kFullMask, top, o));
           top = max(top & 0xffffu, top >> 16);
-          int e = 7 + 127 - static_cast<int>(top >> 7);
-          e = (top >> 7) == 0 ? 0 : min(max(e, -126), 126);
+          // below 2^-119 not as far: multiples of 2^-133 become multiples of 2^-7, exact all the same
+          const int e = min(7 + 127 - static_cast<int>(top >> 7), 126);
           const float raise = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
           if (hc == 0)
             folds[x] = top >= 0x7f80u ? __uint_as_float(0x7fc00000u)

@@ -93,3 +93,13 @@ def test_large_scores(pa, lens, new, k_scale):
             if n > 1:
                 assert (np.isinf(top[..., -2]) | (top[..., -1] - top[..., -2] > 64 * 2.0 ** -23 * np.abs(top[..., -1]))).all()
     both(pa, pool, q, lens, new, D ** -0.5)
+
+
+@pytest.mark.parametrize("lens,new", CUTS)
+def test_queries_below_the_normal_range(pa, lens, new):
+    rng = np.random.default_rng(5)
+    pool = Pool(rng, lens, 2)
+    codes = rng.integers(-100, 101, (sum(new), 12, D))          # multiples of 2^-133, the least bf16
+    q = up((np.abs(codes) | np.where(codes < 0, 0x8000, 0)).astype(np.uint16).view(np.int16)).view(bf16(np.zeros(1)).dtype)
+    assert np.array_equal(q.cpu().double().numpy(), codes * 2.0 ** -133)
+    both(pa, pool, q, lens, new, D ** -0.5 * 2.0 ** 127)
