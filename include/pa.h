@@ -542,7 +542,7 @@ int pa_prefill_fp8_block(const pa_dims* dims, int num_seqs, int num_tokens, cons
  *   cached_lens, new_lens  [S] int32, read only
  *   block_tables   [S][max_blocks] int32, read, and written at the new entries
  *   max_blocks     >= 1, max_blocks * 16 <= 2^31 - 16
- *   free_blocks    [free_capacity] int32, read only; free_capacity >= 0
+ *   free_blocks    [free_capacity] int32, read only; 0 <= free_capacity <= 2^30
  *   num_free       [1] int32;  num_free_out [1] int32, may be num_free itself
  *   num_blocks     >= 1
  *   num_tokens     rows of positions and slot_mapping, 0 <= T <= 2^31 - 16

@@ -646,7 +646,7 @@ int pa_plan_step(const pa_dims* dims, int num_seqs, const int32_t* cached_lens,
                  void* stream) {
   if (const int rc = check_dims(dims)) return rc;
   if (num_seqs < 0 || num_seqs > pa::kMaxDecodeSeqs || num_tokens < 0 || num_tokens > 0x7ffffff0) return PA_ERR_RANGE;
-  if (free_capacity < 0 || num_blocks < 1 || max_blocks < 1 || max_blocks > (0x7fffffff - 15) / 16)
+  if (free_capacity < 0 || free_capacity > pa::kMaxFreeBlocks || num_blocks < 1 || max_blocks < 1 || max_blocks > (0x7fffffff - 15) / 16)
     return PA_ERR_RANGE;
   if (!num_free || !num_free_out || !q_start) return PA_ERR_NULL;
   if (num_seqs > 0 && (!cached_lens || !new_lens || !block_tables || !context_lens || !granted))

@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kThreads) plan_step_kernel(const PlanArgs a, c
   long long r = block_exclusive<kThreads>(rows, row_sums, &all_rows);
   // Needs: of the sequences whose lengths and rows are in order.  Each is at most max_blocks
   // < 2^27 blocks and there are at most 8192, so their sum is kept in 64 bits, and clamped
-  // to 2^31 - 1 where it is stored (a free list is shorter, so the order is unchanged).
+  // to 2^31 - 1 where it is stored (a free list holds at most kMaxFreeBlocks, so the order is unchanged).
   long long need_sum = 0;
   for (int s = s0; s < s1; ++s) {
     const int n = start[s], c = x[s];
