@@ -5,15 +5,19 @@ against this interpreter's PyTorch.
 Each translation unit compiles in parallel with nvcc (-gencode arch=compute_103a,
 code=sm_103a, -O3, -lineinfo); the objects link into one shared library with the CUDA
 runtime linked statically, so loading it needs only the driver.  Rebuilds only when a
-source or header is newer than the library.
+source or header is newer than the library.  Where a host compiler, Python's headers or
+PyTorch's are missing, the library is built all the same, with a warning, and the calls that
+need the native half raise.
 """
 
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 from pathlib import Path
 
@@ -57,13 +61,34 @@ def native_up_to_date() -> bool:
     return all(p.stat().st_mtime <= t for p in [NATIVE_SOURCE, *INCLUDE.glob("*.h")])
 
 
+def cxx() -> str:
+    return os.environ.get("CXX") or "g++"
+
+
+def torch_dir() -> Path | None:
+    """The installed PyTorch, found without importing it."""
+    spec = importlib.util.find_spec("torch")
+    return Path(spec.origin).resolve().parent if spec and spec.origin else None
+
+
+def native_missing() -> str | None:
+    """What the native half of the binding needs and is not there (None: nothing)."""
+    if not shutil.which(cxx()):
+        return f"no host compiler ({cxx()})"
+    torch = torch_dir()
+    if torch is None or not (torch / "include" / "torch" / "csrc" / "autograd" / "python_variable.h").exists():
+        return "no PyTorch with its headers"
+    if not (Path(sysconfig.get_paths()["include"]) / "Python.h").exists():
+        return "no Python headers"
+    return None
+
+
 def _compile_native() -> Path:
     """The binding's object file (its link needs the library)."""
-    import torch
-    inc = Path(torch.__file__).resolve().parent / "include"
+    inc = torch_dir() / "include"
     cuda = Path(nvcc()).resolve().parents[1] / "include"
     obj = BUILD_DIR / "pa_torch.o"
-    cmd = [os.environ.get("CXX") or "g++", "-c", str(NATIVE_SOURCE), "-o", str(obj), "-O2", "-std=c++17", "-fPIC",
+    cmd = [cxx(), "-c", str(NATIVE_SOURCE), "-o", str(obj), "-O2", "-std=c++17", "-fPIC",
            f"-I{INCLUDE}", f"-I{inc}", f"-I{inc}/torch/csrc/api/include", f"-I{cuda}",
            f"-I{sysconfig.get_paths()['include']}"]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -73,10 +98,9 @@ def _compile_native() -> Path:
 
 
 def _link_native(obj: Path) -> None:
-    import torch
-    libs = Path(torch.__file__).resolve().parent / "lib"
+    libs = torch_dir() / "lib"
     tmp = NATIVE.with_name(NATIVE.name + f".tmp{os.getpid()}")
-    cmd = [os.environ.get("CXX") or "g++", "-shared", "-o", str(tmp), str(obj), f"-L{libs}", f"-L{PKG}",
+    cmd = [cxx(), "-shared", "-o", str(tmp), str(obj), f"-L{libs}", f"-L{PKG}",
            "-l:libpa_gb300.so", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda",
            f"-Wl,-rpath,{libs}", "-Wl,-rpath,$ORIGIN"]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -86,12 +110,18 @@ def _link_native(obj: Path) -> None:
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> Path:
-    if not force and up_to_date():
-        if not native_up_to_date():
-            BUILD_DIR.mkdir(exist_ok=True)
-            _link_native(_compile_native())
+    ready = not force and up_to_date()
+    if ready and native_up_to_date():
         return LIBRARY
     BUILD_DIR.mkdir(exist_ok=True)
+    missing = native_missing()
+    if missing:
+        warnings.warn(f"{missing}: {NATIVE.name} is not built, the serving calls of the binding will raise",
+                      RuntimeWarning, stacklevel=2)
+    if ready:
+        if not missing:
+            _link_native(_compile_native())
+        return LIBRARY
     cc = nvcc()
     flags = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
                     f"-I{INCLUDE}", f"-I{CSRC}", "--expt-relaxed-constexpr"] + (extra_flags or [])
@@ -107,7 +137,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
         return obj
 
     with ThreadPoolExecutor(max_workers=max(1, min(12, os.cpu_count() or 1))) as ex:
-        native = ex.submit(_compile_native)
+        native = None if missing else ex.submit(_compile_native)
         objs = list(ex.map(compile_one, _sources()))
     tmp = LIBRARY.with_name(LIBRARY.name + f".tmp{os.getpid()}")
     cmd = [cc, "-shared", "-o", str(tmp)] + ARCH + [str(o) for o in objs]
@@ -115,7 +145,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIBRARY)
-    _link_native(native.result())
+    if native:
+        _link_native(native.result())
     return LIBRARY
 
 
