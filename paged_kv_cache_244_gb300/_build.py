@@ -5,7 +5,8 @@ against this interpreter's PyTorch.
 Each translation unit compiles in parallel with nvcc (-gencode arch=compute_103a,
 code=sm_103a, -O3, -lineinfo); the objects link into one shared library with the CUDA
 runtime linked statically, so loading it needs only the driver.  Rebuilds only when a
-source or header is newer than the library.  Where a host compiler, Python's headers or
+source or header is newer than the library, or the native half was compiled against another
+interpreter or PyTorch.  Where a host compiler, Python's headers or
 PyTorch's are missing, the library is built all the same, with a warning, and the calls that
 need the native half raise.
 """
@@ -54,13 +55,6 @@ def up_to_date() -> bool:
     return all(p.stat().st_mtime <= t for p in _deps())
 
 
-def native_up_to_date() -> bool:
-    if not NATIVE.exists():
-        return False
-    t = NATIVE.stat().st_mtime
-    return all(p.stat().st_mtime <= t for p in [NATIVE_SOURCE, *INCLUDE.glob("*.h")])
-
-
 def cxx() -> str:
     return os.environ.get("CXX") or "g++"
 
@@ -69,6 +63,21 @@ def torch_dir() -> Path | None:
     """The installed PyTorch, found without importing it."""
     spec = importlib.util.find_spec("torch")
     return Path(spec.origin).resolve().parent if spec and spec.origin else None
+
+
+def native_key() -> str:
+    """The interpreter and the PyTorch that the native half is compiled against."""
+    version = torch_dir() / "version.py" if torch_dir() else None
+    text = version.read_text() if version and version.exists() else ""
+    return f"{sysconfig.get_config_var('SOABI')}\n{version}\n{text}"
+
+
+def native_up_to_date() -> bool:
+    key = BUILD_DIR / "pa_torch.key"
+    if not NATIVE.exists() or not key.exists() or key.read_text() != native_key():
+        return False
+    t = NATIVE.stat().st_mtime
+    return all(p.stat().st_mtime <= t for p in [NATIVE_SOURCE, *INCLUDE.glob("*.h")])
 
 
 def native_missing() -> str | None:
@@ -107,6 +116,7 @@ def _link_native(obj: Path) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"linking {NATIVE.name} failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, NATIVE)
+    (BUILD_DIR / "pa_torch.key").write_text(native_key())
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> Path:

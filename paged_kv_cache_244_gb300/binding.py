@@ -521,7 +521,7 @@ def _native():
         try:
             from . import _pa_torch
         except ImportError as e:
-            raise RuntimeError("_pa_torch.so is not built: run __graft_entry__.build()") from e
+            raise RuntimeError(f"_pa_torch.so cannot be loaded ({e}): run __graft_entry__.build()") from e
         _native_module = _pa_torch
     return _native_module
 
