@@ -489,7 +489,8 @@ int pa_decode_step_fp8_block(const pa_dims* dims, const pa_rope* rope, int num_s
  * pa_prefill_fp8_block -- pa_prefill over block-scaled E4M3 caches (whose new tokens
  * pa_rope_kv_store_fp8_block has stored): the queries of a chunk see every cached token, the
  * chunk's own among them, as the cache holds it.  Arguments, checks and errors as pa_prefill,
- * plus kv_scale (read only).  A query whose every block is out of range gives a zero row.
+ * plus kv_scale (read only).  A query whose every block is out of range gives a zero row.  A NaN in
+ * the cache reaches the queries that see its token, and no other.
  * max_context_len also says how far few queries over a long context are spread over the GPU: a bound
  * far above the contexts is right, and costs small calls some microseconds.
  * Launches one kernel.

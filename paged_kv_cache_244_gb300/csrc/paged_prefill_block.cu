@@ -29,7 +29,8 @@
 //   2   converters: 128 threads widen a stage's V codes from the TMA's ring into the f16 operand
 //       ring, 16 codes a load, in the MN-major layout that the MMA reads (two 64-dim halves a
 //       block, 128-byte swizzle).  V rows past the context, and V of absent blocks, are written
-//       as zeros.
+//       as zeros; so is a NaN in a token that some of the tile's rows do not see (0 * NaN would
+//       reach them), and the rows that do get it back when out is written.
 // Tensor memory per CTA (256 columns): S_j in columns 64 (j & 1) .. + 63, O in 128-255; a row's
 // P_j (64 f16, 32 columns) is written by its thread over the S_j it has read, and is the A operand
 // of P V from there.  So S_{j+1} is computed while the softmax works on S_j, and S_{j+2}, which
@@ -87,12 +88,13 @@ constexpr int kBpFoldOff = kBpHdrOff + kBpHeader;    // a float per row
 constexpr int kBpScaleOff = kBpFoldOff + kBpRows * 4;   // a float4 per block of the stage, stage j in slot j % 8
 constexpr int kBpScaleSlots = 8;
 constexpr int kBpMlOff = kBpScaleOff + kBpScaleSlots * kBpKB * 16;   // split: a row's (m, L)
-constexpr int kBpSmem = kBpMlOff + kBpRows * 8 + 1024;   // + alignment of the first stage
+constexpr int kBpNanOff = kBpMlOff + kBpRows * 8;    // a dim's first NaN in V (key of this CTA), and the first of all
+constexpr int kBpSmem = kBpNanOff + (kHeadDim + 4) * 4 + 1024;   // + alignment of the first stage
 static_assert(kBpRows * kHeadDim * 4 <= kBpHdrOff, "the partial rows of a split tile fit the stages");
 static_assert(2 * (kBpSmem + 1024) <= 228 * 1024, "two CTAs per SM");
 constexpr int kBpThreads = 384;
 // registers per thread at launch, and the split (their sums per warpgroup are equal)
-constexpr int kBpRegsSoftmax = 136, kBpRegsIssue = 48, kBpRegsConvert = 56;
+constexpr int kBpRegsSoftmax = 128, kBpRegsIssue = 48, kBpRegsConvert = 64;
 static_assert(kBpRegsSoftmax + kBpRegsIssue + kBpRegsConvert <= 3 * 80, "of the 80 a thread launched with");
 // A tile's keys are split over 2, 4 or 8 CTAs as long as there are at most kSplitCtas CTAs (two per SM) and
 // at least kMinSplitStages stages for each; not below kSplitFrom stages (the exchange costs what some five
@@ -112,7 +114,7 @@ constexpr int kVFull = kCFree + 8 * kBpCRing;        // converters (4) -> MMA (P
 constexpr int kVFree = kVFull + 8 * kBpVRing;        // MMA (P V done) -> converters, MMA (S over P), softmax (O, when it rescales)
 constexpr int kSFull = kVFree + 8 * kBpVRing;        // [2] MMA (S done) -> softmax
 constexpr int kPFull = kSFull + 16;                  // [2] softmax (a warp each: 4) -> MMA
-constexpr int kDone = kPFull + 16;                   // MMA: its last MMAs finished
+constexpr int kDone = kPFull + 16;                   // MMA: its last MMAs finished; its own arrival passes on the converters'
 constexpr int kQReady = kDone + 8;                   // softmax (one thread, all rows in place) -> MMA
 constexpr int kTmemAt = kQReady + 8;
 static_assert(kTmemAt + 4 <= kBpHeader, "header");
@@ -136,6 +138,23 @@ __device__ __forceinline__ void split_e4m3(uint32_t w0, uint32_t w1, float raise
   }
   hi = h[0] | (static_cast<uint32_t>(h[1]) << 16);
   lo = l[0] | (static_cast<uint32_t>(l[1]) << 16);
+}
+
+// The top bit of each byte that is a NaN among four codes.
+__device__ __forceinline__ uint32_t e4m3_nans(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+
+// Zeros in the place of the NaN among 16 codes of V (dims d .. d + 15), `key` noted as the dim's first.
+__device__ __forceinline__ void take_nans(uint32_t* codes, int* nan_from, int d, int key) {
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t nan = e4m3_nans(codes[i]);
+    if (nan == 0) continue;
+    codes[i] &= ~((nan >> 7) * 0xffu);
+#pragma unroll 1
+    for (int u = 0; u < 4; ++u)
+      if ((nan >> (8 * u)) & 0x80u) atomicMin(nan_from + d + 4 * i + u, key);
+    atomicMin(nan_from + kHeadDim, key);
+  }
 }
 
 template <bool kSplit, bool kJitter>
@@ -208,6 +227,9 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     const int id = __shfl_sync(kFullMask, ids, ((kBpKB * j) & 31) + (lane & (kBpKB - 1)));
     return static_cast<int>(__ballot_sync(kFullMask, in_pool(id)) & ((1u << kBpKB) - 1));
   };
+  int* const nan_from = reinterpret_cast<int*>(base + kBpNanOff);
+  const int key0 = kBpKeys * j0;                    // this CTA's first key
+  if (threadIdx.x <= kHeadDim) nan_from[threadIdx.x] = 0x7fffffff;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kBpKRing; ++i) {
       mbar_init(hdr + kKFull + 8 * i, 1);
@@ -225,7 +247,7 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       mbar_init(hdr + kPFull + 8 * i, 4);
       mbar_init(hdr + kSFull + 8 * i, 1);
     }
-    mbar_init(hdr + kDone, 1);
+    mbar_init(hdr + kDone, 2);
     mbar_init(hdr + kQReady, 1);
     fence_mbar_init();
   }
@@ -272,14 +294,31 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         failed = true;
         break;
       }
-      const unsigned char* codes = base + kBpCOff + cst * kBpCodes;
+      unsigned char* const codes = base + kBpCOff + cst * kBpCodes;
       unsigned char* const ops = base + kBpVOff + vst * kBpVStage;
       uint4 w[kBpKB];
+      auto load_codes = [&] {
 #pragma unroll
-      for (int b = 0; b < kBpKB; ++b) {
-        w[b] = *reinterpret_cast<const uint4*>(codes + b * kBpTile + in_off);
-        const bool live = ((mask >> b) & 1) && (kBpKB * j + b != last_blk || r8 < valid_last);
-        if (!live) w[b] = make_uint4(0u, 0u, 0u, 0u);
+        for (int b = 0; b < kBpKB; ++b) {
+          w[b] = *reinterpret_cast<const uint4*>(codes + b * kBpTile + in_off);
+          const bool live = ((mask >> b) & 1) && (kBpKB * j + b != last_blk || r8 < valid_last);
+          if (!live) w[b] = make_uint4(0u, 0u, 0u, 0u);
+        }
+      };
+      load_codes();
+      if (kBpKeys * (j + 1) > pos0 + 1 - key0) {    // keys that some rows do not see
+        uint32_t nan = 0;
+#pragma unroll
+        for (int b = 0; b < kBpKB; ++b) nan |= e4m3_nans(w[b].x) | e4m3_nans(w[b].y) | e4m3_nans(w[b].z) | e4m3_nans(w[b].w);
+        if (nan) {
+#pragma unroll 1
+          for (int b = 0; b < kBpKB; ++b) {
+            const int key = kBpKeys * j + kBlockSize * b + r8;
+            if (key0 + key > pos0 && key0 + key < ctx && ((mask >> b) & 1))
+              take_nans(reinterpret_cast<uint32_t*>(codes + b * kBpTile + in_off), nan_from, kBlockSize * c, key);
+          }
+          load_codes();
+        }
       }
 #pragma unroll
       for (int b = 0; b < kBpKB; ++b) {
@@ -440,6 +479,7 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       if (elect_one()) umma_commit(hdr + kDone);    // a commit follows the MMAs of its own thread
       if (lane == 0) {
         if (failed) raise_flag(a.status, PA_FLAG_TIMEOUT);
+        mbar_arrive(hdr + kDone);
         mbar_wait_parked(hdr + kDone, 0);
       }
     }
@@ -625,6 +665,8 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     // A warp that gave up still takes part in the barriers below (its rows' values are undefined).
     const bool ok = !failed && __all_sync(kFullMask, mbar_wait_parked(hdr + kDone, 0));
     if (!ok && lane == 0) raise_flag(a.status, PA_FLAG_TIMEOUT);
+    const int last_key = p_r - key0;
+    const bool spoiled = nan_from[kHeadDim] <= last_key;   // the row sees a NaN that the converters took out of V
     if constexpr (kSplit) {
       // Every MMA of this CTA is done, so its stages are free; the others' partial rows come there.
       reinterpret_cast<float2*>(base + kBpMlOff)[r] = make_float2(m, l);
@@ -668,6 +710,15 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
           if (xi < rows_q) st_cluster_f4(cluster_addr(stages + at, to), v);
         }
       }
+      if (spoiled && xi < rows_q) {
+#pragma unroll 1
+        for (int dim = 0; dim < kHeadDim; ++dim) {
+          if (nan_from[dim] > last_key) continue;
+          const int to = dim >> (7 - log_ranks), d = dim - to * dims;
+          st_cluster_f1(cluster_addr(stages + (rank * kBpRows + r) * dims * 4 + (((d >> 2) ^ turn) << 4) + 4 * (d & 3), to),
+                        __uint_as_float(0x7fc00000u));
+        }
+      }
       folds[r] = total == 0.f ? 0.f : 1.f / total;  // read by the CTA's threads after the barrier
       cluster_sync();
     } else {
@@ -692,6 +743,12 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
               o[u] = pack_bf16x2(__uint_as_float(ov[8 * k + 2 * u]) * inv, __uint_as_float(ov[8 * k + 2 * u + 1]) * inv);
             *reinterpret_cast<uint4*>(qbuf + r * 128 + (((4 * q2 + k) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
           }
+        }
+        if (spoiled) {
+#pragma unroll 1
+          for (int d = 0; d < 64; ++d)
+            if (nan_from[64 * part + d] <= last_key)
+              *reinterpret_cast<uint16_t*>(qbuf + r * 128 + (((d >> 3) ^ (r & 7)) << 4) + 2 * (d & 7)) = 0x7fc0;
         }
         named_barrier(1, 128);
 #pragma unroll

@@ -103,3 +103,37 @@ def test_queries_below_the_normal_range(pa, lens, new):
     q = up((np.abs(codes) | np.where(codes < 0, 0x8000, 0)).astype(np.uint16).view(np.int16)).view(bf16(np.zeros(1)).dtype)
     assert np.array_equal(q.cpu().double().numpy(), codes * 2.0 ** -133)
     both(pa, pool, q, lens, new, D ** -0.5 * 2.0 ** 127)
+
+
+@pytest.mark.parametrize("hq,kv", [(12, 2), (8, 8), (8, 1)])
+@pytest.mark.parametrize("lens,new", CUTS + [([130, 260], [130, 130])])
+def test_nan_in_a_later_token_leaves_earlier_queries_alone(pa, lens, new, hq, kv):
+    """A NaN in K spoils the rows that see its token, one in V their dim of it; the rows before it have none."""
+    rng = np.random.default_rng(6)
+    pool = Pool(rng, lens, kv)
+    q = normal(rng, sum(new), hq, D)
+    qs = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    k, v = pool.k.copy(), pool.v.copy()
+    hit = []
+    for s, (n, m) in enumerate(zip(lens, new)):
+        for i in range(6):
+            t, g, d = int(rng.integers(n - m, n)), int(rng.integers(kv)), int(rng.integers(D))
+            which = "k" if i == 0 else "v"
+            (k if which == "k" else v)[pool.tables[s, t // B], g, t % B, d] = 0x7F if i % 2 else 0xFF
+            hit.append((s, t, g, d, which))
+    args = (up(k), up(v), up(pool.scale), up(pool.tables), up(pool.lens))
+    out = pa.prefill_fp8_block(bf16(q), up(qs), *args, max(new), max(lens), D ** -0.5).cpu().double().numpy()
+    clean(pa)
+    for s, (n, m) in enumerate(zip(lens, new)):
+        wrong = [h for h in hit if h[0] == s]
+        for _, t, g, d, which in wrong:                          # codes of zero for the rows that do not see them
+            (pool.k if which == "k" else pool.v)[pool.tables[s, t // B], g, t % B, d] = 0
+        ref, mag = pool.attention(s, q[qs[s]:qs[s + 1]], D ** -0.5, n - m)
+        nan = np.zeros(ref.shape, bool)
+        G = hq // kv
+        for _, t, g, d, which in wrong:
+            heads, dims = slice(g * G, (g + 1) * G), slice(None) if which == "k" else d
+            nan[max(t - (n - m), 0):, heads, dims] = True
+        got = out[qs[s]:qs[s + 1]]
+        assert np.array_equal(np.isnan(got), nan), (s, np.argwhere(np.isnan(got) != nan)[:4])
+        close(np.where(nan, 0.0, got), np.where(nan, 0.0, ref), mag, s)
