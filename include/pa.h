@@ -283,6 +283,8 @@ int pa_decode_step(const pa_dims* dims, int num_seqs, const void* q, const void*
  *   max_context_len   host bound of context_lens, 1 <= it <= max_blocks * 16
  *   scale             softmax scale, finite and > 0
  *   out               [T][Hq][D] bf16, written at the rows of valid sequences
+ * A NaN or an infinity in V of a sequence's new tokens may also reach its queries up to 63 positions
+ * before it.
  * Returns PA_OK or a PA_ERR_* code (nothing launched on error).  Launches one kernel.
  */
 int pa_prefill(const pa_dims* dims, int num_seqs, int num_tokens, const void* q,
@@ -396,8 +398,9 @@ typedef struct pa_rope_scaling {
 
 /*
  * pa_rope_table -- build cos_sin [max_pos][rotary_dim] on the GPU.  The angles per position are
- * computed on the host in 64 bits; the kernel forms p w_i modulo a whole turn in 64-bit fixed
- * point, so a far position loses nothing, and rounds cos and sin to fp32.
+ * computed on the host in 64 bits, within 2^-55 of a turn; the kernel forms p w_i modulo a whole turn
+ * in 64-bit fixed point, so that error times the position (2^-38 of a turn at 131,072) is all that a far
+ * position adds, and rounds cos and sin to fp32.
  *   max_pos     rows, >= 1
  *   cos_sin     [max_pos][rotary_dim] fp32, written
  * Returns PA_OK, PA_ERR_NULL, PA_ERR_SHAPE (rotary_dim), PA_ERR_RANGE, PA_ERR_ALIGN or
@@ -440,7 +443,7 @@ int pa_rope_kv_store_form(const pa_dims* dims, const pa_rope* rope, int num_toke
  *    power of two except for codes that become subnormal -- and where it is not, they are left.
  *    The tokens' codes are E4M3(fp32(x) * fp32(1 / scale)), coded as above (saturating, NaN kept).
  *  - A block is written by one sequence only (a shared block is copied before it is written, its
- *    scales with it).
+ *    codes and its scales, by the caller: pa_copy_blocks takes bf16 caches).
  */
 
 /*
@@ -489,7 +492,9 @@ int pa_decode_step_fp8_block(const pa_dims* dims, const pa_rope* rope, int num_s
  * pa_prefill_fp8_block -- pa_prefill over block-scaled E4M3 caches (whose new tokens
  * pa_rope_kv_store_fp8_block has stored): the queries of a chunk see every cached token, the
  * chunk's own among them, as the cache holds it.  Arguments, checks and errors as pa_prefill,
- * plus kv_scale (read only).  A query whose every block is out of range gives a zero row.  A NaN in
+ * plus kv_scale (read only).  q enters the products as the sum of two E4M3 rows after a power of two for
+ * each row: any finite magnitude does, each element within 2^-17 of its row's largest (exact from 2^-9 of
+ * it up); an infinity or a NaN makes its head's row NaN.  A query whose every block is out of range gives a zero row.  A NaN in
  * the cache reaches the queries that see its token, and no other.
  * max_context_len also says how far few queries over a long context are spread over the GPU: a bound
  * far above the contexts is right, and costs small calls some microseconds.

@@ -553,8 +553,8 @@ def _on(stream, allocate):
 
 def rope_table(max_pos, rotary_dim=128, theta=1e4, scaling="none", factor=1.0, original_max_pos=0,
                low=0.0, high=0.0, magnitude=0.0, out=None, stream=None):
-    """RoPE table cos | sin [max_pos, rotary_dim] fp32 (pa_rope_table), angles exact at any
-    position.  scaling: "none", "linear", "ntk", "yarn" (low, high: turns over original_max_pos
+    """RoPE table cos | sin [max_pos, rotary_dim] fp32 (pa_rope_table), angles within
+    position * 2^-55 of a turn.  scaling: "none", "linear", "ntk", "yarn" (low, high: turns over original_max_pos
     below / above which a pair is interpolated / kept; magnitude 0 gives 0.1 ln(factor) + 1) or
     "banded" (low, high: the same, mixed linearly in the turns)."""
     if scaling not in ROPE_SCALINGS:

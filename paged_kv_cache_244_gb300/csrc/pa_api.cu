@@ -319,7 +319,7 @@ int decode_step(const pa_dims* dims, int num_seqs, const void* q, const void* k,
                                                                                  : PA_ERR_CUDA;
 }
 
-// Host checks of the E4M3 scale arrays (after the shape and count checks their callers share).
+// Host checks of a block-scaled call's kv_scale, with the shape and the count that they depend on.
 int block_scale_ok(const pa_dims* dims, int num_seqs, const float* kv_scale) {
   if (const int rc = check_dims(dims)) return rc;
   if (num_seqs < 0) return PA_ERR_RANGE;
@@ -328,6 +328,7 @@ int block_scale_ok(const pa_dims* dims, int num_seqs, const float* kv_scale) {
   return aligned16(kv_scale) ? PA_OK : PA_ERR_ALIGN;
 }
 
+// Host checks of the E4M3 scale arrays (after the shape and count checks their callers share).
 int scales_ok(const pa_dims* dims, int num_seqs, const float* k_scale, const float* v_scale) {
   if (const int rc = check_dims(dims)) return rc;
   if (num_seqs < 0 || num_seqs > pa::kMaxDecodeSeqs) return PA_ERR_RANGE;

@@ -26,8 +26,9 @@ namespace pa {
 // Decode limits: sequences per call (their block-count prefix lives in shared memory) and
 // warps of the persistent grid (bounds the partial slots the workspace must hold).
 constexpr int kMaxDecodeSeqs = 8192;
-constexpr int kMaxFreeBlocks = 1 << 30;  // of pa_plan_step
 constexpr int kMaxDecodeWarps = 2048;
+// Entries of a step plan's free list: sums of needs, clamped to 2^31 - 1, keep their order against it.
+constexpr int kMaxFreeBlocks = 1 << 30;
 // KV heads per layer (the decode kernel packs the KV head index into 16 bits of a job word).
 constexpr int kMaxKvHeads = 4096;
 

@@ -19,8 +19,8 @@
 //
 // K codes are the B operand as they lie in the cache (kind::f8f6f4).  A bf16 q has 8 significant
 // bits and E4M3 four, so a row of q, scaled by a power of two to put its largest magnitude in
-// [128, 256), is the sum of two E4M3 rows, q = hi + lo, exact down to 2^-10 against that
-// largest (values below 2^-18 of it are lost): S = hi K + lo K, two products of twice the f16
+// [128, 256), is the sum of two E4M3 rows, q = hi + lo, exact for values of 2^-9 of that largest and
+// more, within 2^-17 of it for smaller ones: S = hi K + lo K, two products of twice the f16
 // rate, with no K tile to widen.  V codes widen exactly to f16 (P V in f16 keeps P's 11 bits).
 //
 // Warpgroups of a CTA (registers split with setmaxnreg):

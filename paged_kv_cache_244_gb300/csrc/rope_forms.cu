@@ -290,8 +290,9 @@ __global__ void __launch_bounds__(kFormWarps * 32, 4) rope_block_store_kernel(co
 
 // ---- the table -------------------------------------------------------------------------------
 // Pair i at position p turns by p * turns[i] / 2^64 of a whole turn, modulo 1: the low 64 bits of
-// the product are exact but for the 2^-65 to which turns[i] was rounded (2^-34 of a turn at
-// position 2^31).  The nearest quarter turn is taken off in the product's high word, so that what
+// the product are exact but for the error of turns[i], which the host forms as a double: within 2^-55
+// of a turn (the fastest pair's; over the five scalings, against 200-bit arithmetic), so 2^-38 of a turn at
+// position 131,072 and 2^-24 at 2^31.  The nearest quarter turn is taken off in the product's high word, so that what
 // is rounded to fp32 is an angle of at most pi/4, relative to its own size (the low word joins in
 // one FMA), and sin and cos keep their relative accuracy next to their zeros.  On that interval
 // the Taylor sums of sin to x^9 and of cos to x^10 are within 2^-29; both are formed for two pairs
