@@ -74,9 +74,9 @@ METRIC = "paged GQA decode: KV-cache HBM GB/s (% of GB300 peak) and attention to
 # the step form and a hash of the CUDA sources it was taken on: once a kernel changes, the
 # hash no longer matches and roofline.traffic is reported as null until it is captured again.
 MEASURED_TRAFFIC = {
-    ("mix64", "fused", "f2331d72aaf0f753"): 122105088 + 2981632 + 4186368,
-    ("prefix32", "fused", "f2331d72aaf0f753"): 4346112 + 0 + 3823616,
-    ("long4", "fused", "f2331d72aaf0f753"): 83979264 + 2099200 + 4824064,
+    ("mix64", "fused", "9592a9c3810c52c2"): 122099456 + 3022336 + 4186112,
+    ("prefix32", "fused", "9592a9c3810c52c2"): 4346112 + 0 + 3823872,
+    ("long4", "fused", "9592a9c3810c52c2"): 83978240 + 1852672 + 4824064,
 }
 FLUSH_BYTES = 512 << 20
 FALLBACK_HBM_GBS = 6800.0

@@ -35,11 +35,11 @@
 //   p_t: a block of tiny V scale (an attention sink) may carry most of the weight with a p_t below
 //   f16.
 //
-// What bounds it: 64 sequences of 64-4096 tokens, us replayed from a graph.  12 / 2 heads (66 MB): 18.5,
+// What bounds it: 64 sequences of 64-4096 tokens, us replayed from a graph.  12 / 2 heads (66 MB): 18.4,
 // of which some 2.5 before the first tile (lengths, table, tile: dependent cold reads), some 10 streaming at the
 // copy rate, 2.4 between the first SM done and the last, the rest launch and merge; a kernel that only
-// gathers the same tiles takes 13.7.  Fused step with 32 / 8 heads (276 MB): 50.8, 5.4 TB/s (gather 43.8).
-// One sequence of 2048 tokens: 6.1, latency (an empty kernel: 1.9).
+// gathers the same tiles takes 13.7.  Fused step with 32 / 8 heads (276 MB): 50.6, 5.5 TB/s (gather 43.8).
+// One sequence of 2048 tokens: 6.2, latency (an empty kernel: 1.9).
 //
 // Per stage: [K tile 0 | K tile 1 | V tile 0 | V tile 1 | q rows | (step) cos/sin row, k row, v row];
 // 16-byte chunk c of row r of a tile (16 x 128 codes) lies at c ^ (r % 8) of its row.
@@ -630,7 +630,9 @@ constexpr int kMergeCta = 4;        // warps of a CTA at least
 // Warps of a pair, 16, 4 or 1, by the number of pairs: the fewer there are the more pieces each has, and the
 // more warps the GPU has room for.  Contexts of 2000-2900 tokens, us of the whole call with 16 / 4 / 1:
 // 96 pairs 9.3 / 11.7 / 16.3, 192: 11.0 / 12.3 / 16.4, 384: 15.4 / 13.5 / 15.7, 768: 22.8 / 17.0 / 18.3,
-// 1200: 38.3 / 30.3 / 28.6, 2048: 74.2 / 61.2 / 58.3.
+// 1200: 38.3 / 30.3 / 28.6, 2048: 74.2 / 61.2 / 58.3.  (Even contexts: one sequence far longer than the others has
+// pieces that this does not see; 60,000 tokens among 199 sequences of 64, 8 / 1 heads: 89.6 us, 11.3 where the same
+// tokens lie in equal sequences.)
 constexpr int kWidePairs = 304, kMidPairs = 1024;
 
 template <int kGroups>

@@ -39,12 +39,13 @@
 // V codes, two 16 KiB stages of f16 V, barriers, the scales of 8 stages: 106 KiB.  Every wait is
 // bounded.
 //
-// What bounds it: the path of shared and tensor memory in an SM, 90% busy (ncu, 4 x 2048 tokens, 12 / 2
-// heads: loads and stores 53.7% of its wavefronts, the tensor core's reads of A and B 18.4% each) with
-// the tensor pipe 37% active.  A tile of 128 rows and 64 keys puts q hi and lo (32 KiB), K twice (16),
+// What bounds it: the path of shared and tensor memory in an SM, 87% busy (ncu, 4 x 2048 tokens, 12 / 2
+// heads: loads and stores 51.3% of its wavefronts, the tensor core's reads of A and B 18.1% each) with
+// the tensor pipe 36% active.  A tile of 128 rows and 64 keys puts q hi and lo (32 KiB), K twice (16),
 // f16 V (16), S out (32), P in (16), the codes of V in and f16 V out (24) and the TMA's writes (16) on
-// it.  4 x 2048 tokens: 63.1 us, 0.42 of the measured bf16 peak; 16 chunks of 256 over 1792: 61.7 us (with S_{j+2}
-// issued right behind P_j V_j, an order that nothing guarantees: 61.8-62.7 and 59.6-60.7).  A
+// it.  4 x 2048 tokens: 64.0-64.9 us, 0.41-0.42 of the measured bf16 peak; 16 chunks of 256 over 1792: 62.6-63.3 us
+// (61.8-62.7 and 59.6-60.7 with S_{j+2} issued right behind P_j V_j, an order that nothing guarantees, and V's NaN left
+// to reach earlier rows).  A
 // first form that widened K too and gave each thread its own row of q and out to load and store: 87 us.
 // Measured and left: S of two stages by one product of 128 keys (a q operand read half as often, but S
 // no longer double: 71 us); two threads a row, 16 softmax warps on an SM (65 us); one lane waiting for its
@@ -57,7 +58,7 @@
 // row's (m, L) through distributed shared memory, scale their O to the common shift, and CTA r
 // collects dims 128 r / C .. of every row from all of them, in rank order: no workspace, one launch,
 // the same sums whatever the timing.  11 sequences of one new token after 10,812 cached, 28 / 4 heads:
-// 50.3 us, 142.8 unsplit; 4 of 71 after 2342, 32 / 8 heads: 32.9.
+// 50.9 us, 142.8 unsplit; 4 of 71 after 2342, 32 / 8 heads: 32.5-33.2.
 
 #include <atomic>
 #include <mutex>
@@ -99,7 +100,7 @@ static_assert(kBpRegsSoftmax + kBpRegsIssue + kBpRegsConvert <= 3 * 80, "of the 
 // A tile's keys are split over 2, 4 or 8 CTAs as long as there are at most kSplitCtas CTAs (two per SM) and
 // at least kMinSplitStages stages for each; not below kSplitFrom stages (the exchange costs what some five
 // stages do).
-// The stages are those of the host's bound.  16 sequences of 16 tokens over 1000, 12 / 2 heads: 13.4 us, 20.3
+// The stages are those of the host's bound.  16 sequences of 16 tokens over 1000, 12 / 2 heads: 13.6 us, 20.2
 // with a bound of 131,072 (27.0 when a cluster's CTAs beyond what the sequence wants stood idle: the working
 // ones then share fewer SMs).
 constexpr int kSplitCtas = 304, kMinSplitStages = 3, kSplitFrom = 10;

@@ -38,7 +38,8 @@ constexpr int kPlanMaxCtas = 152;
 // A call of more rows than those hold takes CTAs of twice the threads; smaller ones stay at 512, whose sums are
 // shorter: 548,864 rows 6.4 us (6.9 with 512), 2 M rows 15.1 (18.2), but 262,144 rows 6.1 (4.7), 256 rows 4.2 (3.9).
 constexpr int kPlanManyThreads = 1024, kPlanManyRows = kPlanMaxCtas * kPlanRowsPerCta;
-// Sequences of a CTA where the count is not in place (an in-place count of several CTAs is a launch more):
+// Sequences of a CTA where the count is not in place (an in-place count of several CTAs is a launch more: 8192 sequences
+// of one token 17.6 us in place, 11.3 not):
 // 2048 sequences of one token 6.9 us (9.0 in one CTA), 8192: 10.0 (13.2).
 constexpr int kPlanSeqsPerCta = 512;
 

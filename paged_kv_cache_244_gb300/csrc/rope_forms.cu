@@ -152,8 +152,8 @@ __global__ void __launch_bounds__(kFormWarps * 32, kGroup == 2 ? 4 : 1) rope_for
 // KV head, K or V) units: the run's up to 16 rows are loaded at once (4 KiB a warp), K rotated,
 // the magnitudes reduced over the warp, and the codes written.  CTAs behind them rotate q.
 // Bytes bound it.  8,270 rows of 16 ragged prompts, 32 / 8 heads (191 MB): 33.4 us, 5.7 TB/s, with four CTAs of
-// 64 registers an SM and q two passes at a time (three CTAs of 80 registers, four passes: 34.5 us; q's CTAs
-// first: 39.5; loads marked as streaming: 35.0).
+// 64 registers (24 to 32 bytes spilled) an SM and q two passes at a time (three CTAs of 80 registers, four passes:
+// 34.5 us; q's CTAs first: 39.5; loads marked as streaming: 35.0).
 constexpr int kGap = 16;                       // a row that follows one of its block within kGap rows is in its run
 constexpr int kRunWindow = 64;                 // most rows of a window
 constexpr int kRunTail = kGap * kBlockSize;    // rows past the window that its last run may take
