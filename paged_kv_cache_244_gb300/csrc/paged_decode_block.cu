@@ -465,6 +465,7 @@ decode_block_kernel(const DecodeArgs a, const int pool) {
       f00 = f01 = f10 = f11 = 1.f;
       e0 = e1 = 0.f;
     }
+    __syncwarp();                                    // heads differ in it; the matrix instructions want the whole warp
     auto exponents = [&](float sh0, float sh1) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {

@@ -607,6 +607,7 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         for (int c = 0; c < kBpKeys; ++c)
           if (!there[c / kBlockSize] || c > lim) sc[c] = -INFINITY;
       }
+      __syncwarp();                                 // rows differ in `far`; the tensor-memory accesses want the whole warp
       float mrow = -INFINITY;
 #pragma unroll
       for (int b = 0; b < kBpKB; ++b) {             // 16 -> 6 -> 2 -> 1, then the block's scale
@@ -693,6 +694,7 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       // warps without a query's row, and CTAs without stages, have nothing to send
 #pragma unroll 1
       for (int q4 = nst > 0 && __any_sync(kFullMask, xi < rows_q) ? 0 : 4; q4 < 4; ++q4) {   // 32 dims of O at a time
+        __syncwarp();                               // rows without a query skipped the stores below
         uint32_t ov[32];
         if (ok) {
           tmem_ld32(trow + kBpOCol + 32 * q4, ov);
@@ -751,6 +753,7 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             if (nan_from[64 * part + d] <= last_key)
               *reinterpret_cast<uint16_t*>(qbuf + r * 128 + (((d >> 3) ^ (r & 7)) << 4) + 2 * (d & 7)) = 0x7fc0;
         }
+        __syncwarp();
         named_barrier(1, 128);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {

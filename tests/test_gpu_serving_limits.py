@@ -137,3 +137,29 @@ def test_nan_in_a_later_token_leaves_earlier_queries_alone(pa, lens, new, hq, kv
         got = out[qs[s]:qs[s + 1]]
         assert np.array_equal(np.isnan(got), nan), (s, np.argwhere(np.isnan(got) != nan)[:4])
         close(np.where(nan, 0.0, got), np.where(nan, 0.0, ref), mag, s)
+
+
+@pytest.mark.parametrize("lens,new", CUTS)
+def test_rows_of_very_different_factors_side_by_side(pa, lens, new):
+    """Heads and rows of one tile, and blocks of one stage, on both sides of where an exponent takes two steps."""
+    rng = np.random.default_rng(7)
+    pool = Pool(rng, lens, 2)
+    pool.scale[..., 0] = 2.0 ** rng.integers(-12, 25, pool.scale.shape[:2])
+    q = R.bf16_round(normal(rng, sum(new), 12, D) * 2.0 ** rng.integers(-45, 3, (sum(new), 12, 1)))
+    qs = np.concatenate([[0], np.cumsum(new)])
+    args = (*pool.dev(), up(pool.tables), up(pool.lens))
+    pre = pa.prefill_fp8_block(bf16(q), up(qs.astype(np.int32)), *args, max(new), max(lens), D ** -0.5).cpu().double().numpy()
+    dec = pa.decode_fp8_block(bf16(q[qs[1:] - 1]), *args, max(lens), D ** -0.5).cpu().double().numpy()
+    clean(pa)
+    assert np.isfinite(pre).all() and np.isfinite(dec).all()
+    checked = 0
+    for s, (n, m) in enumerate(zip(lens, new)):
+        rows = q[qs[s]:qs[s + 1]]
+        ref, mag = pool.attention(s, rows, D ** -0.5, n - m)
+        top = pool.scale[pool.tables[s][: (n + B - 1) // B], :, 0].max(axis=0).repeat(6)
+        # a score is off by 2^-17 of sum |q| 448 k at most: rows where that is below 2^-12 are compared
+        small = np.abs(rows).max(axis=2) * D * 448 * top * D ** -0.5 * 2.0 ** -17 < 2.0 ** -12
+        checked += small.sum()
+        close(np.where(small[..., None], pre[qs[s]:qs[s + 1]], 0.0), np.where(small[..., None], ref, 0.0), mag, ("prefill", s))
+        close(np.where(small[-1:, :, None], dec[s:s + 1], 0.0), np.where(small[-1:, :, None], ref[-1:], 0.0), mag[-1:], ("decode", s))
+    assert checked > 12
