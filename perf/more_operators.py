@@ -12,13 +12,13 @@ Common shapes: head_dim 128, 16-token blocks, block tables [sequences][max_block
 uint8 [num_blocks][kv_heads][2208]; a record holds one (block, KV head):
 
   0     K codes, 64 bytes a token: the 32-bit word of dims 32 g + 8 i .. + 7 is word 4 i + g of the
-        token's sixteen, dim n of its eight in bits 4 n .. 4 n + 3
+        token's sixteen
   1024  V codes, 64 bytes a token: dims 32 u .. 32 u + 31 are its 16-byte unit u ^ (token / 2 % 4),
-        dim n of the unit in bits 4 n .. 4 n + 3
+        eight dims a word, in order
   2048  K scales, four 16-bit words a token, one for each 32 dims
   2176  V scales, a 16-bit word a token
 
-A scale word is the bf16 pattern of s, whose last four bits (s has four significant bits) hold the zero
+The eight codes of a word, from its lowest bits: dims 0, 2, 4, 6, 1, 3, 5, 7 of the eight.  A scale word is the bf16 pattern of s, whose last four bits (s has four significant bits) hold the zero
 point z: element = s (code - z).
 """
 
@@ -321,9 +321,16 @@ def _quantised(x, groups):
     return c.flatten(-2), word
 
 
-def _packed(nibbles):
-    """Codes [..., 2 n] as bytes [..., n], the even one low."""
-    return nibbles[..., 0::2] | (nibbles[..., 1::2] << 4)
+def _packed(codes):
+    """Codes [..., 8 n] as the bytes [..., 4 n] of their words."""
+    c = codes.unflatten(-1, (-1, 2, 2, 2)).movedim(-1, -3)     # dim 4 a + 2 b + o is nibble 4 o + 2 a + b
+    return (c[..., 0] | (c[..., 1] << 4)).flatten(-3)
+
+
+def _nibbles(b):
+    """Bytes [..., 4 n] of words as codes [..., 8 n]."""
+    c = torch.stack((b & 15, b >> 4), dim=-1).unflatten(-2, (-1, 2, 2))
+    return c.movedim(-3, -1).flatten(-4)
 
 
 def _put(cache, k, v, blk, off):
@@ -344,18 +351,15 @@ def _elements(cache, ids):
     rec = cache[ids].transpose(1, 2)                      # [S, kv, n, record]
     shape = rec.shape[:3] + (B,)
 
-    def nibbles(b):
-        return torch.stack((b & 15, b >> 4), dim=-1).flatten(-2)
-
     def words(part, groups):
         w = rec[..., part:part + 2 * B * groups].contiguous().view(torch.int16).view(shape + (groups, 1))
         return (w & ~15).view(torch.bfloat16).float(), (w & 15).float()
 
     s, z = words(K_SCALES, 4)
-    k = nibbles(rec[..., :V_CODES].reshape(shape + (4, 4, 4))).transpose(-3, -2).flatten(-2)    # [.., group, 32]
+    k = _nibbles(rec[..., :V_CODES].reshape(shape + (4, 4, 4))).transpose(-3, -2).flatten(-2)    # [.., group, 32]
     k = ((k.float() - z) * s).flatten(-2)
     unit = torch.arange(4, device=rec.device)[None, :] ^ (torch.arange(B, device=rec.device)[:, None] // 2 % 4)
-    v = nibbles(rec[..., V_CODES:K_SCALES].reshape(shape + (4, 16)))
+    v = _nibbles(rec[..., V_CODES:K_SCALES].reshape(shape + (4, 16)))
     v = v.gather(4, unit[:, :, None].expand(shape + (4, 32)))
     s, z = words(V_SCALES, 1)
     v = ((v.flatten(-2).float() - z[..., 0]) * s[..., 0])
@@ -396,18 +400,15 @@ def _plain_read(s):
     def part(at, n):
         return s["cache"][blk[:, None, None], h, (at + off[:, None] * n + torch.arange(n, device=row.device))[:, None, :]]
 
-    def nibbles(b):
-        return torch.stack((b & 15, b >> 4), dim=-1).flatten(-2)
-
     def values(codes, words):
         w = words.contiguous().view(torch.int16)
         c = codes.unflatten(-1, (w.shape[-1], -1)).float()
         return ((c - (w & 15).float()[..., None]) * (w & ~15).view(torch.bfloat16).float()[..., None]).flatten(-2)
 
-    k = nibbles(part(0, 64)).unflatten(-1, (4, 4, 8)).transpose(-3, -2).flatten(-3)
+    k = _nibbles(part(0, 64)).unflatten(-1, (4, 4, 8)).transpose(-3, -2).flatten(-3)
     unit = torch.arange(4, device=row.device)[None, :] ^ (off[:, None] // 2 % 4)
     v = part(V_CODES, 64).unflatten(-1, (4, 16))
-    v = nibbles(v.gather(2, unit[:, None, :, None].expand(v.shape)).flatten(-2))
+    v = _nibbles(v.gather(2, unit[:, None, :, None].expand(v.shape)).flatten(-2))
     s["k_out"].copy_(values(k, part(K_SCALES, 8)))
     s["v_out"].copy_(values(v, part(V_SCALES, 2)))
     return dict(k=s["k_out"], v=s["v_out"])
@@ -506,7 +507,7 @@ def _exact_blocks(cache, ids):
     v_word = V_CODES // 4 + tok * 16 + 4 * ((dims // 32) ^ (tok // 2 % 4)) + dims % 32 // 8
     out = []
     for word, scale in ((k_word, K_SCALES // 2 + 4 * tok + dims // 32), (v_word, V_SCALES // 2 + tok + 0 * dims)):
-        code = (w[:, :, word] >> (4 * (dims % 8))) & 15
+        code = (w[:, :, word] >> (4 * (dims % 8 // 2 + 4 * (dims % 2)))) & 15
         m = half[:, :, scale]
         s = torch.ldexp(1.0 + (m >> 4 & 7).double() / 8, (m >> 7 & 255) - 127)
         out.append(((code - (m & 15)) * s).permute(1, 0, 2, 3).reshape(rec.shape[1], -1, D))
