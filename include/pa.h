@@ -507,6 +507,98 @@ int pa_prefill_fp8_block(const pa_dims* dims, int num_seqs, int num_tokens, cons
                          int max_context_len, float scale, void* out, void* stream);
 
 /*
+ * 4-bit cache -- K and V as 4-bit codes with scales of their own for every token ([NV] §学习要点: INT4
+ * quantisation; the pages fix no format, the reading below is this library's).
+ *
+ *  - cache [num_blocks][Hkv][PA_INT4_RECORD_BYTES] uint8: a record holds the 16 tokens of one (block, KV head), K and
+ *    V.  4.3 bits an element, all told.
+ *  - element = s (c - z): code c and zero point z in 0 .. 15; the scale s has four significant bits and is in [2^-40,
+ *    2^40].  An element has at most eight significant bits, so it is a bf16 value exactly.  K has (s, z) for each
+ *    token and 32 dims, since keys have channels far larger than the others; V has one for each token.
+ *  - A scale word (16 bits) is the bf16 pattern of s, whose last four bits hold z.
+ *  - Quantising values x (bf16): lo = min(0, x), hi = max(0, x) over the finite ones; s is the smallest there is with
+ *    15 s >= fp32(hi - lo); z = min(15, round(-lo / s)); c = round(x / s) + z, clamped to 0 .. 15; ties away from zero.
+ *    So a finite x is off by s/2 at most, infinities become the ends of the range, and a NaN makes s NaN: every element of
+ *    its 32 dims of K, or of its token of V, reads as NaN.
+ *  - Record, by byte offset: 0 K codes, 64 bytes a token (dims 32 g + 8 i .. + 7 are 32-bit word 4 i + g of the 16); 1024 V
+ *    codes, 64 bytes a token (dims 32 u .. + 31 are 16-byte unit u ^ (token / 2 % 4), eight dims a word in order); 2048 K
+ *    scale words, four a token; 2176 V scale words, one a token.  The codes of a word's eight dims, from its lowest
+ *    bits: dims 0, 2, 4, 6, 1, 3, 5, 7.
+ *  - A row is quantised by itself: a store writes the bytes of its slots and no others, and depends on nothing that
+ *    the block held before.  A block (Hkv records) is copied as bytes, by the caller: pa_copy_blocks takes bf16
+ *    caches.
+ */
+#define PA_INT4_RECORD_BYTES 2208
+
+/*
+ * pa_rope_kv_store_int4 -- pa_rope_kv_store_form into the 4-bit cache: the rotated k as bf16, and v, quantised into
+ * the record at slot_mapping[t].  Everything else as pa_rope_kv_store_form.
+ *   cache   [num_blocks][Hkv][PA_INT4_RECORD_BYTES], written at the slots only
+ * Launches one kernel.
+ */
+int pa_rope_kv_store_int4(const pa_dims* dims, const pa_rope* rope, int num_tokens, const void* q,
+                          void* q_out, const void* k, const void* v, const int32_t* positions,
+                          const float* cos_sin, int max_pos, const int64_t* slot_mapping, void* cache,
+                          int num_blocks, void* stream);
+
+/*
+ * pa_read_kv_int4 -- cached tokens of sequences read back as bf16 rows, exactly as the attention calls see them: for
+ * another form of attention, a cache of another type, or a check.
+ * Sequence s has n_s = row_start[s+1] - row_start[s] rows; row row_start[s] + i of k_out and v_out is its token
+ * first[s] + i, reached through block_tables as in pa_decode.  No other row is written.
+ * Device-side errors: row_start[s] < 0, n_s < 0 or > max_rows, row_start[s+1] > num_rows, first[s] < 0 or first[s] + n_s
+ * > max_blocks * 16 -> the sequence is skipped, PA_FLAG_CONTEXT_LEN_OOB; a block id outside [0, num_blocks) -> the block's
+ * rows are left as they were, PA_FLAG_BLOCK_ID_OOB.
+ *   num_seqs      0 <= S <= 65535 (0 is a no-op)
+ *   num_rows      rows of k_out and v_out (0 is a no-op)
+ *   row_start     [S + 1] int32, device
+ *   first         [S] int32, device; NULL means 0 for every sequence
+ *   max_rows      host bound of every n_s, 1 <= it <= max_blocks * 16
+ *   block_tables  [S][max_blocks] int32, max_blocks * 16 <= 2^31 - 16
+ *   k_out, v_out  [num_rows][Hkv][128] bf16, written
+ * Returns PA_OK or a PA_ERR_* code (nothing launched on error).  Launches one kernel.
+ */
+int pa_read_kv_int4(const pa_dims* dims, int num_seqs, int num_rows, const int32_t* row_start,
+                    const int32_t* first, int max_rows, const void* cache, int num_blocks,
+                    const int32_t* block_tables, int max_blocks, void* k_out, void* v_out, void* stream);
+
+/*
+ * pa_decode_int4 -- pa_decode over the 4-bit cache.  Arguments, workspace (same size:
+ * pa_decode_workspace_size), checks and errors as pa_decode.  q enters the products in f16 after a power of two for each
+ * head, so any finite magnitude does; an infinity or a NaN in it makes its head's row NaN, and a NaN in the cache the rows of
+ * the sequences that see its token.  A sequence whose every block is out of range gives zeros.  Launches one
+ * kernel plus the merge.
+ */
+int pa_decode_int4(const pa_dims* dims, int num_seqs, const void* q, const void* cache, int num_blocks,
+                   const int32_t* block_tables, int max_blocks, const int32_t* context_lens,
+                   int max_context_len, float scale, int partition_tokens, void* workspace,
+                   size_t workspace_bytes, void* out, void* stream);
+
+/*
+ * pa_decode_step_int4 -- pa_decode_step over the 4-bit cache with a RoPE form: equals pa_rope_kv_store_int4 (position
+ * context_lens[s] - 1, that position's slot; cache and out bit for bit) followed by pa_decode_int4, with q left
+ * unchanged.  A position without a cos/sin row: as pa_decode_step.  Arguments as pa_decode_step plus rope (as
+ * pa_rope_kv_store_form).
+ */
+int pa_decode_step_int4(const pa_dims* dims, const pa_rope* rope, int num_seqs, const void* q,
+                        const void* k, const void* v, const float* cos_sin, int max_pos, void* cache,
+                        int num_blocks, const int32_t* block_tables, int max_blocks,
+                        const int32_t* context_lens, int max_context_len, float scale,
+                        int partition_tokens, void* workspace, size_t workspace_bytes, void* out,
+                        unsigned flags, void* stream);
+
+/*
+ * pa_prefill_int4 -- pa_prefill over the 4-bit cache (whose new tokens pa_rope_kv_store_int4 has stored): the
+ * queries of a chunk see every cached token, the chunk's own among them, as the cache holds it.  Arguments, checks and
+ * errors as pa_prefill; q, NaN, rows without a block and loose bounds as pa_prefill_fp8_block, but q is exact.  Launches
+ * one kernel.
+ */
+int pa_prefill_int4(const pa_dims* dims, int num_seqs, int num_tokens, const void* q,
+                    const int32_t* q_start, int max_query_len, const void* cache, int num_blocks,
+                    const int32_t* block_tables, int max_blocks, const int32_t* context_lens,
+                    int max_context_len, float scale, void* out, void* stream);
+
+/*
  * pa_plan_step -- the metadata of one serving step built on the GPU from request lengths ([ME]
  * §3.1: the block table of a sequence, grown by blocks taken from the free list; §3.2
  * append_slot, for any number of new tokens; §3.3: the rows of a chunk): what pa_rope_kv_store*,
@@ -626,8 +718,8 @@ int pa_stage_copy(void* dst, const void* src, size_t bytes, void* stream);
 
 /*
  * pa_set_timing_jitter -- test hook for the pipelined kernels' barriers: from the next launch
- * on, every role of the pa_prefill and pa_prefill_fp8_block kernels (softmax warps, TMA warps, MMA
- * warp, converters) sleeps a
+ * on, every role of the pa_prefill, pa_prefill_fp8_block and pa_prefill_int4 kernels (softmax warps, TMA
+ * warps, MMA warp, converters) sleeps a
  * pseudo-random time below max_ns (the same for the whole warp, a function of seed, the CTA,
  * the role and the step) at each step of its pipeline loop, so that tests can drive the
  * barriers through orders of arrival that undisturbed runs rarely take.  Results must not

@@ -503,9 +503,15 @@ def _declare_serving(L):
                                            sz, p, ctypes.c_uint, p]
     L.pa_prefill_fp8_block.argtypes = [pd, i, i, p, p, i, p, p, p, i, p, i, p, i, f, p, p]
     L.pa_plan_step.argtypes = [pd, i, p, p, p, i, p, i, p, p, i, i, p, p, p, p, p, p]
+    L.pa_rope_kv_store_int4.argtypes = [pd, pr, i, p, p, p, p, p, p, i, p, p, i, p]
+    L.pa_read_kv_int4.argtypes = [pd, i, i, p, p, i, p, i, p, i, p, p, p]
+    L.pa_decode_int4.argtypes = [pd, i, p, p, i, p, i, p, i, f, i, p, sz, p, p]
+    L.pa_decode_step_int4.argtypes = [pd, pr, i, p, p, p, p, i, p, i, p, i, p, i, f, i, p, sz, p, ctypes.c_uint, p]
+    L.pa_prefill_int4.argtypes = [pd, i, i, p, p, i, p, i, p, i, p, i, f, p, p]
     for name in ("pa_rope_table", "pa_rope_kv_store_form", "pa_rope_kv_store_fp8_block",
                  "pa_decode_fp8_block", "pa_decode_step_fp8_block", "pa_prefill_fp8_block",
-                 "pa_plan_step"):
+                 "pa_plan_step", "pa_rope_kv_store_int4", "pa_read_kv_int4", "pa_decode_int4",
+                 "pa_decode_step_int4", "pa_prefill_int4"):
         getattr(L, name).restype = i
 
 
@@ -670,3 +676,91 @@ def plan_step(cached_lens, new_lens, block_tables, free_blocks, num_free, num_bl
     _check(_native().plan_step(cached_lens, new_lens, block_tables, free_blocks, num_free, num_free_out, num_blocks,
                                num_tokens, *plan, _handle(stream)), "pa_plan_step")
     return plan
+
+
+# ---- 4-bit caches: one uint8 tensor of records, [num_blocks, Hkv, INT4_RECORD_BYTES] -----
+
+INT4_RECORD_BYTES = 2208   # PA_INT4_RECORD_BYTES: 16 tokens of K and V of one KV head, codes and scales
+
+
+def int4_cache(num_blocks, num_kv_heads, device="cuda") -> torch.Tensor:
+    """An empty 4-bit cache: 16-token blocks, head_dim 128 (no initialisation is needed before tokens are stored)."""
+    return torch.zeros((num_blocks, num_kv_heads, INT4_RECORD_BYTES), dtype=torch.uint8, device=device)
+
+
+def decode_workspace_int4(q, cache, max_context_len, partition_tokens=0) -> torch.Tensor:
+    """Allocate the workspace of decode_int4 and decode_step_int4 for these shapes (no initialisation needed)."""
+    n = decode_workspace_size(q.shape[1], cache.shape[1], q.shape[0], max_context_len, partition_tokens)
+    if n == 0:
+        raise PaError(PA_ERR_RANGE, "pa_decode_workspace_size")
+    return torch.empty((n + 3) // 4, dtype=torch.float32, device=q.device)
+
+
+def rope_kv_store_int4(q, k, v, positions, cos_sin, slot_mapping, cache, layout="half", q_out=None, stream=None):
+    """rope_kv_store_form into a 4-bit cache (pa_rope_kv_store_int4): rotates, quantises and stores; returns the
+    rotated q (q_out, or q itself when that is None).  cache as int4_cache gives it, updated."""
+    q_out = q if q_out is None else q_out
+    _check(_native().rope_kv_store_int4(q, k, v, positions, cos_sin, slot_mapping, cache, _layout(layout), q_out,
+                                        _handle(stream)), "pa_rope_kv_store_int4")
+    return q_out
+
+
+def read_kv_int4(cache, row_start, first, block_tables, max_rows, num_rows=None, k_out=None, v_out=None, stream=None):
+    """Cached tokens back as bf16 rows (pa_read_kv_int4): rows row_start[s] .. row_start[s + 1] - 1 of the results are
+    tokens first[s] .. of sequence s (None: from its start).  Returns k, v [rows, Hkv, 128].
+
+    row_start [S + 1], first [S], block_tables [S, max_blocks] int32; max_rows a host int bounding a sequence's rows.
+    Without k_out and v_out, num_rows (a host int) says how many rows there are.
+    """
+    if k_out is None or v_out is None:
+        if num_rows is None:
+            raise ValueError("num_rows is needed where k_out and v_out are not given")
+        make = lambda: torch.empty((num_rows, cache.shape[1], 128), dtype=torch.bfloat16, device=cache.device)  # noqa: E731
+        k_out = _on(stream, make) if k_out is None else k_out
+        v_out = _on(stream, make) if v_out is None else v_out
+    _check(_native().read_kv_int4(cache, row_start, first, block_tables, max_rows, k_out, v_out, _handle(stream)),
+           "pa_read_kv_int4")
+    return k_out, v_out
+
+
+def decode_int4(q, cache, block_tables, context_lens, max_context_len, scale, partition_tokens=0, workspace=None,
+                out=None, stream=None):
+    """Decode attention over a 4-bit cache (pa_decode_int4).  Returns out [S, Hq, 128] bf16; workspace from
+    decode_workspace_int4, allocated here when None."""
+    if out is None:
+        out = _on(stream, lambda: torch.empty_like(q))
+    if q.shape[0] == 0:
+        return out
+    if workspace is None:
+        workspace = _on(stream, lambda: decode_workspace_int4(q, cache, max_context_len, partition_tokens))
+    _check(_native().decode_int4(q, cache, block_tables, context_lens, max_context_len, scale, partition_tokens, workspace,
+                                 out, _handle(stream)), "pa_decode_int4")
+    return out
+
+
+def decode_step_int4(q, k, v, cos_sin, cache, block_tables, context_lens, max_context_len, scale, layout="half",
+                     partition_tokens=0, workspace=None, out=None, stream=None, early_metadata=False):
+    """The fused decode step over a 4-bit cache with a RoPE form (pa_decode_step_int4; q left unchanged);
+    early_metadata as for decode_step."""
+    if out is None:
+        out = _on(stream, lambda: torch.empty_like(q))
+    if q.shape[0] == 0:
+        return out
+    if workspace is None:
+        workspace = _on(stream, lambda: decode_workspace_int4(q, cache, max_context_len, partition_tokens))
+    _check(_native().decode_step_int4(q, k, v, cos_sin, cache, block_tables, context_lens, max_context_len, scale,
+                                      _layout(layout), partition_tokens, workspace, out,
+                                      PA_STEP_EARLY_METADATA if early_metadata else 0, _handle(stream)),
+           "pa_decode_step_int4")
+    return out
+
+
+def prefill_int4(q, q_start, cache, block_tables, context_lens, max_query_len, max_context_len, scale, out=None,
+                 stream=None):
+    """Paged (chunked) prefill attention over a 4-bit cache (pa_prefill_int4).  Returns out [T, Hq, 128] bf16;
+    arguments as for prefill()."""
+    if out is None:
+        out = _on(stream, lambda: torch.empty_like(q))
+    _check(_native().prefill_int4(q, q_start, cache, block_tables, context_lens, max_query_len, max_context_len, scale,
+                                  out, _handle(stream)), "pa_prefill_int4")
+    return out

@@ -1,0 +1,157 @@
+// The 4-bit cache's record, its quantisation and its reading, shared by the kernels that touch it.
+//
+// A record holds the 16 tokens of one (block, KV head), K and V, in one run of memory: the attention
+// kernels bring it in whole.  element = s (c - z) with a code c and a zero point z in 0 .. 15.  The
+// scale s has four significant bits, so that an element has at most eight and is exact in bf16, and a
+// scale word holds both numbers: the bf16 pattern of s, whose last four bits are free for z.
+//
+//   0     K codes: word 4 i + g of a token's sixteen 32-bit words has dims 32 g + 8 i .. + 7, so that the
+//         16 bytes i of a token are the share of one of four lanes in each of the four groups
+//   1024  V codes: dims 32 u .. + 31 at 16-byte unit u ^ (token / 2 % 4), the order in which eight tokens'
+//         units lie on distinct banks
+//   2048  K scales: a word for each 32 dims of a token
+//   2176  V scales: a word a token
+//
+// In a word, code pair j (bits 4j .. 4j + 3 of both halves) is dims 2j and 2j + 1 of its eight, so that one mask gives a
+// pair of 16-bit integers: with 0x4300 in each half the bf16 pair 128 + c, shifted a pair of small f16 values.
+#pragma once
+
+#include "pa_device.cuh"
+
+namespace pa {
+
+constexpr int kInt4Record = PA_INT4_RECORD_BYTES;
+constexpr int kInt4VCodes = 1024, kInt4KScales = 2048, kInt4VScales = 2176;
+static_assert(kInt4VScales + 2 * kBlockSize == kInt4Record && kInt4Record % 32 == 0, "record");
+
+constexpr uint32_t kPairLo = 0x000f000fu;
+
+// Byte offsets in a record: the word of dims 8 ch .. 8 ch + 7 of token t.
+__device__ __forceinline__ int int4_k_word(int t, int ch) { return 64 * t + 16 * (ch & 3) + 4 * (ch >> 2); }
+__device__ __forceinline__ int int4_v_word(int t, int ch) {
+  return kInt4VCodes + 64 * t + 16 * ((ch >> 2) ^ ((t >> 1) & 3)) + 4 * (ch & 3);
+}
+
+// ---- quantisation --------------------------------------------------------------------------
+// Of a set of values: the largest, and the largest of the negated ones, as bf16 magnitudes in the
+// halves of a word (at least 0; infinities do not count; 0x7fc0 in both where there is a NaN).
+// Sets join by __vmaxu2.
+__device__ __forceinline__ uint32_t int4_extremes(uint4 w) {
+  uint32_t nan = 0;
+  const uint32_t top = __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
+  if (__vcmpgeu2(top, 0x7f807f80u)) {
+    nan = __vcmpgtu2(top, 0x7f807f80u) ? 0x7fc07fc0u : 0u;
+    w.x &= __vcmpltu2(w.x & 0x7fff7fffu, 0x7f807f80u);
+    w.y &= __vcmpltu2(w.y & 0x7fff7fffu, 0x7f807f80u);
+    w.z &= __vcmpltu2(w.z & 0x7fff7fffu, 0x7f807f80u);
+    w.w &= __vcmpltu2(w.w & 0x7fff7fffu, 0x7f807f80u);
+  }
+  // as signed 16-bit integers positive values order as they are and stand above all negative ones, which
+  // order the other way round: unsigned maxima find the smallest value, if one is negative
+  const uint32_t hi = __vmaxs2(__vmaxs2(w.x, w.y), __vmaxs2(w.z, w.w));
+  const uint32_t lo = __vmaxu2(__vmaxu2(w.x, w.y), __vmaxu2(w.z, w.w));
+  const uint32_t high = __vmaxs2(__byte_perm(hi, hi, 0x1032), hi), low = __vmaxu2(__byte_perm(lo, lo, 0x1032), lo);
+  const uint32_t p = (high & 0x8000u) ? 0u : high & 0x7fffu, n = (low & 0x8000u) ? low & 0x7fffu : 0u;
+  return __vmaxu2(p | (n << 16), nan);
+}
+
+struct Int4Scale {
+  float inv;       // 1 / s, 2^-20 of it larger
+  float origin;    // 2^23 + 2^22 + z
+  uint32_t word;
+};
+
+// The smallest s of four significant bits with 15 s >= hi - lo (rounded to fp32), in [2^-40, 2^40], and
+// z = -lo / s rounded, for extremes as above.  Quotients round to the nearest integer, ties away from
+// zero: a bf16 value over such an s is a tie or 2^-9 of itself away from one, so 1 / s made 2^-20 larger
+// settles ties and moves nothing else.
+__device__ __forceinline__ Int4Scale int4_scale(uint32_t extremes) {
+  const float hi = __uint_as_float(extremes << 16), neg = __uint_as_float(extremes & 0xffff0000u);
+  const float range = hi + neg;
+  uint32_t s = (__float_as_uint(range * (1.f / 15.f)) + 0x000fffffu) & 0xfff00000u;
+  if (15.f * __uint_as_float(s - 0x00100000u) >= range) s -= 0x00100000u;
+  else if (15.f * __uint_as_float(s) < range) s += 0x00100000u;
+  const float scale = fminf(fmaxf(__uint_as_float(s), 0x1p-40f), 0x1p40f);
+  Int4Scale q;
+  q.inv = rcp_ftz(scale) * (1.f + 0x1p-20f);
+  q.origin = fmaf(fminf(neg * q.inv, 15.f), 1.f, 12582912.f);
+  q.word = (__float_as_uint(scale) >> 16) | (__float_as_uint(q.origin) & 15u);
+  if ((extremes & 0xffffu) == 0x7fc0u) q.word = 0x7fc0u;
+  return q;
+}
+
+// The code of x (in the low four bits of the result, whose others are those of 2^23 + 2^22): the sum
+// rounds the quotient to an integer.
+__device__ __forceinline__ uint32_t int4_code(float x, const Int4Scale& q) {
+  return __float_as_uint(fminf(fmaxf(fmaf(x, q.inv, q.origin), 12582912.f), 12582927.f));
+}
+
+// Codes of eight neighbouring dims (four bf16 pairs) as a word.
+__device__ __forceinline__ uint32_t int4_word(uint4 w, const Int4Scale& q) {
+  // each shift by four moves the upper bits of 12582912 along; what they add up to is taken off
+  constexpr uint32_t kBase = 0x4b400000u;
+  constexpr uint32_t kSum = kBase * 0x11111111u;
+  uint32_t r = int4_code(bf16hi(w.w), q);
+  r = r * 16 + int4_code(bf16hi(w.z), q);
+  r = r * 16 + int4_code(bf16hi(w.y), q);
+  r = r * 16 + int4_code(bf16hi(w.x), q);
+  r = r * 16 + int4_code(bf16lo(w.w), q);
+  r = r * 16 + int4_code(bf16lo(w.z), q);
+  r = r * 16 + int4_code(bf16lo(w.y), q);
+  r = r * 16 + int4_code(bf16lo(w.x), q);
+  return r - kSum;
+}
+
+// ---- reading -------------------------------------------------------------------------------
+__device__ __forceinline__ float int4_scale_of(uint32_t word) { return __uint_as_float((word & 0xfff0u) << 16); }
+
+__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// A scale word as the bf16 pairs (s, s) and (128 + z, 128 + z).
+__device__ __forceinline__ void int4_unpack_scale(uint32_t word, uint32_t& s2, uint32_t& z2) {
+  const uint32_t w = __byte_perm(word, word, 0x1010);
+  s2 = w & 0xfff0fff0u;
+  z2 = (w & kPairLo) | 0x43004300u;
+}
+// The eight elements of a word as bf16, exact: (128 + c) - (128 + z) is an integer of at most 15, its product with s
+// has eight significant bits.
+__device__ __forceinline__ uint4 int4_elements(uint32_t w, uint32_t s2, uint32_t z2) {
+  uint4 r;
+  r.x = mul_bf16x2(sub_bf16x2((w & kPairLo) | 0x43004300u, z2), s2);
+  r.y = mul_bf16x2(sub_bf16x2(((w >> 4) & kPairLo) | 0x43004300u, z2), s2);
+  r.z = mul_bf16x2(sub_bf16x2(((w >> 8) & kPairLo) | 0x43004300u, z2), s2);
+  r.w = mul_bf16x2(sub_bf16x2(((w >> 12) & kPairLo) | 0x43004300u, z2), s2);
+  return r;
+}
+
+// ---- rotation ------------------------------------------------------------------------------
+// x c - y s rounded to fp32 and to bf16, for a bf16 pair and fp32 cos and sin: diff_of_products is
+// within two ulps, so only a value within four of a border of the bf16 rounding is formed again in 64
+// bits, where the products are exact.  A code then never depends on how the products were formed.
+__device__ __forceinline__ float turned(float a, float b, float c, float d) {
+  float r = diff_of_products(a, b, c, d);
+  if (((__float_as_uint(r) + 0x8004u) & 0xffffu) <= 8u)
+    r = __double2float_rn(static_cast<double>(a) * b - static_cast<double>(c) * d);
+  return r;
+}
+__device__ __forceinline__ void int4_rotate_pairs(uint32_t& lo, uint32_t& hi, float2 c, float2 s) {
+  const float x0 = bf16lo(lo), x1 = bf16hi(lo), y0 = bf16lo(hi), y1 = bf16hi(hi);
+  lo = pack_bf16x2(turned(x0, c.x, y0, s.x), turned(x1, c.y, y1, s.y));
+  hi = pack_bf16x2(turned(y0, c.x, -x0, s.x), turned(y1, c.y, -x1, s.y));
+}
+__device__ __forceinline__ void int4_rotate_interleaved(uint32_t& w0, uint32_t& w1, float2 c, float2 s) {
+  uint32_t lo = __byte_perm(w0, w1, 0x5410), hi = __byte_perm(w0, w1, 0x7632);
+  int4_rotate_pairs(lo, hi, c, s);
+  w0 = __byte_perm(lo, hi, 0x5410);
+  w1 = __byte_perm(lo, hi, 0x7632);
+}
+
+}  // namespace pa

@@ -1,0 +1,230 @@
+// The fused RoPE + quantising store into the 4-bit cache, and reading cached rows back, for sm_103a.
+//
+// "Pico-vLLM：从零手写的工业级LLM推理引擎实现", §1 模型实现层 (RoPE) and §2 Kernel层 (RoPE fused with
+// the KV cache store); "从零实现 LLM 推理引擎：深挖 vLLM 的六大核心优化", §3.1 (16-token blocks);
+// "nano-vllm：vLLM 极简实现与大模型推理流程解析", §学习要点 (4-bit quantisation).
+//
+// A token's scales are its own, so a row is quantised by the lanes that hold it and touches nothing of
+// its block's other tokens: the store is the bf16 store of a RoPE form (eight lanes a head vector, four
+// vectors a pass) with a few bytes out in the place of a row.
+
+#include "int4_cache.cuh"
+#include "int4_launch.h"
+#include "rope_form.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kStoreWarps = 8;
+
+template <bool kInterleaved>
+__device__ __forceinline__ void int4_rotate_chunks(uint4& x, uint4& y, const Angles& a) {
+  const float2 c0 = make_float2(a.c0.x, a.c0.y), c1 = make_float2(a.c0.z, a.c0.w);
+  const float2 c2 = make_float2(a.c1.x, a.c1.y), c3 = make_float2(a.c1.z, a.c1.w);
+  const float2 s0 = make_float2(a.s0.x, a.s0.y), s1 = make_float2(a.s0.z, a.s0.w);
+  const float2 s2 = make_float2(a.s1.x, a.s1.y), s3 = make_float2(a.s1.z, a.s1.w);
+  if constexpr (kInterleaved) {
+    int4_rotate_interleaved(x.x, x.y, c0, s0);
+    int4_rotate_interleaved(x.z, x.w, c1, s1);
+    int4_rotate_interleaved(y.x, y.y, c2, s2);
+    int4_rotate_interleaved(y.z, y.w, c3, s3);
+  } else {
+    int4_rotate_pairs(x.x, y.x, c0, s0);
+    int4_rotate_pairs(x.y, y.y, c1, s1);
+    int4_rotate_pairs(x.z, y.z, c2, s2);
+    int4_rotate_pairs(x.w, y.w, c3, s3);
+  }
+}
+
+// One warp, one token: its groups of 4 kGroup head vectors part, part + parts, ..: queries rotated into
+// q_out, keys (rotated) and values quantised into the token's slot.
+template <bool kInterleaved, int kGroup>
+__global__ void __launch_bounds__(kStoreWarps * 32) rope_int4_store_kernel(const RopeFormArgs a) {
+  __shared__ uint4 s_extremes[kStoreWarps][4][4];   // of a pass's vectors, a word for each 8 dims
+  pdl_wait_prior_grid();
+  pdl_allow_next_grid();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int t = blockIdx.x * kStoreWarps + warp;
+  if (t >= a.num_tokens) return;
+  const int j = lane & 7, sub = lane >> 3;
+  const int R = a.rotary_dim;
+  const int Hq = a.num_q_heads, Hkv = a.num_kv_heads;
+  const int all = Hq + 2 * Hkv;
+  int ca, cb;
+  lane_chunks<kInterleaved>(j, R, ca, cb);
+  uint4 x[kGroup], y[kGroup];
+  auto load_group = [&](int base) {
+#pragma unroll
+    for (int p = 0; p < kGroup; ++p) {
+      const int i = base + 4 * p + sub;
+      x[p] = y[p] = make_uint4(0u, 0u, 0u, 0u);
+      if (i >= all) continue;
+      const __nv_bfloat16* src;
+      if (i < Hq) src = a.q + (static_cast<size_t>(t) * Hq + i) * kHeadDim;
+      else if (i < Hq + Hkv) src = a.k + (static_cast<size_t>(t) * Hkv + (i - Hq)) * kHeadDim;
+      else src = a.v + (static_cast<size_t>(t) * Hkv + (i - Hq - Hkv)) * kHeadDim;
+      x[p] = reinterpret_cast<const uint4*>(src)[ca];
+      y[p] = reinterpret_cast<const uint4*>(src)[cb];
+    }
+  };
+  const int pos = a.positions[t];
+  const int64_t slot = a.slot_mapping[t];
+  const int first = 4 * kGroup * static_cast<int>(blockIdx.y), step = 4 * kGroup * static_cast<int>(gridDim.y);
+  load_group(first);
+  const bool has_pos = pos >= 0 && pos < a.max_pos;
+  if (!has_pos && lane == 0) raise_flag(a.status, PA_FLAG_POSITION_OOB);
+  bool store = has_pos && slot >= 0;
+  if (store && slot >= static_cast<int64_t>(a.num_blocks) * kBlockSize) {
+    if (lane == 0) raise_flag(a.status, PA_FLAG_SLOT_OOB);
+    store = false;
+  }
+  if (!has_pos && a.q == a.q_out) return;  // left as it is
+  const int64_t blk = store ? slot / kBlockSize : 0;
+  const int off = store ? static_cast<int>(slot - blk * kBlockSize) : 0;
+  uint8_t* const records = static_cast<uint8_t*>(a.k_cache) + static_cast<size_t>(blk) * Hkv * kInt4Record;
+  const bool turns = has_pos && j < (R >> 4);
+  Angles ang = {};
+  if (turns) ang = load_angles(a.cos_sin, pos, R, j);
+  const int items = store ? all : Hq;
+  for (int base = first; base < items; base += step) {
+    if (base != first) load_group(base);
+#pragma unroll
+    for (int p = 0; p < kGroup; ++p) {
+      if (base + 4 * p >= items) break;
+      const int i = base + 4 * p + sub;
+      if (i < Hq) {
+        if (turns) rotate_chunks<kInterleaved>(x[p], y[p], ang);
+        uint4* dst = reinterpret_cast<uint4*>(a.q_out + (static_cast<size_t>(t) * Hq + i) * kHeadDim);
+        dst[ca] = x[p];
+        dst[cb] = y[p];
+      }
+      if (base + 4 * p + 3 < Hq) continue;          // the same for the whole warp
+      if (items == Hq) continue;
+      // keys and values (lanes of a query, or past the last vector, go along)
+      const bool is_k = i < Hq + Hkv, mine = i >= Hq && i < all;
+      if (turns && mine && is_k) int4_rotate_chunks<kInterleaved>(x[p], y[p], ang);
+      __syncwarp();
+      uint32_t ex = int4_extremes(x[p]), ey = int4_extremes(y[p]);
+      uint32_t* const words = reinterpret_cast<uint32_t*>(s_extremes[warp][sub]);
+      words[ca] = ex;
+      words[cb] = ey;
+      __syncwarp();
+      if (is_k) {
+        const uint4 ga = s_extremes[warp][sub][ca >> 2], gb = s_extremes[warp][sub][cb >> 2];
+        ex = __vmaxu2(__vmaxu2(ga.x, ga.y), __vmaxu2(ga.z, ga.w));
+        ey = __vmaxu2(__vmaxu2(gb.x, gb.y), __vmaxu2(gb.z, gb.w));
+      }
+      __syncwarp();                                 // before the next pass writes the words
+      ex = is_k ? ex : __vmaxu2(ex, ey);
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) {
+        const uint32_t other = __shfl_xor_sync(kFullMask, ex, o);
+        if (!is_k) ex = __vmaxu2(ex, other);
+      }
+      if (!mine) continue;
+      const Int4Scale qa = int4_scale(ex);
+      const Int4Scale qb = is_k ? int4_scale(ey) : qa;
+      uint8_t* const rec = records + static_cast<size_t>(is_k ? i - Hq : i - Hq - Hkv) * kInt4Record;
+      const uint32_t wa = int4_word(x[p], qa), wb = int4_word(y[p], qb);
+      if (is_k) {
+        *reinterpret_cast<uint32_t*>(rec + int4_k_word(off, ca)) = wa;
+        *reinterpret_cast<uint32_t*>(rec + int4_k_word(off, cb)) = wb;
+        uint16_t* const scales = reinterpret_cast<uint16_t*>(rec + kInt4KScales + 8 * off);
+        if ((ca & 3) == 0) scales[ca >> 2] = static_cast<uint16_t>(qa.word);
+        if ((cb & 3) == 0) scales[cb >> 2] = static_cast<uint16_t>(qb.word);
+      } else {
+        *reinterpret_cast<uint32_t*>(rec + int4_v_word(off, ca)) = wa;
+        *reinterpret_cast<uint32_t*>(rec + int4_v_word(off, cb)) = wb;
+        if (j == 0) *reinterpret_cast<uint16_t*>(rec + kInt4VScales + 2 * off) = static_cast<uint16_t>(qa.word);
+      }
+    }
+  }
+}
+
+// ---- reading back ------------------------------------------------------------------------------
+// A warp takes one record: half a warp a token, a lane the word of 8 dims, K and V of the 16 tokens with
+// all loads ahead of the stores.  Each store instruction writes two rows of 256 bytes.
+constexpr int kReadWarps = 8;
+
+__global__ void __launch_bounds__(kReadWarps * 32) read_int4_kernel(const ReadInt4Args a) {
+  pdl_wait_prior_grid();
+  pdl_allow_next_grid();
+  const int lane = threadIdx.x & 31;
+  const int Hkv = a.num_kv_heads;
+  const int s = blockIdx.y;
+  const int r0 = a.row_start[s], n = a.row_start[s + 1] - r0;
+  const int first = a.first ? a.first[s] : 0;
+  if (r0 < 0 || n < 0 || n > a.max_rows || r0 > a.num_rows - n || first < 0 ||
+      first > a.max_blocks * kBlockSize - n) {
+    if (threadIdx.x == 0 && blockIdx.x == 0) raise_flag(a.status, PA_FLAG_CONTEXT_LEN_OOB);
+    return;
+  }
+  if (n == 0) return;
+  const int b0 = first / kBlockSize, nb = (first + n - 1) / kBlockSize - b0 + 1;
+  const long long unit = static_cast<long long>(blockIdx.x) * kReadWarps + (threadIdx.x >> 5);
+  if (unit >= static_cast<long long>(nb) * Hkv) return;
+  const int b = static_cast<int>(unit / Hkv), g = static_cast<int>(unit - static_cast<long long>(b) * Hkv);
+  const int blk = a.block_tables[static_cast<size_t>(s) * a.max_blocks + b0 + b];
+  if (blk < 0 || blk >= a.num_blocks) {
+    if (lane == 0) raise_flag(a.status, PA_FLAG_BLOCK_ID_OOB);
+    return;
+  }
+  const uint8_t* const rec = a.cache + (static_cast<size_t>(blk) * Hkv + g) * kInt4Record;
+  const int ch = lane & 15, odd = lane >> 4;
+  uint32_t kw[8], vw[8], ks[8], vs[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int t = 2 * i + odd;
+    kw[i] = *reinterpret_cast<const uint32_t*>(rec + int4_k_word(t, ch));
+    vw[i] = *reinterpret_cast<const uint32_t*>(rec + int4_v_word(t, ch));
+    ks[i] = *reinterpret_cast<const uint16_t*>(rec + kInt4KScales + 8 * t + 2 * (ch >> 2));
+    vs[i] = *reinterpret_cast<const uint16_t*>(rec + kInt4VScales + 2 * t);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int row = kBlockSize * (b0 + b) + 2 * i + odd - first;
+    if (row < 0 || row >= n) continue;
+    const size_t at = ((static_cast<size_t>(r0) + row) * Hkv + g) * (kHeadDim / 8) + ch;
+    uint32_t s2, z2;
+    int4_unpack_scale(ks[i], s2, z2);
+    reinterpret_cast<uint4*>(a.k_out)[at] = int4_elements(kw[i], s2, z2);
+    int4_unpack_scale(vs[i], s2, z2);
+    reinterpret_cast<uint4*>(a.v_out)[at] = int4_elements(vw[i], s2, z2);
+  }
+}
+
+cudaLaunchConfig_t chained(dim3 grid, unsigned threads, cudaLaunchAttribute* attr, cudaStream_t stream) {
+  attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr->val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
+}  // namespace
+
+cudaError_t launch_rope_int4_store(const RopeFormArgs& a, cudaStream_t stream) {
+  cudaLaunchAttribute attr;
+  const unsigned token_ctas = static_cast<unsigned>((static_cast<long long>(a.num_tokens) + kStoreWarps - 1) / kStoreWarps);
+  // Where tokens are few, each group of a token's vectors has a warp of its own.
+  const int groups = (a.num_q_heads + 2 * a.num_kv_heads + 7) / 8;
+  const int room = 304 / static_cast<int>(token_ctas > 304 ? 304 : token_ctas);
+  cudaLaunchConfig_t cfg = chained(dim3(token_ctas, groups < room ? groups : room), kStoreWarps * 32, &attr, stream);
+  return a.interleaved ? cudaLaunchKernelEx(&cfg, rope_int4_store_kernel<true, 2>, a)
+                       : cudaLaunchKernelEx(&cfg, rope_int4_store_kernel<false, 2>, a);
+}
+
+cudaError_t launch_read_int4(const ReadInt4Args& a, cudaStream_t stream) {
+  cudaLaunchAttribute attr;
+  // a sequence's rows may begin and end inside a block
+  const long long units = ((static_cast<long long>(a.max_rows) + kBlockSize - 2) / kBlockSize + 1) * a.num_kv_heads;
+  cudaLaunchConfig_t cfg = chained(dim3(static_cast<unsigned>((units + kReadWarps - 1) / kReadWarps), a.num_seqs),
+                                   kReadWarps * 32, &attr, stream);
+  return cudaLaunchKernelEx(&cfg, read_int4_kernel, a);
+}
+
+}  // namespace pa

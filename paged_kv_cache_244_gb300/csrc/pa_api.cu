@@ -9,6 +9,7 @@
 
 #include <cuda_runtime.h>
 
+#include "int4_launch.h"
 #include "pa.h"
 #include "pa_launch.h"
 
@@ -216,11 +217,14 @@ int check_rope(const pa_rope* rope, int* rotary_dim, int* interleaved) {
   return PA_OK;
 }
 
-// pa_rope_kv_store_form, and with kv_scale its block-scaled E4M3 form.
+// What a store with a RoPE form writes into.
+enum class FormCache { kBf16, kBlockScaled, kInt4 };
+
+// pa_rope_kv_store_form, and its forms for block-scaled E4M3 caches (kv_scale) and the 4-bit cache (k_cache).
 int rope_store_form(const pa_dims* dims, const pa_rope* rope, int num_tokens, const void* q, void* q_out,
                     const void* k, const void* v, const int32_t* positions, const float* cos_sin,
                     int max_pos, const int64_t* slot_mapping, void* k_cache, void* v_cache,
-                    float* kv_scale, bool block_scaled, int num_blocks, void* stream) {
+                    float* kv_scale, FormCache type, int num_blocks, void* stream) {
   if (const int rc = check_dims(dims)) return rc;
   pa::RopeFormArgs a{};
   if (const int rc = check_rope(rope, &a.rotary_dim, &a.interleaved)) return rc;
@@ -228,7 +232,7 @@ int rope_store_form(const pa_dims* dims, const pa_rope* rope, int num_tokens, co
   if (num_tokens == 0) return PA_OK;
   if (!q || !q_out || !k || !v || !positions || !cos_sin || !slot_mapping || !k_cache || !v_cache)
     return PA_ERR_NULL;
-  if (block_scaled && !kv_scale) return PA_ERR_NULL;
+  if (type == FormCache::kBlockScaled && !kv_scale) return PA_ERR_NULL;
   if (max_pos < 1 || num_blocks < 1) return PA_ERR_RANGE;
   const void* ptrs[] = {q, q_out, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, kv_scale};
   for (const void* p : ptrs)
@@ -249,8 +253,10 @@ int rope_store_form(const pa_dims* dims, const pa_rope* rope, int num_tokens, co
   a.num_kv_heads = dims->num_kv_heads;
   a.max_pos = max_pos;
   a.num_blocks = num_blocks;
-  return pa::launch_rope_form_store(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK
-                                                                                         : PA_ERR_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return (type == FormCache::kInt4 ? pa::launch_rope_int4_store(a, st) : pa::launch_rope_form_store(a, st)) == cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
 }
 
 // The angles per position of pair i of R/2 (see PA_ROPE_SCALE_*), in 64 bits.
@@ -288,7 +294,7 @@ int decode_step(const pa_dims* dims, int num_seqs, const void* q, const void* k,
                 const int32_t* block_tables, int max_blocks, const int32_t* context_lens,
                 int max_context_len, float scale, int partition_tokens, void* workspace,
                 size_t workspace_bytes, void* out, unsigned flags, void* stream,
-                float* kv_scale = nullptr, int rotary_dim = 128, int interleaved = 0) {
+                float* kv_scale = nullptr, int rotary_dim = 128, int interleaved = 0, bool int4 = false) {
   // The new token's arguments first (host checks only), then everything pa_decode checks.
   if (const int rc = check_dims(dims)) return rc;
   if (flags & ~PA_STEP_EARLY_METADATA) return PA_ERR_RANGE;
@@ -315,8 +321,8 @@ int decode_step(const pa_dims* dims, int num_seqs, const void* q, const void* k,
   a.rotary_dim = rotary_dim;
   a.interleaved = interleaved;
   a.early_metadata = (flags & PA_STEP_EARLY_METADATA) ? 1 : 0;
-  return pa::launch_decode(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK
-                                                                                 : PA_ERR_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return (int4 ? pa::launch_decode_int4(a, st) : pa::launch_decode(a, st)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 // Host checks of a block-scaled call's kv_scale, with the shape and the count that they depend on.
@@ -490,11 +496,11 @@ int pa_decode_fp8(const pa_dims* dims, int num_seqs, const void* q, const void* 
 
 namespace {
 
-// pa_prefill, and with kv_scale its block-scaled E4M3 form.
+// pa_prefill, with kv_scale its block-scaled E4M3 form, or its form for the 4-bit cache (k_cache).
 int prefill(const pa_dims* dims, int num_seqs, int num_tokens, const void* q, const int32_t* q_start,
             int max_query_len, const void* k_cache, const void* v_cache, const float* kv_scale,
             int num_blocks, const int32_t* block_tables, int max_blocks, const int32_t* context_lens,
-            int max_context_len, float scale, void* out, void* stream) {
+            int max_context_len, float scale, void* out, void* stream, bool int4 = false) {
   if (const int rc = check_dims(dims)) return rc;
   if (num_seqs < 0 || num_tokens < 0) return PA_ERR_RANGE;
   if (num_seqs == 0 || num_tokens == 0) return PA_OK;
@@ -533,8 +539,10 @@ int prefill(const pa_dims* dims, int num_seqs, int num_tokens, const void* q, co
   a.status = status;
   a.kv_scale = reinterpret_cast<const float2*>(kv_scale);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return (kv_scale ? pa::launch_prefill_block(a, st) : pa::launch_prefill(a, st)) == cudaSuccess ? PA_OK
-                                                                                               : PA_ERR_CUDA;
+  const cudaError_t err = int4       ? pa::launch_prefill_int4(a, st)
+                          : kv_scale ? pa::launch_prefill_block(a, st)
+                                     : pa::launch_prefill(a, st);
+  return err == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 }  // namespace
@@ -597,7 +605,7 @@ int pa_rope_kv_store_form(const pa_dims* dims, const pa_rope* rope, int num_toke
                           const float* cos_sin, int max_pos, const int64_t* slot_mapping,
                           void* k_cache, void* v_cache, int num_blocks, void* stream) {
   return rope_store_form(dims, rope, num_tokens, q, q_out, k, v, positions, cos_sin, max_pos, slot_mapping,
-                         k_cache, v_cache, nullptr, false, num_blocks, stream);
+                         k_cache, v_cache, nullptr, FormCache::kBf16, num_blocks, stream);
 }
 
 int pa_rope_kv_store_fp8_block(const pa_dims* dims, const pa_rope* rope, int num_tokens,
@@ -606,7 +614,77 @@ int pa_rope_kv_store_fp8_block(const pa_dims* dims, const pa_rope* rope, int num
                                const int64_t* slot_mapping, void* k_cache, void* v_cache,
                                float* kv_scale, int num_blocks, void* stream) {
   return rope_store_form(dims, rope, num_tokens, q, q_out, k, v, positions, cos_sin, max_pos, slot_mapping,
-                         k_cache, v_cache, kv_scale, true, num_blocks, stream);
+                         k_cache, v_cache, kv_scale, FormCache::kBlockScaled, num_blocks, stream);
+}
+
+int pa_rope_kv_store_int4(const pa_dims* dims, const pa_rope* rope, int num_tokens, const void* q,
+                          void* q_out, const void* k, const void* v, const int32_t* positions,
+                          const float* cos_sin, int max_pos, const int64_t* slot_mapping, void* cache,
+                          int num_blocks, void* stream) {
+  return rope_store_form(dims, rope, num_tokens, q, q_out, k, v, positions, cos_sin, max_pos, slot_mapping, cache,
+                         cache, nullptr, FormCache::kInt4, num_blocks, stream);
+}
+
+int pa_read_kv_int4(const pa_dims* dims, int num_seqs, int num_rows, const int32_t* row_start,
+                    const int32_t* first, int max_rows, const void* cache, int num_blocks,
+                    const int32_t* block_tables, int max_blocks, void* k_out, void* v_out, void* stream) {
+  if (const int rc = check_dims(dims)) return rc;
+  if (num_seqs < 0 || num_seqs > 65535 || num_rows < 0) return PA_ERR_RANGE;
+  if (num_seqs == 0 || num_rows == 0) return PA_OK;
+  if (!row_start || !cache || !block_tables || !k_out || !v_out) return PA_ERR_NULL;
+  if (num_blocks < 1 || max_blocks < 1 || max_blocks > (0x7fffffff - 15) / 16) return PA_ERR_RANGE;
+  if (max_rows < 1 || max_rows > max_blocks * dims->block_size) return PA_ERR_RANGE;
+  const void* ptrs[] = {row_start, first, cache, block_tables, k_out, v_out};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return PA_ERR_ALIGN;
+  pa::ReadInt4Args a{};
+  if (const int rc = status_word(&a.status)) return rc;
+  a.cache = static_cast<const uint8_t*>(cache);
+  a.row_start = row_start;
+  a.first = first;
+  a.block_tables = block_tables;
+  a.k_out = static_cast<__nv_bfloat16*>(k_out);
+  a.v_out = static_cast<__nv_bfloat16*>(v_out);
+  a.num_seqs = num_seqs;
+  a.num_rows = num_rows;
+  a.max_rows = max_rows;
+  a.num_kv_heads = dims->num_kv_heads;
+  a.num_blocks = num_blocks;
+  a.max_blocks = max_blocks;
+  return pa::launch_read_int4(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+int pa_decode_int4(const pa_dims* dims, int num_seqs, const void* q, const void* cache, int num_blocks,
+                   const int32_t* block_tables, int max_blocks, const int32_t* context_lens,
+                   int max_context_len, float scale, int partition_tokens, void* workspace,
+                   size_t workspace_bytes, void* out, void* stream) {
+  pa::DecodeArgs a{};
+  const int rc = decode_args(dims, num_seqs, q, cache, cache, num_blocks, block_tables, max_blocks, context_lens,
+                             max_context_len, scale, partition_tokens, workspace, workspace_bytes, out, &a);
+  if (rc != PA_OK || num_seqs == 0) return rc;
+  return pa::launch_decode_int4(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+int pa_decode_step_int4(const pa_dims* dims, const pa_rope* rope, int num_seqs, const void* q,
+                        const void* k, const void* v, const float* cos_sin, int max_pos, void* cache,
+                        int num_blocks, const int32_t* block_tables, int max_blocks,
+                        const int32_t* context_lens, int max_context_len, float scale,
+                        int partition_tokens, void* workspace, size_t workspace_bytes, void* out,
+                        unsigned flags, void* stream) {
+  int rotary_dim = 0, interleaved = 0;
+  if (const int rc = check_dims(dims)) return rc;
+  if (const int rc = check_rope(rope, &rotary_dim, &interleaved)) return rc;
+  return decode_step(dims, num_seqs, q, k, v, cos_sin, max_pos, cache, cache, nullptr, nullptr, num_blocks,
+                     block_tables, max_blocks, context_lens, max_context_len, scale, partition_tokens, workspace,
+                     workspace_bytes, out, flags, stream, nullptr, rotary_dim, interleaved, true);
+}
+
+int pa_prefill_int4(const pa_dims* dims, int num_seqs, int num_tokens, const void* q,
+                    const int32_t* q_start, int max_query_len, const void* cache, int num_blocks,
+                    const int32_t* block_tables, int max_blocks, const int32_t* context_lens,
+                    int max_context_len, float scale, void* out, void* stream) {
+  return prefill(dims, num_seqs, num_tokens, q, q_start, max_query_len, cache, cache, nullptr, num_blocks,
+                 block_tables, max_blocks, context_lens, max_context_len, scale, out, stream, true);
 }
 
 int pa_rope_table(const pa_rope_scaling* scaling, int rotary_dim, int max_pos, float* cos_sin,

@@ -46,6 +46,7 @@
 
 #include <mutex>
 
+#include "int4_launch.h"
 #include "pa_device.cuh"
 #include "pa_launch.h"
 
@@ -824,6 +825,10 @@ cudaError_t launch_decode_block(const DecodeArgs& args, cudaStream_t stream) {
                      : (once ? decode_block_kernel<false, true> : decode_block_kernel<false, false>);
   err = cudaLaunchKernelEx(&cfg, kernel, a, pool);
   if (err != cudaSuccess) return err;
+  return launch_block_merge(a, cfg);
+}
+
+cudaError_t launch_block_merge(const DecodeArgs& a, cudaLaunchConfig_t cfg) {
   const long long pairs = static_cast<long long>(a.num_seqs) * a.num_q_heads;
   const int groups = pairs <= kWidePairs ? 16 : pairs <= kMidPairs ? 4 : 1;
   const int per_cta = groups > kMergeCta ? groups : kMergeCta;

@@ -1,0 +1,669 @@
+// Single-token paged GQA decode attention over the 4-bit cache, for sm_103a, with the fused step (RoPE
+// form + quantising store of the new token).
+//
+// "Pico-vLLM：从零手写的工业级LLM推理引擎实现": §2 Kernel层 (PagedAttention decode kernel), §H200上的详细对比
+// (Flash Decode); "从零实现 LLM 推理引擎：深挖 vLLM 的六大核心优化", §3.1 Paged KV Cache; "nano-vllm：vLLM
+// 极简实现与大模型推理流程解析", §学习要点 (4-bit quantisation of the cache).
+//
+// The work is cut as in the other decode kernels (pa_device.cuh): one axis of (sequence, KV head, block),
+// an equal contiguous range for each warp of a persistent grid, each warp its own producer and consumer,
+// pieces of split segments merged by a kernel after it.  The mathematics, with K element (t, d) =
+// s_tg (c_td - z_tg) for d in group g of 32 dims, V element s_t (c_td - z_t), and head column h:
+//
+//   score   x_th = sum_g s_tg sum_{d in g} q_hd c_td - sum_g s_tg z_tg Q_hg,   Q_hg = sum_{d in g} q_hd
+//   weight  e_th = scale_log2 x_th + log2 s_t,   p_th = 2^(e_th - m_h)
+//   output  out_hd = (sum_t p_th c_td - sum_t p_th z_t) / L_h,   L_h = sum_t p_th / s_t
+//
+// Codes enter the matrix instructions with no conversion: a pair masked out of a shifted word is a pair of small
+// f16 values, c 2^-21 or c 2^-17, exact (below 2^-13 an f16 pattern is its integer times 2^-24), and the products
+// with a normal q or p are normal fp32 numbers.  Eight codes cost six integer instructions.  (Masked as they lie, at
+// 2^-24 and 2^-20, they cost five, but the instruction aligns a subnormal operand by its exponent field, and the last
+// bits of what is added to a large product were lost: 2^-13 of it.)  The factor of 16 between the two kinds of
+// pair is taken out of q for K, and out of the accumulators for V at the end.  The two sums over zero points are
+// matrix instructions as well:
+//   - sum_g s_tg z_tg Q_hg is one bf16 instruction a block: s z is exact in bf16, and each Q_hg goes in as
+//     three bf16 numbers that add up to it.
+//   - sum_t p_th z_t is one f16 instruction a block whose A operand has the zero points in every row, so each
+//     lane gets the sum for its own head columns, over the same rounded p as the codes' sums.
+// V's scale acts on the exponent and cancels in L, so p stays within f16 whatever the scales: the shift m is
+// set 7 below the largest contribution and moves when one passes it by more than 15.  L adds the unrounded p.
+//
+// A job is up to four neighbouring blocks of a piece, 8.6 KiB in one stage of the warp's ring, brought in by
+// cp.async, one commit group a job, with q of a piece's first job and the step's rows.
+
+#include <mutex>
+
+#include "int4_cache.cuh"
+#include "int4_launch.h"
+
+namespace pa {
+namespace {
+
+constexpr int kDiWarps = 12;                         // of a CTA at most (registers)
+constexpr int kDiJob = 4;                            // blocks of a job at most
+constexpr int kDiQOff = kDiJob * kInt4Record;
+// A stage: records, q rows of G heads, and for the step cos/sin (R <= 128 floats), k and v.
+__host__ __device__ inline int di_stage(int G, bool step) {
+  return kDiQOff + G * kHeadDim * 2 + (step ? kHeadDim * 4 + 2 * kHeadDim * 2 : 0);
+}
+constexpr int kDiMaxStages = 32;                     // of a CTA
+constexpr int kDiMaxRing = 8;                        // of a warp
+constexpr int kDiSmemMax = 226 * 1024;               // beside the static part of build_prefix
+constexpr int kDiPrefixOff = kDiMaxStages * 16;      // after the jobs' descriptors
+
+// Fields of a job's flag word: kFirst .. kGap, rows of the last block at bits 8-12, blocks (1 .. 4) at 16-18,
+// which of them are there at 20-23.
+constexpr int kBlocksAt = 16, kHereAt = 20;
+
+// Pairs of codes as f16: of a word's neighbouring pairs shifted by 3, the first c 2^-21 and the second c 2^-17.
+constexpr uint32_t kPairA = 0x00780078u, kPairB = 0x07800780u;
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <bool kStep>
+__global__ void __launch_bounds__(kDiWarps * 32, 1) decode_int4_kernel(const DecodeArgs a, const int pool) {
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t raw = smem_addr(smem_raw);
+  int* prefix = reinterpret_cast<int*>(smem_raw + kDiPrefixOff);
+  unsigned char* last_rows = smem_raw + kDiPrefixOff + (((a.num_seqs + 1) * 4 + 15) & ~15);
+  const uint32_t tile_base = raw + kDiPrefixOff + prefix_bytes(a.num_seqs);
+  // With early metadata the lengths and block table are read, and the work resolved, before the
+  // preceding kernel has finished; copies and writes wait for it (below).
+  const bool early = a.early_metadata != 0;
+  if (!early) pdl_wait_prior_grid();
+  pdl_allow_next_grid();
+
+  const int S = a.num_seqs;
+  const int Hkv = a.num_kv_heads;
+  const int G = a.num_q_heads / Hkv;
+  const int warps = static_cast<int>(blockDim.x >> 5);
+  const int stage_bytes = di_stage(G, kStep);
+  const int cos_off = kDiQOff + G * kHeadDim * 2;    // (step)
+  build_prefix<kDiWarps>(a, prefix, last_rows, blockDim.x);
+  const long long T = static_cast<long long>(Hkv) * prefix[S];
+  const Ranges R = make_ranges(T, a);
+  // Range v goes to warp v / grid of CTA v % grid; the CTA's stages are shared out among its warps
+  // that have a range, the first of them taking one more where they do not divide.
+  const int my_v = static_cast<int>(blockIdx.x) + warp * static_cast<int>(gridDim.x);
+  if (my_v >= R.V) {
+    if (early) pdl_wait_prior_grid();
+    return;
+  }
+  const int active = min(warps, (R.V - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) /
+                                       static_cast<int>(gridDim.x));
+  const int share = pool / active + (warp < pool % active ? 1 : 0);
+  const int st0 = warp * (pool / active) + min(warp, pool % active);
+  const int n_st = min(share, kDiMaxRing);
+  int4* descs = reinterpret_cast<int4*>(smem_raw) + st0;
+  const uint32_t tiles = tile_base + st0 * stage_bytes;
+  const int gq = lane >> 2;  // fragment row group
+  const int cq = lane & 3;   // fragment column pair
+  const long long x0 = R.begin(my_v), x1 = R.begin(my_v + 1);
+  const uint8_t* const cache = reinterpret_cast<const uint8_t*>(a.k_cache);
+
+  // ---- lookahead: window = up to 32 consecutive blocks of the range, lane j resolves block j ----
+  struct Window {
+    long long x;
+    int n;
+    int blk, seg, fl, slot, pos;
+  };
+  auto resolve = [&](Window& W) {
+    W.blk = -1;
+    W.seg = W.fl = W.slot = W.pos = 0;
+    if (lane >= W.n) return;
+    const long long p = W.x + lane;
+    int lo = 0, hi = S;                              // largest s with Hkv * N_s <= p
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (static_cast<long long>(Hkv) * prefix[mid] <= p) lo = mid;
+      else hi = mid;
+    }
+    const int s = lo;
+    const int ns = prefix[s + 1] - prefix[s];
+    const int off = static_cast<int>(p - static_cast<long long>(Hkv) * prefix[s]);
+    const int g = off / ns;
+    const int j = off - g * ns;
+    const long long Xi = static_cast<long long>(Hkv) * prefix[s] + static_cast<long long>(g) * ns;
+    W.blk = a.block_tables[static_cast<size_t>(s) * a.max_blocks + j];
+    W.seg = s * Hkv + g;
+    const int tail = last_rows[s];
+    const int valid = j == ns - 1 ? tail : kBlockSize;
+    const int chunk = a.chunk_blocks;
+    const int part = chunk ? j / chunk : 0;
+    const bool p_first = chunk && j == part * chunk;
+    const bool p_last = chunk && j == part * chunk + chunk - 1;
+    uint32_t flags = ((p == x0 || j == 0 || p_first) ? kFirst : 0u) |
+                     ((p == x1 - 1 || j == ns - 1 || p_last) ? kLast : 0u) |
+                     ((Xi >= x0 && Xi + ns <= x1 && (chunk == 0 || ns <= chunk)) ? kWhole : 0u) |
+                     ((p == x0 && j > 0 && p_first) ? kGap : 0u);
+    if (kStep) {
+      W.pos = (ns - 1) * kBlockSize + tail - 1;      // position of the sequence's new token
+      if (j == ns - 1) flags |= kNew;
+      if (W.pos < a.max_pos) flags |= kRope;
+    }
+    W.fl = static_cast<int>(flags | (static_cast<uint32_t>(valid) << 8) | (static_cast<uint32_t>(g) << 16));
+    W.slot = static_cast<int>(piece_slot(my_v, W.seg, part, a.max_parts));
+  };
+  auto next_of = [&](const Window& W, Window& N) {
+    N.x = W.x + W.n;
+    N.n = static_cast<int>(min(32ll, x1 - N.x));
+  };
+  Window cur, nxt;
+  cur.x = x0;
+  cur.n = static_cast<int>(min(32ll, x1 - x0));
+  resolve(cur);
+  next_of(cur, nxt);   // resolved behind the first jobs
+  bool nxt_there = false;
+  uint32_t lasts = __ballot_sync(kFullMask, (cur.fl & kLast) != 0);   // blocks of `cur` that end a piece
+  int pk = 0;  // next block of `cur`
+
+  // Emit the next job into stage st, as one commit group; false when the range is used up.
+  auto produce = [&](int st) -> bool {
+    if (pk == cur.n) {
+      if (nxt.n == 0) return false;
+      if (!nxt_there) resolve(nxt);
+      cur = nxt;
+      pk = 0;
+      next_of(cur, nxt);
+      resolve(nxt);
+      nxt_there = true;
+      lasts = __ballot_sync(kFullMask, (cur.fl & kLast) != 0);
+    }
+    const int to_last = __ffs(static_cast<int>(lasts >> pk));           // 0: none left in the window
+    const int nb = min(min(kDiJob, cur.n - pk), to_last ? to_last : kDiJob);
+    const int fl0 = __shfl_sync(kFullMask, cur.fl, pk);
+    const int fl1 = __shfl_sync(kFullMask, cur.fl, pk + nb - 1);
+    const int seg = __shfl_sync(kFullMask, cur.seg, pk);
+    const int slot = __shfl_sync(kFullMask, cur.slot, pk);
+    const int pos = kStep ? __shfl_sync(kFullMask, cur.pos, pk) : 0;
+    const int g = fl0 >> 16;
+    const bool ok = cur.blk >= 0 && cur.blk < a.num_blocks;
+    const uint32_t here = (__ballot_sync(kFullMask, ok) >> pk) & ((1u << nb) - 1);
+    const int row = ok ? cur.blk * Hkv + g : 0;      // record of this lane's block, if it is one of the job's
+    const int row_last = __shfl_sync(kFullMask, row, pk + nb - 1);
+    const uint32_t dst = tiles + st * stage_bytes;
+    // Fused step: a position without a cos/sin row leaves the token out -- q unrotated, nothing stored.
+    const bool rope = kStep && (fl0 & kRope);
+    const bool fresh = rope && (fl1 & kNew) && ((here >> (nb - 1)) & 1);    // the new token's record is here
+    if (fl0 & kFirst) {
+      const char* q = reinterpret_cast<const char*>(a.q + static_cast<size_t>(seg) * G * kHeadDim);
+      for (int c = lane; c < G * 16; c += 32) cp_async16(dst + kDiQOff + 16 * c, q + 16 * c);
+    }
+    if (kStep && rope && ((fl0 & kFirst) || fresh) && lane < a.rotary_dim / 4)
+      cp_async16(dst + cos_off + 16 * lane, a.cos_sin + static_cast<size_t>(pos) * a.rotary_dim + 4 * lane);
+    if (kStep && fresh) {
+      const __nv_bfloat16* src = (lane < 16 ? a.k_new : a.v_new) + static_cast<size_t>(seg) * kHeadDim;
+      cp_async16(dst + cos_off + kHeadDim * 4 + 16 * lane, src + 8 * (lane & 15));
+    }
+#pragma unroll
+    for (int b = 0; b < kDiJob; ++b) {
+      const int r = __shfl_sync(kFullMask, row, (pk + b) & 31);
+      if ((here >> b) & 1) {
+        const uint8_t* src = cache + static_cast<size_t>(r) * kInt4Record + lane * 16;
+        const uint32_t to = dst + b * kInt4Record + lane * 16;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) cp_async16(to + 512 * i, src + 512 * i);
+        if (lane < (kInt4Record - 2048) / 16) cp_async16(to + 2048, src + 2048);
+      }
+    }
+    cp_async_commit();
+    pk += nb;
+    if (lane == 0) {
+      if (here != (1u << nb) - 1) raise_flag(a.status, PA_FLAG_BLOCK_ID_OOB);
+      if (kStep && (fl1 & kNew) && !rope) raise_flag(a.status, PA_FLAG_POSITION_OOB);
+      // flags of the job: the first block's kFirst and kGap, the last one's kLast, kNew and rows
+      const uint32_t fl = (static_cast<uint32_t>(fl0) & (kFirst | kGap | kWhole | kRope)) |
+                          (static_cast<uint32_t>(fl1) & (kLast | 0x1f00u)) | (fresh ? kNew : 0u) |
+                          (static_cast<uint32_t>(nb) << kBlocksAt) | (here << kHereAt);
+      descs[st] = make_int4(seg, static_cast<int>(fl), slot, row_last);
+    }
+    return true;
+  };
+
+  // ---------------------------------------------------------------- consumer state --
+  // V rows of this lane's ldmatrix addresses: token r + 8 (i & 1), 16-byte unit u of its row at u ^ (r / 2 % 4)
+  const int mi = lane >> 3, r8 = lane & 7;
+  const uint32_t v_row = static_cast<uint32_t>(kInt4VCodes + 64 * (r8 + 8 * (mi & 1)));
+  const int v_unit = mi >> 1, v_turn = (r8 >> 1) & 3;
+  uint32_t qb[8][2];                      // B operand: dims 32c + 8cq .. + 7 of head gq, k permuted as the codes are
+  uint32_t qsum[2];                       // B operand: -Q of group cq of head gq as three bf16 numbers
+  float kf0 = 0.f, kf1 = 0.f;             // what turns x of head columns 2cq, 2cq + 1 into the exponent
+  float m0 = -INFINITY, m1 = -INFINITY;   // softmax shifts of those columns
+  float l0 = 0.f, l1 = 0.f;               // this lane's share of L
+  float o[8][4];                          // sums of p c: [2u + i] = rows gq, gq + 8: code pairs 2i, 2i + 1 of unit u
+  float z[4];                             // sums of p z (two and two alike)
+
+  // The new token (row `row` of the stage's record at `rec`, in the cache record `tile_row`) is rotated and
+  // quantised into both.
+  auto store_new = [&](unsigned char* stage, unsigned char* rec, int row, int tile_row) {
+    const float* cs = reinterpret_cast<const float*>(stage + cos_off);
+    uint32_t* kn = reinterpret_cast<uint32_t*>(stage + cos_off + kHeadDim * 4);
+    const int rot = a.rotary_dim;
+    // Lane l < R/4 turns two words (dim pairs) of the row: of the half layout words l and l + R/4, of the
+    // interleaved one 2l and 2l + 1.
+    if (lane < rot / 4) {
+      const int wa = a.interleaved ? 2 * lane : lane, wb = a.interleaved ? 2 * lane + 1 : lane + rot / 4;
+      uint32_t kx = kn[wa], ky = kn[wb];
+      const float2 co = reinterpret_cast<const float2*>(cs)[lane];
+      const float2 si = reinterpret_cast<const float2*>(cs + rot / 2)[lane];
+      if (a.interleaved) int4_rotate_interleaved(kx, ky, co, si);
+      else int4_rotate_pairs(kx, ky, co, si);
+      kn[wa] = kx;
+      kn[wb] = ky;
+    }
+    __syncwarp();
+    // half-lanes: 0-15 the chunks of 8 dims of k, 16-31 those of v
+    const int ch = lane & 15;
+    const bool is_k = lane < 16;
+    const uint4 w = reinterpret_cast<const uint4*>(kn)[lane];
+    uint32_t e = int4_extremes(w);
+#pragma unroll
+    for (int x = 1; x < 16; x <<= 1) {
+      const uint32_t other = __shfl_xor_sync(kFullMask, e, x);
+      if (x < 4 || !is_k) e = __vmaxu2(e, other);
+    }
+    const Int4Scale qs = int4_scale(e);
+    const uint32_t code = int4_word(w, qs);
+    uint8_t* const dst = reinterpret_cast<uint8_t*>(a.k_store) + static_cast<size_t>(tile_row) * kInt4Record;
+    const int at = is_k ? int4_k_word(row, ch) : int4_v_word(row, ch);
+    *reinterpret_cast<uint32_t*>(rec + at) = code;
+    *reinterpret_cast<uint32_t*>(dst + at) = code;
+    const int sat = is_k ? kInt4KScales + 8 * row + 2 * (ch >> 2) : kInt4VScales + 2 * row;
+    if (is_k ? (ch & 3) == 0 : ch == 0) {
+      *reinterpret_cast<uint16_t*>(rec + sat) = static_cast<uint16_t>(qs.word);
+      *reinterpret_cast<uint16_t*>(dst + sat) = static_cast<uint16_t>(qs.word);
+    }
+    __syncwarp();
+  };
+
+  // q rows of the piece: rotated (step), scaled and rounded to f16.
+  auto load_q = [&](const unsigned char* stage, uint32_t fl) {
+    const uint4* qrow = reinterpret_cast<const uint4*>(stage + kDiQOff + (gq < G ? gq : 0) * kHeadDim * 2);
+    uint32_t w[4][4];                     // dims 32c + 8cq + 2j, + 1
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const uint4 v = gq < G ? qrow[4 * c + cq] : make_uint4(0u, 0u, 0u, 0u);
+      w[c][0] = v.x;
+      w[c][1] = v.y;
+      w[c][2] = v.z;
+      w[c][3] = v.w;
+    }
+    if (kStep && (fl & kRope)) {
+      const int rot = a.rotary_dim, half = rot / 2;
+      const float* cs = reinterpret_cast<const float*>(stage + cos_off);
+      if (!a.interleaved && rot == kHeadDim) {       // partners 64 dims away, in the same lane
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int d = 32 * c + 8 * cq + 2 * j;
+            rope_rotate_pairs(w[c][j], w[c + 2][j], *reinterpret_cast<const float2*>(cs + d),
+                              *reinterpret_cast<const float2*>(cs + 64 + d));
+          }
+        }
+      } else {
+        // dims below R turn: within neighbouring words when interleaved, else with the dims R/2 away, read
+        // from the row (R/2 is a multiple of 8: a lane's eight dims lie on one side)
+        const uint32_t* row = reinterpret_cast<const uint32_t*>(qrow);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int d = 32 * c + 8 * cq;
+          if (d >= rot || gq >= G) continue;
+          if (a.interleaved) {
+#pragma unroll
+            for (int j = 0; j < 4; j += 2)
+              rope_rotate_interleaved(w[c][j], w[c][j + 1], *reinterpret_cast<const float2*>(cs + d / 2 + j),
+                                      *reinterpret_cast<const float2*>(cs + half + d / 2 + j));
+          } else {
+            const int i = d < half ? d : d - half;   // angle of the first dim
+            const int other_dim = d < half ? d + half : i;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t other = row[other_dim / 2 + j];
+              const float2 co = *reinterpret_cast<const float2*>(cs + i + 2 * j);
+              const float2 si = *reinterpret_cast<const float2*>(cs + half + i + 2 * j);
+              if (d < half) rope_rotate_pairs(w[c][j], other, co, si);
+              else rope_rotate_pairs(other, w[c][j], co, si);
+            }
+          }
+        }
+      }
+    }
+    __syncwarp();
+    uint32_t top = 0;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) top = __vmaxu2(top, w[c][j] & 0x7fff7fffu);
+    top = __vmaxu2(top, __shfl_xor_sync(kFullMask, top, 1));
+    top = __vmaxu2(top, __shfl_xor_sync(kFullMask, top, 2));
+    top = max(top & 0xffffu, top >> 16);             // the head's largest magnitude
+    // to [128, 256); below 2^-119 not as far: multiples of 2^-133 become multiples of 2^-7, exact all the same
+    const int e = min(7 + 127 - static_cast<int>(top >> 7), 126);
+    const float raise = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+    // Pairs j = 0 and 2 meet codes of 2^-21 and go in 16 times larger, pairs 1 and 3 codes of 2^-17.
+    float part[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      float s = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float f = (j & 1) ? 1.f : 16.f;
+        const uint32_t h = pack_f16x2(bf16lo(w[c][j]) * raise * f, bf16hi(w[c][j]) * raise * f);
+        qb[2 * c + (j >> 1)][j & 1] = h;
+        s = fmaf(f16lo(h) + f16hi(h), 1.f / f, s);
+      }
+      part[c] = s;
+    }
+    float mine = 0.f;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      part[c] += __shfl_xor_sync(kFullMask, part[c], 1);
+      part[c] += __shfl_xor_sync(kFullMask, part[c], 2);
+      if (c == cq) mine = part[c];
+    }
+    mine *= -0x1p-17f;
+    const uint32_t hi = pack_bf16x2(mine, 0.f);
+    const float rest = mine - bf16lo(hi);
+    const uint32_t mid = pack_bf16x2(rest, 0.f);
+    qsum[0] = hi | (mid << 16);
+    qsum[1] = pack_bf16x2(rest - bf16lo(mid), 0.f);
+    // x is 2^-17 raise of the product of q and K; an infinity or a NaN in q makes the head's scores NaN
+    const float fold = top >= 0x7f80u ? __uint_as_float(0x7fc00000u)
+                                      : row_factor(a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23)) * 0x1p17f;
+    kf0 = __shfl_sync(kFullMask, fold, 8 * cq);
+    kf1 = __shfl_sync(kFullMask, fold, 8 * cq + 4);
+  };
+
+  auto consume = [&](int st) {
+    const int4 d = descs[st];
+    const uint32_t fl = static_cast<uint32_t>(d.y);
+    const uint32_t kt = tiles + st * stage_bytes;
+    unsigned char* const stage = smem_raw + (kt - raw);
+    if (fl & kFirst) {
+      load_q(stage, fl);
+      m0 = m1 = -INFINITY;
+      l0 = l1 = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+      z[0] = z[1] = z[2] = z[3] = 0.f;
+      if ((fl & kGap) && lane < G)                   // mark the skipped slot before this piece empty
+        a.ws_ml[(static_cast<size_t>(d.z) - 1) * G + lane] = make_float2(-INFINITY, 0.f);
+    }
+    const int nb = static_cast<int>((fl >> kBlocksAt) & 7u);
+    const uint32_t here = (fl >> kHereAt) & 15u;
+    const int valid = static_cast<int>((fl >> 8) & 0x1fu);   // rows of the job's last block
+    if (kStep && (fl & kNew)) store_new(stage, stage + (nb - 1) * kInt4Record, valid - 1, d.w);
+    const bool whole = here == (1u << nb) - 1 && valid == kBlockSize;
+
+    // Exponents before the shift: [i][0] = (token gq of block i, head 2cq), [1] = (gq, 2cq + 1), [2] = (gq + 8,
+    // 2cq), [3] = (gq + 8, 2cq + 1); and 1 / s of V of tokens gq, gq + 8.
+    float y[kDiJob][4], iv[kDiJob][2];
+#pragma unroll
+    for (int i = 0; i < kDiJob; ++i) {
+      y[i][0] = y[i][1] = y[i][2] = y[i][3] = -INFINITY;
+      iv[i][0] = iv[i][1] = 0.f;
+      if (i >= nb) continue;
+      const uint32_t rec = kt + i * kInt4Record;
+      const uint4 wa = lds128(rec + 64 * gq + 16 * cq), wb = lds128(rec + 64 * gq + 512 + 16 * cq);
+      const uint2 sa = lds64(rec + kInt4KScales + 8 * gq), sb = lds64(rec + kInt4KScales + 64 + 8 * gq);
+      const uint32_t ga = lds16(rec + kInt4KScales + 8 * gq + 2 * cq), gb = lds16(rec + kInt4KScales + 64 + 8 * gq + 2 * cq);
+      const float va = int4_scale_of(lds16(rec + kInt4VScales + 2 * gq));
+      const float vb = int4_scale_of(lds16(rec + kInt4VScales + 16 + 2 * gq));
+      float x[4] = {0.f, 0.f, 0.f, 0.f};
+      {  // - sum_g s z Q: A rows = tokens, this lane's four k indices all stand for group cq
+        const uint32_t w = __byte_perm(ga, gb, 0x5410);
+        const uint32_t sz = mul_bf16x2(w & 0xfff0fff0u, sub_bf16x2((w & kPairLo) | 0x43004300u, 0x43004300u));
+        const uint32_t ra = __byte_perm(sz, sz, 0x1010), rb = __byte_perm(sz, sz, 0x3232);
+        mma_bf16_16816(x, ra, rb, ra, rb, qsum[0], qsum[1]);
+      }
+      auto group = [&](int c, uint32_t u, uint32_t v, float fu, float fv) {
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint32_t u0 = u << 3, v0 = v << 3, u1 = u >> 5, v1 = v >> 5;
+        mma_f16_16816(acc, u0 & kPairA, v0 & kPairA, u0 & kPairB, v0 & kPairB, qb[2 * c][0], qb[2 * c][1]);
+        mma_f16_16816(acc, u1 & kPairA, v1 & kPairA, u1 & kPairB, v1 & kPairB, qb[2 * c + 1][0], qb[2 * c + 1][1]);
+        x[0] = fmaf(fu, acc[0], x[0]);
+        x[1] = fmaf(fu, acc[1], x[1]);
+        x[2] = fmaf(fv, acc[2], x[2]);
+        x[3] = fmaf(fv, acc[3], x[3]);
+      };
+      group(0, wa.x, wb.x, int4_scale_of(sa.x), int4_scale_of(sb.x));
+      group(1, wa.y, wb.y, __uint_as_float(sa.x & 0xfff00000u), __uint_as_float(sb.x & 0xfff00000u));
+      group(2, wa.z, wb.z, int4_scale_of(sa.y), int4_scale_of(sb.y));
+      group(3, wa.w, wb.w, __uint_as_float(sa.y & 0xfff00000u), __uint_as_float(sb.y & 0xfff00000u));
+      const float ea = lg2(va), eb = lg2(vb);
+      y[i][0] = fmaf(x[0], kf0, ea);
+      y[i][1] = fmaf(x[1], kf1, ea);
+      y[i][2] = fmaf(x[2], kf0, eb);
+      y[i][3] = fmaf(x[3], kf1, eb);
+      iv[i][0] = rcp_ftz(va);
+      iv[i][1] = rcp_ftz(vb);
+      if (!whole) {
+        // tokens past the context, and absent blocks, may hold anything
+        const int n = !((here >> i) & 1) ? 0 : i == nb - 1 ? valid : kBlockSize;
+        if (gq >= n) y[i][0] = y[i][1] = -INFINITY, iv[i][0] = 0.f;
+        if (gq + 8 >= n) y[i][2] = y[i][3] = -INFINITY, iv[i][1] = 0.f;
+      }
+    }
+    float top0 = -INFINITY, top1 = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kDiJob; ++i) {
+      top0 = fmax3(top0, y[i][0], y[i][2]);
+      top1 = fmax3(top1, y[i][1], y[i][3]);
+    }
+    if (__any_sync(kFullMask, top0 - m0 > 15.f || top1 - m1 > 15.f)) {
+      // A shift has to move (at a piece's first job from -infinity): the maxima over the tokens, and what
+      // was summed so far scaled to the new shifts.
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) {
+        top0 = fmaxf(top0, __shfl_xor_sync(kFullMask, top0, x));
+        top1 = fmaxf(top1, __shfl_xor_sync(kFullMask, top1, x));
+      }
+      const float mn0 = top0 - m0 > 15.f ? top0 - 7.f : m0, mn1 = top1 - m1 > 15.f ? top1 - 7.f : m1;
+      const float al0 = mn0 == m0 ? 1.f : ex2_ftz(m0 - mn0), al1 = mn1 == m1 ? 1.f : ex2_ftz(m1 - mn1);
+      m0 = mn0;
+      m1 = mn1;
+      l0 *= al0;
+      l1 *= al1;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        o[i][0] *= al0;
+        o[i][1] *= al1;
+        o[i][2] *= al0;
+        o[i][3] *= al1;
+      }
+      z[0] *= al0;
+      z[1] *= al1;
+      z[2] *= al0;
+      z[3] *= al1;
+    }
+    // a column without a key so far keeps the shift at -infinity: weights 0, not NaN
+    const float sh0 = m0 == -INFINITY ? 0.f : m0, sh1 = m1 == -INFINITY ? 0.f : m1;
+#pragma unroll
+    for (int i = 0; i < kDiJob; ++i) {
+      if (i >= nb) continue;
+      const uint32_t rec = kt + i * kInt4Record;
+      const float p0 = ex2_ftz(y[i][0] - sh0), p1 = ex2_ftz(y[i][1] - sh1);
+      const float p2 = ex2_ftz(y[i][2] - sh0), p3 = ex2_ftz(y[i][3] - sh1);
+      l0 = fmaf(p0, iv[i][0], fmaf(p2, iv[i][1], l0));
+      l1 = fmaf(p1, iv[i][0], fmaf(p3, iv[i][1], l1));
+      // B operand P^T: tokens 2cq, 2cq + 1 (+ 8) of head gq
+      const uint32_t b0 = movmatrix_trans(pack_f16x2(p0, p1)), b1 = movmatrix_trans(pack_f16x2(p2, p3));
+      const uint32_t za = (lds32(rec + kInt4VScales + 4 * cq) << 7) & kPairB;
+      const uint32_t zb = (lds32(rec + kInt4VScales + 16 + 4 * cq) << 7) & kPairB;
+      mma_f16_16816(z, za, za, zb, zb, b0, b1);
+      // The transposing ldmatrix takes four codes for an element: lane (gq, cq) gets tokens 2cq and 2cq + 1 of
+      // eight bytes' dims in the halves of a word, so that a masked pair is a pair along the tokens.
+#pragma unroll
+      for (int u = 0; u < 4; u += 2) {
+        uint32_t w[4];
+        ldsm_x4_trans(rec + v_row + (((u + v_unit) ^ v_turn) << 4), w[0], w[1], w[2], w[3]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t u0 = w[2 * h] << 3, v0 = w[2 * h + 1] << 3, u1 = w[2 * h] >> 5, v1 = w[2 * h + 1] >> 5;
+          mma_f16_16816(o[2 * (u + h)], u0 & kPairA, u0 & kPairB, v0 & kPairA, v0 & kPairB, b0, b1);
+          mma_f16_16816(o[2 * (u + h) + 1], u1 & kPairA, u1 & kPairB, v1 & kPairA, v1 & kPairB, b0, b1);
+        }
+      }
+    }
+    if (fl & kLast) {
+      float L0 = l0, L1 = l1;                        // the 8 lanes sharing cq hold disjoint tokens
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) {
+        L0 += __shfl_xor_sync(kFullMask, L0, x);
+        L1 += __shfl_xor_sync(kFullMask, L1, x);
+      }
+      const bool piece_whole = (fl & kWhole) != 0;
+      // a sequence whose every block is out of range has L = 0 and gives zeros
+      const float f0 = piece_whole ? (L0 == 0.f ? 0.f : 1.f / L0) : 1.f, f1 = piece_whole ? (L1 == 0.f ? 0.f : 1.f / L1) : 1.f;
+      const size_t row = (piece_whole ? static_cast<size_t>(d.x) : static_cast<size_t>(d.z)) * G + 2 * cq;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          // Column gq of the unit's eight has dims 8 (gq / 2) + gq % 2 + 2j, j = 0 .. 3.  Neighbouring columns
+          // exchange two of them each and hold four dims in a row: 32u + 4gq .. + 3.
+          const float zh = z[h], f = (h ? f1 : f0) * 0x1p17f;
+          const float v0 = fmaf(o[2 * u][h], 16.f, -zh) * f, v1 = (o[2 * u][2 + h] - zh) * f;
+          const float v2 = fmaf(o[2 * u + 1][h], 16.f, -zh) * f, v3 = (o[2 * u + 1][2 + h] - zh) * f;
+          const bool odd = gq & 1;
+          const float g0 = __shfl_xor_sync(kFullMask, odd ? v0 : v2, 4), g1 = __shfl_xor_sync(kFullMask, odd ? v1 : v3, 4);
+          const float4 v = odd ? make_float4(g0, v2, g1, v3) : make_float4(v0, g0, v1, g1);
+          if (2 * cq + h >= G) continue;
+          if (piece_whole)
+            *reinterpret_cast<uint2*>(a.out + (row + h) * kHeadDim + 32 * u + 4 * gq) =
+                make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+          else
+            *reinterpret_cast<float4*>(a.ws_o + (row + h) * kHeadDim + 32 * u + 4 * gq) = v;
+        }
+      }
+      if (!piece_whole && gq == 0) {
+        if (2 * cq < G) a.ws_ml[row] = make_float2(m0, L0);
+        if (2 * cq + 1 < G) a.ws_ml[row + 1] = make_float2(m1, L1);
+      }
+    }
+  };
+
+  // ---------------------------------------------------------------- pipeline --------
+  int ahead = 0;           // jobs emitted and not yet consumed
+  int pst = 0, cst = 0;
+  bool more = true;
+  if (early) pdl_wait_prior_grid();
+  while (more && ahead < n_st) {
+    more = produce(pst);
+    if (more) {
+      ++ahead;
+      if (++pst == n_st) pst = 0;
+    }
+  }
+  if (!nxt_there) {
+    resolve(nxt);
+    nxt_there = true;
+  }
+  __syncwarp();
+  while (ahead > 0) {
+    cp_async_wait_but(ahead - 1);      // the oldest job's copies; the warp barrier shows them to every lane
+    __syncwarp();
+    consume(cst);
+    --ahead;
+    if (++cst == n_st) cst = 0;
+    __syncwarp();
+    if (more) {
+      more = produce(pst);
+      if (more) {
+        ++ahead;
+        if (++pst == n_st) pst = 0;
+      }
+    }
+    __syncwarp();
+  }
+}
+
+// CTAs of the persistent grid: one per SM, capped to kMaxDecodeWarps warps (looked up once per
+// device, with the shared-memory opt-in of both variants).
+cudaError_t int4_ctas(int* ctas) {
+  static std::mutex mu;
+  static int cached[64] = {};
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lock(mu);
+  if (!cached[dev]) {
+    auto opt_in = [&](auto kernel) {
+      if (err == cudaSuccess)
+        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kDiSmemMax);
+    };
+    opt_in(decode_int4_kernel<false>);
+    opt_in(decode_int4_kernel<true>);
+    int sms = 0;
+    if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (err != cudaSuccess) return err;
+    cached[dev] = min(sms, kMaxDecodeWarps / kDiWarps);
+  }
+  *ctas = cached[dev];
+  return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_decode_int4(const DecodeArgs& args, cudaStream_t stream) {
+  DecodeArgs a = args;
+  const bool step = a.k_new != nullptr;
+  int max_ctas = 0;
+  cudaError_t err = int4_ctas(&max_ctas);
+  if (err != cudaSuccess) return err;
+  // Stages: what fits.  The warps are those that the step has room for, with and without it, so that both
+  // cut sequences alike and give the same bits.
+  const int G = a.num_q_heads / a.num_kv_heads;
+  const int fixed = kDiPrefixOff + prefix_bytes(a.num_seqs);
+  const int stage = di_stage(G, step);
+  const int pool = min(kDiMaxStages, (kDiSmemMax - fixed) / stage);
+  const int warps = min(kDiWarps, (kDiSmemMax - fixed) / di_stage(G, true));
+  // no more CTAs than there can be ranges (they are dealt to the CTAs one at a time)
+  const long long jobs = static_cast<long long>(a.num_seqs) * a.num_kv_heads *
+                         ((a.max_context_len + kBlockSize - 1) / kBlockSize);
+  const long long ctas = min(static_cast<long long>(max_ctas), (jobs + kMinRangeBlocks - 1) / kMinRangeBlocks);
+  a.num_warps = static_cast<int>(ctas) * warps;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(static_cast<unsigned>(warps * 32));
+  cfg.dynamicSmemBytes = fixed + pool * stage;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  err = cudaLaunchKernelEx(&cfg, step ? decode_int4_kernel<true> : decode_int4_kernel<false>, a, pool);
+  if (err != cudaSuccess) return err;
+  return launch_block_merge(a, cfg);
+}
+
+}  // namespace pa

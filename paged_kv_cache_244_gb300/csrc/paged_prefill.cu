@@ -50,6 +50,7 @@
 
 #include <cuda.h>
 
+#include "int4_launch.h"
 #include "pa_device.cuh"
 #include "pa_launch.h"
 #include "umma_desc.h"
@@ -603,7 +604,7 @@ extern "C" int pa_set_timing_jitter(uint32_t max_ns, uint32_t seed) {
   if (max_ns > 1000000u) return PA_ERR_RANGE;
   const uint32_t v[2] = {max_ns, seed};
   return cudaMemcpyToSymbol(pa::c_pf_jitter, v, sizeof v) == cudaSuccess &&
-                 pa::set_prefill_block_jitter(v) == cudaSuccess
+                 pa::set_prefill_block_jitter(v) == cudaSuccess && pa::set_prefill_int4_jitter(v) == cudaSuccess
              ? PA_OK
              : PA_ERR_CUDA;
 }

@@ -132,6 +132,21 @@ pa_dims dims_of(const at::Tensor& q, const Cache& c) {
   return pa_dims{size32(q, 1), c.kv_heads, c.head_dim, c.block_size};
 }
 
+// The 4-bit cache: one tensor of records.
+struct Cache4 {
+  const at::Tensor& t;
+  int num_blocks, kv_heads;
+  Cache4(Args& a, int i) : t(a.tensor(i, "cache", kU8)) {
+    require(t.dim() == 3 && t.size(2) == PA_INT4_RECORD_BYTES, "cache must be [num_blocks, num_kv_heads, 2208]");
+    num_blocks = size32(t, 0);
+    kv_heads = size32(t, 1);
+  }
+  pa_dims dims(const at::Tensor& q) const {
+    require(q.dim() == 3 && q.size(2) == 128, "q must be [rows, num_q_heads, 128]");
+    return pa_dims{size32(q, 1), kv_heads, 128, 16};
+  }
+};
+
 pa_rope rope_of(const at::Tensor& cos_sin, int layout) {
   require(cos_sin.dim() == 2, "cos_sin must be [max_pos, rotary_dim]");
   return pa_rope{size32(cos_sin, 1), layout};
@@ -284,6 +299,140 @@ PyObject* prefill(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
+// q, k, v, positions, cos_sin, slot_mapping, cache, layout, q_out, stream
+PyObject* rope_store_int4(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&] {
+    Args a(args, n, 10);
+    const at::Tensor& q = a.tensor(0, "q", kBf16);
+    const at::Tensor& k = a.tensor(1, "k", kBf16);
+    const at::Tensor& v = a.tensor(2, "v", kBf16);
+    const at::Tensor& pos = a.tensor(3, "positions", kI32);
+    const at::Tensor& cs = a.tensor(4, "cos_sin", kF32);
+    const at::Tensor& slots = a.tensor(5, "slot_mapping", kI64);
+    const Cache4 c(a, 6);
+    const pa_rope rope = rope_of(cs, a.integer(7));
+    const at::Tensor& out = a.tensor(8, "q_out", kBf16);
+    const pa_dims d = c.dims(q);
+    const int T = size32(q, 0);
+    require(is(k, {T, c.kv_heads, 128}) && k.sizes() == v.sizes(), "k and v must be [rows of q, num_kv_heads, 128]");
+    require(out.sizes() == q.sizes(), "q_out must have the shape of q");
+    require(is(pos, {T}) && is(slots, {T}), "positions and slot_mapping must be [rows of q]");
+    const int P = size32(cs, 0);
+    void* stream = a.stream(9);
+    return without_gil([&] {
+      return pa_rope_kv_store_int4(&d, &rope, T, q.data_ptr(), out.data_ptr(), k.data_ptr(), v.data_ptr(), ptr<int32_t>(pos),
+                                   ptr<float>(cs), P, ptr<int64_t>(slots), c.t.data_ptr(), c.num_blocks, stream);
+    });
+  });
+}
+
+// cache, row_start, first (or None), block_tables, max_rows, k_out, v_out, stream
+PyObject* read_kv_int4(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&] {
+    Args a(args, n, 8);
+    const Cache4 c(a, 0);
+    const at::Tensor& starts = a.tensor(1, "row_start", kI32);
+    require(starts.dim() == 1 && starts.size(0) >= 1, "row_start must be [num_seqs + 1]");
+    const int S = size32(starts, 0) - 1;
+    const int32_t* first = nullptr;
+    if (args[2] != Py_None) {
+      const at::Tensor& f = a.tensor(2, "first", kI32);
+      require(is(f, {S}), "first must be [num_seqs]");
+      first = ptr<int32_t>(f);
+    }
+    const at::Tensor& tables = a.tensor(3, "block_tables", kI32);
+    require(tables.dim() == 2 && tables.size(0) == S, "block_tables must be [num_seqs, max_blocks]");
+    const int max_rows = a.integer(4), max_blocks = size32(tables, 1);
+    const at::Tensor& k = a.tensor(5, "k_out", kBf16);
+    const at::Tensor& v = a.tensor(6, "v_out", kBf16);
+    require(k.dim() == 3 && k.size(1) == c.kv_heads && k.size(2) == 128 && k.sizes() == v.sizes(),
+            "k_out and v_out must be [rows, num_kv_heads, 128]");
+    const int rows = size32(k, 0);
+    const pa_dims d{c.kv_heads, c.kv_heads, 128, 16};
+    void* stream = a.stream(7);
+    return without_gil([&] {
+      return pa_read_kv_int4(&d, S, rows, ptr<int32_t>(starts), first, max_rows, c.t.data_ptr(), c.num_blocks,
+                             ptr<int32_t>(tables), max_blocks, k.data_ptr(), v.data_ptr(), stream);
+    });
+  });
+}
+
+// q, cache, block_tables, context_lens, max_context_len, scale, partition_tokens, workspace, out, stream
+PyObject* decode_int4(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&] {
+    Args a(args, n, 10);
+    const at::Tensor& q = a.tensor(0, "q", kBf16);
+    const Cache4 c(a, 1);
+    const pa_dims d = c.dims(q);
+    const int S = size32(q, 0);
+    const Batch b(a, 2, S);
+    const at::Tensor& ws = a.tensor(7, "workspace", kF32);
+    const at::Tensor& out = a.tensor(8, "out", kBf16);
+    require(out.sizes() == q.sizes(), "out must have the shape of q");
+    const int max_ctx = a.integer(4), P = a.integer(6);
+    const float sm = static_cast<float>(a.real(5));
+    void* stream = a.stream(9);
+    return without_gil([&] {
+      return pa_decode_int4(&d, S, q.data_ptr(), c.t.data_ptr(), c.num_blocks, ptr<int32_t>(b.tables), b.max_blocks,
+                            ptr<int32_t>(b.lens), max_ctx, sm, P, ws.data_ptr(), static_cast<size_t>(ws.numel()) * 4,
+                            out.data_ptr(), stream);
+    });
+  });
+}
+
+// q, k, v, cos_sin, cache, block_tables, context_lens, max_context_len, scale, layout, partition_tokens, workspace,
+// out, flags, stream
+PyObject* decode_step_int4(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&] {
+    Args a(args, n, 15);
+    const at::Tensor& q = a.tensor(0, "q", kBf16);
+    const at::Tensor& k = a.tensor(1, "k", kBf16);
+    const at::Tensor& v = a.tensor(2, "v", kBf16);
+    const at::Tensor& cs = a.tensor(3, "cos_sin", kF32);
+    const Cache4 c(a, 4);
+    const pa_dims d = c.dims(q);
+    const int S = size32(q, 0);
+    const Batch b(a, 5, S);
+    require(is(k, {S, c.kv_heads, 128}) && k.sizes() == v.sizes(), "k and v must be [num_seqs, num_kv_heads, 128]");
+    const pa_rope rope = rope_of(cs, a.integer(9));
+    const at::Tensor& ws = a.tensor(11, "workspace", kF32);
+    const at::Tensor& out = a.tensor(12, "out", kBf16);
+    require(out.sizes() == q.sizes(), "out must have the shape of q");
+    const int max_ctx = a.integer(7), P = a.integer(10), rows = size32(cs, 0);
+    const unsigned flags = static_cast<unsigned>(a.integer(13));
+    const float sm = static_cast<float>(a.real(8));
+    void* stream = a.stream(14);
+    return without_gil([&] {
+      return pa_decode_step_int4(&d, &rope, S, q.data_ptr(), k.data_ptr(), v.data_ptr(), ptr<float>(cs), rows, c.t.data_ptr(),
+                                 c.num_blocks, ptr<int32_t>(b.tables), b.max_blocks, ptr<int32_t>(b.lens), max_ctx, sm, P,
+                                 ws.data_ptr(), static_cast<size_t>(ws.numel()) * 4, out.data_ptr(), flags, stream);
+    });
+  });
+}
+
+// q, q_start, cache, block_tables, context_lens, max_query_len, max_context_len, scale, out, stream
+PyObject* prefill_int4(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&] {
+    Args a(args, n, 10);
+    const at::Tensor& q = a.tensor(0, "q", kBf16);
+    const at::Tensor& starts = a.tensor(1, "q_start", kI32);
+    const Cache4 c(a, 2);
+    const pa_dims d = c.dims(q);
+    require(starts.dim() == 1 && starts.size(0) >= 1, "q_start must be [num_seqs + 1]");
+    const int S = size32(starts, 0) - 1;
+    const Batch b(a, 3, S);
+    const at::Tensor& out = a.tensor(8, "out", kBf16);
+    require(out.sizes() == q.sizes(), "out must have the shape of q");
+    const int T = size32(q, 0), max_q = a.integer(5), max_ctx = a.integer(6);
+    const float sm = static_cast<float>(a.real(7));
+    void* stream = a.stream(9);
+    return without_gil([&] {
+      return pa_prefill_int4(&d, S, T, q.data_ptr(), ptr<int32_t>(starts), max_q, c.t.data_ptr(), c.num_blocks,
+                             ptr<int32_t>(b.tables), b.max_blocks, ptr<int32_t>(b.lens), max_ctx, sm, out.data_ptr(), stream);
+    });
+  });
+}
+
 // cached_lens, new_lens, block_tables, free_blocks, num_free, num_free_out, num_blocks, num_tokens, context_lens,
 // q_start, positions, slot_mapping, granted, stream
 PyObject* plan_step(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -328,6 +477,11 @@ PyMethodDef kMethods[] = {PA_FAST("rope_table", rope_table),
                           PA_FAST("decode_step_fp8_block", decode_step),
                           PA_FAST("prefill_fp8_block", prefill),
                           PA_FAST("plan_step", plan_step),
+                          PA_FAST("rope_kv_store_int4", rope_store_int4),
+                          PA_FAST("read_kv_int4", read_kv_int4),
+                          PA_FAST("decode_int4", decode_int4),
+                          PA_FAST("decode_step_int4", decode_step_int4),
+                          PA_FAST("prefill_int4", prefill_int4),
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_pa_torch", "Native half of binding.py.", -1, kMethods,
                        nullptr,               nullptr,     nullptr,                      nullptr};
