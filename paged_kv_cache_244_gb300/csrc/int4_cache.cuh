@@ -33,32 +33,33 @@ __device__ __forceinline__ int int4_v_word(int t, int ch) {
 }
 
 // ---- quantisation --------------------------------------------------------------------------
-// Of a set of values: the largest, and the largest of the negated ones, as bf16 magnitudes in the
-// halves of a word (at least 0; infinities do not count; 0x7fc0 in both where there is a NaN).
-// Sets join by __vmaxu2.
-__device__ __forceinline__ uint32_t int4_extremes(uint4 w) {
-  uint32_t nan = 0;
-  const uint32_t top = __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
-  if (__vcmpgeu2(top, 0x7f807f80u)) {
-    nan = __vcmpgtu2(top, 0x7f807f80u) ? 0x7fc07fc0u : 0u;
-    w.x &= __vcmpltu2(w.x & 0x7fff7fffu, 0x7f807f80u);
-    w.y &= __vcmpltu2(w.y & 0x7fff7fffu, 0x7f807f80u);
-    w.z &= __vcmpltu2(w.z & 0x7fff7fffu, 0x7f807f80u);
-    w.w &= __vcmpltu2(w.w & 0x7fff7fffu, 0x7f807f80u);
-  }
+// Of a set of values: the largest, and the largest of the negated ones, as bf16 magnitudes in the low and high
+// half of a word (at least 0; infinities do not count; 0x7fc0 in both where there is a NaN).  Sets join by
+// __vmaxu2.  `wild` is set where there was an infinity or a NaN.
+__device__ __forceinline__ uint32_t int4_extremes(uint4 w, bool& wild) {
   // as signed 16-bit integers positive values order as they are and stand above all negative ones, which
   // order the other way round: unsigned maxima find the smallest value, if one is negative
-  const uint32_t hi = __vmaxs2(__vmaxs2(w.x, w.y), __vmaxs2(w.z, w.w));
-  const uint32_t lo = __vmaxu2(__vmaxu2(w.x, w.y), __vmaxu2(w.z, w.w));
-  const uint32_t high = __vmaxs2(__byte_perm(hi, hi, 0x1032), hi), low = __vmaxu2(__byte_perm(lo, lo, 0x1032), lo);
-  const uint32_t p = (high & 0x8000u) ? 0u : high & 0x7fffu, n = (low & 0x8000u) ? low & 0x7fffu : 0u;
-  return __vmaxu2(p | (n << 16), nan);
+  auto join = [](uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    const uint32_t hi = __vmaxs2(__vmaxs2(a, b), __vmaxs2(c, d)), lo = __vmaxu2(__vmaxu2(a, b), __vmaxu2(c, d));
+    // (largest, smallest) of the low halves and of the high ones, joined
+    const uint32_t e = __vmaxs2(__byte_perm(hi, lo ^ 0x80008000u, 0x5410), __byte_perm(hi, lo ^ 0x80008000u, 0x7632));
+    return __vmaxs2(e, 0u);
+  };
+  uint32_t e = join(w.x, w.y, w.z, w.w);
+  if (__vcmpgeu2(e, 0x7f807f80u)) {                 // an infinity or a NaN
+    auto finite = [](uint32_t x) { return x & __vcmpltu2(x & 0x7fff7fffu, 0x7f807f80u); };
+    const bool nan = __vcmpgtu2(e, 0x7f807f80u) != 0;
+    wild = true;
+    e = nan ? 0x7fc07fc0u : join(finite(w.x), finite(w.y), finite(w.z), finite(w.w));
+  }
+  return e;
 }
 
 struct Int4Scale {
   float inv;       // 1 / s, 2^-20 of it larger
   float origin;    // 2^23 + 2^22 + z
   uint32_t word;
+  bool wild;       // the range is more than 15 s
 };
 
 // The smallest s of four significant bits with 15 s >= hi - lo (rounded to fp32), in [2^-40, 2^40], and
@@ -76,30 +77,39 @@ __device__ __forceinline__ Int4Scale int4_scale(uint32_t extremes) {
   q.inv = rcp_ftz(scale) * (1.f + 0x1p-20f);
   q.origin = fmaf(fminf(neg * q.inv, 15.f), 1.f, 12582912.f);
   q.word = (__float_as_uint(scale) >> 16) | (__float_as_uint(q.origin) & 15u);
+  q.wild = !(range <= 0x1p43f);
   if ((extremes & 0xffffu) == 0x7fc0u) q.word = 0x7fc0u;
   return q;
 }
 
 // The code of x (in the low four bits of the result, whose others are those of 2^23 + 2^22): the sum
-// rounds the quotient to an integer.
+// rounds the quotient to an integer.  Within a range that s covers it is at least 0, as round(lo / s) = -z, and may
+// be 16 where both ends round up; `wild`: no such range.
+template <bool kWild>
 __device__ __forceinline__ uint32_t int4_code(float x, const Int4Scale& q) {
-  return __float_as_uint(fminf(fmaxf(fmaf(x, q.inv, q.origin), 12582912.f), 12582927.f));
+  float c = fmaf(x, q.inv, q.origin);
+  if (kWild) c = fmaxf(c, 12582912.f);
+  return __float_as_uint(fminf(c, 12582927.f));
 }
 
 // Codes of eight neighbouring dims (four bf16 pairs) as a word.
-__device__ __forceinline__ uint32_t int4_word(uint4 w, const Int4Scale& q) {
+template <bool kWild>
+__device__ __forceinline__ uint32_t int4_word_of(uint4 w, const Int4Scale& q) {
   // each shift by four moves the upper bits of 12582912 along; what they add up to is taken off
   constexpr uint32_t kBase = 0x4b400000u;
   constexpr uint32_t kSum = kBase * 0x11111111u;
-  uint32_t r = int4_code(bf16hi(w.w), q);
-  r = r * 16 + int4_code(bf16hi(w.z), q);
-  r = r * 16 + int4_code(bf16hi(w.y), q);
-  r = r * 16 + int4_code(bf16hi(w.x), q);
-  r = r * 16 + int4_code(bf16lo(w.w), q);
-  r = r * 16 + int4_code(bf16lo(w.z), q);
-  r = r * 16 + int4_code(bf16lo(w.y), q);
-  r = r * 16 + int4_code(bf16lo(w.x), q);
+  uint32_t r = int4_code<kWild>(bf16hi(w.w), q);
+  r = r * 16 + int4_code<kWild>(bf16hi(w.z), q);
+  r = r * 16 + int4_code<kWild>(bf16hi(w.y), q);
+  r = r * 16 + int4_code<kWild>(bf16hi(w.x), q);
+  r = r * 16 + int4_code<kWild>(bf16lo(w.w), q);
+  r = r * 16 + int4_code<kWild>(bf16lo(w.z), q);
+  r = r * 16 + int4_code<kWild>(bf16lo(w.y), q);
+  r = r * 16 + int4_code<kWild>(bf16lo(w.x), q);
   return r - kSum;
+}
+__device__ __forceinline__ uint32_t int4_word(uint4 w, const Int4Scale& q, bool wild) {
+  return wild || q.wild ? int4_word_of<true>(w, q) : int4_word_of<false>(w, q);
 }
 
 // ---- reading -------------------------------------------------------------------------------
@@ -133,25 +143,52 @@ __device__ __forceinline__ uint4 int4_elements(uint32_t w, uint32_t s2, uint32_t
 }
 
 // ---- rotation ------------------------------------------------------------------------------
-// x c - y s rounded to fp32 and to bf16, for a bf16 pair and fp32 cos and sin: diff_of_products is
-// within two ulps, so only a value within four of a border of the bf16 rounding is formed again in 64
-// bits, where the products are exact.  A code then never depends on how the products were formed.
-__device__ __forceinline__ float turned(float a, float b, float c, float d) {
-  float r = diff_of_products(a, b, c, d);
-  if (((__float_as_uint(r) + 0x8004u) & 0xffffu) <= 8u)
-    r = __double2float_rn(static_cast<double>(a) * b - static_cast<double>(c) * d);
-  return r;
+// a b - c d rounded to fp32, as if from its exact value: the products and their difference, each with what its
+// rounding left (Knuth's sum: s + t is p - q).
+__device__ __forceinline__ float exact_difference(float a, float b, float c, float d) {
+  const float p = __fmul_rn(a, b), q = __fmul_rn(c, d);
+  const float rest = __fsub_rn(__fmaf_rn(a, b, -p), __fmaf_rn(c, d, -q));
+  const float s = __fsub_rn(p, q), back = __fsub_rn(s, p);
+  const float t = __fsub_rn(__fsub_rn(p, __fsub_rn(s, back)), __fadd_rn(q, back));
+  return __fadd_rn(s, __fadd_rn(t, rest));
 }
-__device__ __forceinline__ void int4_rotate_pairs(uint32_t& lo, uint32_t& hi, float2 c, float2 s) {
+
+// A row that is quantised is rotated as if exactly, rounded to fp32 and then to bf16: a code never depends on how the
+// products were formed.  rope_rotate_pairs is within two ulps of fp32, so it does wherever no value lies within four
+// of a border of the bf16 rounding; `border` collects how near the values came (the halves of a word, at most 8 where
+// one did), and where it says so the values are formed again by int4_rotate_exactly.
+// (Again in 64 bits, value by value: 320 us for a 16,384-row store; value by value in fp32: 100 us.)
+__device__ __forceinline__ uint32_t round_pair(float a, float b, uint32_t& border) {
+  border = __viaddmin_u16x2(__byte_perm(__float_as_uint(a), __float_as_uint(b), 0x5410), 0x80048004u, border);
+  return pack_bf16x2(a, b);
+}
+__device__ __forceinline__ bool at_border(uint32_t border) { return min(border & 0xffffu, border >> 16) <= 8u; }
+
+__device__ __forceinline__ void int4_rotate_pairs(uint32_t& lo, uint32_t& hi, float2 c, float2 s, uint32_t& border) {
   const float x0 = bf16lo(lo), x1 = bf16hi(lo), y0 = bf16lo(hi), y1 = bf16hi(hi);
-  lo = pack_bf16x2(turned(x0, c.x, y0, s.x), turned(x1, c.y, y1, s.y));
-  hi = pack_bf16x2(turned(y0, c.x, -x0, s.x), turned(y1, c.y, -x1, s.y));
+  lo = round_pair(diff_of_products(x0, c.x, y0, s.x), diff_of_products(x1, c.y, y1, s.y), border);
+  hi = round_pair(diff_of_products(y0, c.x, -x0, s.x), diff_of_products(y1, c.y, -x1, s.y), border);
 }
-__device__ __forceinline__ void int4_rotate_interleaved(uint32_t& w0, uint32_t& w1, float2 c, float2 s) {
-  uint32_t lo = __byte_perm(w0, w1, 0x5410), hi = __byte_perm(w0, w1, 0x7632);
-  int4_rotate_pairs(lo, hi, c, s);
-  w0 = __byte_perm(lo, hi, 0x5410);
-  w1 = __byte_perm(lo, hi, 0x7632);
+__device__ __forceinline__ void int4_rotate_exactly(uint32_t& lo, uint32_t& hi, float2 c, float2 s) {
+  const float x0 = bf16lo(lo), x1 = bf16hi(lo), y0 = bf16lo(hi), y1 = bf16hi(hi);
+  lo = pack_bf16x2(exact_difference(x0, c.x, y0, s.x), exact_difference(x1, c.y, y1, s.y));
+  hi = pack_bf16x2(exact_difference(y0, c.x, -x0, s.x), exact_difference(y1, c.y, -x1, s.y));
+}
+
+// Two adjacent pairs, halves apart (kInterleaved: (x0, y0), (x1, y1)), by the first form and where it asks for it by
+// the second.
+template <bool kInterleaved>
+__device__ __forceinline__ void int4_rotate(uint32_t& w0, uint32_t& w1, float2 c, float2 s) {
+  uint32_t lo = kInterleaved ? __byte_perm(w0, w1, 0x5410) : w0, hi = kInterleaved ? __byte_perm(w0, w1, 0x7632) : w1;
+  uint32_t border = 0xffffffffu, a = lo, b = hi;
+  int4_rotate_pairs(a, b, c, s, border);
+  if (at_border(border)) {
+    a = lo;
+    b = hi;
+    int4_rotate_exactly(a, b, c, s);
+  }
+  w0 = kInterleaved ? __byte_perm(a, b, 0x5410) : a;
+  w1 = kInterleaved ? __byte_perm(a, b, 0x7632) : b;
 }
 
 }  // namespace pa

@@ -19,27 +19,47 @@ constexpr int kStoreWarps = 8;
 
 template <bool kInterleaved>
 __device__ __forceinline__ void int4_rotate_chunks(uint4& x, uint4& y, const Angles& a) {
-  const float2 c0 = make_float2(a.c0.x, a.c0.y), c1 = make_float2(a.c0.z, a.c0.w);
-  const float2 c2 = make_float2(a.c1.x, a.c1.y), c3 = make_float2(a.c1.z, a.c1.w);
-  const float2 s0 = make_float2(a.s0.x, a.s0.y), s1 = make_float2(a.s0.z, a.s0.w);
-  const float2 s2 = make_float2(a.s1.x, a.s1.y), s3 = make_float2(a.s1.z, a.s1.w);
+  const float2 c[4] = {{a.c0.x, a.c0.y}, {a.c0.z, a.c0.w}, {a.c1.x, a.c1.y}, {a.c1.z, a.c1.w}};
+  const float2 s[4] = {{a.s0.x, a.s0.y}, {a.s0.z, a.s0.w}, {a.s1.x, a.s1.y}, {a.s1.z, a.s1.w}};
+  uint32_t lo[4] = {x.x, x.y, x.z, x.w}, hi[4] = {y.x, y.y, y.z, y.w};
   if constexpr (kInterleaved) {
-    int4_rotate_interleaved(x.x, x.y, c0, s0);
-    int4_rotate_interleaved(x.z, x.w, c1, s1);
-    int4_rotate_interleaved(y.x, y.y, c2, s2);
-    int4_rotate_interleaved(y.z, y.w, c3, s3);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {                   // word pairs (x.x, x.y), (x.z, x.w), (y.x, y.y), (y.z, y.w)
+      const uint32_t u = i == 0 ? x.x : i == 1 ? x.z : i == 2 ? y.x : y.z, v = i == 0 ? x.y : i == 1 ? x.w : i == 2 ? y.y : y.w;
+      lo[i] = __byte_perm(u, v, 0x5410);
+      hi[i] = __byte_perm(u, v, 0x7632);
+    }
+  }
+  uint32_t p[4], q[4], border = 0xffffffffu;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    p[i] = lo[i];
+    q[i] = hi[i];
+    int4_rotate_pairs(p[i], q[i], c[i], s[i], border);
+  }
+  if (at_border(border)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      p[i] = lo[i];
+      q[i] = hi[i];
+      int4_rotate_exactly(p[i], q[i], c[i], s[i]);
+    }
+  }
+  if constexpr (kInterleaved) {
+    x = make_uint4(__byte_perm(p[0], q[0], 0x5410), __byte_perm(p[0], q[0], 0x7632), __byte_perm(p[1], q[1], 0x5410),
+                   __byte_perm(p[1], q[1], 0x7632));
+    y = make_uint4(__byte_perm(p[2], q[2], 0x5410), __byte_perm(p[2], q[2], 0x7632), __byte_perm(p[3], q[3], 0x5410),
+                   __byte_perm(p[3], q[3], 0x7632));
   } else {
-    int4_rotate_pairs(x.x, y.x, c0, s0);
-    int4_rotate_pairs(x.y, y.y, c1, s1);
-    int4_rotate_pairs(x.z, y.z, c2, s2);
-    int4_rotate_pairs(x.w, y.w, c3, s3);
+    x = make_uint4(p[0], p[1], p[2], p[3]);
+    y = make_uint4(q[0], q[1], q[2], q[3]);
   }
 }
 
 // One warp, one token: its groups of 4 kGroup head vectors part, part + parts, ..: queries rotated into
 // q_out, keys (rotated) and values quantised into the token's slot.
 template <bool kInterleaved, int kGroup>
-__global__ void __launch_bounds__(kStoreWarps * 32) rope_int4_store_kernel(const RopeFormArgs a) {
+__global__ void __launch_bounds__(kStoreWarps * 32, 3) rope_int4_store_kernel(const RopeFormArgs a) {
   __shared__ uint4 s_extremes[kStoreWarps][4][4];   // of a pass's vectors, a word for each 8 dims
   pdl_wait_prior_grid();
   pdl_allow_next_grid();
@@ -104,7 +124,8 @@ __global__ void __launch_bounds__(kStoreWarps * 32) rope_int4_store_kernel(const
       const bool is_k = i < Hq + Hkv, mine = i >= Hq && i < all;
       if (turns && mine && is_k) int4_rotate_chunks<kInterleaved>(x[p], y[p], ang);
       __syncwarp();
-      uint32_t ex = int4_extremes(x[p]), ey = int4_extremes(y[p]);
+      bool wild = false;
+      uint32_t ex = int4_extremes(x[p], wild), ey = int4_extremes(y[p], wild);
       uint32_t* const words = reinterpret_cast<uint32_t*>(s_extremes[warp][sub]);
       words[ca] = ex;
       words[cb] = ey;
@@ -125,7 +146,7 @@ __global__ void __launch_bounds__(kStoreWarps * 32) rope_int4_store_kernel(const
       const Int4Scale qa = int4_scale(ex);
       const Int4Scale qb = is_k ? int4_scale(ey) : qa;
       uint8_t* const rec = records + static_cast<size_t>(is_k ? i - Hq : i - Hq - Hkv) * kInt4Record;
-      const uint32_t wa = int4_word(x[p], qa), wb = int4_word(y[p], qb);
+      const uint32_t wa = int4_word(x[p], qa, wild), wb = int4_word(y[p], qb, wild);
       if (is_k) {
         *reinterpret_cast<uint32_t*>(rec + int4_k_word(off, ca)) = wa;
         *reinterpret_cast<uint32_t*>(rec + int4_k_word(off, cb)) = wb;

@@ -6,8 +6,8 @@
 // 极简实现与大模型推理流程解析", §学习要点 (4-bit quantisation of the cache).
 //
 // The work is cut as in the other decode kernels (pa_device.cuh): one axis of (sequence, KV head, block),
-// an equal contiguous range for each warp of a persistent grid, each warp its own producer and consumer,
-// pieces of split segments merged by a kernel after it.  The mathematics, with K element (t, d) =
+// an equal contiguous range for each warp of a persistent grid, pieces of split segments merged by a kernel
+// after it.  The mathematics, with K element (t, d) =
 // s_tg (c_td - z_tg) for d in group g of 32 dims, V element s_t (c_td - z_t), and head column h:
 //
 //   score   x_th = sum_g s_tg sum_{d in g} q_hd c_td - sum_g s_tg z_tg Q_hg,   Q_hg = sum_{d in g} q_hd
@@ -28,8 +28,12 @@
 // V's scale acts on the exponent and cancels in L, so p stays within f16 whatever the scales: the shift m is
 // set 7 below the largest contribution and moves when one passes it by more than 15.  L adds the unrounded p.
 //
-// A job is up to four neighbouring blocks of a piece, 8.6 KiB in one stage of the warp's ring, brought in by
-// cp.async, one commit group a job, with q of a piece's first job and the step's rows.
+// A job is up to two neighbouring blocks of a piece in one stage of the warp's ring.  A record is one run of memory, so
+// each of a stage's few runs (two records, q of a piece's first job, the step's rows) is one bulk copy.  Where 16
+// tokens are 2.2 KB, what a job costs whatever its size counts as much as its products: walking the range, table
+// look-ups, flags and copies took a warp 120 instructions a block, of 366 in all.  So one warp of the CTA
+// does it for all the others, a lane for each: a pass of its loop emits the next job of every consumer that has a
+// free stage.
 
 #include <mutex>
 
@@ -39,21 +43,27 @@
 namespace pa {
 namespace {
 
-constexpr int kDiWarps = 12;                         // of a CTA at most (registers)
-constexpr int kDiJob = 4;                            // blocks of a job at most
-constexpr int kDiQOff = kDiJob * kInt4Record;
-// A stage: records, q rows of G heads, and for the step cos/sin (R <= 128 floats), k and v.
+constexpr int kDiConsumers = 11;                     // warps of a CTA that have ranges, at most; one more feeds them
+constexpr int kDiJob = 2;                            // blocks of a job at most
+// A stage: its job's descriptor, records, q rows of G heads, and for the step cos/sin (R <= 128 floats), k and v.
+constexpr int kDiRecOff = 32;
+constexpr int kDiQOff = kDiRecOff + kDiJob * kInt4Record;
 __host__ __device__ inline int di_stage(int G, bool step) {
   return kDiQOff + G * kHeadDim * 2 + (step ? kHeadDim * 4 + 2 * kHeadDim * 2 : 0);
 }
-constexpr int kDiMaxStages = 32;                     // of a CTA
-constexpr int kDiMaxRing = 8;                        // of a warp
+constexpr int kDiMaxRing = 8;                        // stages of a warp
 constexpr int kDiSmemMax = 226 * 1024;               // beside the static part of build_prefix
-constexpr int kDiPrefixOff = kDiMaxStages * 16;      // after the jobs' descriptors
+// Shared memory: per consumer and stage a barrier that the copies complete and one that the consumer does, a word set
+// when a wait has run out, the prefix, the stages.
+constexpr int kDiBarOff = 0;
+constexpr int kDiFailOff = kDiConsumers * kDiMaxRing * 16;
+constexpr int kDiPrefixOff = kDiFailOff + 16;
 
-// Fields of a job's flag word: kFirst .. kGap, rows of the last block at bits 8-12, blocks (1 .. 4) at 16-18,
-// which of them are there at 20-23.
-constexpr int kBlocksAt = 16, kHereAt = 20;
+// More job flags: two blocks, and which of them are there (valid tokens of the last one at bits 8-12).
+constexpr uint32_t kTwo = 1u << 13, kHas0 = 1u << 14, kHas1 = 1u << 15;
+
+// A shift below every score (they are finite, and below 2^123): weights of no key so far are 0, not NaN.
+constexpr float kNoShift = -3.402823466e38f;
 
 // Pairs of codes as f16: of a word's neighbouring pairs shifted by 3, the first c 2^-21 and the second c 2^-17.
 constexpr uint32_t kPairA = 0x00780078u, kPairB = 0x07800780u;
@@ -78,14 +88,36 @@ __device__ __forceinline__ uint32_t lds16(uint32_t addr) {
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
   return v;
 }
+// Whether phase `parity` of the barrier is over, without waiting.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
 __device__ __forceinline__ float lg2(float x) {
   float y;
-  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
+// D = A B of f16 (bf16) operands: the accumulator begins at zero.
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void mma_bf16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 template <bool kStep>
-__global__ void __launch_bounds__(kDiWarps * 32, 1) decode_int4_kernel(const DecodeArgs a, const int pool) {
+__global__ void __launch_bounds__((kDiConsumers + 1) * 32, 1) decode_int4_kernel(const DecodeArgs a, const int pool) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -102,149 +134,152 @@ __global__ void __launch_bounds__(kDiWarps * 32, 1) decode_int4_kernel(const Dec
   const int S = a.num_seqs;
   const int Hkv = a.num_kv_heads;
   const int G = a.num_q_heads / Hkv;
-  const int warps = static_cast<int>(blockDim.x >> 5);
+  const int warps = static_cast<int>(blockDim.x >> 5) - 1;   // consumers
   const int stage_bytes = di_stage(G, kStep);
   const int cos_off = kDiQOff + G * kHeadDim * 2;    // (step)
-  build_prefix<kDiWarps>(a, prefix, last_rows, blockDim.x);
+  for (int i = threadIdx.x; i < warps * kDiMaxRing * 2; i += blockDim.x) mbar_init(raw + kDiBarOff + 8 * i, 1);
+  volatile int* const fail = reinterpret_cast<volatile int*>(smem_raw + kDiFailOff);
+  if (threadIdx.x == 0) *fail = 0;
+  fence_mbar_init();
+  build_prefix<kDiConsumers + 1>(a, prefix, last_rows, blockDim.x);   // (a barrier of the CTA behind the above)
   const long long T = static_cast<long long>(Hkv) * prefix[S];
   const Ranges R = make_ranges(T, a);
-  // Range v goes to warp v / grid of CTA v % grid; the CTA's stages are shared out among its warps
+  // Range v goes to consumer v / grid of CTA v % grid; the CTA's stages are shared out among its consumers
   // that have a range, the first of them taking one more where they do not divide.
-  const int my_v = static_cast<int>(blockIdx.x) + warp * static_cast<int>(gridDim.x);
-  if (my_v >= R.V) {
+  const int active = min(warps, max(0, (R.V - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) /
+                                           static_cast<int>(gridDim.x)));
+  const int who = warp < warps ? warp : lane;        // consumer: this warp, or the one that this lane feeds
+  if (active == 0 || (warp < warps && warp >= active)) {
     if (early) pdl_wait_prior_grid();
     return;
   }
-  const int active = min(warps, (R.V - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) /
-                                       static_cast<int>(gridDim.x));
-  const int share = pool / active + (warp < pool % active ? 1 : 0);
-  const int st0 = warp * (pool / active) + min(warp, pool % active);
-  const int n_st = min(share, kDiMaxRing);
-  int4* descs = reinterpret_cast<int4*>(smem_raw) + st0;
-  const uint32_t tiles = tile_base + st0 * stage_bytes;
+  const int my_v = static_cast<int>(blockIdx.x) + who * static_cast<int>(gridDim.x);
+  const int n_st = min(pool / active + (who < pool % active ? 1 : 0), kDiMaxRing);
+  const uint32_t ring = tile_base + (who * (pool / active) + min(who, pool % active)) * stage_bytes;
+  const uint32_t ring_end = ring + n_st * stage_bytes;
+  const uint32_t full_bars = raw + kDiBarOff + who * kDiMaxRing * 16;   // the stage's other barrier 8 bytes behind
+
+  if (warp == warps) {
+    // ---------------------------------------------------------------- feeder ----------
+    const uint8_t* const cache = reinterpret_cast<const uint8_t*>(a.k_cache);
+    const bool mine = lane < active;
+    const long long x0 = mine ? R.begin(my_v) : 0;
+    const int len = mine ? static_cast<int>(R.begin(my_v + 1) - x0) : 0;
+    // The next job: block `rel` of the range is block j of ns of (sequence s, KV head g).
+    int rel = 0, s = 0, g = 0, j = 0, ns = 1, id0 = -1, id1 = -1;
+    uint32_t fl = 0;
+    const int chunk = a.chunk_blocks;
+    // flags of the job at hand, its block ids asked for
+    auto look = [&] {
+      const int part = chunk ? j / chunk : 0;
+      const bool p_first = chunk && j == part * chunk;
+      auto ends = [&](int d) { return rel + d == len - 1 || j + d == ns - 1 || (chunk && j + d == part * chunk + chunk - 1); };
+      const bool two = !ends(0);                     // a piece ends at the range's end at the latest
+      const bool whole = rel >= j && rel - j + ns <= len && (chunk == 0 || ns <= chunk);
+      const bool tail = j + (two ? 1 : 0) == ns - 1; // the job reaches the sequence's last block
+      fl = ((rel == 0 || j == 0 || p_first) ? kFirst : 0u) | (ends(two ? 1 : 0) ? kLast : 0u) | (whole ? kWhole : 0u) |
+           ((rel == 0 && j > 0 && p_first) ? kGap : 0u) | (two ? kTwo : 0u) | (tail ? kNew : 0u);
+      fl |= static_cast<uint32_t>(tail ? last_rows[s] : kBlockSize) << 8;
+      const int32_t* ids = a.block_tables + static_cast<size_t>(s) * a.max_blocks + j;
+      id0 = ids[0];
+      if (two) id1 = ids[1];
+    };
+    if (mine) {
+      int lo = 0, hi = S;                            // largest s with Hkv * N_s <= x0
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (static_cast<long long>(Hkv) * prefix[mid] <= x0) lo = mid;
+        else hi = mid;
+      }
+      s = lo;
+      ns = prefix[s + 1] - prefix[s];
+      const int off = static_cast<int>(x0 - static_cast<long long>(Hkv) * prefix[s]);
+      g = off / ns;
+      j = off - g * ns;
+      look();
+    }
+    if (early) pdl_wait_prior_grid();
+    uint32_t at = ring, bar = full_bars, phase = 1;  // parity of the stage's last release
+    int fills = 0;
+    uint64_t since = 0;                              // of waiting with nothing to do
+    while (__any_sync(kFullMask, rel < len)) {
+      bool ready = rel < len;
+      if (ready && fills >= n_st) ready = mbar_test(bar + 8, phase);
+      if (!__any_sync(kFullMask, ready)) {
+        if (*fail) break;
+        const uint64_t now = global_ns();
+        if (since == 0) since = now;
+        if (__any_sync(kFullMask, now - since > kWaitLimitNs)) {
+          if (lane == 0) raise_flag(a.status, PA_FLAG_TIMEOUT);
+          break;
+        }
+        __nanosleep(32);
+        continue;
+      }
+      since = 0;
+      if (ready) {
+        const bool two = (fl & kTwo) != 0;
+        const bool here0 = id0 >= 0 && id0 < a.num_blocks, here1 = two && id1 >= 0 && id1 < a.num_blocks;
+        const int row0 = id0 * Hkv + g, row1 = id1 * Hkv + g;
+        const int seg = s * Hkv + g;
+        const int part = chunk ? j / chunk : 0;
+        // Fused step: a position without a cos/sin row leaves the token out -- q unrotated, nothing stored.
+        const int pos = (ns - 1) * kBlockSize + last_rows[s] - 1;
+        const bool rope = kStep && pos < a.max_pos;
+        const bool fresh = rope && (fl & kNew) && (two ? here1 : here0);    // the new token's record is here
+        const bool turns = rope && ((fl & kFirst) || fresh);
+        if (kStep && (fl & kNew) && !rope) raise_flag(a.status, PA_FLAG_POSITION_OOB);
+        if (!here0 || (two && !here1)) raise_flag(a.status, PA_FLAG_BLOCK_ID_OOB);
+        const uint32_t flags = (fl & ~kNew) | (fresh ? kNew : 0u) | (rope ? kRope : 0u) | (here0 ? kHas0 : 0u) | (here1 ? kHas1 : 0u);
+        *reinterpret_cast<int4*>(smem_raw + (at - raw)) =
+            make_int4(seg, static_cast<int>(flags), static_cast<int>(piece_slot(my_v, seg, part, a.max_parts)), two ? row1 : row0);
+        uint32_t bytes = (static_cast<uint32_t>(here0) + static_cast<uint32_t>(here1)) * kInt4Record;
+        if (fl & kFirst) bytes += G * kHeadDim * 2;
+        if (kStep) bytes += (turns ? a.rotary_dim * 4 : 0) + (fresh ? 2 * kHeadDim * 2 : 0);
+        if (bytes) mbar_arrive_expect_tx(bar, bytes);
+        else mbar_arrive(bar);
+        if (fl & kFirst) bulk_copy_g2s(at + kDiQOff, a.q + static_cast<size_t>(seg) * G * kHeadDim, G * kHeadDim * 2, bar);
+        if (kStep && turns)
+          bulk_copy_g2s(at + cos_off, a.cos_sin + static_cast<size_t>(pos) * a.rotary_dim, a.rotary_dim * 4, bar);
+        if (kStep && fresh) {
+          bulk_copy_g2s(at + cos_off + kHeadDim * 4, a.k_new + static_cast<size_t>(seg) * kHeadDim, kHeadDim * 2, bar);
+          bulk_copy_g2s(at + cos_off + kHeadDim * 6, a.v_new + static_cast<size_t>(seg) * kHeadDim, kHeadDim * 2, bar);
+        }
+        if (here0) bulk_copy_g2s(at + kDiRecOff, cache + static_cast<size_t>(row0) * kInt4Record, kInt4Record, bar);
+        if (here1) bulk_copy_g2s(at + kDiRecOff + kInt4Record, cache + static_cast<size_t>(row1) * kInt4Record, kInt4Record, bar);
+        ++fills;
+        at += stage_bytes;
+        bar += 16;
+        if (at == ring_end) {
+          at = ring;
+          bar = full_bars;
+          phase ^= 1u;
+        }
+        rel += two ? 2 : 1;
+        j += two ? 2 : 1;
+        if (rel < len) {
+          if (j == ns) {
+            j = 0;
+            if (++g == Hkv) {
+              g = 0;
+              do ++s;
+              while (prefix[s + 1] == prefix[s]);    // blocks are left, so a later sequence has some
+              ns = prefix[s + 1] - prefix[s];
+            }
+          }
+          look();
+        }
+      }
+      __syncwarp();
+      if (__all_sync(kFullMask, fills >= n_st || rel >= len)) __nanosleep(20);
+    }
+    // let the copies still in flight land before the CTA exits (they have, in a normal run, but for the last ones)
+    for (int k = max(0, fills - n_st); k < fills; ++k) mbar_wait_bounded(full_bars + 16 * (k % n_st), (k / n_st) & 1);
+    return;
+  }
+  if (early) pdl_wait_prior_grid();
   const int gq = lane >> 2;  // fragment row group
   const int cq = lane & 3;   // fragment column pair
-  const long long x0 = R.begin(my_v), x1 = R.begin(my_v + 1);
-  const uint8_t* const cache = reinterpret_cast<const uint8_t*>(a.k_cache);
-
-  // ---- lookahead: window = up to 32 consecutive blocks of the range, lane j resolves block j ----
-  struct Window {
-    long long x;
-    int n;
-    int blk, seg, fl, slot, pos;
-  };
-  auto resolve = [&](Window& W) {
-    W.blk = -1;
-    W.seg = W.fl = W.slot = W.pos = 0;
-    if (lane >= W.n) return;
-    const long long p = W.x + lane;
-    int lo = 0, hi = S;                              // largest s with Hkv * N_s <= p
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (static_cast<long long>(Hkv) * prefix[mid] <= p) lo = mid;
-      else hi = mid;
-    }
-    const int s = lo;
-    const int ns = prefix[s + 1] - prefix[s];
-    const int off = static_cast<int>(p - static_cast<long long>(Hkv) * prefix[s]);
-    const int g = off / ns;
-    const int j = off - g * ns;
-    const long long Xi = static_cast<long long>(Hkv) * prefix[s] + static_cast<long long>(g) * ns;
-    W.blk = a.block_tables[static_cast<size_t>(s) * a.max_blocks + j];
-    W.seg = s * Hkv + g;
-    const int tail = last_rows[s];
-    const int valid = j == ns - 1 ? tail : kBlockSize;
-    const int chunk = a.chunk_blocks;
-    const int part = chunk ? j / chunk : 0;
-    const bool p_first = chunk && j == part * chunk;
-    const bool p_last = chunk && j == part * chunk + chunk - 1;
-    uint32_t flags = ((p == x0 || j == 0 || p_first) ? kFirst : 0u) |
-                     ((p == x1 - 1 || j == ns - 1 || p_last) ? kLast : 0u) |
-                     ((Xi >= x0 && Xi + ns <= x1 && (chunk == 0 || ns <= chunk)) ? kWhole : 0u) |
-                     ((p == x0 && j > 0 && p_first) ? kGap : 0u);
-    if (kStep) {
-      W.pos = (ns - 1) * kBlockSize + tail - 1;      // position of the sequence's new token
-      if (j == ns - 1) flags |= kNew;
-      if (W.pos < a.max_pos) flags |= kRope;
-    }
-    W.fl = static_cast<int>(flags | (static_cast<uint32_t>(valid) << 8) | (static_cast<uint32_t>(g) << 16));
-    W.slot = static_cast<int>(piece_slot(my_v, W.seg, part, a.max_parts));
-  };
-  auto next_of = [&](const Window& W, Window& N) {
-    N.x = W.x + W.n;
-    N.n = static_cast<int>(min(32ll, x1 - N.x));
-  };
-  Window cur, nxt;
-  cur.x = x0;
-  cur.n = static_cast<int>(min(32ll, x1 - x0));
-  resolve(cur);
-  next_of(cur, nxt);   // resolved behind the first jobs
-  bool nxt_there = false;
-  uint32_t lasts = __ballot_sync(kFullMask, (cur.fl & kLast) != 0);   // blocks of `cur` that end a piece
-  int pk = 0;  // next block of `cur`
-
-  // Emit the next job into stage st, as one commit group; false when the range is used up.
-  auto produce = [&](int st) -> bool {
-    if (pk == cur.n) {
-      if (nxt.n == 0) return false;
-      if (!nxt_there) resolve(nxt);
-      cur = nxt;
-      pk = 0;
-      next_of(cur, nxt);
-      resolve(nxt);
-      nxt_there = true;
-      lasts = __ballot_sync(kFullMask, (cur.fl & kLast) != 0);
-    }
-    const int to_last = __ffs(static_cast<int>(lasts >> pk));           // 0: none left in the window
-    const int nb = min(min(kDiJob, cur.n - pk), to_last ? to_last : kDiJob);
-    const int fl0 = __shfl_sync(kFullMask, cur.fl, pk);
-    const int fl1 = __shfl_sync(kFullMask, cur.fl, pk + nb - 1);
-    const int seg = __shfl_sync(kFullMask, cur.seg, pk);
-    const int slot = __shfl_sync(kFullMask, cur.slot, pk);
-    const int pos = kStep ? __shfl_sync(kFullMask, cur.pos, pk) : 0;
-    const int g = fl0 >> 16;
-    const bool ok = cur.blk >= 0 && cur.blk < a.num_blocks;
-    const uint32_t here = (__ballot_sync(kFullMask, ok) >> pk) & ((1u << nb) - 1);
-    const int row = ok ? cur.blk * Hkv + g : 0;      // record of this lane's block, if it is one of the job's
-    const int row_last = __shfl_sync(kFullMask, row, pk + nb - 1);
-    const uint32_t dst = tiles + st * stage_bytes;
-    // Fused step: a position without a cos/sin row leaves the token out -- q unrotated, nothing stored.
-    const bool rope = kStep && (fl0 & kRope);
-    const bool fresh = rope && (fl1 & kNew) && ((here >> (nb - 1)) & 1);    // the new token's record is here
-    if (fl0 & kFirst) {
-      const char* q = reinterpret_cast<const char*>(a.q + static_cast<size_t>(seg) * G * kHeadDim);
-      for (int c = lane; c < G * 16; c += 32) cp_async16(dst + kDiQOff + 16 * c, q + 16 * c);
-    }
-    if (kStep && rope && ((fl0 & kFirst) || fresh) && lane < a.rotary_dim / 4)
-      cp_async16(dst + cos_off + 16 * lane, a.cos_sin + static_cast<size_t>(pos) * a.rotary_dim + 4 * lane);
-    if (kStep && fresh) {
-      const __nv_bfloat16* src = (lane < 16 ? a.k_new : a.v_new) + static_cast<size_t>(seg) * kHeadDim;
-      cp_async16(dst + cos_off + kHeadDim * 4 + 16 * lane, src + 8 * (lane & 15));
-    }
-#pragma unroll
-    for (int b = 0; b < kDiJob; ++b) {
-      const int r = __shfl_sync(kFullMask, row, (pk + b) & 31);
-      if ((here >> b) & 1) {
-        const uint8_t* src = cache + static_cast<size_t>(r) * kInt4Record + lane * 16;
-        const uint32_t to = dst + b * kInt4Record + lane * 16;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) cp_async16(to + 512 * i, src + 512 * i);
-        if (lane < (kInt4Record - 2048) / 16) cp_async16(to + 2048, src + 2048);
-      }
-    }
-    cp_async_commit();
-    pk += nb;
-    if (lane == 0) {
-      if (here != (1u << nb) - 1) raise_flag(a.status, PA_FLAG_BLOCK_ID_OOB);
-      if (kStep && (fl1 & kNew) && !rope) raise_flag(a.status, PA_FLAG_POSITION_OOB);
-      // flags of the job: the first block's kFirst and kGap, the last one's kLast, kNew and rows
-      const uint32_t fl = (static_cast<uint32_t>(fl0) & (kFirst | kGap | kWhole | kRope)) |
-                          (static_cast<uint32_t>(fl1) & (kLast | 0x1f00u)) | (fresh ? kNew : 0u) |
-                          (static_cast<uint32_t>(nb) << kBlocksAt) | (here << kHereAt);
-      descs[st] = make_int4(seg, static_cast<int>(fl), slot, row_last);
-    }
-    return true;
-  };
 
   // ---------------------------------------------------------------- consumer state --
   // V rows of this lane's ldmatrix addresses: token r + 8 (i & 1), 16-byte unit u of its row at u ^ (r / 2 % 4)
@@ -254,7 +289,7 @@ __global__ void __launch_bounds__(kDiWarps * 32, 1) decode_int4_kernel(const Dec
   uint32_t qb[8][2];                      // B operand: dims 32c + 8cq .. + 7 of head gq, k permuted as the codes are
   uint32_t qsum[2];                       // B operand: -Q of group cq of head gq as three bf16 numbers
   float kf0 = 0.f, kf1 = 0.f;             // what turns x of head columns 2cq, 2cq + 1 into the exponent
-  float m0 = -INFINITY, m1 = -INFINITY;   // softmax shifts of those columns
+  float m0 = kNoShift, m1 = kNoShift;     // softmax shifts of those columns
   float l0 = 0.f, l1 = 0.f;               // this lane's share of L
   float o[8][4];                          // sums of p c: [2u + i] = rows gq, gq + 8: code pairs 2i, 2i + 1 of unit u
   float z[4];                             // sums of p z (two and two alike)
@@ -272,8 +307,8 @@ __global__ void __launch_bounds__(kDiWarps * 32, 1) decode_int4_kernel(const Dec
       uint32_t kx = kn[wa], ky = kn[wb];
       const float2 co = reinterpret_cast<const float2*>(cs)[lane];
       const float2 si = reinterpret_cast<const float2*>(cs + rot / 2)[lane];
-      if (a.interleaved) int4_rotate_interleaved(kx, ky, co, si);
-      else int4_rotate_pairs(kx, ky, co, si);
+      if (a.interleaved) int4_rotate<true>(kx, ky, co, si);
+      else int4_rotate<false>(kx, ky, co, si);
       kn[wa] = kx;
       kn[wb] = ky;
     }
@@ -282,14 +317,15 @@ __global__ void __launch_bounds__(kDiWarps * 32, 1) decode_int4_kernel(const Dec
     const int ch = lane & 15;
     const bool is_k = lane < 16;
     const uint4 w = reinterpret_cast<const uint4*>(kn)[lane];
-    uint32_t e = int4_extremes(w);
+    bool wild = false;
+    uint32_t e = int4_extremes(w, wild);
 #pragma unroll
     for (int x = 1; x < 16; x <<= 1) {
       const uint32_t other = __shfl_xor_sync(kFullMask, e, x);
       if (x < 4 || !is_k) e = __vmaxu2(e, other);
     }
     const Int4Scale qs = int4_scale(e);
-    const uint32_t code = int4_word(w, qs);
+    const uint32_t code = int4_word(w, qs, wild);
     uint8_t* const dst = reinterpret_cast<uint8_t*>(a.k_store) + static_cast<size_t>(tile_row) * kInt4Record;
     const int at = is_k ? int4_k_word(row, ch) : int4_v_word(row, ch);
     *reinterpret_cast<uint32_t*>(rec + at) = code;
@@ -401,14 +437,14 @@ __global__ void __launch_bounds__(kDiWarps * 32, 1) decode_int4_kernel(const Dec
     kf1 = __shfl_sync(kFullMask, fold, 8 * cq + 4);
   };
 
-  auto consume = [&](int st) {
-    const int4 d = descs[st];
+  auto consume = [&](uint32_t at) -> int {
+    unsigned char* const stage = smem_raw + (at - raw);
+    const int4 d = *reinterpret_cast<const int4*>(stage);
     const uint32_t fl = static_cast<uint32_t>(d.y);
-    const uint32_t kt = tiles + st * stage_bytes;
-    unsigned char* const stage = smem_raw + (kt - raw);
+    const uint32_t kt = at + kDiRecOff;
     if (fl & kFirst) {
       load_q(stage, fl);
-      m0 = m1 = -INFINITY;
+      m0 = m1 = kNoShift;
       l0 = l1 = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
@@ -416,37 +452,31 @@ __global__ void __launch_bounds__(kDiWarps * 32, 1) decode_int4_kernel(const Dec
       if ((fl & kGap) && lane < G)                   // mark the skipped slot before this piece empty
         a.ws_ml[(static_cast<size_t>(d.z) - 1) * G + lane] = make_float2(-INFINITY, 0.f);
     }
-    const int nb = static_cast<int>((fl >> kBlocksAt) & 7u);
-    const uint32_t here = (fl >> kHereAt) & 15u;
+    const bool two = (fl & kTwo) != 0;
     const int valid = static_cast<int>((fl >> 8) & 0x1fu);   // rows of the job's last block
-    if (kStep && (fl & kNew)) store_new(stage, stage + (nb - 1) * kInt4Record, valid - 1, d.w);
-    const bool whole = here == (1u << nb) - 1 && valid == kBlockSize;
+    if (kStep && (fl & kNew)) store_new(stage, stage + kDiRecOff + (two ? kInt4Record : 0), valid - 1, d.w);
 
     // Exponents before the shift: [i][0] = (token gq of block i, head 2cq), [1] = (gq, 2cq + 1), [2] = (gq + 8,
     // 2cq), [3] = (gq + 8, 2cq + 1); and 1 / s of V of tokens gq, gq + 8.
     float y[kDiJob][4], iv[kDiJob][2];
-#pragma unroll
-    for (int i = 0; i < kDiJob; ++i) {
-      y[i][0] = y[i][1] = y[i][2] = y[i][3] = -INFINITY;
-      iv[i][0] = iv[i][1] = 0.f;
-      if (i >= nb) continue;
+    auto scores = [&](int i) {
       const uint32_t rec = kt + i * kInt4Record;
       const uint4 wa = lds128(rec + 64 * gq + 16 * cq), wb = lds128(rec + 64 * gq + 512 + 16 * cq);
       const uint2 sa = lds64(rec + kInt4KScales + 8 * gq), sb = lds64(rec + kInt4KScales + 64 + 8 * gq);
       const uint32_t ga = lds16(rec + kInt4KScales + 8 * gq + 2 * cq), gb = lds16(rec + kInt4KScales + 64 + 8 * gq + 2 * cq);
       const float va = int4_scale_of(lds16(rec + kInt4VScales + 2 * gq));
       const float vb = int4_scale_of(lds16(rec + kInt4VScales + 16 + 2 * gq));
-      float x[4] = {0.f, 0.f, 0.f, 0.f};
+      float x[4];
       {  // - sum_g s z Q: A rows = tokens, this lane's four k indices all stand for group cq
         const uint32_t w = __byte_perm(ga, gb, 0x5410);
         const uint32_t sz = mul_bf16x2(w & 0xfff0fff0u, sub_bf16x2((w & kPairLo) | 0x43004300u, 0x43004300u));
         const uint32_t ra = __byte_perm(sz, sz, 0x1010), rb = __byte_perm(sz, sz, 0x3232);
-        mma_bf16_16816(x, ra, rb, ra, rb, qsum[0], qsum[1]);
+        mma_bf16_first(x, ra, rb, ra, rb, qsum[0], qsum[1]);
       }
       auto group = [&](int c, uint32_t u, uint32_t v, float fu, float fv) {
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+        float acc[4];
         const uint32_t u0 = u << 3, v0 = v << 3, u1 = u >> 5, v1 = v >> 5;
-        mma_f16_16816(acc, u0 & kPairA, v0 & kPairA, u0 & kPairB, v0 & kPairB, qb[2 * c][0], qb[2 * c][1]);
+        mma_f16_first(acc, u0 & kPairA, v0 & kPairA, u0 & kPairB, v0 & kPairB, qb[2 * c][0], qb[2 * c][1]);
         mma_f16_16816(acc, u1 & kPairA, v1 & kPairA, u1 & kPairB, v1 & kPairB, qb[2 * c + 1][0], qb[2 * c + 1][1]);
         x[0] = fmaf(fu, acc[0], x[0]);
         x[1] = fmaf(fu, acc[1], x[1]);
@@ -464,12 +494,25 @@ __global__ void __launch_bounds__(kDiWarps * 32, 1) decode_int4_kernel(const Dec
       y[i][3] = fmaf(x[3], kf1, eb);
       iv[i][0] = rcp_ftz(va);
       iv[i][1] = rcp_ftz(vb);
-      if (!whole) {
+    };
+    // Most jobs are two whole blocks: theirs is a path without a branch, whose blocks interleave.
+    const bool full = (fl & (kTwo | kHas0 | kHas1)) == (kTwo | kHas0 | kHas1) && valid == kBlockSize;
+    if (full) {
+#pragma unroll
+      for (int i = 0; i < kDiJob; ++i) scores(i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kDiJob; ++i) {
+        y[i][0] = y[i][1] = y[i][2] = y[i][3] = -INFINITY;
+        iv[i][0] = iv[i][1] = 0.f;
+        if (i == 1 && !two) continue;
+        scores(i);
         // tokens past the context, and absent blocks, may hold anything
-        const int n = !((here >> i) & 1) ? 0 : i == nb - 1 ? valid : kBlockSize;
+        const int n = !(fl & (i ? kHas1 : kHas0)) ? 0 : i == 1 || !two ? valid : kBlockSize;
         if (gq >= n) y[i][0] = y[i][1] = -INFINITY, iv[i][0] = 0.f;
         if (gq + 8 >= n) y[i][2] = y[i][3] = -INFINITY, iv[i][1] = 0.f;
       }
+      __syncwarp();
     }
     float top0 = -INFINITY, top1 = -INFINITY;
 #pragma unroll
@@ -478,7 +521,7 @@ __global__ void __launch_bounds__(kDiWarps * 32, 1) decode_int4_kernel(const Dec
       top1 = fmax3(top1, y[i][1], y[i][3]);
     }
     if (__any_sync(kFullMask, top0 - m0 > 15.f || top1 - m1 > 15.f)) {
-      // A shift has to move (at a piece's first job from -infinity): the maxima over the tokens, and what
+      // A shift has to move (at a piece's first job from kNoShift): the maxima over the tokens, and what
       // was summed so far scaled to the new shifts.
 #pragma unroll
       for (int x = 4; x < 32; x <<= 1) {
@@ -503,14 +546,10 @@ __global__ void __launch_bounds__(kDiWarps * 32, 1) decode_int4_kernel(const Dec
       z[2] *= al0;
       z[3] *= al1;
     }
-    // a column without a key so far keeps the shift at -infinity: weights 0, not NaN
-    const float sh0 = m0 == -INFINITY ? 0.f : m0, sh1 = m1 == -INFINITY ? 0.f : m1;
-#pragma unroll
-    for (int i = 0; i < kDiJob; ++i) {
-      if (i >= nb) continue;
+    auto values = [&](int i) {
       const uint32_t rec = kt + i * kInt4Record;
-      const float p0 = ex2_ftz(y[i][0] - sh0), p1 = ex2_ftz(y[i][1] - sh1);
-      const float p2 = ex2_ftz(y[i][2] - sh0), p3 = ex2_ftz(y[i][3] - sh1);
+      const float p0 = ex2_ftz(y[i][0] - m0), p1 = ex2_ftz(y[i][1] - m1);
+      const float p2 = ex2_ftz(y[i][2] - m0), p3 = ex2_ftz(y[i][3] - m1);
       l0 = fmaf(p0, iv[i][0], fmaf(p2, iv[i][1], l0));
       l1 = fmaf(p1, iv[i][0], fmaf(p3, iv[i][1], l1));
       // B operand P^T: tokens 2cq, 2cq + 1 (+ 8) of head gq
@@ -531,6 +570,14 @@ __global__ void __launch_bounds__(kDiWarps * 32, 1) decode_int4_kernel(const Dec
           mma_f16_16816(o[2 * (u + h) + 1], u1 & kPairA, u1 & kPairB, v1 & kPairA, v1 & kPairB, b0, b1);
         }
       }
+    };
+    if (full) {
+#pragma unroll
+      for (int i = 0; i < kDiJob; ++i) values(i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kDiJob; ++i)
+        if (i == 0 || two) values(i);
     }
     if (fl & kLast) {
       float L0 = l0, L1 = l1;                        // the 8 lanes sharing cq hold disjoint tokens
@@ -568,44 +615,35 @@ __global__ void __launch_bounds__(kDiWarps * 32, 1) decode_int4_kernel(const Dec
         if (2 * cq + 1 < G) a.ws_ml[row + 1] = make_float2(m1, L1);
       }
     }
+    return two ? 2 : 1;
   };
 
   // ---------------------------------------------------------------- pipeline --------
-  int ahead = 0;           // jobs emitted and not yet consumed
-  int pst = 0, cst = 0;
-  bool more = true;
-  if (early) pdl_wait_prior_grid();
-  while (more && ahead < n_st) {
-    more = produce(pst);
-    if (more) {
-      ++ahead;
-      if (++pst == n_st) pst = 0;
-    }
-  }
-  if (!nxt_there) {
-    resolve(nxt);
-    nxt_there = true;
-  }
-  __syncwarp();
-  while (ahead > 0) {
-    cp_async_wait_but(ahead - 1);      // the oldest job's copies; the warp barrier shows them to every lane
-    __syncwarp();
-    consume(cst);
-    --ahead;
-    if (++cst == n_st) cst = 0;
-    __syncwarp();
-    if (more) {
-      more = produce(pst);
-      if (more) {
-        ++ahead;
-        if (++pst == n_st) pst = 0;
+  // The k-th use of a stage completes phase k & 1 of its barriers.
+  uint32_t at = ring, bar = full_bars, phase = 0;
+  for (int left = static_cast<int>(R.begin(my_v + 1) - R.begin(my_v)); left > 0;) {
+    if (!__all_sync(kFullMask, *fail == 0 && mbar_wait_parked(bar, phase))) {
+      if (lane == 0) {
+        raise_flag(a.status, PA_FLAG_TIMEOUT);
+        *fail = 1;
       }
+      break;
     }
+    left -= consume(at);
+    fence_proxy_async_smem();   // what this warp read and wrote in the stage before the copies that follow
     __syncwarp();
+    if (lane == 0) mbar_arrive(bar + 8);
+    at += stage_bytes;
+    bar += 16;
+    if (at == ring_end) {
+      at = ring;
+      bar = full_bars;
+      phase ^= 1u;
+    }
   }
 }
 
-// CTAs of the persistent grid: one per SM, capped to kMaxDecodeWarps warps (looked up once per
+// CTAs of the persistent grid: one per SM, capped to kMaxDecodeWarps ranges (looked up once per
 // device, with the shared-memory opt-in of both variants).
 cudaError_t int4_ctas(int* ctas) {
   static std::mutex mu;
@@ -625,7 +663,7 @@ cudaError_t int4_ctas(int* ctas) {
     int sms = 0;
     if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (err != cudaSuccess) return err;
-    cached[dev] = min(sms, kMaxDecodeWarps / kDiWarps);
+    cached[dev] = min(sms, kMaxDecodeWarps / kDiConsumers);
   }
   *ctas = cached[dev];
   return cudaSuccess;
@@ -639,13 +677,13 @@ cudaError_t launch_decode_int4(const DecodeArgs& args, cudaStream_t stream) {
   int max_ctas = 0;
   cudaError_t err = int4_ctas(&max_ctas);
   if (err != cudaSuccess) return err;
-  // Stages: what fits.  The warps are those that the step has room for, with and without it, so that both
+  // Stages: what fits.  The warps are those that the step has two stages for, with and without it, so that both
   // cut sequences alike and give the same bits.
   const int G = a.num_q_heads / a.num_kv_heads;
   const int fixed = kDiPrefixOff + prefix_bytes(a.num_seqs);
   const int stage = di_stage(G, step);
-  const int pool = min(kDiMaxStages, (kDiSmemMax - fixed) / stage);
-  const int warps = min(kDiWarps, (kDiSmemMax - fixed) / di_stage(G, true));
+  const int pool = (kDiSmemMax - fixed) / stage;
+  const int warps = min(kDiConsumers, (kDiSmemMax - fixed) / di_stage(G, true) / 2);
   // no more CTAs than there can be ranges (they are dealt to the CTAs one at a time)
   const long long jobs = static_cast<long long>(a.num_seqs) * a.num_kv_heads *
                          ((a.max_context_len + kBlockSize - 1) / kBlockSize);
@@ -656,7 +694,7 @@ cudaError_t launch_decode_int4(const DecodeArgs& args, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-  cfg.blockDim = dim3(static_cast<unsigned>(warps * 32));
+  cfg.blockDim = dim3(static_cast<unsigned>((warps + 1) * 32));
   cfg.dynamicSmemBytes = fixed + pool * stage;
   cfg.stream = stream;
   cfg.attrs = attr;
