@@ -125,9 +125,9 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// A scale word as the bf16 pairs (s, s) and (128 + z, 128 + z).
-__device__ __forceinline__ void int4_unpack_scale(uint32_t word, uint32_t& s2, uint32_t& z2) {
-  const uint32_t w = __byte_perm(word, word, 0x1010);
+// A scale word (the low or the high half of `words`) as the bf16 pairs (s, s) and (128 + z, 128 + z).
+__device__ __forceinline__ void int4_unpack_scale(uint32_t words, int high, uint32_t& s2, uint32_t& z2) {
+  const uint32_t w = __byte_perm(words, words, high ? 0x3232 : 0x1010);
   s2 = w & 0xfff0fff0u;
   z2 = (w & kPairLo) | 0x43004300u;
 }

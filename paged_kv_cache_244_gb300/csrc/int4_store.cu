@@ -207,9 +207,9 @@ __global__ void __launch_bounds__(kReadWarps * 32) read_int4_kernel(const ReadIn
     if (row < 0 || row >= n) continue;
     const size_t at = ((static_cast<size_t>(r0) + row) * Hkv + g) * (kHeadDim / 8) + ch;
     uint32_t s2, z2;
-    int4_unpack_scale(ks[i], s2, z2);
+    int4_unpack_scale(ks[i], 0, s2, z2);
     reinterpret_cast<uint4*>(a.k_out)[at] = int4_elements(kw[i], s2, z2);
-    int4_unpack_scale(vs[i], s2, z2);
+    int4_unpack_scale(vs[i], 0, s2, z2);
     reinterpret_cast<uint4*>(a.v_out)[at] = int4_elements(vw[i], s2, z2);
   }
 }

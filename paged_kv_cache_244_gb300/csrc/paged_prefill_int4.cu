@@ -79,14 +79,6 @@ static_assert(kTmemAt + 4 <= kIpHeader, "header");
 __constant__ uint32_t c_ip_jitter[2];
 std::atomic<bool> jitter_on{false};
 
-// What a converter lane holds of a block: token r and r + 8, 16-byte unit i of their K and V codes, and the
-// tokens' scale words.
-struct Raw {
-  uint4 k[2], v[2];
-  uint2 ks[2];
-  uint32_t vs[2];
-};
-
 template <bool kSplit, bool kJitter>
 __global__ void __launch_bounds__(kIpThreads, 2)
 prefill_int4_kernel(const PrefillArgs a) {
@@ -189,56 +181,66 @@ prefill_int4_kernel(const PrefillArgs a) {
     const int cw = warp - 8;
     const int r8 = lane & 7, i = lane >> 3;         // tokens r8 and r8 + 8, 16-byte unit i of their codes
     const uint8_t* const cache = reinterpret_cast<const uint8_t*>(a.k_cache);
-    auto load_raw = [&](int id, Raw& w) {           // a block that is not there gives nothing
-      if (!in_pool(id)) return;
-      const uint8_t* rec = cache + (static_cast<size_t>(id) * Hkv + g) * kInt4Record;
+    // A stage's codes and scale words are asked for as soon as those of the stage before are widened.  (A block that is
+    // not there is read as the pool's first; its keys are masked and its V is written as zeros.)
+    uint4 k[2], v[2];
+    uint2 ks[2];
+    uint32_t vs[2];
+    auto record = [&](int id) { return cache + (static_cast<size_t>(in_pool(id) ? id : 0) * Hkv + g) * kInt4Record; };
+    auto load_k = [&](const uint8_t* rec) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        w.k[h] = *reinterpret_cast<const uint4*>(rec + 512 * h + 64 * r8 + 16 * i);
-        w.v[h] = *reinterpret_cast<const uint4*>(rec + kInt4VCodes + 512 * h + 64 * r8 + 16 * i);
-        w.ks[h] = *reinterpret_cast<const uint2*>(rec + kInt4KScales + 64 * h + 8 * r8);
-        w.vs[h] = *reinterpret_cast<const uint16_t*>(rec + kInt4VScales + 16 * h + 2 * r8);
+        k[h] = *reinterpret_cast<const uint4*>(rec + 512 * h + 64 * r8 + 16 * i);
+        ks[h] = *reinterpret_cast<const uint2*>(rec + kInt4KScales + 64 * h + 8 * r8);
+      }
+    };
+    auto load_v = [&](const uint8_t* rec) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        v[h] = *reinterpret_cast<const uint4*>(rec + kInt4VCodes + 512 * h + 64 * r8 + 16 * i);
+        vs[h] = *reinterpret_cast<const uint16_t*>(rec + kInt4VScales + 16 * h + 2 * r8);
       }
     };
     const int vu = i ^ ((r8 >> 1) & 3);             // the unit of V's dims that lies at i (token r8 + 8 as r8)
-    Raw w = {};
+    // byte offsets of this lane's 16-byte chunks in a 128-byte row of an operand, swizzled
+    const uint32_t k_at = (kBlockSize * cw + r8) * 128, k_even = (i ^ r8) << 4, k_odd = ((4 + i) ^ r8) << 4;
+    const uint32_t v_at = (2 * cw + (vu >> 1)) * kIpTile + r8 * 128, v_chunk = 4 * (vu & 1);
     int id = __shfl_sync(kFullMask, ids, cw);
-    load_raw(id, w);
+    {
+      const uint8_t* rec = record(id);
+      load_k(rec);
+      load_v(rec);
+    }
     bool failed = false;
     for (int j = 0; j < nst; ++j) {
       const int st = j % kIpRing;
       if constexpr (kJitter) jitter_sleep(c_ip_jitter, warp, j);
-      // the next stage's record is asked for while this one's is widened
-      Raw w_next = {};
-      int id_next = -1;
-      if (j + 1 < nst) {
-        next_window(j + 1);
-        id_next = __shfl_sync(kFullMask, ids, ((kIpKB * (j + 1)) & 31) + cw);
-        load_raw(id_next, w_next);
-      }
       const bool there = in_pool(id);
       if (!there && kIpKB * j + cw < nblocks && lane == 0) raise_flag(a.status, PA_FLAG_BLOCK_ID_OOB);
-      // K: the scores of a block that is not there are masked, whatever its slot holds
+      const uint8_t* next = nullptr;
+      if (j + 1 < nst) {
+        next_window(j + 1);
+        id = __shfl_sync(kFullMask, ids, ((kIpKB * (j + 1)) & 31) + cw);
+        next = record(id);
+      }
       if (j >= kIpRing && !__all_sync(kFullMask, mbar_wait_parked(hdr + kKFree + 8 * st, ((j / kIpRing) - 1) & 1))) {
         failed = true;
         break;
       }
-      if (there) {
-        unsigned char* const ops = base + st * kIpStage;
+      {
+        unsigned char* const ops = base + st * kIpStage + k_at;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int row = kBlockSize * cw + 8 * h + r8;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {             // dims 32c + 8i .. + 7: chunk 4c + i of the row
-            const uint32_t code = c == 0 ? w.k[h].x : c == 1 ? w.k[h].y : c == 2 ? w.k[h].z : w.k[h].w;
-            const uint32_t pair = c < 2 ? w.ks[h].x : w.ks[h].y;
+          for (int c = 0; c < 4; ++c) {             // dims 32c + 8i .. + 7: chunk 4c + i of the token's row
+            const uint32_t code = c == 0 ? k[h].x : c == 1 ? k[h].y : c == 2 ? k[h].z : k[h].w;
             uint32_t s2, z2;
-            int4_unpack_scale((c & 1) ? pair >> 16 : pair, s2, z2);
-            *reinterpret_cast<uint4*>(ops + (c >> 1) * kIpHalf + row * 128 + (((4 * (c & 1) + i) ^ r8) << 4)) =
-                int4_elements(code, s2, z2);
+            int4_unpack_scale(c < 2 ? ks[h].x : ks[h].y, c & 1, s2, z2);
+            *reinterpret_cast<uint4*>(ops + (c >> 1) * kIpHalf + 1024 * h + ((c & 1) ? k_odd : k_even)) = int4_elements(code, s2, z2);
           }
         }
       }
+      if (next) load_k(next);
       fence_proxy_async_smem();                     // before the tensor core reads them
       __syncwarp();
       if (lane == 0) mbar_arrive(hdr + kKFull + 8 * st);
@@ -247,30 +249,29 @@ prefill_int4_kernel(const PrefillArgs a) {
         break;
       }
       {
-        unsigned char* const ops = base + kIpVOff + st * kIpStage + 2 * cw * kIpTile + (vu >> 1) * kIpTile;
+        unsigned char* const ops = base + kIpVOff + st * kIpStage + v_at;
+        // tokens of this lane's block that the context has
+        const int inside = there ? ctx - key0 - kIpKeys * j - kBlockSize * cw : 0;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int key = kIpKeys * j + kBlockSize * cw + 8 * h + r8;   // from this CTA's first
-          const uint32_t word = w.vs[h];
-          const bool nan = (word & 0x7fffu) > 0x7f8fu;
-          const bool inside = there && key0 + key < ctx;
-          if (inside && nan && i == 0) atomicMin(nan_from, key);
-          const bool live = inside && !nan;
           uint32_t s2, z2;
-          int4_unpack_scale(word, s2, z2);
+          int4_unpack_scale(vs[h], 0, s2, z2);
+          if (8 * h + r8 >= inside || vs[h] > 0x7f8fu) {   // past the context, absent, or a scale of NaN
+            if (8 * h + r8 < inside) atomicMin(nan_from, kIpKeys * j + kBlockSize * cw + 8 * h + r8);
+            s2 = 0u;                                // c - z is finite: zeros
+          }
 #pragma unroll
           for (int c = 0; c < 4; ++c) {             // dims 32 vu + 8c .. + 7: chunk 4 (vu & 1) + c of the half's row
-            const uint32_t code = c == 0 ? w.v[h].x : c == 1 ? w.v[h].y : c == 2 ? w.v[h].z : w.v[h].w;
-            const uint4 e = live ? int4_elements(code, s2, z2) : make_uint4(0u, 0u, 0u, 0u);
-            *reinterpret_cast<uint4*>(ops + (8 * h + r8) * 128 + (((4 * (vu & 1) + c) ^ r8) << 4)) = e;
+            const uint32_t code = c == 0 ? v[h].x : c == 1 ? v[h].y : c == 2 ? v[h].z : v[h].w;
+            *reinterpret_cast<uint4*>(ops + 1024 * h + (((v_chunk + c) ^ r8) << 4)) = int4_elements(code, s2, z2);
           }
         }
+        __syncwarp();
       }
+      if (next) load_v(next);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(hdr + kVFull + 8 * st);
-      w = w_next;
-      id = id_next;
     }
     if (failed) raise_flag(a.status, PA_FLAG_TIMEOUT);
     if constexpr (kSplit) {
