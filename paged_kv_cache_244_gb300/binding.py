@@ -690,6 +690,8 @@ def int4_cache(num_blocks, num_kv_heads, device="cuda") -> torch.Tensor:
 
 def decode_workspace_int4(q, cache, max_context_len, partition_tokens=0) -> torch.Tensor:
     """Allocate the workspace of decode_int4 and decode_step_int4 for these shapes (no initialisation needed)."""
+    if q.dim() != 3 or cache.dim() != 3 or cache.shape[2] != INT4_RECORD_BYTES:
+        raise ValueError("q must be [rows, num_q_heads, 128] and cache [num_blocks, num_kv_heads, 2208]")
     n = decode_workspace_size(q.shape[1], cache.shape[1], q.shape[0], max_context_len, partition_tokens)
     if n == 0:
         raise PaError(PA_ERR_RANGE, "pa_decode_workspace_size")

@@ -220,7 +220,7 @@ __global__ void __launch_bounds__((kDiConsumers + 1) * 32, 1) decode_int4_kernel
       if (ready) {
         const bool two = (fl & kTwo) != 0;
         const bool here0 = id0 >= 0 && id0 < a.num_blocks, here1 = two && id1 >= 0 && id1 < a.num_blocks;
-        const int row0 = id0 * Hkv + g, row1 = id1 * Hkv + g;
+        const int row0 = here0 ? id0 * Hkv + g : 0, row1 = here1 ? id1 * Hkv + g : 0;
         const int seg = s * Hkv + g;
         const int part = chunk ? j / chunk : 0;
         // Fused step: a position without a cos/sin row leaves the token out -- q unrotated, nothing stored.
@@ -271,7 +271,6 @@ __global__ void __launch_bounds__((kDiConsumers + 1) * 32, 1) decode_int4_kernel
         }
       }
       __syncwarp();
-      if (__all_sync(kFullMask, fills >= n_st || rel >= len)) __nanosleep(20);
     }
     // let the copies still in flight land before the CTA exits (they have, in a normal run, but for the last ones)
     for (int k = max(0, fills - n_st); k < fills; ++k) mbar_wait_bounded(full_bars + 16 * (k % n_st), (k / n_st) & 1);

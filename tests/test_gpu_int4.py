@@ -588,3 +588,159 @@ def test_long_context_sums(pa):
     # a warp's range of the even split has some 1.4 blocks here and the pieces are joined in fp32; with a partition
     # for the whole context a piece is what a range holds all the same
     close(pa.decode_int4(bf16(q), p.dev(), up(p.tables), up(p.lens), n, D ** -0.5), ref, steps=64)
+
+
+# ---- at the limits ------------------------------------------------------------------------
+
+@pytest.mark.parametrize("step", [False, True])
+def test_most_sequences_of_a_call(pa, step):
+    """8192 sequences: their block-count prefix leaves fewer stages and warps; most contexts are a few tokens or none."""
+    rng = np.random.default_rng(30)
+    n = 8192
+    lens = rng.integers(1 if step else 0, 12, n)
+    lens[[5, 4000, 8191]] = [300, 65, 17]
+    p = Pool(rng, lens.tolist(), 1)
+    q = normal(rng, n, 8, D)
+    cache = p.dev()
+    if step:
+        k, v = normal(rng, n, 1, D), normal(rng, n, 1, D)
+        cs = table_of(310, 64)
+        got = pa.decode_step_int4(bf16(q), bf16(k), bf16(v), up(cs), cache, up(p.tables), up(p.lens), 300, 0.1)
+        pos = (p.lens - 1).astype(np.int32)
+        slots = p.tables[np.arange(n), pos // B].astype(np.int64) * B + pos % B
+        other = p.dev()
+        qr = pa.rope_kv_store_int4(bf16(q), bf16(k), bf16(v), up(pos), up(cs), up(slots), other)
+        assert torch.equal(cache, other)
+        q, p.cache = f64(qr), cache.cpu().numpy()
+        assert np.array_equal(bits(got), bits(pa.decode_int4(qr, cache, up(p.tables), up(p.lens), 300, 0.1)))
+    else:
+        got = pa.decode_int4(bf16(q), cache, up(p.tables), up(p.lens), 300, 0.1)
+    for s in [0, 1, 5, 4000, 8190, 8191, *rng.integers(0, n, 60)]:
+        close(got[s:s + 1], p.attention(s, q[s:s + 1], 0.1), s, steps=int(lens[s]) // 16 + 1)
+    clean(pa)
+
+
+def test_many_heads(pa):
+    rng = np.random.default_rng(31)
+    lens, kv = [40, 17], 257
+    p = Pool(rng, lens, kv)
+    q = normal(rng, 2, kv, D)
+    got = pa.decode_int4(bf16(q), p.dev(), up(p.tables), up(p.lens), 40, 0.1)
+    pre = pa.prefill_int4(bf16(q), up(np.array([0, 1, 2], np.int32)), p.dev(), up(p.tables), up(p.lens), 1, 40, 0.1)
+    for s in range(2):
+        ref = p.attention(s, q[s:s + 1], 0.1)
+        close(got[s:s + 1], ref, s, steps=4)
+        close(pre[s:s + 1], ref, s, prefill=True)
+    clean(pa)
+
+
+def test_read_of_thousands_of_sequences(pa):
+    rng = np.random.default_rng(32)
+    n = 5000
+    rows = rng.integers(0, 3, n)
+    rows[77] = 200
+    first = rng.integers(0, 30, n)
+    p = Pool(rng, (first + rows).tolist(), 2, canary=False)
+    starts = np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
+    k, v = pa.read_kv_int4(p.dev(), up(starts), up(first.astype(np.int32)), up(p.tables), 200, num_rows=int(starts[-1]))
+    seq = np.repeat(np.arange(n), rows)
+    at = np.arange(starts[-1]) - starts[seq] + first[seq]
+    K, V = (x[np.arange(len(at)), :, at % B] for x in R.unpack(p.cache[p.tables[seq, at // B]]))
+    assert np.array_equal(f64(k), K) and np.array_equal(f64(v), V)
+    clean(pa)
+
+
+def test_a_layer_chain_with_early_metadata(pa):
+    """The steps of many layers, each started while the one before it finishes, give what they give one by one."""
+    rng = np.random.default_rng(33)
+    lens, layers = [5, 300, 64, 33] * 8, 12
+    pools = [Pool(rng, lens, 2) for _ in range(layers)]
+    q, k, v = (bf16(normal(rng, layers, len(lens), h, D)) for h in (12, 2, 2))
+    cs = up(table_of(310, 128))
+    tabs, ctx = [up(p.tables) for p in pools], up(pools[0].lens)
+    ws = pa.decode_workspace_int4(q[0], pools[0].dev(), 300)
+
+    def chain(early):
+        caches = [p.dev() for p in pools]
+        outs = [torch.empty_like(q[0]) for _ in range(layers)]
+        torch.cuda.synchronize()
+        for i in range(layers):
+            pa.decode_step_int4(q[i], k[i], v[i], cs, caches[i], tabs[i], ctx, 300, 0.1, workspace=ws, out=outs[i], early_metadata=early)
+        torch.cuda.synchronize()
+        return outs, caches
+    (o1, c1), (o2, c2) = chain(False), chain(True)
+    assert all(torch.equal(a, b) for a, b in zip(o1 + c1, o2 + c2))
+    clean(pa)
+
+
+def test_two_graphs_in_turn_share_a_workspace(pa):
+    rng = np.random.default_rng(34)
+    pools = [Pool(rng, lens, 4) for lens in ([700, 20], [33, 5, 900])]
+    ws = torch.empty(1 << 22, device="cuda")
+    calls = []
+    for p in pools:
+        q = bf16(normal(rng, len(p.lens), 28, D))
+        calls.append((q, p.dev(), up(p.tables), up(p.lens), int(p.lens.max()), 0.1))
+    want = [bits(pa.decode_int4(*c)) for c in calls]
+    outs, graphs = [torch.empty_like(c[0]) for c in calls], []
+    for c, o in zip(calls, outs):
+        pa.decode_int4(*c, workspace=ws, out=o)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            pa.decode_int4(*c, workspace=ws, out=o)
+        graphs.append(g)
+    for _ in range(5):
+        for o in outs:
+            o.zero_()
+        for g in graphs:
+            g.replay()
+        assert all(np.array_equal(bits(o), w) for o, w in zip(outs, want))
+    clean(pa)
+
+
+def test_the_binding_refuses_wrong_tensors(pa):
+    rng = np.random.default_rng(35)
+    p = Pool(rng, [20, 20], 2)
+    q, cache, t, n = bf16(normal(rng, 2, 4, D)), p.dev(), up(p.tables), up(p.lens)
+    starts = up(np.array([0, 1, 2], np.int32))
+    for bad in (cache[..., :2000].contiguous(), cache[0], cache.to(torch.int8), cache.transpose(0, 1), cache.cpu()):
+        with pytest.raises((ValueError, pa.PaError)):
+            pa.decode_int4(q, bad, t, n, 20, 0.1)
+        with pytest.raises((ValueError, pa.PaError)):
+            pa.prefill_int4(q, starts, bad, t, n, 1, 20, 0.1)
+        with pytest.raises((ValueError, pa.PaError)):
+            pa.read_kv_int4(bad, starts, None, t, 20, k_out=q[:, :2].contiguous(), v_out=q[:, 2:].contiguous())
+    for args in ((q.half(), cache, t, n), (q[:1], cache, t, n), (q, cache, t.long(), n), (q, cache, t, n[:1]), (q[..., :64].contiguous(), cache, t, n)):
+        with pytest.raises((ValueError, pa.PaError)):
+            pa.decode_int4(*args, 20, 0.1)
+    with pytest.raises((ValueError, pa.PaError)):
+        pa.read_kv_int4(cache, starts, n[:1], t, 20, num_rows=2)
+    with pytest.raises((ValueError, pa.PaError)):
+        pa.rope_kv_store_int4(q, q, q, n, up(table_of(30, 128)), up(np.zeros(2, np.int64)), cache)   # k of 4 KV heads
+    with pytest.raises(pa.PaError) as e:
+        pa.decode_int4(q, cache, t, n, 20, -1.0)
+    assert e.value.code == pa.PA_ERR_RANGE
+    with pytest.raises(pa.PaError) as e:
+        pa.decode_int4(q, cache, t, n, 20, 0.1, workspace=torch.empty(8, device="cuda"))
+    assert e.value.code == pa.PA_ERR_WORKSPACE
+    assert pa.decode_int4(q[:0], cache, t[:0], n[:0], 20, 0.1).shape == (0, 4, D)
+    clean(pa)
+
+
+def test_a_call_on_a_stream_of_its_own_with_what_it_allocates(pa):
+    rng = np.random.default_rng(36)
+    p = Pool(rng, [900, 40], 2)
+    q = bf16(normal(rng, 2, 12, D))
+    args = (p.dev(), up(p.tables), up(p.lens), 900, 0.1)
+    want = bits(pa.decode_int4(q, *args))
+    rows = up(np.array([0, 1, 2], np.int32))
+    want_p = bits(pa.prefill_int4(q, rows, *args[:3], 1, 900, 0.1))
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    for _ in range(10):
+        a = pa.decode_int4(q, *args, stream=st)
+        b = pa.prefill_int4(q, rows, *args[:3], 1, 900, 0.1, stream=st)
+        k, v = pa.read_kv_int4(args[0], up(np.array([0, 900, 940], np.int32)), None, args[1], 900, num_rows=940, stream=st)
+        torch.cuda.current_stream().wait_stream(st)
+        assert np.array_equal(bits(a), want) and np.array_equal(bits(b), want_p)
+    clean(pa)
