@@ -532,7 +532,8 @@ int pa_prefill_fp8_block(const pa_dims* dims, int num_seqs, int num_tokens, cons
 
 /*
  * pa_rope_kv_store_int4 -- pa_rope_kv_store_form into the 4-bit cache: the rotated k as bf16, and v, quantised into
- * the record at slot_mapping[t].  Everything else as pa_rope_kv_store_form.
+ * the record at slot_mapping[t].  An infinity in k that is rotated stays one, and makes the dim it turns with NaN, as
+ * there.  Everything else as pa_rope_kv_store_form.
  *   cache   [num_blocks][Hkv][PA_INT4_RECORD_BYTES], written at the slots only
  * Launches one kernel.
  */

@@ -169,10 +169,16 @@ __device__ __forceinline__ void int4_rotate_pairs(uint32_t& lo, uint32_t& hi, fl
   lo = round_pair(diff_of_products(x0, c.x, y0, s.x), diff_of_products(x1, c.y, y1, s.y), border);
   hi = round_pair(diff_of_products(y0, c.x, -x0, s.x), diff_of_products(y1, c.y, -x1, s.y), border);
 }
-__device__ __forceinline__ void int4_rotate_exactly(uint32_t& lo, uint32_t& hi, float2 c, float2 s) {
-  const float x0 = bf16lo(lo), x1 = bf16hi(lo), y0 = bf16lo(hi), y1 = bf16hi(hi);
-  lo = pack_bf16x2(exact_difference(x0, c.x, y0, s.x), exact_difference(x1, c.y, y1, s.y));
-  hi = pack_bf16x2(exact_difference(y0, c.x, -x0, s.x), exact_difference(y1, c.y, -x1, s.y));
+// x and y rotated again, to lo and hi, which hold the first form's values: those stay where a number is infinite
+// or a product passes fp32, and this form would say NaN.
+__device__ __forceinline__ void int4_rotate_exactly(uint32_t x, uint32_t y, float2 c, float2 s, uint32_t& lo, uint32_t& hi) {
+  auto take = [](uint32_t exact, uint32_t& at) {
+    const uint32_t finite = __vcmpltu2(exact & 0x7fff7fffu, 0x7f807f80u);
+    at = (exact & finite) | (at & ~finite);
+  };
+  const float x0 = bf16lo(x), x1 = bf16hi(x), y0 = bf16lo(y), y1 = bf16hi(y);
+  take(pack_bf16x2(exact_difference(x0, c.x, y0, s.x), exact_difference(x1, c.y, y1, s.y)), lo);
+  take(pack_bf16x2(exact_difference(y0, c.x, -x0, s.x), exact_difference(y1, c.y, -x1, s.y)), hi);
 }
 
 // Two adjacent pairs, halves apart (kInterleaved: (x0, y0), (x1, y1)), by the first form and where it asks for it by
@@ -182,11 +188,7 @@ __device__ __forceinline__ void int4_rotate(uint32_t& w0, uint32_t& w1, float2 c
   uint32_t lo = kInterleaved ? __byte_perm(w0, w1, 0x5410) : w0, hi = kInterleaved ? __byte_perm(w0, w1, 0x7632) : w1;
   uint32_t border = 0xffffffffu, a = lo, b = hi;
   int4_rotate_pairs(a, b, c, s, border);
-  if (at_border(border)) {
-    a = lo;
-    b = hi;
-    int4_rotate_exactly(a, b, c, s);
-  }
+  if (at_border(border)) int4_rotate_exactly(lo, hi, c, s, a, b);
   w0 = kInterleaved ? __byte_perm(a, b, 0x5410) : a;
   w1 = kInterleaved ? __byte_perm(a, b, 0x7632) : b;
 }

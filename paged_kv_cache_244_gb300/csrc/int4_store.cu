@@ -39,11 +39,7 @@ __device__ __forceinline__ void int4_rotate_chunks(uint4& x, uint4& y, const Ang
   }
   if (at_border(border)) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      p[i] = lo[i];
-      q[i] = hi[i];
-      int4_rotate_exactly(p[i], q[i], c[i], s[i]);
-    }
+    for (int i = 0; i < 4; ++i) int4_rotate_exactly(lo[i], hi[i], c[i], s[i], p[i], q[i]);
   }
   if constexpr (kInterleaved) {
     x = make_uint4(__byte_perm(p[0], q[0], 0x5410), __byte_perm(p[0], q[0], 0x7632), __byte_perm(p[1], q[1], 0x5410),

@@ -230,6 +230,32 @@ def test_store_of_extreme_rows(pa):
     clean(pa)
 
 
+def test_a_rotated_infinity_is_the_same_in_every_row(pa):
+    """An infinity stays one under a rotation, and its partner becomes NaN (a difference with an infinite product), however
+    near the other values of the row come to a border of their rounding."""
+    rng = np.random.default_rng(10)
+    n = 8192
+    k = normal(rng, n, 1, D)
+    k[:, 0, 9] = math.inf
+    cs = table_of(n, 128)                                  # row 0 turns by nothing: inf * 0
+    pos = 1 + np.arange(n, dtype=np.int32) % (n - 1)
+    cache = pa.int4_cache(n // B, 1)
+    q = torch.zeros((n, 1, D), dtype=torch.bfloat16, device="cuda")
+    args = (bf16(k), bf16(k), up(pos), up(cs), up(np.arange(n)))
+    pa.rope_kv_store_int4(q, *args, cache)
+    got, _ = pa.read_kv_int4(cache, up(np.array([0, n], np.int32)), None, up(np.arange(n // B, dtype=np.int32)[None]), n, n)
+    got = f64(got)[:, 0]
+    assert np.isfinite(got[:, :64]).all()                  # dim 9 reads as an end of its range
+    assert np.isnan(got[:, 64:96]).all()                   # the dims of its partner, 73
+    assert np.isfinite(got[:, 96:]).all()
+    # the fused step stores the same bytes
+    stored, step, one = pa.int4_cache(n, 1), pa.int4_cache(n, 1), up(cs[7:8])
+    pa.rope_kv_store_int4(q, bf16(k), bf16(k), torch.zeros_like(up(pos)), one, up(B * np.arange(n)), stored)
+    pa.decode_step_int4(q, bf16(k), bf16(k), one, step, up(np.arange(n, dtype=np.int32)[:, None]), up(np.ones(n, np.int32)), B, 0.1)
+    assert torch.equal(step, stored)
+    clean(pa)
+
+
 def test_store_skips_bad_positions_and_slots(pa):
     rng = np.random.default_rng(9)
     q, k, v = normal(rng, 5, 6, D), normal(rng, 5, 2, D), normal(rng, 5, 2, D)
