@@ -7,6 +7,13 @@
 // A token's scales are its own, so a row is quantised by the lanes that hold it and touches nothing of
 // its block's other tokens: the store is the bf16 store of a RoPE form (eight lanes a head vector, four
 // vectors a pass) with a few bytes out in the place of a row.
+//
+// Bound: rows in, q and codes out.  23,738 rows of 32 / 8 heads (525 MB with a cos/sin row each; 77 us at the copy rate)
+// take 95.7 us, 5.5 TB/s: the row's arithmetic (2,780 warp instructions a token, extremes and codes most of them) keeps
+// the issue slots 57% busy between the loads.  256 rows of 12 / 2 heads: 2.8 us, an empty kernel's 1.9 and the load
+// latencies.  CTAs of 2 / 4 / 8 / 16 warps, as many an SM: 95.7 / 96.2 / 97.8 / 115 us (2.8 / 2.8 / 3.1 / 3.4): a token
+// that is done makes room for the next.  24 warps of 80 registers an SM and two passes of loads ahead: with 32 or 40
+// warps, or one pass or three, 95 - 109.
 
 #include "int4_cache.cuh"
 #include "int4_launch.h"
@@ -15,7 +22,7 @@
 namespace pa {
 namespace {
 
-constexpr int kStoreWarps = 8;
+constexpr int kStoreWarps = 2;
 
 template <bool kInterleaved>
 __device__ __forceinline__ void int4_rotate_chunks(uint4& x, uint4& y, const Angles& a) {
@@ -55,7 +62,7 @@ __device__ __forceinline__ void int4_rotate_chunks(uint4& x, uint4& y, const Ang
 // One warp, one token: its groups of 4 kGroup head vectors part, part + parts, ..: queries rotated into
 // q_out, keys (rotated) and values quantised into the token's slot.
 template <bool kInterleaved, int kGroup>
-__global__ void __launch_bounds__(kStoreWarps * 32, 3) rope_int4_store_kernel(const RopeFormArgs a) {
+__global__ void __launch_bounds__(kStoreWarps * 32, 24 / kStoreWarps) rope_int4_store_kernel(const RopeFormArgs a) {
   __shared__ uint4 s_extremes[kStoreWarps][4][4];   // of a pass's vectors, a word for each 8 dims
   pdl_wait_prior_grid();
   pdl_allow_next_grid();
@@ -160,7 +167,8 @@ __global__ void __launch_bounds__(kStoreWarps * 32, 3) rope_int4_store_kernel(co
 
 // ---- reading back ------------------------------------------------------------------------------
 // A warp takes one record: half a warp a token, a lane the word of 8 dims, K and V of the 16 tokens with
-// all loads ahead of the stores.  Each store instruction writes two rows of 256 bytes.
+// all loads ahead of the stores.  Each store instruction writes two rows of 256 bytes.  64 prefixes, 99,801 rows of 8 heads
+// (519 MB): 80.6 us, 6.44 TB/s, 0.95 of the copy rate; one of 2,000 rows, 2 heads: 2.9 us, latency.
 constexpr int kReadWarps = 8;
 
 __global__ void __launch_bounds__(kReadWarps * 32) read_int4_kernel(const ReadInt4Args a) {
@@ -227,9 +235,10 @@ cudaLaunchConfig_t chained(dim3 grid, unsigned threads, cudaLaunchAttribute* att
 cudaError_t launch_rope_int4_store(const RopeFormArgs& a, cudaStream_t stream) {
   cudaLaunchAttribute attr;
   const unsigned token_ctas = static_cast<unsigned>((static_cast<long long>(a.num_tokens) + kStoreWarps - 1) / kStoreWarps);
-  // Where tokens are few, each group of a token's vectors has a warp of its own.
+  // Where tokens are few, each group of a token's vectors has a warp of its own, up to 16 warps an SM.
   const int groups = (a.num_q_heads + 2 * a.num_kv_heads + 7) / 8;
-  const int room = 304 / static_cast<int>(token_ctas > 304 ? 304 : token_ctas);
+  constexpr unsigned kRoom = 2432 / kStoreWarps;
+  const int room = static_cast<int>(kRoom / (token_ctas > kRoom ? kRoom : token_ctas));
   cudaLaunchConfig_t cfg = chained(dim3(token_ctas, groups < room ? groups : room), kStoreWarps * 32, &attr, stream);
   return a.interleaved ? cudaLaunchKernelEx(&cfg, rope_int4_store_kernel<true, 2>, a)
                        : cudaLaunchKernelEx(&cfg, rope_int4_store_kernel<false, 2>, a);
