@@ -554,7 +554,7 @@ int pa_rope_kv_store_int4(const pa_dims* dims, const pa_rope* rope, int num_toke
  *   num_rows      rows of k_out and v_out (0 is a no-op)
  *   row_start     [S + 1] int32, device
  *   first         [S] int32, device; NULL means 0 for every sequence
- *   max_rows      host bound of every n_s, 1 <= it <= max_blocks * 16, and (max_rows / 16 + 2) Hkv < 2^34
+ *   max_rows      host bound of every n_s, 1 <= it <= max_blocks * 16, and (max_rows / 16 + 2) Hkv < 2^32 - 2
  *   block_tables  [S][max_blocks] int32, max_blocks * 16 <= 2^31 - 16
  *   k_out, v_out  [num_rows][Hkv][128] bf16, written
  * Returns PA_OK or a PA_ERR_* code (nothing launched on error).  Launches one kernel.

@@ -6,6 +6,8 @@
 
 namespace pa {
 
+constexpr int kInt4ReadWarps = 2;   // of a CTA that reads rows back, a record each
+
 // Rows of sequences read back: row_start[s] + i of k_out and v_out is token first[s] + i.
 struct ReadInt4Args {
   const uint8_t* cache;             // [num_blocks][Hkv][PA_INT4_RECORD_BYTES]

@@ -168,10 +168,9 @@ __global__ void __launch_bounds__(kStoreWarps * 32, 24 / kStoreWarps) rope_int4_
 // ---- reading back ------------------------------------------------------------------------------
 // A warp takes one record: half a warp a token, a lane the word of 8 dims, K and V of the 16 tokens with
 // all loads ahead of the stores.  Each store instruction writes two rows of 256 bytes.  64 prefixes, 99,801 rows of 8 heads
-// (519 MB): 80.6 us, 6.44 TB/s, 0.95 of the copy rate; one of 2,000 rows, 2 heads: 2.9 us, latency.
-constexpr int kReadWarps = 8;
-
-__global__ void __launch_bounds__(kReadWarps * 32) read_int4_kernel(const ReadInt4Args a) {
+// (519 MB): 80.4 us, 6.46 TB/s, 0.95 of the copy rate; one of 2,000 rows, 2 heads: 2.3 us, latency (CTAs of 8 warps: 80.6
+// and 2.9).
+__global__ void __launch_bounds__(kInt4ReadWarps * 32) read_int4_kernel(const ReadInt4Args a) {
   pdl_wait_prior_grid();
   pdl_allow_next_grid();
   const int lane = threadIdx.x & 31;
@@ -186,7 +185,7 @@ __global__ void __launch_bounds__(kReadWarps * 32) read_int4_kernel(const ReadIn
   }
   if (n == 0) return;
   const int b0 = first / kBlockSize, nb = (first + n - 1) / kBlockSize - b0 + 1;
-  const long long unit = static_cast<long long>(blockIdx.x) * kReadWarps + (threadIdx.x >> 5);
+  const long long unit = static_cast<long long>(blockIdx.x) * kInt4ReadWarps + (threadIdx.x >> 5);
   if (unit >= static_cast<long long>(nb) * Hkv) return;
   const int b = static_cast<int>(unit / Hkv), g = static_cast<int>(unit - static_cast<long long>(b) * Hkv);
   const int blk = a.block_tables[static_cast<size_t>(s) * a.max_blocks + b0 + b];
@@ -248,8 +247,8 @@ cudaError_t launch_read_int4(const ReadInt4Args& a, cudaStream_t stream) {
   cudaLaunchAttribute attr;
   // a sequence's rows may begin and end inside a block
   const long long units = ((static_cast<long long>(a.max_rows) + kBlockSize - 2) / kBlockSize + 1) * a.num_kv_heads;
-  cudaLaunchConfig_t cfg = chained(dim3(static_cast<unsigned>((units + kReadWarps - 1) / kReadWarps), a.num_seqs),
-                                   kReadWarps * 32, &attr, stream);
+  cudaLaunchConfig_t cfg = chained(dim3(static_cast<unsigned>((units + kInt4ReadWarps - 1) / kInt4ReadWarps), a.num_seqs),
+                                   kInt4ReadWarps * 32, &attr, stream);
   return cudaLaunchKernelEx(&cfg, read_int4_kernel, a);
 }
 

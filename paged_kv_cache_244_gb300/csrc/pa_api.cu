@@ -634,7 +634,8 @@ int pa_read_kv_int4(const pa_dims* dims, int num_seqs, int num_rows, const int32
   if (!row_start || !cache || !block_tables || !k_out || !v_out) return PA_ERR_NULL;
   if (num_blocks < 1 || max_blocks < 1 || max_blocks > (0x7fffffff - 15) / 16) return PA_ERR_RANGE;
   if (max_rows < 1 || max_rows > max_blocks * dims->block_size) return PA_ERR_RANGE;
-  if ((max_rows / dims->block_size + 2ll) * dims->num_kv_heads / 8 >= 0x7fffffffll) return PA_ERR_RANGE;   // CTAs
+  if ((max_rows / dims->block_size + 2ll) * dims->num_kv_heads / pa::kInt4ReadWarps >= 0x7fffffffll)
+    return PA_ERR_RANGE;                              // CTAs of a sequence
   const void* ptrs[] = {row_start, first, cache, block_tables, k_out, v_out};
   for (const void* p : ptrs)
     if (!aligned16(p)) return PA_ERR_ALIGN;

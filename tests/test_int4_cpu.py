@@ -97,7 +97,7 @@ def test_read_refusals(pa):
     for kw in (dict(S=-1), dict(S=65536), dict(rows=-1), dict(max_rows=0), dict(max_rows=65), dict(nb=0), dict(mb=0),
                dict(mb=2 ** 27)):
         assert call(**kw) == pa.PA_ERR_RANGE, kw
-    # units of eight records are one launch dimension: 2^31 - 1 at most
+    # pairs of records are one launch dimension: 2^31 - 1 at most
     assert call(d=dims(pa, 1024, 1024), mb=2 ** 27 - 1, max_rows=2 ** 31 - 16) == pa.PA_ERR_RANGE
     for name in ("starts", "cache", "bt", "k", "v"):
         assert call(**{name: None}) == pa.PA_ERR_NULL, name
