@@ -34,6 +34,18 @@
 // look-ups, flags and copies took a warp 120 instructions a block, of 366 in all.  So one warp of the CTA
 // does it for all the others, a lane for each: a pass of its loop emits the next job of every consumer that has a
 // free stage.
+//
+// What bounds it: us replayed from a graph, 64 sequences of 64-4096 tokens.  12 / 2 heads (39 MB) 17.7; 32 / 8 heads (156
+// MB, 23.0 at the copy rate) 42.0, the fused step 48.0; one sequence of 2048 tokens 6.7, latency.  Of the 42 about 30 go
+// between a CTA's first record and its last; before them 1.4 for the prefix and 3 for lengths, ids and record, after
+// them the merge's 2.7.  Without the products the same call takes 33, without copies and feeder 32: matrix operands cost
+// 80 masks and shifts a block and head, and with the scales and the softmax 134 instructions of 280 go to the ALU,
+// which takes one in two cycles; bulk copies of this size leave an SM one in about 80 cycles.  Both together cover most
+// of the 52,000 cycles, and what was tried moves between them (32 / 8 heads): each warp feeding itself 44.6; the feeder
+// describing jobs and each warp asking for its own copies 47.5, by cp.async 48.1; cp.async by 1, 2, 3 or 4 feeders 60,
+// 46.0, 43.4, 44.0; two feeders for bulk copies 43.2; block ids asked for a job ahead 45.0; 7, 13 or 15 consumers 48.4,
+// 44.1, 43.0 (the last with 128 registers); the right shift as a product's upper half 44.8; jobs of four blocks 46.7.
+// The step's 6 us over the decode: quantising and storing 2, rotating q 1.5, its rows 1.2, fewer stages the rest.
 
 #include <mutex>
 
