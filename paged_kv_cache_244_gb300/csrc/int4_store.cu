@@ -9,11 +9,13 @@
 // vectors a pass) with a few bytes out in the place of a row.
 //
 // Bound: rows in, q and codes out.  23,738 rows of 32 / 8 heads (525 MB with a cos/sin row each; 77 us at the copy rate)
-// take 95.7 us, 5.5 TB/s: the row's arithmetic (2,780 warp instructions a token, extremes and codes most of them) keeps
-// the issue slots 57% busy between the loads.  256 rows of 12 / 2 heads: 2.8 us, an empty kernel's 1.9 and the load
-// latencies.  CTAs of 2 / 4 / 8 / 16 warps, as many an SM: 95.7 / 96.2 / 97.8 / 115 us (2.8 / 2.8 / 3.1 / 3.4): a token
-// that is done makes room for the next.  24 warps of 80 registers an SM and two passes of loads ahead: with 32 or 40
-// warps, or one pass or three, 95 - 109.
+// take 85.2 us, 6.16 TB/s.  The row's arithmetic (3,000 warp instructions a token, extremes and codes most of them) fills 70%
+// of the issue slots, so a warp's next rows have to be on their way meanwhile: by cp.async, six passes ahead.  (Rows of two
+// passes asked for at once and waited for 95.7; their registers loaded again as soon as a pass is done 112, as the compiler
+// then waits for them before the next; three to eight passes ahead 84.5 - 86.5.)  256 rows of 12 / 2 heads: 2.8 us, an
+// empty kernel's 1.9 and the load latencies.  18 warps an SM, so that none spills: 16, 20 - 24, 32 warps 86.5, 85.6 - 90.7,
+// 91.7.  CTAs of two warps, as a token that is done makes room for the next (of 8: 2% more, and 3.1 for 256 rows); warps
+// that go through tokens in a fixed order 99 - 113.
 
 #include "int4_cache.cuh"
 #include "int4_launch.h"
@@ -59,11 +61,16 @@ __device__ __forceinline__ void int4_rotate_chunks(uint4& x, uint4& y, const Ang
   }
 }
 
-// One warp, one token: its groups of 4 kGroup head vectors part, part + parts, ..: queries rotated into
-// q_out, keys (rotated) and values quantised into the token's slot.
-template <bool kInterleaved, int kGroup>
-__global__ void __launch_bounds__(kStoreWarps * 32, 24 / kStoreWarps) rope_int4_store_kernel(const RopeFormArgs a) {
+// One warp, one token: its pairs of passes of four head vectors part, part + parts, ..: queries rotated into q_out, keys
+// (rotated) and values quantised into the token's slot.  Rows come by cp.async, kStoreAhead passes ahead, and every lane
+// reads the chunks that it asked for.
+constexpr int kStoreAhead = 6;
+static_assert(kStoreAhead <= 8, "groups that a wait can name");
+
+template <bool kInterleaved>
+__global__ void __launch_bounds__(kStoreWarps * 32, 18 / kStoreWarps) rope_int4_store_kernel(const RopeFormArgs a) {
   __shared__ uint4 s_extremes[kStoreWarps][4][4];   // of a pass's vectors, a word for each 8 dims
+  __shared__ uint4 s_rows[kStoreWarps][kStoreAhead][2][32];
   pdl_wait_prior_grid();
   pdl_allow_next_grid();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -75,25 +82,25 @@ __global__ void __launch_bounds__(kStoreWarps * 32, 24 / kStoreWarps) rope_int4_
   const int all = Hq + 2 * Hkv;
   int ca, cb;
   lane_chunks<kInterleaved>(j, R, ca, cb);
-  uint4 x[kGroup], y[kGroup];
-  auto load_group = [&](int base) {
-#pragma unroll
-    for (int p = 0; p < kGroup; ++p) {
-      const int i = base + 4 * p + sub;
-      x[p] = y[p] = make_uint4(0u, 0u, 0u, 0u);
-      if (i >= all) continue;
+  const int part = static_cast<int>(blockIdx.y), parts = static_cast<int>(gridDim.y);
+  auto first_of = [&](int n) { return 8 * (part + (n >> 1) * parts) + 4 * (n & 1); };   // vector of the n-th pass
+  const uint32_t rows = smem_addr(s_rows[warp]) + 16 * lane;
+  auto ask = [&](int n, int slot) {
+    const int i = first_of(n) + sub;
+    if (i < all) {
       const __nv_bfloat16* src;
       if (i < Hq) src = a.q + (static_cast<size_t>(t) * Hq + i) * kHeadDim;
       else if (i < Hq + Hkv) src = a.k + (static_cast<size_t>(t) * Hkv + (i - Hq)) * kHeadDim;
       else src = a.v + (static_cast<size_t>(t) * Hkv + (i - Hq - Hkv)) * kHeadDim;
-      x[p] = reinterpret_cast<const uint4*>(src)[ca];
-      y[p] = reinterpret_cast<const uint4*>(src)[cb];
+      cp_async16(rows + 1024 * slot, reinterpret_cast<const uint4*>(src) + ca);
+      cp_async16(rows + 1024 * slot + 512, reinterpret_cast<const uint4*>(src) + cb);
     }
+    cp_async_commit();
   };
   const int pos = a.positions[t];
   const int64_t slot = a.slot_mapping[t];
-  const int first = 4 * kGroup * static_cast<int>(blockIdx.y), step = 4 * kGroup * static_cast<int>(gridDim.y);
-  load_group(first);
+#pragma unroll
+  for (int n = 0; n < kStoreAhead; ++n) ask(n, n);
   const bool has_pos = pos >= 0 && pos < a.max_pos;
   if (!has_pos && lane == 0) raise_flag(a.status, PA_FLAG_POSITION_OOB);
   bool store = has_pos && slot >= 0;
@@ -101,7 +108,10 @@ __global__ void __launch_bounds__(kStoreWarps * 32, 24 / kStoreWarps) rope_int4_
     if (lane == 0) raise_flag(a.status, PA_FLAG_SLOT_OOB);
     store = false;
   }
-  if (!has_pos && a.q == a.q_out) return;  // left as it is
+  if (!has_pos && a.q == a.q_out) {                 // left as it is
+    cp_async_wait_but(0);
+    return;
+  }
   const int64_t blk = store ? slot / kBlockSize : 0;
   const int off = store ? static_cast<int>(slot - blk * kBlockSize) : 0;
   uint8_t* const records = static_cast<uint8_t*>(a.k_cache) + static_cast<size_t>(blk) * Hkv * kInt4Record;
@@ -109,60 +119,60 @@ __global__ void __launch_bounds__(kStoreWarps * 32, 24 / kStoreWarps) rope_int4_
   Angles ang = {};
   if (turns) ang = load_angles(a.cos_sin, pos, R, j);
   const int items = store ? all : Hq;
-  for (int base = first; base < items; base += step) {
-    if (base != first) load_group(base);
+  int at = 0;
+  // (a pass's place is asked for again when it is done, by the lanes that read it)
+  for (int n = 0; first_of(n) < items; ask(n + kStoreAhead, at), ++n, at = at + 1 == kStoreAhead ? 0 : at + 1) {
+    const int base = first_of(n), i = base + sub;
+    cp_async_wait_but(kStoreAhead - 1);
+    __syncwarp();
+    uint4 x = s_rows[warp][at][0][lane], y = s_rows[warp][at][1][lane];
+    if (i < Hq) {
+      if (turns) rotate_chunks<kInterleaved>(x, y, ang);
+      uint4* dst = reinterpret_cast<uint4*>(a.q_out + (static_cast<size_t>(t) * Hq + i) * kHeadDim);
+      dst[ca] = x;
+      dst[cb] = y;
+    }
+    if (base + 3 < Hq || items == Hq) continue;     // the same for the whole warp
+    // keys and values (lanes of a query, or past the last vector, go along)
+    const bool is_k = i < Hq + Hkv, mine = i >= Hq && i < all;
+    if (turns && mine && is_k) int4_rotate_chunks<kInterleaved>(x, y, ang);
+    __syncwarp();
+    bool wild = false;
+    uint32_t ex = int4_extremes(x, wild), ey = int4_extremes(y, wild);
+    uint32_t* const words = reinterpret_cast<uint32_t*>(s_extremes[warp][sub]);
+    words[ca] = ex;
+    words[cb] = ey;
+    __syncwarp();
+    if (is_k) {
+      const uint4 ga = s_extremes[warp][sub][ca >> 2], gb = s_extremes[warp][sub][cb >> 2];
+      ex = __vmaxu2(__vmaxu2(ga.x, ga.y), __vmaxu2(ga.z, ga.w));
+      ey = __vmaxu2(__vmaxu2(gb.x, gb.y), __vmaxu2(gb.z, gb.w));
+    }
+    __syncwarp();                                 // before the next pass writes the words
+    ex = is_k ? ex : __vmaxu2(ex, ey);
 #pragma unroll
-    for (int p = 0; p < kGroup; ++p) {
-      if (base + 4 * p >= items) break;
-      const int i = base + 4 * p + sub;
-      if (i < Hq) {
-        if (turns) rotate_chunks<kInterleaved>(x[p], y[p], ang);
-        uint4* dst = reinterpret_cast<uint4*>(a.q_out + (static_cast<size_t>(t) * Hq + i) * kHeadDim);
-        dst[ca] = x[p];
-        dst[cb] = y[p];
-      }
-      if (base + 4 * p + 3 < Hq) continue;          // the same for the whole warp
-      if (items == Hq) continue;
-      // keys and values (lanes of a query, or past the last vector, go along)
-      const bool is_k = i < Hq + Hkv, mine = i >= Hq && i < all;
-      if (turns && mine && is_k) int4_rotate_chunks<kInterleaved>(x[p], y[p], ang);
-      __syncwarp();
-      bool wild = false;
-      uint32_t ex = int4_extremes(x[p], wild), ey = int4_extremes(y[p], wild);
-      uint32_t* const words = reinterpret_cast<uint32_t*>(s_extremes[warp][sub]);
-      words[ca] = ex;
-      words[cb] = ey;
-      __syncwarp();
-      if (is_k) {
-        const uint4 ga = s_extremes[warp][sub][ca >> 2], gb = s_extremes[warp][sub][cb >> 2];
-        ex = __vmaxu2(__vmaxu2(ga.x, ga.y), __vmaxu2(ga.z, ga.w));
-        ey = __vmaxu2(__vmaxu2(gb.x, gb.y), __vmaxu2(gb.z, gb.w));
-      }
-      __syncwarp();                                 // before the next pass writes the words
-      ex = is_k ? ex : __vmaxu2(ex, ey);
-#pragma unroll
-      for (int o = 1; o < 8; o <<= 1) {
-        const uint32_t other = __shfl_xor_sync(kFullMask, ex, o);
-        if (!is_k) ex = __vmaxu2(ex, other);
-      }
-      if (!mine) continue;
-      const Int4Scale qa = int4_scale(ex);
-      const Int4Scale qb = is_k ? int4_scale(ey) : qa;
-      uint8_t* const rec = records + static_cast<size_t>(is_k ? i - Hq : i - Hq - Hkv) * kInt4Record;
-      const uint32_t wa = int4_word(x[p], qa, wild), wb = int4_word(y[p], qb, wild);
-      if (is_k) {
-        *reinterpret_cast<uint32_t*>(rec + int4_k_word(off, ca)) = wa;
-        *reinterpret_cast<uint32_t*>(rec + int4_k_word(off, cb)) = wb;
-        uint16_t* const scales = reinterpret_cast<uint16_t*>(rec + kInt4KScales + 8 * off);
-        if ((ca & 3) == 0) scales[ca >> 2] = static_cast<uint16_t>(qa.word);
-        if ((cb & 3) == 0) scales[cb >> 2] = static_cast<uint16_t>(qb.word);
-      } else {
-        *reinterpret_cast<uint32_t*>(rec + int4_v_word(off, ca)) = wa;
-        *reinterpret_cast<uint32_t*>(rec + int4_v_word(off, cb)) = wb;
-        if (j == 0) *reinterpret_cast<uint16_t*>(rec + kInt4VScales + 2 * off) = static_cast<uint16_t>(qa.word);
-      }
+    for (int o = 1; o < 8; o <<= 1) {
+      const uint32_t other = __shfl_xor_sync(kFullMask, ex, o);
+      if (!is_k) ex = __vmaxu2(ex, other);
+    }
+    if (!mine) continue;
+    const Int4Scale qa = int4_scale(ex);
+    const Int4Scale qb = is_k ? int4_scale(ey) : qa;
+    uint8_t* const rec = records + static_cast<size_t>(is_k ? i - Hq : i - Hq - Hkv) * kInt4Record;
+    const uint32_t wa = int4_word(x, qa, wild), wb = int4_word(y, qb, wild);
+    if (is_k) {
+      *reinterpret_cast<uint32_t*>(rec + int4_k_word(off, ca)) = wa;
+      *reinterpret_cast<uint32_t*>(rec + int4_k_word(off, cb)) = wb;
+      uint16_t* const scales = reinterpret_cast<uint16_t*>(rec + kInt4KScales + 8 * off);
+      if ((ca & 3) == 0) scales[ca >> 2] = static_cast<uint16_t>(qa.word);
+      if ((cb & 3) == 0) scales[cb >> 2] = static_cast<uint16_t>(qb.word);
+    } else {
+      *reinterpret_cast<uint32_t*>(rec + int4_v_word(off, ca)) = wa;
+      *reinterpret_cast<uint32_t*>(rec + int4_v_word(off, cb)) = wb;
+      if (j == 0) *reinterpret_cast<uint16_t*>(rec + kInt4VScales + 2 * off) = static_cast<uint16_t>(qa.word);
     }
   }
+  cp_async_wait_but(0);
 }
 
 // ---- reading back ------------------------------------------------------------------------------
@@ -239,8 +249,8 @@ cudaError_t launch_rope_int4_store(const RopeFormArgs& a, cudaStream_t stream) {
   constexpr unsigned kRoom = 2432 / kStoreWarps;
   const int room = static_cast<int>(kRoom / (token_ctas > kRoom ? kRoom : token_ctas));
   cudaLaunchConfig_t cfg = chained(dim3(token_ctas, groups < room ? groups : room), kStoreWarps * 32, &attr, stream);
-  return a.interleaved ? cudaLaunchKernelEx(&cfg, rope_int4_store_kernel<true, 2>, a)
-                       : cudaLaunchKernelEx(&cfg, rope_int4_store_kernel<false, 2>, a);
+  return a.interleaved ? cudaLaunchKernelEx(&cfg, rope_int4_store_kernel<true>, a)
+                       : cudaLaunchKernelEx(&cfg, rope_int4_store_kernel<false>, a);
 }
 
 cudaError_t launch_read_int4(const ReadInt4Args& a, cudaStream_t stream) {
