@@ -162,7 +162,7 @@ def test_read_skips_what_is_out_of_range(pa):
 
 @pytest.mark.parametrize("layout", ["half", "interleaved"])
 @pytest.mark.parametrize("Rr,T,hq,kv", [(128, 37, 12, 2), (64, 1, 8, 8), (16, 50, 5, 1), (96, 19, 9, 3), (112, 330, 4, 4),
-                                        (48, 9, 64, 8), (80, 70, 28, 4), (32, 3, 7, 7)])
+                                        (48, 9, 64, 8), (80, 70, 28, 4), (32, 3, 7, 7), (128, 3, 1, 1), (16, 2600, 3, 3)])
 def test_store_bit_for_bit(pa, layout, Rr, T, hq, kv):
     rng = np.random.default_rng(Rr + T)
     nb = (T + B - 1) // B + 3
