@@ -524,6 +524,9 @@ int pa_prefill_fp8_block(const pa_dims* dims, int num_seqs, int num_tokens, cons
  *    codes, 64 bytes a token (dims 32 u .. + 31 are 16-byte unit u ^ (token / 2 % 4), eight dims a word in order); 2048 K
  *    scale words, four a token; 2176 V scale words, one a token.  The codes of a word's eight dims, from its lowest
  *    bits: dims 0, 2, 4, 6, 1, 3, 5, 7.
+ *  - A slot of zeros, as a cleared cache has them, reads as zeros in every call: a token within the context that nothing
+ *    was stored in (a store or a fused step that left it out) counts with a score and a value of 0.  Other words whose s
+ *    is outside the range have no meaning.
  *  - A row is quantised by itself: a store writes the bytes of its slots and no others, and depends on nothing that
  *    the block held before.  A block (Hkv records) is copied as bytes, by the caller: pa_copy_blocks takes bf16
  *    caches.

@@ -684,7 +684,7 @@ INT4_RECORD_BYTES = 2208   # PA_INT4_RECORD_BYTES: 16 tokens of K and V of one K
 
 
 def int4_cache(num_blocks, num_kv_heads, device="cuda") -> torch.Tensor:
-    """An empty 4-bit cache: 16-token blocks, head_dim 128 (no initialisation is needed before tokens are stored)."""
+    """An empty 4-bit cache: 16-token blocks, head_dim 128.  Slots that nothing is stored in read as zeros."""
     return torch.zeros((num_blocks, num_kv_heads, INT4_RECORD_BYTES), dtype=torch.uint8, device=device)
 
 

@@ -498,13 +498,16 @@ __global__ void __launch_bounds__((kDiConsumers + 1) * 32, 1) decode_int4_kernel
       group(1, wa.y, wb.y, __uint_as_float(sa.x & 0xfff00000u), __uint_as_float(sb.x & 0xfff00000u));
       group(2, wa.z, wb.z, int4_scale_of(sa.y), int4_scale_of(sb.y));
       group(3, wa.w, wb.w, __uint_as_float(sa.y & 0xfff00000u), __uint_as_float(sb.y & 0xfff00000u));
-      const float ea = lg2(va), eb = lg2(vb);
+      // 2^-65 more: nothing to a scale of 2^-40 or more, and a slot of zeros (a cleared cache that nothing was stored in)
+      // counts in L like any token of its score, with codes of zero
+      const float sva = va + 0x1p-65f, svb = vb + 0x1p-65f;
+      const float ea = lg2(sva), eb = lg2(svb);
       y[i][0] = fmaf(x[0], kf0, ea);
       y[i][1] = fmaf(x[1], kf1, ea);
       y[i][2] = fmaf(x[2], kf0, eb);
       y[i][3] = fmaf(x[3], kf1, eb);
-      iv[i][0] = rcp_ftz(va);
-      iv[i][1] = rcp_ftz(vb);
+      iv[i][0] = rcp_ftz(sva);
+      iv[i][1] = rcp_ftz(svb);
     };
     // Most jobs are two whole blocks: theirs is a path without a branch, whose blocks interleave.
     const bool full = (fl & (kTwo | kHas0 | kHas1)) == (kTwo | kHas0 | kHas1) && valid == kBlockSize;
