@@ -27,6 +27,8 @@
 //     lane gets the sum for its own head columns, over the same rounded p as the codes' sums.
 // V's scale acts on the exponent and cancels in L, so p stays within f16 whatever the scales: the shift m is
 // set 7 below the largest contribution and moves when one passes it by more than 15.  L adds the unrounded p.
+// Where a shift passes 2^10, log2 s would be rounded away next to the score, and the piece forms e_th as
+// (scale_log2 x_th - base) + log2 s_t from there on (kFarShift).
 //
 // A job is up to two neighbouring blocks of a piece in one stage of the warp's ring.  A record is one run of memory, so
 // each of a stage's few runs (two records, q of a piece's first job, the step's rows) is one bulk copy.  Where 16
@@ -48,6 +50,7 @@
 // The step's 6 us over the decode: quantising and storing 2, rotating q 1.5, its rows 1.2, fewer stages the rest.
 
 #include <mutex>
+#include <type_traits>
 
 #include "int4_cache.cuh"
 #include "int4_launch.h"
@@ -76,6 +79,11 @@ constexpr uint32_t kTwo = 1u << 13, kHas0 = 1u << 14, kHas1 = 1u << 15;
 
 // A shift below every score (they are finite, and below 2^123): weights of no key so far are 0, not NaN.
 constexpr float kNoShift = -3.402823466e38f;
+
+// Shifts up to this size (in the exponent, so scores up to 710 or so) keep log2 s to 2^-14 where it is added to a score.
+// Past it the addition would round the scales of V away (by 2^-4 at 2^20, whole at 2^26) while L still divides by them, so
+// a piece goes on with each head's scores counted from its largest one, which leaves near ones exact.
+constexpr float kFarShift = 0x1p10f;
 
 // Pairs of codes as f16: of a word's neighbouring pairs shifted by 3, the first c 2^-21 and the second c 2^-17.
 constexpr uint32_t kPairA = 0x00780078u, kPairB = 0x07800780u;
@@ -300,7 +308,9 @@ __global__ void __launch_bounds__((kDiConsumers + 1) * 32, 1) decode_int4_kernel
   uint32_t qb[8][2];                      // B operand: dims 32c + 8cq .. + 7 of head gq, k permuted as the codes are
   uint32_t qsum[2];                       // B operand: -Q of group cq of head gq as three bf16 numbers
   float kf0 = 0.f, kf1 = 0.f;             // what turns x of head columns 2cq, 2cq + 1 into the exponent
-  float m0 = kNoShift, m1 = kNoShift;     // softmax shifts of those columns
+  float m0 = kNoShift, m1 = kNoShift;     // softmax shifts of those columns, from their bases:
+  float base0 = 0.f, base1 = 0.f;         // 0, or with `far` the largest score so far
+  bool far = false;                       // of the piece, the same in every lane
   float l0 = 0.f, l1 = 0.f;               // this lane's share of L
   float o[8][4];                          // sums of p c: [2u + i] = rows gq, gq + 8: code pairs 2i, 2i + 1 of unit u
   float z[4];                             // sums of p z (two and two alike)
@@ -456,6 +466,8 @@ __global__ void __launch_bounds__((kDiConsumers + 1) * 32, 1) decode_int4_kernel
     if (fl & kFirst) {
       load_q(stage, fl);
       m0 = m1 = kNoShift;
+      base0 = base1 = 0.f;
+      far = false;
       l0 = l1 = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
@@ -470,7 +482,8 @@ __global__ void __launch_bounds__((kDiConsumers + 1) * 32, 1) decode_int4_kernel
     // Exponents before the shift: [i][0] = (token gq of block i, head 2cq), [1] = (gq, 2cq + 1), [2] = (gq + 8,
     // 2cq), [3] = (gq + 8, 2cq + 1); and 1 / s of V of tokens gq, gq + 8.
     float y[kDiJob][4], iv[kDiJob][2];
-    auto scores = [&](int i) {
+    float ev[kDiJob][2];                             // log2 s of V of tokens gq, gq + 8 (used with `far`)
+    auto scores = [&](int i, auto apart) {           // apart: y without log2 s of V
       const uint32_t rec = kt + i * kInt4Record;
       const uint4 wa = lds128(rec + 64 * gq + 16 * cq), wb = lds128(rec + 64 * gq + 512 + 16 * cq);
       const uint2 sa = lds64(rec + kInt4KScales + 8 * gq), sb = lds64(rec + kInt4KScales + 64 + 8 * gq);
@@ -502,45 +515,99 @@ __global__ void __launch_bounds__((kDiConsumers + 1) * 32, 1) decode_int4_kernel
       // counts in L like any token of its score, with codes of zero
       const float sva = va + 0x1p-65f, svb = vb + 0x1p-65f;
       const float ea = lg2(sva), eb = lg2(svb);
-      y[i][0] = fmaf(x[0], kf0, ea);
-      y[i][1] = fmaf(x[1], kf1, ea);
-      y[i][2] = fmaf(x[2], kf0, eb);
-      y[i][3] = fmaf(x[3], kf1, eb);
+      if constexpr (decltype(apart)::value) {
+        y[i][0] = __fmul_rn(x[0], kf0);
+        y[i][1] = __fmul_rn(x[1], kf1);
+        y[i][2] = __fmul_rn(x[2], kf0);
+        y[i][3] = __fmul_rn(x[3], kf1);
+        ev[i][0] = ea;
+        ev[i][1] = eb;
+      } else {
+        y[i][0] = fmaf(x[0], kf0, ea);
+        y[i][1] = fmaf(x[1], kf1, ea);
+        y[i][2] = fmaf(x[2], kf0, eb);
+        y[i][3] = fmaf(x[3], kf1, eb);
+      }
       iv[i][0] = rcp_ftz(sva);
       iv[i][1] = rcp_ftz(svb);
     };
     // Most jobs are two whole blocks: theirs is a path without a branch, whose blocks interleave.
     const bool full = (fl & (kTwo | kHas0 | kHas1)) == (kTwo | kHas0 | kHas1) && valid == kBlockSize;
-    if (full) {
-#pragma unroll
-      for (int i = 0; i < kDiJob; ++i) scores(i);
-    } else {
+    auto each_block = [&](auto apart) {
 #pragma unroll
       for (int i = 0; i < kDiJob; ++i) {
         y[i][0] = y[i][1] = y[i][2] = y[i][3] = -INFINITY;
         iv[i][0] = iv[i][1] = 0.f;
         if (i == 1 && !two) continue;
-        scores(i);
+        scores(i, apart);
         // tokens past the context, and absent blocks, may hold anything
         const int n = !(fl & (i ? kHas1 : kHas0)) ? 0 : i == 1 || !two ? valid : kBlockSize;
         if (gq >= n) y[i][0] = y[i][1] = -INFINITY, iv[i][0] = 0.f;
         if (gq + 8 >= n) y[i][2] = y[i][3] = -INFINITY, iv[i][1] = 0.f;
       }
       __syncwarp();
-    }
-    float top0 = -INFINITY, top1 = -INFINITY;
+    };
+    float top0, top1;
+    auto tops = [&] {                                // of this lane's tokens
+      top0 = top1 = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < kDiJob; ++i) {
-      top0 = fmax3(top0, y[i][0], y[i][2]);
-      top1 = fmax3(top1, y[i][1], y[i][3]);
-    }
-    if (__any_sync(kFullMask, top0 - m0 > 15.f || top1 - m1 > 15.f)) {
-      // A shift has to move (at a piece's first job from kNoShift): the maxima over the tokens, and what
-      // was summed so far scaled to the new shifts.
+      for (int i = 0; i < kDiJob; ++i) {
+        top0 = fmax3(top0, y[i][0], y[i][2]);
+        top1 = fmax3(top1, y[i][1], y[i][3]);
+      }
+    };
+    auto over_tokens = [&] {
 #pragma unroll
       for (int x = 4; x < 32; x <<= 1) {
         top0 = fmaxf(top0, __shfl_xor_sync(kFullMask, top0, x));
         top1 = fmaxf(top1, __shfl_xor_sync(kFullMask, top1, x));
+      }
+    };
+    if (!far) {
+      if (full) {
+#pragma unroll
+        for (int i = 0; i < kDiJob; ++i) scores(i, std::false_type{});
+      } else {
+        each_block(std::false_type{});
+      }
+      tops();
+    }
+    const bool near = !far && !__any_sync(kFullMask, top0 - m0 > 15.f || top1 - m1 > 15.f);
+    if (!near) {
+      // A shift may have to move (at a piece's first job from kNoShift): the maxima over the tokens, and what
+      // was summed so far scaled to the new shifts.
+      if (!far) {
+        over_tokens();
+        far = __any_sync(kFullMask, (top0 - m0 > 15.f && fabsf(top0) > kFarShift) || (top1 - m1 > 15.f && fabsf(top1) > kFarShift));
+        if (far) {                                   // what there is so far is counted from its shift
+          if (m0 != kNoShift) base0 = m0, m0 = 0.f;
+          if (m1 != kNoShift) base1 = m1, m1 = 0.f;
+        }
+      }
+      if (far) {
+        // Scores by themselves, rounded; their differences to the base are exact where they matter, and log2 s is added
+        // to those.  A base moves up to the largest score, so that one is at most 0 from it and a shift some
+        // 90 at most; without keys so far it is set to it.
+        each_block(std::true_type{});
+        tops();
+        over_tokens();
+        auto rebase = [](float top, float& base, float& m) {
+          const float to = m == kNoShift ? (top == -INFINITY ? base : top) : fmaxf(base, top);
+          if (m != kNoShift) m -= to - base;
+          base = to;
+        };
+        rebase(top0, base0, m0);
+        rebase(top1, base1, m1);
+#pragma unroll
+        for (int i = 0; i < kDiJob; ++i) {
+          if (i == 1 && !two) continue;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (y[i][c] != -INFINITY) y[i][c] = y[i][c] - ((c & 1) ? base1 : base0) + ev[i][c >> 1];
+        }
+        __syncwarp();
+        tops();
+        over_tokens();
       }
       const float mn0 = top0 - m0 > 15.f ? top0 - 7.f : m0, mn1 = top1 - m1 > 15.f ? top1 - 7.f : m1;
       const float al0 = mn0 == m0 ? 1.f : ex2_ftz(m0 - mn0), al1 = mn1 == m1 ? 1.f : ex2_ftz(m1 - mn1);
@@ -602,7 +669,15 @@ __global__ void __launch_bounds__((kDiConsumers + 1) * 32, 1) decode_int4_kernel
       }
       const bool piece_whole = (fl & kWhole) != 0;
       // a sequence whose every block is out of range has L = 0 and gives zeros
-      const float f0 = piece_whole ? (L0 == 0.f ? 0.f : 1.f / L0) : 1.f, f1 = piece_whole ? (L1 == 0.f ? 0.f : 1.f / L1) : 1.f;
+      float f0 = piece_whole ? (L0 == 0.f ? 0.f : 1.f / L0) : 1.f, f1 = piece_whole ? (L1 == 0.f ? 0.f : 1.f / L1) : 1.f;
+      if (far && !piece_whole) {
+        // the merge's shift is one number: the base, and the rest goes into the sums (2^m, |m| of some 90 at most)
+        if (m0 != kNoShift) f0 = ex2_ftz(m0), m0 = base0;
+        if (m1 != kNoShift) f1 = ex2_ftz(m1), m1 = base1;
+        L0 *= f0;
+        L1 *= f1;
+      }
+      __syncwarp();
       const size_t row = (piece_whole ? static_cast<size_t>(d.x) : static_cast<size_t>(d.z)) * G + 2 * cq;
 #pragma unroll
       for (int u = 0; u < 4; ++u) {

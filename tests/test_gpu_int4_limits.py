@@ -1,6 +1,8 @@
-"""The 4-bit cache's attention where test_gpu_int4 does not go: slots that nothing was stored in.
+"""The 4-bit cache's attention where test_gpu_int4 does not go: slots that nothing was stored in, and scores far from zero.
 
-Tolerances are those of test_gpu_int4 (`close`), derived there.
+Tolerances are those of test_gpu_int4 (`close`), derived there.  Scores here are exact in fp32 where they are large: q has
+powers of two and small multiples of 1/2 in two dims, K small integers, and the softmax scale is the number whose product
+with log2 e rounds to 1, so that a rounding of the score itself is in no bound.
 """
 
 from __future__ import annotations
@@ -10,9 +12,19 @@ import pytest
 import torch
 
 import int4_ref as R
+import serving_ref as S
 from test_gpu_int4 import B, D, Pool, bf16, bits, clean, close, f64, normal, pa, table_of, turned, up  # noqa: F401
 
 pytestmark = pytest.mark.gpu
+
+
+def unit_scale() -> float:
+    """The fp32 number whose fp32 product with log2 e is 1."""
+    x = np.float32(np.log(2.0))
+    for c in (x, np.nextafter(x, np.float32(0)), np.nextafter(x, np.float32(1))):
+        if np.float32(c) * np.float32(1.4426950408889634) == np.float32(1.0):
+            return float(c)
+    raise AssertionError
 
 
 # ---- slots that nothing was stored in ------------------------------------------------------
@@ -91,3 +103,126 @@ def test_step_past_the_table_into_a_cleared_cache(pa):
     p.cache = cache.cpu().numpy()
     # rotated as the store rotates, which may be a bf16 step from 64 bits: the test is that the row is a number
     assert np.isfinite(f64(out[1])).all()
+
+
+# ---- scores far from zero ------------------------------------------------------------------
+
+CUTS = [[70, 33, 1], [2000, 900]]                           # whole pieces, and split ones
+
+
+@pytest.mark.parametrize("lens", CUTS)
+@pytest.mark.parametrize("size", [1.0, 2.0 ** 11, 2.0 ** 16, 2.0 ** 24, 2.0 ** 60, 3e38])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_tied_scores_of_any_size(pa, lens, size, sign):
+    """Keys that are all alike weigh the same however large their score is, and the scales of V decide nothing."""
+    rng = np.random.default_rng(43)
+    kv, hq = 2, 6
+    p = Pool(rng, lens, kv)
+    row = rng.integers(0, 256, 64, dtype=np.uint8)
+    words = np.array([0x3F80, 0x3FB5, 0x3F17, 0x3FC9], np.uint16).view(np.uint8)
+    for t in range(B):
+        live = p.cache[..., R.V_SCALES + 2 * t + 1] != 0xFF  # canaries stay
+        p.cache[live, 64 * t:64 * t + 64] = row
+        p.cache[live, R.K_SCALES + 8 * t:R.K_SCALES + 8 * t + 8] = words
+        e = rng.integers(-6, 7, live.sum()) + 127
+        word = (e << 7 | rng.integers(0, 8, live.sum()) << 4 | rng.integers(3, 13, live.sum())).astype(np.uint16)
+        p.cache[live, R.V_SCALES + 2 * t:R.V_SCALES + 2 * t + 2] = word[:, None].view(np.uint8)
+    q = sign * size * np.abs(np.sign(normal(rng, len(lens), hq, D)))
+    args = (p.dev(), up(p.tables), up(p.lens))
+    dec = pa.decode_int4(bf16(q), *args, max(lens), 1.0)
+    pre = pa.prefill_int4(bf16(q), up(np.arange(len(lens) + 1, dtype=np.int32)), *args, 1, max(lens), 1.0)
+    for s, n in enumerate(lens):
+        ref = p.attention(s, np.zeros((1, hq, D)), 1.0)     # even weights
+        close(dec[s:s + 1], ref, ("decode", s), steps=n // 16 + 1)
+        close(pre[s:s + 1], ref, ("prefill", s), prefill=True)
+    clean(pa)
+
+
+def levels(cache, ids, kv, level):
+    """K of the blocks `ids` [n] (tokens in order): dim 0 is level [16 n], dim 32 is 15, in units; dims 1 - 31 and 33 - 63 as the
+    codes are."""
+    one = torch.tensor([0x80, 0x3F], dtype=torch.uint8, device=cache.device)       # s = 1, z = 0
+    level = level.view(-1, B).to(torch.uint8)
+    for t in range(B):
+        a = cache[ids, :, 64 * t]
+        cache[ids, :, 64 * t] = (a & 0xF0) | level[:, t, None]
+        b = cache[ids, :, 64 * t + 4]
+        cache[ids, :, 64 * t + 4] = b | 0x0F
+        cache[ids, :, R.K_SCALES + 8 * t:R.K_SCALES + 8 * t + 2] = one
+        cache[ids, :, R.K_SCALES + 8 * t + 2:R.K_SCALES + 8 * t + 4] = one
+
+
+def random_cache(seed, nb, kv):
+    """Random records, made on the GPU: elements of K and V of a few units of 2^-3, V of scales over 2^-6 .. 2^0."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    cache = torch.randint(0, 256, (nb, kv, R.RECORD), dtype=torch.uint8, device="cuda", generator=gen)
+
+    def some(lo, hi, n):
+        return torch.randint(lo, hi, (nb, kv, n), device="cuda", generator=gen)
+
+    n = (R.RECORD - R.K_SCALES) // 2
+    word = (some(121, 128, n) << 7 | some(0, 8, n) << 4 | some(3, 13, n)).to(torch.int16)
+    cache[..., R.K_SCALES:] = word.view(torch.uint8)
+    return cache
+
+
+def rising(n, period):
+    """Levels 0 to 3 of a period: a quarter, a quarter, half but one token, one token.  A level's tokens together weigh
+    less than the one behind them, by 16.5 in the exponent, yet as many as they are they show."""
+    at = torch.arange(n) % period
+    lv = (at >= period // 4).int() + (at >= period // 2).int() + (at == period - 1).int()
+    return lv.cuda()
+
+
+@pytest.mark.parametrize("base", [0.0, 66.0, -66.0, 2.0 ** 8, -(2.0 ** 8), 2.0 ** 16, -(2.0 ** 16)])
+@pytest.mark.parametrize("seqs,n,kv", [(64, 4096, 8), (3, 300, 2), (1, 5000, 1)])
+def test_maxima_that_rise_within_a_warp(pa, base, seqs, n, kv):
+    """The running maximum rises by 16.5 up to three times a period of 312 tokens or of the whole context, over scores of 0 or of
+    15 `base`; from 66 the last rise passes 2^10.  64 sequences of 4096 tokens: a warp goes through some 78 blocks, 39 jobs."""
+    hq, nb = 2 * kv, seqs * ((n + B - 1) // B) + 3
+    mb = (n + B - 1) // B
+    cache = random_cache(44, nb, kv)
+    gen = torch.Generator(device="cuda").manual_seed(45)
+    tables = torch.randperm(nb, device="cuda", generator=gen)[: seqs * mb].view(seqs, mb)
+    for s in range(seqs):
+        levels(cache, tables[s], kv, rising(mb * B, 312 if s % 2 else n))
+    q = np.zeros((seqs, hq, D))
+    q[:, ::2, 0], q[:, 1::2, 0] = 16.5, -16.5               # odd heads see the maximum first
+    q[:, :, 32] = base
+    scale = unit_scale()
+    lens = torch.full((seqs,), n, dtype=torch.int32, device="cuda")
+    t32 = tables.to(torch.int32)
+    dec = pa.decode_int4(bf16(q), cache, t32, lens, n, scale)
+    pre = pa.prefill_int4(bf16(q), torch.arange(seqs + 1, dtype=torch.int32, device="cuda"), cache, t32, lens, 1, n, scale)
+    for s in sorted({0, 1, seqs // 2, seqs - 1} & set(range(seqs))):
+        own = cache[tables[s]].cpu().numpy()
+        ref = R.attention(q[s:s + 1], own, np.arange(mb), n, scale)
+        close(dec[s:s + 1], ref, ("decode", s), steps=n // 16 + 1)
+        close(pre[s:s + 1], ref, ("prefill", s), prefill=True)
+    clean(pa)
+
+
+@pytest.mark.parametrize("down", [False, True])
+@pytest.mark.parametrize("seqs,n,kv", [(32, 4096, 8), (3, 300, 2), (1, 5000, 1)])
+def test_near_and_far_heads_side_by_side(pa, down, seqs, n, kv):
+    """Heads of one group whose scores pass 2^10 on either side, at different tokens or never; levels that rise, or fall."""
+    group, mb = np.array([700.0, -700.0, 0.5, -16.5, 400.0, 2.0 ** 30, -(2.0 ** 30)]), (n + B - 1) // B
+    hq, nb = len(group) * kv, seqs * mb + 3
+    cache = random_cache(50, nb, kv)
+    tables = torch.randperm(nb, device="cuda", generator=torch.Generator(device="cuda").manual_seed(51))[: seqs * mb].view(seqs, mb)
+    for s in range(seqs):
+        lv = rising(mb * B, 312 if s % 2 else n)
+        levels(cache, tables[s], kv, 3 - lv if down else lv)
+    q = np.zeros((seqs, hq, D))
+    q[:, :, 0] = np.tile(group, kv)
+    lens, t32 = torch.full((seqs,), n, dtype=torch.int32, device="cuda"), tables.to(torch.int32)
+    scale = unit_scale()
+    assert np.array_equal(f64(bf16(group)), S.bf16_round(group))
+    q = f64(bf16(q))
+    dec = pa.decode_int4(bf16(q), cache, t32, lens, n, scale)
+    pre = pa.prefill_int4(bf16(q), torch.arange(seqs + 1, dtype=torch.int32, device="cuda"), cache, t32, lens, 1, n, scale)
+    for s in sorted({0, 1, seqs - 1} & set(range(seqs))):
+        ref = R.attention(q[s:s + 1], cache[tables[s]].cpu().numpy(), np.arange(mb), n, scale)
+        close(dec[s:s + 1], ref, ("decode", s), steps=n // 16 + 1)
+        close(pre[s:s + 1], ref, ("prefill", s), prefill=True)
+    clean(pa)
