@@ -226,7 +226,7 @@ __global__ void __launch_bounds__((kDiConsumers + 1) * 32, 1) decode_int4_kernel
       bool ready = rel < len;
       if (ready && fills >= n_st) ready = mbar_test(bar + 8, phase);
       if (!__any_sync(kFullMask, ready)) {
-        if (*fail) break;
+        if (__any_sync(kFullMask, *fail != 0)) break;   // together: the loop's votes want every lane
         const uint64_t now = global_ns();
         if (since == 0) since = now;
         if (__any_sync(kFullMask, now - since > kWaitLimitNs)) {
