@@ -241,6 +241,7 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32
 // Allocate `cols` columns (a power of two >= 32) for this CTA; the base address is written to
 // shared memory at `slot`.  Warp-collective; one warp allocates and later frees.
 __device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t cols) {
+  __syncwarp();  // the aligned form wants the whole warp at once, wherever its lanes come from
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols)
                : "memory");
 }
@@ -550,6 +551,7 @@ __device__ __forceinline__ void st_cluster_f4(uint32_t addr, float4 v) {
 
 // Barrier of `threads` threads of the block (named barrier `id`, 1..15).
 __device__ __forceinline__ void named_barrier(int id, int threads) {
+  __syncwarp();  // bar.sync is the aligned form
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 

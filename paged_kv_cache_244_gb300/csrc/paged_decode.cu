@@ -414,6 +414,7 @@ decode_partition_kernel(const __grid_constant__ CUtensorMap tm_k,
       for (int mt = 0; mt < 8; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
       if ((fl & kGap) && lane < G)  // mark the skipped slot before this piece empty
         a.ws_ml[(static_cast<size_t>(d.z) - 1) * G + lane] = make_float2(-INFINITY, 0.f);
+      __syncwarp();                                  // some lanes have stored; what follows wants the whole warp
     }
     if (fl & kHasData) {
       const int valid = static_cast<int>((fl >> 8) & 0xffu);

@@ -408,6 +408,7 @@ decode_block_kernel(const DecodeArgs a, const int pool) {
       for (int mt = 0; mt < 8; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
       if ((fl & kGap) && lane < G)                   // mark the skipped slot before this piece empty
         a.ws_ml[(static_cast<size_t>(d.z) - 1) * G + lane] = make_float2(-INFINITY, 0.f);
+      __syncwarp();                                  // some lanes have stored; what follows wants the whole warp
     }
     const bool two = (fl & kTwo) != 0;
     float4 sv = scales[st];

@@ -474,6 +474,7 @@ __global__ void __launch_bounds__((kDiConsumers + 1) * 32, 1) decode_int4_kernel
       z[0] = z[1] = z[2] = z[3] = 0.f;
       if ((fl & kGap) && lane < G)                   // mark the skipped slot before this piece empty
         a.ws_ml[(static_cast<size_t>(d.z) - 1) * G + lane] = make_float2(-INFINITY, 0.f);
+      __syncwarp();                                  // some lanes have stored; what follows wants the whole warp
     }
     const bool two = (fl & kTwo) != 0;
     const int valid = static_cast<int>((fl >> 8) & 0x1fu);   // rows of the job's last block

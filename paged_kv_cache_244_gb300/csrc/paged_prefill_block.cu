@@ -753,7 +753,6 @@ prefill_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             if (nan_from[64 * part + d] <= last_key)
               *reinterpret_cast<uint16_t*>(qbuf + r * 128 + (((d >> 3) ^ (r & 7)) << 4) + 2 * (d & 7)) = 0x7fc0;
         }
-        __syncwarp();
         named_barrier(1, 128);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {

@@ -596,7 +596,6 @@ prefill_int4_kernel(const PrefillArgs a) {
             *reinterpret_cast<uint4*>(qbuf + r * 128 + (((4 * q2 + k) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
           }
         }
-        __syncwarp();
         named_barrier(1, 128);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
