@@ -606,7 +606,7 @@ __device__ __forceinline__ void cp_async_wait_but(int later) {
 
 // Per CTA in shared memory: the block-count prefix N_s (S + 1 ints), then per sequence the
 // valid rows of its last block (1..16; one byte each).
-__host__ __device__ inline int prefix_bytes(int num_seqs) {
+__host__ __device__ constexpr int prefix_bytes(int num_seqs) {
   return (((num_seqs + 1) * 4 + 15) & ~15) + ((num_seqs + 15) & ~15);
 }
 

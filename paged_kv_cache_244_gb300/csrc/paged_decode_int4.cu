@@ -58,12 +58,12 @@
 namespace pa {
 namespace {
 
-constexpr int kDiConsumers = 11;                     // warps of a CTA that have ranges, at most; one more feeds them
+constexpr int kDiConsumers = 11;                     // warps of a CTA that have ranges; one more feeds them
 constexpr int kDiJob = 2;                            // blocks of a job at most
 // A stage: its job's descriptor, records, q rows of G heads, and for the step cos/sin (R <= 128 floats), k and v.
 constexpr int kDiRecOff = 32;
 constexpr int kDiQOff = kDiRecOff + kDiJob * kInt4Record;
-__host__ __device__ inline int di_stage(int G, bool step) {
+__host__ __device__ constexpr int di_stage(int G, bool step) {
   return kDiQOff + G * kHeadDim * 2 + (step ? kHeadDim * 4 + 2 * kHeadDim * 2 : 0);
 }
 constexpr int kDiMaxRing = 8;                        // stages of a warp
@@ -73,6 +73,9 @@ constexpr int kDiSmemMax = 226 * 1024;               // beside the static part o
 constexpr int kDiBarOff = 0;
 constexpr int kDiFailOff = kDiConsumers * kDiMaxRing * 16;
 constexpr int kDiPrefixOff = kDiFailOff + 16;
+// The largest call's step has two stages for every consumer, so all calls have the same ones, with and without the step: both
+// cut sequences alike and give the same bits.
+static_assert((kDiSmemMax - kDiPrefixOff - prefix_bytes(kMaxDecodeSeqs)) / di_stage(8, true) >= 2 * kDiConsumers, "stages");
 
 // More job flags: two blocks, and which of them are there (valid tokens of the last one at bits 8-12).
 constexpr uint32_t kTwo = 1u << 13, kHas0 = 1u << 14, kHas1 = 1u << 15;
@@ -154,14 +157,14 @@ __global__ void __launch_bounds__((kDiConsumers + 1) * 32, 1) decode_int4_kernel
   const int S = a.num_seqs;
   const int Hkv = a.num_kv_heads;
   const int G = a.num_q_heads / Hkv;
-  const int warps = static_cast<int>(blockDim.x >> 5) - 1;   // consumers
+  constexpr int warps = kDiConsumers;
   const int stage_bytes = di_stage(G, kStep);
   const int cos_off = kDiQOff + G * kHeadDim * 2;    // (step)
-  for (int i = threadIdx.x; i < warps * kDiMaxRing * 2; i += blockDim.x) mbar_init(raw + kDiBarOff + 8 * i, 1);
+  for (int i = threadIdx.x; i < warps * kDiMaxRing * 2; i += (warps + 1) * 32) mbar_init(raw + kDiBarOff + 8 * i, 1);
   volatile int* const fail = reinterpret_cast<volatile int*>(smem_raw + kDiFailOff);
   if (threadIdx.x == 0) *fail = 0;
   fence_mbar_init();
-  build_prefix<kDiConsumers + 1>(a, prefix, last_rows, blockDim.x);   // (a barrier of the CTA behind the above)
+  build_prefix<kDiConsumers + 1>(a, prefix, last_rows);   // (a barrier of the CTA behind the above)
   const long long T = static_cast<long long>(Hkv) * prefix[S];
   const Ranges R = make_ranges(T, a);
   // Range v goes to consumer v / grid of CTA v % grid; the CTA's stages are shared out among its consumers
@@ -767,24 +770,22 @@ cudaError_t launch_decode_int4(const DecodeArgs& args, cudaStream_t stream) {
   int max_ctas = 0;
   cudaError_t err = int4_ctas(&max_ctas);
   if (err != cudaSuccess) return err;
-  // Stages: what fits.  The warps are those that the step has two stages for, with and without it, so that both
-  // cut sequences alike and give the same bits.
+  // Stages: what fits.
   const int G = a.num_q_heads / a.num_kv_heads;
   const int fixed = kDiPrefixOff + prefix_bytes(a.num_seqs);
   const int stage = di_stage(G, step);
   const int pool = (kDiSmemMax - fixed) / stage;
-  const int warps = min(kDiConsumers, (kDiSmemMax - fixed) / di_stage(G, true) / 2);
   // no more CTAs than there can be ranges (they are dealt to the CTAs one at a time)
   const long long jobs = static_cast<long long>(a.num_seqs) * a.num_kv_heads *
                          ((a.max_context_len + kBlockSize - 1) / kBlockSize);
   const long long ctas = min(static_cast<long long>(max_ctas), (jobs + kMinRangeBlocks - 1) / kMinRangeBlocks);
-  a.num_warps = static_cast<int>(ctas) * warps;
+  a.num_warps = static_cast<int>(ctas) * kDiConsumers;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-  cfg.blockDim = dim3(static_cast<unsigned>((warps + 1) * 32));
+  cfg.blockDim = dim3(static_cast<unsigned>((kDiConsumers + 1) * 32));
   cfg.dynamicSmemBytes = fixed + pool * stage;
   cfg.stream = stream;
   cfg.attrs = attr;

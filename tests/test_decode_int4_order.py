@@ -43,3 +43,16 @@ def test_copies_in_flight_land_before_the_feeder_leaves():
     drain = "for (int k = max(0, fills - n_st); k < fills; ++k) mbar_wait_bounded(full_bars + 16 * (k % n_st), (k / n_st) & 1);"
     assert drain in source
     assert source.index(drain) < source.index("return;", source.index("while (__any_sync(kFullMask, rel < len)) {"))
+
+
+def test_every_call_has_the_same_consumers():
+    """11 warps at the limits of a call (8192 sequences, 8 heads a group), so none have fewer: the count is a constant."""
+    source = text()
+    number = {k: int(v) for k, v in re.findall(r"constexpr int (kDiConsumers|kDiMaxRing) = (\d+);", source)}
+    smem = eval(re.search(r"kDiSmemMax = ([\d* ]+);", source).group(1))          # noqa: S307
+    fixed = number["kDiConsumers"] * number["kDiMaxRing"] * 16 + 16 + (8193 * 4 + 15) // 16 * 16 + 8192
+    stage = 32 + 2 * 2208 + 8 * 256 + 512 + 2 * 256
+    assert (smem - fixed) // stage >= 2 * number["kDiConsumers"]
+    assert re.search(r"static_assert\(\(kDiSmemMax - kDiPrefixOff - prefix_bytes\(kMaxDecodeSeqs\)\) / di_stage\(8, true\) >= 2 \* kDiConsumers", source)
+    launch = source[source.index("cudaError_t launch_decode_int4("):]
+    assert "warps = min(" not in launch and "static_cast<int>(ctas) * kDiConsumers" in launch
