@@ -681,7 +681,6 @@ __global__ void __launch_bounds__((kDiConsumers + 1) * 32, 1) decode_int4_kernel
         L0 *= f0;
         L1 *= f1;
       }
-      __syncwarp();
       const size_t row = (piece_whole ? static_cast<size_t>(d.x) : static_cast<size_t>(d.z)) * G + 2 * cq;
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
