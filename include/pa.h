@@ -149,7 +149,7 @@ int pa_rope_kv_store(const pa_dims* dims, int num_tokens, void* q, const void* k
  * (log-sum-exp merge, in axis order).  P changes how the partial results are grouped, not how
  * the work is spread over the GPU.  Returns the request (0 or a positive multiple of
  * block_size) or a negative PA_ERR_* code (PA_ERR_RANGE also for num_seqs > 8192 or
- * max_context_len < 1).
+ * max_context_len < 1 or > 2^31 - 16, as in every decode call).
  */
 int pa_decode_partition_tokens(const pa_dims* dims, int num_seqs, int max_context_len,
                                int partition_tokens);

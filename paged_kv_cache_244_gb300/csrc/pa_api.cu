@@ -20,6 +20,9 @@ __device__ unsigned int g_pa_status;
 
 constexpr int kMaxDevices = 64;
 
+// Lengths that a decode call's bound may have: a length is rounded up to whole blocks in 32 bits.
+constexpr int kMaxDecodeLen = 0x7ffffff0;
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int check_dims(const pa_dims* d) {
@@ -36,7 +39,7 @@ int check_dims(const pa_dims* d) {
 // block size.  Returns it, or a negative PA_ERR_* code.
 int check_partition(const pa_dims* d, int num_seqs, int max_context_len, int requested) {
   if (const int rc = check_dims(d)) return rc;
-  if (num_seqs < 0 || num_seqs > pa::kMaxDecodeSeqs || max_context_len < 1) return PA_ERR_RANGE;
+  if (num_seqs < 0 || num_seqs > pa::kMaxDecodeSeqs || max_context_len < 1 || max_context_len > kMaxDecodeLen) return PA_ERR_RANGE;
   if (requested < 0 || requested % d->block_size != 0) return PA_ERR_RANGE;
   return requested;
 }
@@ -405,7 +408,7 @@ int gather_checksum(const pa_dims* dims, int num_seqs, const void* k_cache, cons
   if (num_seqs < 0 || num_seqs > pa::kMaxDecodeSeqs) return PA_ERR_RANGE;
   if (num_seqs == 0) return PA_OK;
   if (!k_cache || !v_cache || !block_tables || !context_lens || !out_xor) return PA_ERR_NULL;
-  if (num_blocks < 1 || max_blocks < 1 || max_context_len < 1) return PA_ERR_RANGE;
+  if (num_blocks < 1 || max_blocks < 1 || max_context_len < 1 || max_context_len > kMaxDecodeLen) return PA_ERR_RANGE;
   if (static_cast<long long>(max_context_len) > static_cast<long long>(max_blocks) * dims->block_size)
     return PA_ERR_RANGE;
   if (static_cast<long long>(num_blocks) * dims->num_kv_heads * dims->block_size > (1ll << 31))

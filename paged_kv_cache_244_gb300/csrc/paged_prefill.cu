@@ -588,7 +588,7 @@ cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((a.max_query_len + Tq - 1) / Tq),
+  cfg.gridDim = dim3(static_cast<unsigned>((a.max_query_len - 1) / Tq + 1),
                      static_cast<unsigned>(a.num_seqs * a.num_kv_heads));
   cfg.blockDim = dim3(static_cast<unsigned>(kPfThreads));
   cfg.dynamicSmemBytes = kPfSmem;

@@ -834,9 +834,9 @@ cudaError_t launch_prefill_block(const PrefillArgs& a, cudaStream_t stream) {
     }
   }
   // Split the keys while the grid leaves SMs without a CTA and each part keeps kMinSplitStages stages.
-  const long long tiles = (a.max_query_len + Tq - 1) / Tq;
+  const long long tiles = (a.max_query_len - 1) / Tq + 1;
   const long long pairs = static_cast<long long>(a.num_seqs) * a.num_kv_heads;
-  const int stages = (a.max_context_len + kBpKeys - 1) / kBpKeys;
+  const int stages = (a.max_context_len - 1) / kBpKeys + 1;
   int ranks = 1;
   while (ranks < 8 && stages >= kSplitFrom && tiles * pairs * ranks * 2 <= kSplitCtas && stages >= 2 * ranks * kMinSplitStages) ranks *= 2;
   cudaLaunchAttribute attr[2];

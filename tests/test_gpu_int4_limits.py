@@ -1,4 +1,4 @@
-"""The 4-bit cache's attention where test_gpu_int4 does not go: slots that nothing was stored in, and scores far from zero.
+"""The 4-bit cache's attention where test_gpu_int4 does not go: slots that nothing was stored in, scores far from zero, bounds near 2^31.
 
 Tolerances are those of test_gpu_int4 (`close`), derived there.  Scores here are exact in fp32 where they are large: q has
 powers of two and small multiples of 1/2 in two dims, K small integers, and the softmax scale is the number whose product
@@ -225,4 +225,28 @@ def test_near_and_far_heads_side_by_side(pa, down, seqs, n, kv):
         ref = R.attention(q[s:s + 1], cache[tables[s]].cpu().numpy(), np.arange(mb), n, scale)
         close(dec[s:s + 1], ref, ("decode", s), steps=n // 16 + 1)
         close(pre[s:s + 1], ref, ("prefill", s), prefill=True)
+    clean(pa)
+
+
+# ---- bounds near 2^31 ----------------------------------------------------------------------
+
+@pytest.mark.parametrize("hq", [1, 3])
+def test_prefill_with_the_loosest_bounds(pa, hq):
+    """A block table as wide as lengths of 32 bits allow, and both bounds at its end: tiles and stages round up without an overflow."""
+    rng = np.random.default_rng(48)
+    p = Pool(rng, [40], 1)
+    q = normal(rng, 5, hq, D)
+    wide, most = 1 << 27, 2 ** 31 - 1
+    tables = torch.full((1, wide), -1, dtype=torch.int32, device="cuda")
+    tables[0, : p.tables.shape[1]] = up(p.tables[0])
+    starts = up(np.array([0, 5], np.int32))
+    got = pa.prefill_int4(bf16(q), starts, p.dev(), tables, up(p.lens), most, most, 0.1)
+    close(got, p.attention(0, q, 0.1, first=35), prefill=True)
+    kc, vc = (x[:, :, :, :].astype(np.float32) for x in R.unpack(p.cache))
+    kb, vb = (bf16(np.nan_to_num(x)) for x in (kc, vc))     # the same elements in a bf16 cache
+    got = pa.prefill(bf16(q), starts, kb, vb, tables, up(p.lens), most, most, 0.1)
+    close(got, p.attention(0, q, 0.1, first=35), prefill=True)
+    k8, v8 = (torch.zeros(kb.shape, dtype=torch.uint8, device="cuda") for _ in range(2))
+    scales = torch.ones((p.nb, 1, 2), device="cuda")
+    assert not pa.prefill_fp8_block(bf16(q), starts, k8, v8, scales, tables, up(p.lens), most, most, 0.1).any()
     clean(pa)
