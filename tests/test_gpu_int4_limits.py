@@ -1,4 +1,5 @@
-"""The 4-bit cache's attention where test_gpu_int4 does not go: slots that nothing was stored in, scores far from zero, bounds near 2^31.
+"""The 4-bit cache's attention where test_gpu_int4 does not go: slots that nothing was stored in, scores far from zero, warps that go
+through many blocks, small elements of q, bounds near 2^31.
 
 Tolerances are those of test_gpu_int4 (`close`), derived there.  Scores here are exact in fp32 where they are large: q has
 powers of two and small multiples of 1/2 in two dims, K small integers, and the softmax scale is the number whose product
@@ -223,6 +224,99 @@ def test_near_and_far_heads_side_by_side(pa, down, seqs, n, kv):
     pre = pa.prefill_int4(bf16(q), torch.arange(seqs + 1, dtype=torch.int32, device="cuda"), cache, t32, lens, 1, n, scale)
     for s in sorted({0, 1, seqs - 1} & set(range(seqs))):
         ref = R.attention(q[s:s + 1], cache[tables[s]].cpu().numpy(), np.arange(mb), n, scale)
+        close(dec[s:s + 1], ref, ("decode", s), steps=n // 16 + 1)
+        close(pre[s:s + 1], ref, ("prefill", s), prefill=True)
+    clean(pa)
+
+
+# ---- many blocks of a warp -----------------------------------------------------------------
+
+@pytest.mark.parametrize("step", [False, True])
+def test_warps_that_go_through_many_blocks(pa, step):
+    """64 sequences of up to 4096 tokens, 8 KV heads, nearly even weights: some 70 blocks a warp, so its ring goes round several
+    times and its sums of codes and of zero points are far larger than what is left of them."""
+    rng = np.random.default_rng(46)
+    seqs, kv, hq, n = 64, 8, 16, 4096
+    lens = rng.integers(n - 600, n + 1, seqs).astype(np.int32)
+    mb = n // B
+    nb = seqs * mb + 3
+    cache = random_cache(47, nb, kv)
+    tables = torch.from_numpy(rng.permutation(nb)[: seqs * mb].reshape(seqs, mb)).cuda()
+    t32, q = tables.to(torch.int32), normal(rng, seqs, hq, D) * 2.0 ** -6
+    if step:
+        cs = table_of(n, 64)
+        k, v = bf16(normal(rng, seqs, kv, D)), bf16(normal(rng, seqs, kv, D))
+        slots = np.take_along_axis(tables.cpu().numpy(), (lens[:, None] - 1) // B, 1)[:, 0].astype(np.int64) * B + (lens - 1) % B
+        other = cache.clone()
+        got = pa.decode_step_int4(bf16(q), k, v, up(cs), cache, t32, up(lens), n, D ** -0.5)
+        qr = pa.rope_kv_store_int4(bf16(q), k, v, up(lens - 1), up(cs), up(slots), other)
+        assert torch.equal(cache, other)
+        assert np.array_equal(bits(got), bits(pa.decode_int4(qr, cache, t32, up(lens), n, D ** -0.5)))
+        q = f64(qr)
+    else:
+        got = pa.decode_int4(bf16(q), cache, t32, up(lens), n, D ** -0.5)
+    for s in (0, 17, 40, 63):
+        ref = R.attention(q[s:s + 1], cache[tables[s]].cpu().numpy(), np.arange(mb), int(lens[s]), D ** -0.5)
+        close(got[s:s + 1], ref, s, steps=int(lens[s]) // 16 + 1)
+    clean(pa)
+
+
+def test_hand_overs_while_the_gpu_is_busy(pa):
+    """Feeder and consumers hand stages over in whatever order the memory gives records: the bits stay what they are alone, while
+    copies and other calls come and go on two more streams."""
+    rng = np.random.default_rng(52)
+    seqs, kv, hq, n = 48, 8, 32, 3000
+    mb = (n + B - 1) // B
+    nb = seqs * mb + 3
+    cache, lens = random_cache(53, nb, kv), up(rng.integers(1, n + 1, seqs).astype(np.int32))
+    t32 = torch.from_numpy(rng.permutation(nb)[: seqs * mb].reshape(seqs, mb).astype(np.int32)).cuda()
+    q, starts = bf16(normal(rng, seqs, hq, D)), torch.arange(seqs + 1, dtype=torch.int32, device="cuda")
+    k, v, cs = bf16(normal(rng, seqs, kv, D)), bf16(normal(rng, seqs, kv, D)), up(table_of(n, 128))
+    big = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    other = torch.empty_like(big)
+    want = bits(pa.decode_int4(q, cache, t32, lens, n, 0.1))
+    c1 = cache.clone()
+    want_step = bits(pa.decode_step_int4(q, k, v, cs, c1, t32, lens, n, 0.1))
+    mine, copies, calls = (torch.cuda.Stream() for _ in range(3))
+    got = []
+    torch.cuda.synchronize()
+    for i in range(20):
+        with torch.cuda.stream(copies):
+            other[: (i + 1) << 23].copy_(big[: (i + 1) << 23])
+        pa.prefill_int4(q, starts, cache, t32, lens, 1, n, 0.1, stream=calls)
+        got.append((pa.decode_int4(q, cache, t32, lens, n, 0.1, stream=mine),
+                    pa.decode_step_int4(q, k, v, cs, c1, t32, lens, n, 0.1, stream=mine)))
+    torch.cuda.synchronize()
+    for a, b in got:
+        assert np.array_equal(bits(a), want) and np.array_equal(bits(b), want_step)
+    clean(pa)
+
+
+# ---- small elements of q -------------------------------------------------------------------
+
+@pytest.mark.parametrize("lens", CUTS)
+def test_elements_of_q_down_to_a_24th_power_count(pa, lens):
+    """The decode's q is f16 after a power of two for each head: elements down to 2^-24 of the head's largest are exact, and here
+    keys make up for them, dim by dim of a word."""
+    rng = np.random.default_rng(54)
+    kv, hq = 2, 16
+    p = Pool(rng, lens, kv)
+    for t in range(B):
+        live = p.cache[..., R.V_SCALES + 2 * t + 1] != 0xFF  # canaries stay
+        n = live.sum()
+        for g, e in ((0, -6), (1, 17), (2, -6), (3, 17)):
+            word = ((e + 127) << 7 | rng.integers(0, 8, n) << 4 | rng.integers(3, 13, n)).astype(np.uint16)
+            at = R.K_SCALES + 8 * t + 2 * g
+            p.cache[live, at:at + 2] = word[:, None].view(np.uint8)
+    q = np.zeros((len(lens), hq, D))
+    q[..., 0], q[..., 70] = 1.0, -0.75
+    for h in range(hq):                                     # the eight dims of a word, in groups 1 and 3
+        q[:, h, (32 if h < 8 else 104) + h % 8] = 2.0 ** -24 * (1 + h / 128)
+    args = (p.dev(), up(p.tables), up(p.lens))
+    dec = pa.decode_int4(bf16(q), *args, max(lens), 1.0)
+    pre = pa.prefill_int4(bf16(q), up(np.arange(len(lens) + 1, dtype=np.int32)), *args, 1, max(lens), 1.0)
+    for s, n in enumerate(lens):
+        ref = p.attention(s, q[s:s + 1], 1.0)
         close(dec[s:s + 1], ref, ("decode", s), steps=n // 16 + 1)
         close(pre[s:s + 1], ref, ("prefill", s), prefill=True)
     clean(pa)
