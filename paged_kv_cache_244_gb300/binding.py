@@ -711,7 +711,8 @@ def read_kv_int4(cache, row_start, first, block_tables, max_rows, num_rows=None,
     """Cached tokens back as bf16 rows (pa_read_kv_int4): rows row_start[s] .. row_start[s + 1] - 1 of the results are
     tokens first[s] .. of sequence s (None: from its start).  Returns k, v [rows, Hkv, 128].
 
-    row_start [S + 1], first [S], block_tables [S, max_blocks] int32; max_rows a host int bounding a sequence's rows.
+    row_start [S + 1], first [S], block_tables [S, max_blocks] int32; max_rows a host int bounding a sequence's rows, the
+    largest best: the call's time follows it.
     Without k_out and v_out, num_rows (a host int) says how many rows there are.
     """
     if k_out is None or v_out is None:

@@ -179,7 +179,8 @@ __global__ void __launch_bounds__(kStoreWarps * 32, 18 / kStoreWarps) rope_int4_
 // A warp takes one record: half a warp a token, a lane the word of 8 dims, K and V of the 16 tokens with
 // all loads ahead of the stores.  Each store instruction writes two rows of 256 bytes.  64 prefixes, 99,801 rows of 8 heads
 // (519 MB): 80.4 us, 6.46 TB/s, 0.95 of the copy rate; one of 2,000 rows, 2 heads: 2.3 us, latency (CTAs of 8 warps: 80.6
-// and 2.9).
+// and 2.9).  The grid is one of num_seqs times the bound's records: CTAs past a sequence's rows load two words and leave,
+// a nanosecond each, so a bound of 131,072 for those 64 costs 2.1 ms, and one of 16,384 rows among 255 of 64 1.05 ms.
 __global__ void __launch_bounds__(kInt4ReadWarps * 32) read_int4_kernel(const ReadInt4Args a) {
   pdl_wait_prior_grid();
   pdl_allow_next_grid();

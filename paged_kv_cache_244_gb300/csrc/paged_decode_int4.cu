@@ -37,13 +37,16 @@
 // does it for all the others, a lane for each: a pass of its loop emits the next job of every consumer that has a
 // free stage.
 //
-// What bounds it: us replayed from a graph, 64 sequences of 64-4096 tokens.  12 / 2 heads (39 MB) 17.7; 32 / 8 heads (156
-// MB, 23.0 at the copy rate) 42.0, the fused step 48.0; one sequence of 2048 tokens 6.7, latency.  Of the 42 about 30 go
-// between a CTA's first record and its last; before them 1.4 for the prefix and 3 for lengths, ids and record, after
-// them the merge's 2.7.  Without the products the same call takes 33, without copies and feeder 32: matrix operands cost
-// 80 masks and shifts a block and head, and with the scales and the softmax 134 instructions of 280 go to the ALU,
-// which takes one in two cycles; bulk copies of this size leave an SM one in about 80 cycles.  Both together cover most
-// of the 52,000 cycles, and what was tried moves between them (32 / 8 heads): each warp feeding itself 44.6; the feeder
+// What bounds it: us replayed from a graph, 64 sequences of 64-4096 tokens.  12 / 2 heads (39 MB) 17.6; 32 / 8 heads (156
+// MB, 23.0 at the copy rate) 42.1, the fused step 48.0; one sequence of 2048 tokens 6.9, latency.  Of the 42.1, 32.5 lie
+// between the first CTA's lengths and the last one's last job: 0.9 for the prefix, 3.3 for ids and the first record, 25.7
+// for the loop (medians of the CTAs; 27.9 the longest); the merge takes 1.9, and the rest are the two kernels' hand-overs
+// and ends.  The whole call without its products takes 33.0, without copies and feeder 34.6 (2 of it to fill the
+// stages once): each is most of the 42.1, and they overlap in part.  Of some 310 instructions a record and kernel 147 go
+// to the ALU, one in two cycles (80 masks and shifts for the operands, the scales, the softmax), and the one feeder is
+// never idle: 77 - 80 cycles a bulk copy of one record.  Neither pipe nor DRAM is full; copies of all KV heads' records
+// of a block (they are adjacent) would take fewer, with another way to cut the work, and are not built.
+// Tried (32 / 8 heads, against 42.0): each warp feeding itself 44.6; the feeder
 // describing jobs and each warp asking for its own copies 47.5, by cp.async 48.1; cp.async by 1, 2, 3 or 4 feeders 60,
 // 46.0, 43.4, 44.0; two feeders for bulk copies 43.2; block ids asked for a job ahead 45.0; 7, 13 or 15 consumers 48.4,
 // 44.1, 43.0 (the last with 128 registers); the right shift as a product's upper half 44.8; jobs of four blocks 46.7.

@@ -19,7 +19,10 @@
 //       (0 * NaN would reach queries that do not see its token), and the rows that do see it become NaN when
 //       out is written.
 // Tensor memory per CTA (256 columns): S_j in columns 64 (j & 1) .. + 63, O in 128-255; a row's P_j (64 bf16,
-// 32 columns) is written by its thread over the S_j it has read, and is the A operand of P V from there.
+// 32 columns) is written by its thread over the S_j it has read, and is the A operand of P V from there.  P is bf16, and l
+// adds it unrounded: both operands of an MMA have one type, and V's elements reach from 2^-40 to 2^44, past f16.  That costs
+// up to 2^-8 of a weight where f16 (the decode, whose V is codes) costs 2^-11: 0.0021 - 0.0023 of the largest value
+// against 64 bits, for 0.0016 - 0.0017.
 // q goes in after a power of two for each row that brings its largest magnitude to [128, 256), so that no
 // product leaves fp32's range whatever the magnitudes of q and of the scales.
 // Shared memory per CTA: q (32 KiB, the A operand of S; out leaves through its first half), two 16 KiB stages
@@ -29,7 +32,8 @@
 // of them written by the converters.  Of a tile's 64 keys (128 bytes a cycle): operands in 256 cycles, S out of tensor
 // memory and P into it 384, q as A operand 256, K and V as B operands 256, rescaling and the ends of a tile the rest: some
 // 1,275 of the 1,637 cycles that two CTAs of an SM take for one tile each.  4 prompts of 2048 tokens, 12 / 2 heads: 70.5
-// us (52 GFLOP, 0.73 PFLOP/s); 16 chunks of 256 over 1792: 72.5; 8 chunks of 5 over 6000, 28 / 4 heads, split: 27.3.
+// us (52 GFLOP, 0.73 PFLOP/s); 16 chunks of 256 over 1792: 72.5 (75 on some boxes); 8 chunks of 5 over 6000, 28 / 4 heads,
+// split: 27.2.
 // Registers loaded only when their stage begins 79.4 / 95.7 / 30.1; K and V by three warps each 80 - 103; records brought
 // to L2 ahead 73 / 76 / 28; softmax warps without a row left out: no change.
 
