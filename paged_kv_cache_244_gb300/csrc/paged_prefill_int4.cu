@@ -32,7 +32,7 @@
 // of them written by the converters.  Of a tile's 64 keys (128 bytes a cycle): operands in 256 cycles, S out of tensor
 // memory and P into it 384, q as A operand 256, K and V as B operands 256, rescaling and the ends of a tile the rest: some
 // 1,275 of the 1,637 cycles that two CTAs of an SM take for one tile each.  4 prompts of 2048 tokens, 12 / 2 heads: 70.5
-// us (52 GFLOP, 0.73 PFLOP/s); 16 chunks of 256 over 1792: 72.5 (75 on some boxes); 8 chunks of 5 over 6000, 28 / 4 heads,
+// us (52 GFLOP, 0.73 PFLOP/s); 16 chunks of 256 over 1792: 72.5 (75 on some GPUs); 8 chunks of 5 over 6000, 28 / 4 heads,
 // split: 27.2.
 // Registers loaded only when their stage begins 79.4 / 95.7 / 30.1; K and V by three warps each 80 - 103; records brought
 // to L2 ahead 73 / 76 / 28; softmax warps without a row left out: no change.

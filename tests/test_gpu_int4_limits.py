@@ -14,7 +14,7 @@ import torch
 
 import int4_ref as R
 import serving_ref as S
-from test_gpu_int4 import B, D, Pool, bf16, bits, clean, close, f64, normal, pa, table_of, turned, up  # noqa: F401
+from test_gpu_int4 import B, D, Pool, bf16, bits, clean, close, f64, normal, pa, table_of, up  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -37,7 +37,7 @@ def test_slots_never_stored_read_as_zeros(pa):
     lens, kv, hq = [40, 16, 1, 700, 33], 2, 12
     p = Pool(rng, lens, kv, canary=False)
     p.cache[:] = 0
-    T, cs = 0, np.concatenate([np.ones((1, 64)), np.zeros((1, 64))], axis=1).astype(np.float32)
+    cs = np.concatenate([np.ones((1, 64)), np.zeros((1, 64))], axis=1).astype(np.float32)
     cache, slots = up(p.cache), []
     for s, n in enumerate(lens):                            # sequence 1 has nothing stored, the others a part
         for t in range(n):
@@ -229,6 +229,24 @@ def test_near_and_far_heads_side_by_side(pa, down, seqs, n, kv):
     clean(pa)
 
 
+@pytest.mark.parametrize("lens", CUTS)
+@pytest.mark.parametrize("size", [2.0 ** 7, 2.0 ** 12, 2.0 ** 70])
+def test_the_step_is_store_then_decode_for_far_scores(pa, lens, size):
+    rng = np.random.default_rng(55)
+    kv, hq, n = 2, 14, len(lens)
+    p = Pool(rng, lens, kv)
+    q, k, v = bf16(size * normal(rng, n, hq, D)), bf16(normal(rng, n, kv, D)), bf16(normal(rng, n, kv, D))
+    cs, c1, c2 = up(table_of(max(lens), 64)), p.dev(), p.dev()
+    pos = (p.lens - 1).astype(np.int32)
+    slots = p.tables[np.arange(n), pos // B].astype(np.int64) * B + pos % B
+    out = pa.decode_step_int4(q, k, v, cs, c1, up(p.tables), up(p.lens), max(lens), 1.0)
+    qr = pa.rope_kv_store_int4(q, k, v, up(pos), cs, up(slots), c2, q_out=torch.empty_like(q))
+    assert torch.equal(c1, c2)
+    assert np.array_equal(bits(out), bits(pa.decode_int4(qr, c2, up(p.tables), up(p.lens), max(lens), 1.0)))
+    assert np.isfinite(f64(out)).all()
+    clean(pa)
+
+
 # ---- many blocks of a warp -----------------------------------------------------------------
 
 @pytest.mark.parametrize("step", [False, True])
@@ -336,8 +354,7 @@ def test_prefill_with_the_loosest_bounds(pa, hq):
     starts = up(np.array([0, 5], np.int32))
     got = pa.prefill_int4(bf16(q), starts, p.dev(), tables, up(p.lens), most, most, 0.1)
     close(got, p.attention(0, q, 0.1, first=35), prefill=True)
-    kc, vc = (x[:, :, :, :].astype(np.float32) for x in R.unpack(p.cache))
-    kb, vb = (bf16(np.nan_to_num(x)) for x in (kc, vc))     # the same elements in a bf16 cache
+    kb, vb = (bf16(np.nan_to_num(x)) for x in R.unpack(p.cache))      # the same elements in a bf16 cache
     got = pa.prefill(bf16(q), starts, kb, vb, tables, up(p.lens), most, most, 0.1)
     close(got, p.attention(0, q, 0.1, first=35), prefill=True)
     k8, v8 = (torch.zeros(kb.shape, dtype=torch.uint8, device="cuda") for _ in range(2))
